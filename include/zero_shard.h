@@ -347,6 +347,135 @@ zs_bf16 *zero_shard_offload_params(zs_offload *o);
 int zero_shard_offload_wait(zs_offload *o);
 int zero_shard_offload_free(zs_offload *o);
 
+/* ---------------------------------------------------------------------------
+ * The optimizer and the norm of the parameters around the shard step: the
+ * Muon update for a rank's weight matrices, and layer norm, whose gains and
+ * biases stay with the shard step.  These calls take no handle: they queue
+ * kernel launches on the descriptor's stream and nothing else (no allocation,
+ * no memset, no synchronisation), so they can be captured in a HIP graph, and
+ * every scratch byte is a workspace the caller owns, which holds nothing
+ * between calls.  Calls that overlap on different streams need different
+ * workspaces.  Same inputs => same bits.  Errors as above: everything is
+ * checked before anything is queued; sizes of zero are valid and queue
+ * nothing, except that gradients of no rows are written as zeros. */
+typedef enum zs_dtype { ZS_F32 = 0, ZS_BF16 = 1, ZS_F16 = 2 } zs_dtype;
+
+/* Layer norm over rows of `cols` elements, column stride 1, row strides ld_*
+ * in elements (0: cols).  Statistics, sums and products are binary32, each
+ * output is rounded once to its type (nearest even). */
+typedef struct zs_layernorm_desc {
+  int64_t rows, cols;  /* rows >= 0, 1 <= cols <= 2^31                        */
+  int32_t dtype;       /* zs_dtype of x, residual, sum, y, dy, dsum, dx       */
+  int32_t param_dtype; /* of gamma, beta, dgamma, dbeta: ZS_F32 or dtype      */
+  float eps;           /* >= 0, finite                                        */
+  int64_t ld_x, ld_residual, ld_sum, ld_y; /* forward                         */
+  int64_t ld_dy, ld_dsum, ld_dx;           /* backward (which uses ld_x too)  */
+  void *stream;        /* hipStream_t, NULL = null stream                     */
+} zs_layernorm_desc;
+
+/* Forward:  s = round(x + residual), stored to sum, or s = x when residual
+ * and sum are NULL (both or neither);
+ *   mean = sum_c s / cols;  rstd = 1 / sqrt(sum_c (s - mean)^2 / cols + eps);
+ *   y = (s - mean) rstd gamma + beta.
+ * gamma and beta (cols elements) may each be NULL (1 and 0); mean and rstd
+ * (fp32[rows]) may each be NULL when no backward pass follows.  A row that
+ * holds an infinity or NaN gives NaN in that row only.  sum may be x's or
+ * residual's own buffer with the same row stride, y may be x's (or
+ * residual's) unless sum is; otherwise outputs overlap nothing.
+ * Errors: ZS_EINVAL, ZS_EALIGN (a pointer not aligned to its element),
+ * ZS_EDEVICE, ZS_EHIP. */
+int zero_shard_layernorm(const zs_layernorm_desc *d, const void *x, const void *residual,
+                         const void *gamma, const void *beta, void *sum, void *y, float *mean,
+                         float *rstd);
+
+/* Bytes of workspace that zero_shard_layernorm_bwd needs for d when dgamma or
+ * dbeta is asked for, or -1 for an invalid descriptor. */
+int64_t zero_shard_layernorm_workspace(const zs_layernorm_desc *d);
+
+/* Backward of y = h gamma + beta, h = (x - mean) rstd, where x is what was
+ * normalised (the forward pass's sum when it had a residual), with its saved
+ * mean and rstd:
+ *   g = dy gamma;  dx = rstd (g - sum_c g / cols - h sum_c (g h) / cols) + dsum
+ *   dgamma = sum_rows dy h;  dbeta = sum_rows dy
+ * dsum, the gradient that reaches the sum from elsewhere (the residual path),
+ * may be NULL; dx is then the gradient of x and of residual alike.  gamma
+ * may be NULL (1); dgamma and dbeta may each be NULL (not computed); they are
+ * written, not added to.  dx may be dy's, x's or dsum's own buffer with the same
+ * row stride.  workspace: device, 16-byte aligned, at least
+ * zero_shard_layernorm_workspace(d) bytes (may be NULL when neither gradient
+ * is asked for).  Errors: ZS_EINVAL, ZS_EALIGN, ZS_EDEVICE, ZS_EHIP. */
+int zero_shard_layernorm_bwd(const zs_layernorm_desc *d, const void *dy, const void *x,
+                             const void *gamma, const float *mean, const float *rstd,
+                             const void *dsum, void *dx, void *dgamma, void *dbeta,
+                             void *workspace, int64_t workspace_bytes);
+
+/* The Muon update over a flat range of n elements: one weight matrix, or
+ * several of the same shape one after another.  A rank owns whole matrices;
+ * contributions are rows as for zero_shard_step.  All arrays 16-byte aligned. */
+typedef struct zs_muon_desc {
+  int64_t n;           /* elements, >= 0                                      */
+  int32_t n_d;         /* contributions averaged, 1..ZS_MAX_ND                */
+  int32_t nesterov;    /* 1: look ahead; 0: plain momentum                    */
+  int32_t dtype;       /* of the update matrix: ZS_F32 or ZS_BF16             */
+  float mu;            /* momentum, in [0, 1)                                 */
+  float weight_decay;  /* >= 0, decoupled                                     */
+  void *stream;        /* hipStream_t, NULL = null stream                     */
+} zs_muon_desc;
+
+/* gbar as in the shard step (binary64 sum in rank order, averaged, rounded to
+ * binary32);  M' = mu M + gbar;  u = gbar + mu M' (nesterov) or M'; binary64
+ * from binary32 values, M' rounded to binary32 and u to its type once each.
+ * contrib: HOST array of n_d device pointers to bf16[n]; m_in, m_out: fp32[n],
+ * may be the same buffer; update: u.
+ * Errors: ZS_EINVAL, ZS_EALIGN, ZS_EDEVICE, ZS_EHIP. */
+int zero_shard_muon_momentum(const zs_muon_desc *d, const zs_bf16 *const *contrib,
+                             const float *m_in, float *m_out, void *update);
+
+/* theta' = theta - (lr wd) theta - (lr scale) o, binary64 from binary32 and
+ * bf16 values, rounded once; p = bf16(theta').  o: bf16[n], the
+ * orthogonalised update; scale: the caller's adjustment for the matrix's
+ * shape, e.g. 0.2 sqrt(max(rows, cols)); master_in, master_out: fp32[n], may be
+ * the same buffer; param_out: bf16[n], the buffer the all-gather sends.
+ * Errors: ZS_EINVAL (lr negative or not finite, ...), ZS_EALIGN, ZS_EDEVICE,
+ * ZS_EHIP. */
+int zero_shard_muon_apply(const zs_muon_desc *d, const zs_bf16 *o, float lr, float scale,
+                          const float *master_in, float *master_out, zs_bf16 *param_out);
+
+#define ZS_ORTHO_MAX_STEPS 32 /* most Newton-Schulz steps of one call */
+
+/* Orthogonalisation of `batch` matrices of rows x cols, column stride 1. */
+typedef struct zs_ortho_desc {
+  int64_t batch, rows, cols;  /* >= 0; batch <= 65535, sides <= 2^20          */
+  int64_t ld_in, ld_out;      /* row strides in elements (0: cols)            */
+  int64_t stride_in, stride_out; /* from matrix to matrix (0: rows * ld); the
+                                 output's matrices must not overlap           */
+  int32_t dtype;              /* zs_dtype of the input                        */
+  int32_t steps;              /* Newton-Schulz steps, 1..ZS_ORTHO_MAX_STEPS    */
+  const float *coeffs;        /* HOST array of 3 * steps floats, (a, b, c) of
+                                 each step; NULL: (3.4445, -4.7750, 2.0315)   */
+  float eps;                  /* >= 0, added to the norm                      */
+  void *stream;               /* hipStream_t, NULL = null stream              */
+} zs_ortho_desc;
+
+/* Bytes of workspace that zero_shard_ortho needs for d, or -1 for an invalid
+ * descriptor. */
+int64_t zero_shard_ortho_workspace(const zs_ortho_desc *d);
+
+/* Per matrix: X = G / (|G|_F + eps) (the norm in binary64), then `steps` times
+ *   A = X X^T;  X = a X + (b A + c A A) X
+ * (X^T X and products from the right when rows > cols); o = bf16(X).
+ * Products are summed in binary32; X, A and a I + b A + c A A are rounded to
+ * binary16 times 2^-11 between products, so their entries must stay below 32
+ * (coefficients that bring singular values in [0, 1] towards 1 keep them
+ * below 4), and entries of X under 2^-36 vanish: a matrix whose norm is far
+ * below eps gives zeros.  A zero matrix gives zeros (eps > 0; NaN with eps = 0);
+ * a matrix that holds an infinity or NaN gives NaN in that matrix only.
+ * g: input; o: bf16 output, overlapping nothing else; workspace: device,
+ * 256-byte aligned, at least zero_shard_ortho_workspace(d) bytes.
+ * Errors: ZS_EINVAL, ZS_EALIGN, ZS_EDEVICE, ZS_EHIP. */
+int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *workspace,
+                     int64_t workspace_bytes);
+
 /* Wait for the handle's stream, release its scratch and the handle.
  * Passing NULL is a no-op returning ZS_OK. */
 int zero_shard_free(zs_handle *h);

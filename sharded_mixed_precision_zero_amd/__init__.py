@@ -20,6 +20,8 @@ LIB_PATH = os.path.join(_HERE, "libzeroshard.so")
 ZS_OK, ZS_EINVAL, ZS_EALIGN, ZS_ENOMEM, ZS_EHIP, ZS_EDEVICE, ZS_ESTATE, ZS_ETOOBIG = (
     0, -1, -2, -3, -4, -5, -6, -7)
 ZS_MAX_ND = 64
+ZS_F32, ZS_BF16, ZS_F16 = 0, 1, 2
+ZS_ORTHO_MAX_STEPS = 32
 # how a call's work is split into kernel launches (zero_shard.h)
 ZS_NORM_LAUNCH_LEN = 1 << 26
 ZS_WIDE_LAUNCH_LEN = 1 << 25
@@ -60,6 +62,53 @@ class zs_desc(ctypes.Structure):  # noqa: N801  (the C name)
         ("q_codes", ctypes.c_void_p),
         ("q_scales", ctypes.c_void_p),
         ("gbar_ws", ctypes.c_void_p),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class zs_layernorm_desc(ctypes.Structure):  # noqa: N801
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("param_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("ld_x", ctypes.c_int64),
+        ("ld_residual", ctypes.c_int64),
+        ("ld_sum", ctypes.c_int64),
+        ("ld_y", ctypes.c_int64),
+        ("ld_dy", ctypes.c_int64),
+        ("ld_dsum", ctypes.c_int64),
+        ("ld_dx", ctypes.c_int64),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class zs_muon_desc(ctypes.Structure):  # noqa: N801
+    _fields_ = [
+        ("n", ctypes.c_int64),
+        ("n_d", ctypes.c_int32),
+        ("nesterov", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("mu", ctypes.c_float),
+        ("weight_decay", ctypes.c_float),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class zs_ortho_desc(ctypes.Structure):  # noqa: N801
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld_in", ctypes.c_int64),
+        ("ld_out", ctypes.c_int64),
+        ("stride_in", ctypes.c_int64),
+        ("stride_out", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("steps", ctypes.c_int32),
+        ("coeffs", ctypes.POINTER(ctypes.c_float)),
+        ("eps", ctypes.c_float),
         ("stream", ctypes.c_void_p),
     ]
 
@@ -124,6 +173,24 @@ _lib.zero_shard_offload_free.restype = ctypes.c_int
 _lib.zero_shard_offload_free.argtypes = [_handle_p]
 _lib.zero_shard_quant.restype = ctypes.c_int
 _lib.zero_shard_quant.argtypes = [_handle_p, ctypes.c_int32]
+_lib.zero_shard_layernorm.restype = ctypes.c_int
+_lib.zero_shard_layernorm.argtypes = [ctypes.POINTER(zs_layernorm_desc)] + [ctypes.c_void_p] * 8
+_lib.zero_shard_layernorm_workspace.restype = ctypes.c_int64
+_lib.zero_shard_layernorm_workspace.argtypes = [ctypes.POINTER(zs_layernorm_desc)]
+_lib.zero_shard_layernorm_bwd.restype = ctypes.c_int
+_lib.zero_shard_layernorm_bwd.argtypes = ([ctypes.POINTER(zs_layernorm_desc)]
+                                          + [ctypes.c_void_p] * 10 + [ctypes.c_int64])
+_lib.zero_shard_muon_momentum.restype = ctypes.c_int
+_lib.zero_shard_muon_momentum.argtypes = [ctypes.POINTER(zs_muon_desc)] + [ctypes.c_void_p] * 4
+_lib.zero_shard_muon_apply.restype = ctypes.c_int
+_lib.zero_shard_muon_apply.argtypes = [ctypes.POINTER(zs_muon_desc), ctypes.c_void_p,
+                                       ctypes.c_float, ctypes.c_float, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_void_p]
+_lib.zero_shard_ortho_workspace.restype = ctypes.c_int64
+_lib.zero_shard_ortho_workspace.argtypes = [ctypes.POINTER(zs_ortho_desc)]
+_lib.zero_shard_ortho.restype = ctypes.c_int
+_lib.zero_shard_ortho.argtypes = [ctypes.POINTER(zs_ortho_desc), ctypes.c_void_p, ctypes.c_void_p,
+                                  ctypes.c_void_p, ctypes.c_int64]
 _lib.zero_shard_free.restype = ctypes.c_int
 _lib.zero_shard_free.argtypes = [_handle_p]
 _lib.zero_shard_strerror.restype = ctypes.c_char_p
@@ -139,7 +206,9 @@ EXPORTS = ("zero_shard_init", "zero_shard_gnorm", "zero_shard_gnorm_noalloc", "z
            "zero_shard_quant", "zero_shard_dequant",
            "zero_shard_host_step", "zero_shard_offload_init", "zero_shard_offload_step",
            "zero_shard_offload_params", "zero_shard_offload_wait", "zero_shard_offload_free",
-           "zero_shard_free", "zero_shard_strerror", "zero_shard_len")
+           "zero_shard_layernorm", "zero_shard_layernorm_workspace", "zero_shard_layernorm_bwd",
+           "zero_shard_muon_momentum", "zero_shard_muon_apply", "zero_shard_ortho_workspace",
+           "zero_shard_ortho", "zero_shard_free", "zero_shard_strerror", "zero_shard_len")
 
 
 class ZeroShardError(RuntimeError):
@@ -151,6 +220,11 @@ class ZeroShardError(RuntimeError):
 def _check(rc: int, what: str) -> None:
     if rc != ZS_OK:
         raise ZeroShardError(rc, what)
+
+
+def check(rc: int) -> None:
+    """Raise ZeroShardError if a C-named call returned a negative status."""
+    _check(rc, "zero_shard call")
 
 
 def _ptr(t) -> int | None:
@@ -349,7 +423,101 @@ def zero_shard_free(h) -> int:
     return _lib.zero_shard_free(h)
 
 
-# ------------------------------------------------------------- owner object
+def dtype_code(dtype) -> int:
+    """zs_dtype of a torch dtype (float32, bfloat16, float16)."""
+    try:
+        return _DTYPES[dtype]
+    except KeyError:
+        raise ZeroShardError(ZS_EINVAL, f"dtype {dtype}") from None
+
+
+_DTYPES = {torch.float32: ZS_F32, torch.bfloat16: ZS_BF16, torch.float16: ZS_F16}
+
+
+def _stream(stream) -> int:
+    """hipStream_t of a torch stream (default: the current one)."""
+    return int((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+
+
+def layernorm_desc(*, rows: int, cols: int, dtype=torch.bfloat16, param_dtype=None,
+                   eps: float = 1e-5, stream=None, **ld: int) -> zs_layernorm_desc:
+    """dtype, param_dtype: torch dtypes (param_dtype defaults to dtype); ld:
+    the row strides ld_x, ld_residual, ... that are not cols; stream: a torch
+    stream (default: the current one)."""
+    return zs_layernorm_desc(
+        rows=int(rows), cols=int(cols), dtype=dtype_code(dtype),
+        param_dtype=dtype_code(dtype if param_dtype is None else param_dtype), eps=eps,
+        stream=_stream(stream), **ld)
+
+
+def zero_shard_layernorm(desc: zs_layernorm_desc, x, residual, gamma, beta, sum_out, y, mean,
+                         rstd) -> int:
+    return _lib.zero_shard_layernorm(ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(gamma),
+                                     _ptr(beta), _ptr(sum_out), _ptr(y), _ptr(mean), _ptr(rstd))
+
+
+def zero_shard_layernorm_workspace(desc: zs_layernorm_desc) -> int:
+    return int(_lib.zero_shard_layernorm_workspace(ctypes.byref(desc)))
+
+
+def zero_shard_layernorm_bwd(desc: zs_layernorm_desc, dy, x, gamma, mean, rstd, dsum, dx, dgamma,
+                             dbeta, workspace) -> int:
+    """workspace: a contiguous device tensor (its size in bytes is passed on)
+    or None."""
+    return _lib.zero_shard_layernorm_bwd(
+        ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dsum),
+        _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), _nbytes(workspace))
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else int(t.numel() * t.element_size())
+
+
+def muon_desc(*, n: int, n_d: int = 1, mu: float = 0.95, nesterov: bool = True,
+              dtype=torch.bfloat16, weight_decay: float = 0.0, stream=None) -> zs_muon_desc:
+    return zs_muon_desc(n=int(n), n_d=int(n_d), nesterov=int(bool(nesterov)),
+                        dtype=dtype_code(dtype), mu=mu, weight_decay=weight_decay,
+                        stream=_stream(stream))
+
+
+def zero_shard_muon_momentum(desc: zs_muon_desc, contrib, m_in, m_out, update) -> int:
+    return _lib.zero_shard_muon_momentum(ctypes.byref(desc), contrib_table(contrib), _ptr(m_in),
+                                         _ptr(m_out), _ptr(update))
+
+
+def zero_shard_muon_apply(desc: zs_muon_desc, o, lr: float, scale: float, master_in, master_out,
+                          param_out) -> int:
+    return _lib.zero_shard_muon_apply(ctypes.byref(desc), _ptr(o), float(lr), float(scale),
+                                      _ptr(master_in), _ptr(master_out), _ptr(param_out))
+
+
+def ortho_desc(*, batch: int = 1, rows: int, cols: int, dtype=torch.bfloat16, steps: int = 5,
+               coeffs=None, eps: float = 1e-7, ld_in: int = 0, ld_out: int = 0,
+               stride_in: int = 0, stride_out: int = 0, stream=None) -> zs_ortho_desc:
+    """coeffs: (a, b, c) of every step, or one (a, b, c) per step, or None."""
+    d = zs_ortho_desc(batch=int(batch), rows=int(rows), cols=int(cols), ld_in=int(ld_in),
+                      ld_out=int(ld_out), stride_in=int(stride_in), stride_out=int(stride_out),
+                      dtype=dtype_code(dtype), steps=int(steps), eps=eps, stream=_stream(stream))
+    if coeffs is not None:
+        each = list(coeffs) if hasattr(coeffs[0], "__len__") else [coeffs] * int(steps)
+        if len(each) != int(steps) or any(len(k) != 3 for k in each):
+            raise ZeroShardError(ZS_EINVAL, "coeffs")
+        d._keep = (ctypes.c_float * (3 * len(each)))(*[float(v) for k in each for v in k])
+        d.coeffs = ctypes.cast(d._keep, ctypes.POINTER(ctypes.c_float))
+    return d
+
+
+def zero_shard_ortho_workspace(desc: zs_ortho_desc) -> int:
+    return int(_lib.zero_shard_ortho_workspace(ctypes.byref(desc)))
+
+
+def zero_shard_ortho(desc: zs_ortho_desc, g, o, workspace) -> int:
+    """workspace: a contiguous device tensor (its size in bytes is passed on)."""
+    return _lib.zero_shard_ortho(ctypes.byref(desc), _ptr(g), _ptr(o), _ptr(workspace),
+                                 _nbytes(workspace))
+
+
+# ------------------------------------------------------------ owner objects
 
 class ZeroShard:
     """One rank's shard step over caller-owned torch tensors.
@@ -443,3 +611,144 @@ class ZeroShard:
                 zero_shard_free(self.h)
         except Exception:
             pass
+
+
+def _require(ok: bool, what: str) -> None:
+    if not ok:
+        raise ZeroShardError(ZS_EINVAL, what)
+
+
+class ZeroLayerNorm:
+    """Layer norm of (rows, cols) tensors, forward and backward, with the
+    saved statistics and the workspace of the gradient reduction.
+
+    All tensors are on the current device; x, residual, sum_out, y, dy, dsum
+    and dx are (rows, cols) of ``dtype`` with column stride 1, the parameters
+    and their gradients contiguous (cols,) of ``param_dtype`` (default:
+    dtype).  ``stream`` is a torch stream (default: the current one at
+    construction)."""
+
+    def __init__(self, *, rows: int, cols: int, dtype=torch.bfloat16, param_dtype=None,
+                 eps: float = 1e-5, stream=None):
+        self.dtype, self.param_dtype = dtype, dtype if param_dtype is None else param_dtype
+        self.shape = (int(rows), int(cols))
+        self._stream = torch.cuda.current_stream() if stream is None else stream
+        self.desc = layernorm_desc(rows=rows, cols=cols, dtype=dtype, param_dtype=param_dtype,
+                                   eps=eps, stream=self._stream)
+        size = zero_shard_layernorm_workspace(self.desc)
+        _require(size >= 0, "layer norm's sizes")
+        with torch.cuda.stream(self._stream):
+            self.mean = torch.empty(rows, device="cuda", dtype=torch.float32)
+            self.rstd = torch.empty(rows, device="cuda", dtype=torch.float32)
+            self.workspace = torch.empty(size, device="cuda", dtype=torch.uint8)
+
+    def _row(self, t, what: str) -> int:
+        """Row stride of a (rows, cols) tensor; 0 for None."""
+        if t is None:
+            return 0
+        _require(t.shape == self.shape and t.dtype == self.dtype and t.is_cuda
+                 and (t.stride(1) == 1 or self.shape[1] == 1), what)
+        return t.stride(0) if self.shape[0] > 1 else 0
+
+    def _param(self, t, what: str) -> None:
+        if t is not None:
+            _require(t.shape == self.shape[1:] and t.dtype == self.param_dtype and t.is_cuda
+                     and t.is_contiguous(), what)
+
+    def forward(self, x, y, *, gamma=None, beta=None, residual=None, sum_out=None) -> None:
+        """y = LN(x), or LN(sum_out) with sum_out = x + residual; keeps the
+        rows' mean and rstd for backward."""
+        d = self.desc
+        d.ld_x, d.ld_y = self._row(x, "x"), self._row(y, "y")
+        d.ld_residual, d.ld_sum = self._row(residual, "residual"), self._row(sum_out, "sum_out")
+        self._param(gamma, "gamma")
+        self._param(beta, "beta")
+        _check(zero_shard_layernorm(d, x, residual, gamma, beta, sum_out, y, self.mean,
+                                    self.rstd), "zero_shard_layernorm")
+
+    def backward(self, dy, x, dx, *, gamma=None, dgamma=None, dbeta=None, dsum=None, mean=None,
+                 rstd=None) -> None:
+        """x: what was normalised (sum_out with a residual); mean, rstd: the
+        saved statistics (default: those of the last forward)."""
+        d = self.desc
+        d.ld_dy, d.ld_x = self._row(dy, "dy"), self._row(x, "x")
+        d.ld_dx, d.ld_dsum = self._row(dx, "dx"), self._row(dsum, "dsum")
+        self._param(gamma, "gamma")
+        self._param(dgamma, "dgamma")
+        self._param(dbeta, "dbeta")
+        for t in (mean, rstd):
+            _require(t is None or (t.shape == self.shape[:1] and t.dtype == torch.float32
+                                   and t.is_cuda and t.is_contiguous()), "mean, rstd")
+        _check(zero_shard_layernorm_bwd(d, dy, x, gamma, self.mean if mean is None else mean,
+                                        self.rstd if rstd is None else rstd, dsum, dx, dgamma,
+                                        dbeta, self.workspace), "zero_shard_layernorm_bwd")
+
+
+class ZeroOrtho:
+    """Newton-Schulz orthogonalisation of (batch, rows, cols) tensors of
+    ``dtype`` into bf16 ones, with its workspace; a 2-D tensor is a batch of
+    one.  Column stride 1; ``stream`` as for ZeroLayerNorm."""
+
+    def __init__(self, *, batch: int = 1, rows: int, cols: int, dtype=torch.bfloat16,
+                 steps: int = 5, coeffs=None, eps: float = 1e-7, stream=None):
+        self.shape, self.dtype = (int(batch), int(rows), int(cols)), dtype
+        self._stream = torch.cuda.current_stream() if stream is None else stream
+        self.desc = ortho_desc(batch=batch, rows=rows, cols=cols, dtype=dtype, steps=steps,
+                               coeffs=coeffs, eps=eps, stream=self._stream)
+        size = zero_shard_ortho_workspace(self.desc)
+        _require(size >= 0, "ortho's sizes")
+        with torch.cuda.stream(self._stream):
+            self.workspace = torch.empty(size, device="cuda", dtype=torch.uint8)
+
+    def _strides(self, t, dtype, what: str) -> tuple[int, int]:
+        b, r, c = self.shape
+        _require((t.shape == self.shape or (b == 1 and t.shape == self.shape[1:]))
+                 and t.dtype == dtype and t.is_cuda and (t.stride(-1) == 1 or c == 1), what)
+        ld = t.stride(-2) if r > 1 else c
+        return ld, t.stride(0) if b > 1 else r * ld
+
+    def __call__(self, g, o) -> None:
+        """o = the orthogonalised g."""
+        d = self.desc
+        d.ld_in, d.stride_in = self._strides(g, self.dtype, "g")
+        d.ld_out, d.stride_out = self._strides(o, torch.bfloat16, "o")
+        _check(zero_shard_ortho(d, g, o, self.workspace), "zero_shard_ortho")
+
+
+class ZeroMuon:
+    """One rank's Muon step over ``batch`` matrices of rows x cols that lie one
+    after another in caller-owned torch tensors.
+
+    master, momentum: float32[n]; param_out: bf16 (or 16-bit) [n], n = batch *
+    rows * cols, 16-byte aligned.  ``update_dtype``: of the momentum's update
+    matrix (bf16 or float32).  ``scale``: the update's scale (default
+    0.2 sqrt(max(rows, cols)), which matches an Adam update's size)."""
+
+    def __init__(self, *, n_d: int, rows: int, cols: int, master, momentum, param_out,
+                 batch: int = 1, mu: float = 0.95, nesterov: bool = True,
+                 weight_decay: float = 0.0, steps: int = 5, coeffs=None, eps: float = 1e-7,
+                 scale: float | None = None, update_dtype=torch.bfloat16, stream=None):
+        n = int(batch) * int(rows) * int(cols)
+        for t, size, what in ((master, 4, "master"), (momentum, 4, "momentum"),
+                              (param_out, 2, "param_out")):
+            _require(t.numel() == n and t.element_size() == size and t.is_contiguous()
+                     and t.is_cuda, what)
+        self._stream = torch.cuda.current_stream() if stream is None else stream
+        self.master, self.momentum, self.param_out = master, momentum, param_out
+        self.scale = 0.2 * max(rows, cols) ** 0.5 if scale is None else float(scale)
+        self.desc = muon_desc(n=n, n_d=n_d, mu=mu, nesterov=nesterov, dtype=update_dtype,
+                              weight_decay=weight_decay, stream=self._stream)
+        self.ortho = ZeroOrtho(batch=batch, rows=rows, cols=cols, dtype=update_dtype, steps=steps,
+                               coeffs=coeffs, eps=eps, stream=self._stream)
+        with torch.cuda.stream(self._stream):
+            self.update = torch.empty(batch, rows, cols, device="cuda", dtype=update_dtype)
+            self.o = torch.empty(batch, rows, cols, device="cuda", dtype=torch.bfloat16)
+
+    def step(self, contrib, lr: float) -> None:
+        """Momentum over the mean of the contributions, its orthogonalisation,
+        and the weight update; param_out holds the bf16 weights."""
+        _check(zero_shard_muon_momentum(self.desc, contrib, self.momentum, self.momentum,
+                                        self.update), "zero_shard_muon_momentum")
+        self.ortho(self.update, self.o)
+        _check(zero_shard_muon_apply(self.desc, self.o, lr, self.scale, self.master, self.master,
+                                     self.param_out), "zero_shard_muon_apply")
