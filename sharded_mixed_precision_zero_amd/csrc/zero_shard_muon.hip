@@ -315,16 +315,19 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("" ::: "memory");
 }
 
-// T x T tiles of C, WR x WC waves.  64 of k at a time go from global memory
-// straight into LDS, double buffered; a row of 64 is eight 16-byte pieces,
-// piece c of row r at position c ^ (r & 7), so the eight rows that one read
-// instruction serves together lie in different banks.
-template <int KIND, int T, int WR, int WC>
+// T x T tiles of C, WR x WC waves, S buffers of BK of k.  The operands go from
+// global memory straight into LDS, S - 2 buffers ahead of their use, so a
+// buffer costs one barrier; a row of BK is BK / 8 pieces of 16 bytes, piece c
+// of row r at position c ^ key(r), so the rows that one read instruction
+// serves together lie in different banks.  The registers of the next 32 of k
+// are read while the matrix cores work on the present ones.
+template <int KIND, int T, int WR, int WC, int BK, int S>
 __global__ void __launch_bounds__(WR *WC * 64) ortho_mul_kernel(const MulArgs A) {
   constexpr int NW = WR * WC, TM = T / WR / 16, TN = T / WC / 16;
-  constexpr int L = T / 8 / NW;  // load instructions per wave and operand
+  constexpr int PIECES = BK / 8, RPI = 64 / PIECES;  // per row; rows per load instruction
+  constexpr int L = T / RPI / NW;  // load instructions per wave, operand and buffer
   constexpr int PITCH = T + 8;
-  constexpr int STAGE = 2 * 2 * T * 64, EPI = T * PITCH;
+  constexpr int BUF = 2 * T * BK, STAGE = S * BUF, EPI = T * PITCH;
   __shared__ __align__(16) _Float16 lds[STAGE > EPI ? STAGE : EPI];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -350,56 +353,85 @@ __global__ void __launch_bounds__(WR *WC * 64) ortho_mul_kernel(const MulArgs A)
     tc = in / rows;
   }
 
-  const int piece = (lane & 7) ^ (lane >> 3);
-  const _Float16 *pg = A.p + mat * A.stride_p +
-                       (int64_t(tr) * T + wave * 8 + (lane >> 3)) * A.k + piece * 8;
-  const _Float16 *qg = A.q + mat * A.stride_q +
-                       (int64_t(tc) * T + wave * 8 + (lane >> 3)) * A.k + piece * 8;
-  const auto stage = [&](int64_t kt, int buf) {
-    _Float16 *base = lds + buf * 2 * T * 64;
+  const auto key = [](int r) { return BK == 64 ? r & 7 : (r >> 1) & 3; };
+  const unsigned row0 = wave * RPI + lane / PIECES;
+  const unsigned off = row0 * unsigned(A.k) + ((lane % PIECES) ^ key(lane / PIECES)) * 8;
+  const _Float16 *pg = A.p + mat * A.stride_p + int64_t(tr) * T * A.k;
+  const _Float16 *qg = A.q + mat * A.stride_q + int64_t(tc) * T * A.k;
+  const auto stage = [&](int kt) {
+    _Float16 *base = lds + kt % S * BUF;
 #pragma unroll
     for (int i = 0; i < L; ++i)
-      __builtin_amdgcn_global_load_lds(ZS_GLOBAL(pg + i * NW * 8 * A.k + kt * 64),
+      __builtin_amdgcn_global_load_lds(ZS_GLOBAL(pg + i * NW * RPI * A.k + kt * BK + off),
                                        ZS_LDS(base + (i * NW + wave) * 512), 16, 0, 0);
 #pragma unroll
     for (int i = 0; i < L; ++i)
-      __builtin_amdgcn_global_load_lds(ZS_GLOBAL(qg + i * NW * 8 * A.k + kt * 64),
-                                       ZS_LDS(base + T * 64 + (i * NW + wave) * 512), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds(ZS_GLOBAL(qg + i * NW * RPI * A.k + kt * BK + off),
+                                       ZS_LDS(base + T * BK + (i * NW + wave) * 512), 16, 0, 0);
   };
-
+  const int nk = int(A.k / BK);
+  // buffer kt is there for all waves, and buffer kt - 2's place is free
+  const auto advance = [&](int kt) {
+    __builtin_amdgcn_sched_barrier(0);
+    if (kt + S - 2 < nk) wait_loads<(S - 3) * 2 * L>();
+    else wait_loads<0>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    if (kt + S - 2 < nk) stage(kt + S - 2);
+  };
+  struct Regs {
+    half8 p[TM], q[TN];
+  };
+  const auto fetch = [&](Regs &f, int u) {  // the u-th 32 of k
+    const int kt = u * 32 / BK, piece = u * 4 % PIECES + (lane >> 4);
+    const int pos = (piece ^ key(lane & 15)) * 8;
+    const _Float16 *base = lds + kt % S * BUF;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+      f.p[i] = *reinterpret_cast<const half8 *>(
+          base + ((wr * TM + i) * 16 + (lane & 15)) * BK + pos);
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      f.q[j] = *reinterpret_cast<const half8 *>(
+          base + T * BK + ((wc * TN + j) * 16 + (lane & 15)) * BK + pos);
+  };
   f32x4 acc[TM][TN] = {};
-  const int64_t nk = A.k / 64;
-  stage(0, 0);
-  for (int64_t kt = 0; kt < nk; ++kt) {
-    const int buf = int(kt & 1);
-    if (kt + 1 < nk) {
-      stage(kt + 1, buf ^ 1);
-      wait_loads<2 * L>();
-    } else {
-      wait_loads<0>();
-    }
-    barrier();
-    const _Float16 *base = lds + buf * 2 * T * 64;
+  const auto multiply = [&](const Regs &f) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      half8 p[TM], q[TN];
-      const int pos = (((lane >> 4) + s * 4) ^ (lane & 7)) * 8;
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-        p[i] = *reinterpret_cast<const half8 *>(
-            base + ((wr * TM + i) * 16 + (lane & 15)) * 64 + pos);
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        q[j] = *reinterpret_cast<const half8 *>(
-            base + T * 64 + ((wc * TN + j) * 16 + (lane & 15)) * 64 + pos);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.p[i], f.q[j], acc[i][j], 0, 0, 0);
+  };
+  // matrix instructions, then one read, and so on
+  const auto interleave = [&] {
+    constexpr int EACH = TM * TN / (TM + TN) > 0 ? TM * TN / (TM + TN) : 1;
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(p[i], q[j], acc[i][j], 0, 0, 0);
+    for (int i = 0; i < TM + TN; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x8, EACH, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
-    barrier();
+  };
+
+  // k is a multiple of 64: two of 32 a turn
+#pragma unroll
+  for (int s = 0; s < S - 2; ++s)
+    if (s < nk) stage(s);
+  Regs f0, f1;
+  advance(0);
+  fetch(f0, 0);
+  for (int u = 0; u < int(A.k / 32); u += 2) {
+    if constexpr (BK == 32) advance(u + 1);
+    fetch(f1, u + 1);
+    multiply(f0);
+    interleave();
+    advance((u + 2) * 32 / BK);
+    fetch(f0, u + 2);  // after the last one: of some buffer, not used
+    multiply(f1);
+    interleave();
   }
+  wait_loads<0>();
 
   // Lane l of a 16 x 16 block holds rows 4 (l / 16) + 0..3 of column l % 16.
   const int br = wr * TM * 16 + (lane >> 4) * 4, bc = wc * TN * 16 + (lane & 15);
@@ -544,9 +576,15 @@ template <int KIND>
 int multiply(const MulArgs &A, int64_t batch, int tile, hipStream_t st) {
   const dim3 grid(unsigned(batch * A.per));
   switch (tile) {
-    case 256: hipLaunchKernelGGL((ortho_mul_kernel<KIND, 256, 2, 4>), grid, dim3(512), 0, st, A); break;
-    case 128: hipLaunchKernelGGL((ortho_mul_kernel<KIND, 128, 2, 2>), grid, dim3(256), 0, st, A); break;
-    default: hipLaunchKernelGGL((ortho_mul_kernel<KIND, 64, 2, 2>), grid, dim3(256), 0, st, A); break;
+    case 256:
+      hipLaunchKernelGGL((ortho_mul_kernel<KIND, 256, 2, 4, 32, 5>), grid, dim3(512), 0, st, A);
+      break;
+    case 128:
+      hipLaunchKernelGGL((ortho_mul_kernel<KIND, 128, 2, 2, 64, 4>), grid, dim3(256), 0, st, A);
+      break;
+    default:
+      hipLaunchKernelGGL((ortho_mul_kernel<KIND, 64, 2, 2, 64, 4>), grid, dim3(256), 0, st, A);
+      break;
   }
   return launched();
 }
