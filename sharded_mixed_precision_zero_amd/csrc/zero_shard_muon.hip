@@ -33,6 +33,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "zero_shard.h"
 #include "zs_args.h"
@@ -315,8 +316,24 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("" ::: "memory");
 }
 
+template <int V>
+using Const = std::integral_constant<int, V>;
+
+// The order of a turn's instructions: G times EACH matrix instructions, the
+// share of N loads that falls to it, one read.
+template <int I, int G, int N, int EACH>
+__device__ __forceinline__ void order() {
+  if constexpr (I < G) {
+    __builtin_amdgcn_sched_group_barrier(0x8, EACH, 0);
+    constexpr int LOADS = (I + 1) * N / G - I * N / G;
+    if constexpr (LOADS > 0) __builtin_amdgcn_sched_group_barrier(0x10, LOADS, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    order<I + 1, G, N, EACH>();
+  }
+}
+
 // T x T tiles of C, WR x WC waves, S buffers of BK of k.  The operands go from
-// global memory straight into LDS, S - 2 buffers ahead of their use, so a
+// global memory straight into LDS, S - 1 buffers ahead of their use, so a
 // buffer costs one barrier; a row of BK is BK / 8 pieces of 16 bytes, piece c
 // of row r at position c ^ key(r), so the rows that one read instruction
 // serves together lie in different banks.  The registers of the next 32 of k
@@ -358,78 +375,82 @@ __global__ void __launch_bounds__(WR *WC * 64) ortho_mul_kernel(const MulArgs A)
   const unsigned off = row0 * unsigned(A.k) + ((lane % PIECES) ^ key(lane / PIECES)) * 8;
   const _Float16 *pg = A.p + mat * A.stride_p + int64_t(tr) * T * A.k;
   const _Float16 *qg = A.q + mat * A.stride_q + int64_t(tc) * T * A.k;
-  const auto stage = [&](int kt) {
-    _Float16 *base = lds + kt % S * BUF;
-#pragma unroll
-    for (int i = 0; i < L; ++i)
-      __builtin_amdgcn_global_load_lds(ZS_GLOBAL(pg + i * NW * RPI * A.k + kt * BK + off),
-                                       ZS_LDS(base + (i * NW + wave) * 512), 16, 0, 0);
-#pragma unroll
-    for (int i = 0; i < L; ++i)
-      __builtin_amdgcn_global_load_lds(ZS_GLOBAL(qg + i * NW * RPI * A.k + kt * BK + off),
-                                       ZS_LDS(base + T * BK + (i * NW + wave) * 512), 16, 0, 0);
+  // The buffers go round: `rd` is read next and `wr_` written next (offsets
+  // into lds), `from` is the k that is loaded next; past the end the last
+  // buffer is loaded once more, so that as many loads are outstanding in
+  // every turn.
+  int rd = 0, wr_ = 0;
+  int64_t from = 0;
+  const auto load = [&](int i) {  // the i-th of a buffer's loads
+    const int at = i % L;
+    __builtin_amdgcn_global_load_lds(
+        ZS_GLOBAL((i < L ? pg : qg) + (from + at * NW * RPI * A.k) + off),
+        ZS_LDS(lds + wr_ + (i < L ? 0 : T * BK) + (at * NW + wave) * 512), 16, 0, 0);
+    if (i == 2 * L - 1) {
+      wr_ = wr_ == (S - 1) * BUF ? 0 : wr_ + BUF;
+      from = from + BK < A.k ? from + BK : from;
+    }
   };
-  const int nk = int(A.k / BK);
-  // buffer kt is there for all waves, and buffer kt - 2's place is free
-  const auto advance = [&](int kt) {
+  // the buffer at rd is there for all waves, and all have read the one before
+  const auto advance = [&] {
     __builtin_amdgcn_sched_barrier(0);
-    if (kt + S - 2 < nk) wait_loads<(S - 3) * 2 * L>();
-    else wait_loads<0>();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    wait_loads<(S - 2) * 2 * L>();
+    barrier();
     __builtin_amdgcn_sched_barrier(0);
-    if (kt + S - 2 < nk) stage(kt + S - 2);
   };
-  struct Regs {
-    half8 p[TM], q[TN];
-  };
-  const auto fetch = [&](Regs &f, int u) {  // the u-th 32 of k
-    const int kt = u * 32 / BK, piece = u * 4 % PIECES + (lane >> 4);
-    const int pos = (piece ^ key(lane & 15)) * 8;
-    const _Float16 *base = lds + kt % S * BUF;
+  half8 regs[2][TM + TN];
+  // where this lane's pieces of a buffer's first and second 32 of k are
+  int pos[BK / 32][2];
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
-      f.p[i] = *reinterpret_cast<const half8 *>(
-          base + ((wr * TM + i) * 16 + (lane & 15)) * BK + pos);
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-      f.q[j] = *reinterpret_cast<const half8 *>(
-          base + T * BK + ((wc * TN + j) * 16 + (lane & 15)) * BK + pos);
+  for (int h = 0; h < BK / 32; ++h) {
+    const int in = (lane & 15) * BK + ((h * 4 + (lane >> 4)) ^ key(lane & 15)) * 8;
+    pos[h][0] = in + wr * TM * 16 * BK;
+    pos[h][1] = in + (T + wc * TN * 16) * BK;
+  }
+  const auto fetch = [&](auto odd, int i) {  // the i-th block of the 32 of k at rd
+    constexpr int h = odd.value % (BK / 32);
+    const int at = i < TM ? pos[h][0] + i * 16 * BK : pos[h][1] + (i - TM) * 16 * BK;
+    regs[odd.value][i] = *reinterpret_cast<const half8 *>(lds + rd + at);
+    if (i == TM + TN - 1 && h == BK / 32 - 1) rd = rd == (S - 1) * BUF ? 0 : rd + BUF;
   };
   f32x4 acc[TM][TN] = {};
-  const auto multiply = [&](const Regs &f) {
+  // 32 of k, while the next 32 are read and, in the first turn after a
+  // barrier, the loads of the buffer that it freed are issued, evenly between
+  // the matrix instructions: all loads at once fill the queue that the reads
+  // need, and the matrix cores wait.
+  const auto turn = [&](auto odd, auto loads) {
+    constexpr int G = TM + TN, N = loads.value ? 2 * L : 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+      for (int i = g * N / G; i < (g + 1) * N / G; ++i) load(i);
+      fetch(Const<1 - odd.value>{}, g);
+    }
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.p[i], f.q[j], acc[i][j], 0, 0, 0);
-  };
-  // matrix instructions, then one read, and so on
-  const auto interleave = [&] {
-    constexpr int EACH = TM * TN / (TM + TN) > 0 ? TM * TN / (TM + TN) : 1;
-#pragma unroll
-    for (int i = 0; i < TM + TN; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x8, EACH, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    }
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+            regs[odd.value][i], regs[odd.value][TM + j], acc[i][j], 0, 0, 0);
+    constexpr int EACH = TM * TN / G > 0 ? TM * TN / G : 1;
+    order<0, G, N, EACH>();
   };
 
-  // k is a multiple of 64: two of 32 a turn
+  // k is a multiple of 64: two turns of 32 at a time
 #pragma unroll
-  for (int s = 0; s < S - 2; ++s)
-    if (s < nk) stage(s);
-  Regs f0, f1;
-  advance(0);
-  fetch(f0, 0);
-  for (int u = 0; u < int(A.k / 32); u += 2) {
-    if constexpr (BK == 32) advance(u + 1);
-    fetch(f1, u + 1);
-    multiply(f0);
-    interleave();
-    advance((u + 2) * 32 / BK);
-    fetch(f0, u + 2);  // after the last one: of some buffer, not used
-    multiply(f1);
-    interleave();
+  for (int s = 0; s < S - 1; ++s)
+#pragma unroll
+    for (int i = 0; i < 2 * L; ++i) load(i);
+  advance();
+#pragma unroll
+  for (int i = 0; i < 2 * L; ++i) load(i);
+#pragma unroll
+  for (int i = 0; i < TM + TN; ++i) fetch(Const<0>{}, i);
+  for (int64_t u = 0; u < A.k; u += 64) {
+    if constexpr (BK == 32) advance();
+    turn(Const<0>{}, Const<BK == 32>{});
+    advance();
+    turn(Const<1>{}, Const<1>{});  // reads past the end: of some buffer, not used
   }
   wait_loads<0>();
 
@@ -577,13 +598,13 @@ int multiply(const MulArgs &A, int64_t batch, int tile, hipStream_t st) {
   const dim3 grid(unsigned(batch * A.per));
   switch (tile) {
     case 256:
-      hipLaunchKernelGGL((ortho_mul_kernel<KIND, 256, 2, 4, 32, 5>), grid, dim3(512), 0, st, A);
+      hipLaunchKernelGGL((ortho_mul_kernel<KIND, 256, 2, 4, 64, 2>), grid, dim3(512), 0, st, A);
       break;
     case 128:
-      hipLaunchKernelGGL((ortho_mul_kernel<KIND, 128, 2, 2, 64, 4>), grid, dim3(256), 0, st, A);
+      hipLaunchKernelGGL((ortho_mul_kernel<KIND, 128, 2, 4, 64, 5>), grid, dim3(512), 0, st, A);
       break;
     default:
-      hipLaunchKernelGGL((ortho_mul_kernel<KIND, 64, 2, 2, 64, 4>), grid, dim3(256), 0, st, A);
+      hipLaunchKernelGGL((ortho_mul_kernel<KIND, 64, 2, 2, 64, 5>), grid, dim3(256), 0, st, A);
       break;
   }
   return launched();
