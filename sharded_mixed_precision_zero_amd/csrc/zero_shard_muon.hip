@@ -199,12 +199,14 @@ __global__ void __launch_bounds__(kThreads) apply_kernel(const ApplyArgs A) {
 
 constexpr float kScale = 2048.0f;  // 2^11: X, A and B are held times this
 constexpr int kNormBlocks = 256;   // partial sums of squares per matrix
+constexpr int kCutTiles = kThreads; // most tiles of a product that are cut along k
 constexpr int kNormRun = 2048;     // consecutive elements a workgroup sums
 
 struct InArgs {
   const void *g;
   int64_t rows, cols, ld, stride;  // of the input, elements
   double *partials;                // [batch][kNormBlocks]
+  int32_t *arrived;                // [kCutTiles], zeroed
   _Float16 *x, *xt;                // [batch][mp][np] and [batch][np][mp]
   int64_t mp, np;
   double eps;
@@ -226,6 +228,7 @@ __device__ __forceinline__ double block_sum(double v, double *lds) {
 template <class TG>
 __global__ void __launch_bounds__(kThreads) ortho_norm_kernel(const InArgs A) {
   __shared__ double lds[kThreads / 64];
+  if (blockIdx.x + blockIdx.y == 0) A.arrived[threadIdx.x] = 0;
   const typename TG::raw *g =
       static_cast<const typename TG::raw *>(A.g) + int64_t(blockIdx.y) * A.stride;
   const int64_t runs = (A.cols + kNormRun - 1) / kNormRun;
@@ -283,25 +286,28 @@ enum Product {
 };
 
 struct MulArgs {
-  const _Float16 *p, *q;      // [batch][rows][k], [batch][cols][k]
-  int64_t stride_p, stride_q; // elements per matrix
-  int64_t k;
-  int32_t tiles_r, tiles_c;   // of C; symmetric products: tiles_r == tiles_c
-  int32_t per;                // tiles computed per matrix
-  _Float16 *c, *ct;           // C (row length ld_c) and C^T (row length ld_ct)
-  int64_t ld_c, ld_ct, stride_c;
-  float a, b, cc;             // kPoly's coefficients
+  const _Float16 *p, *q;       // [batch][rows][k], [batch][cols][k]
+  int64_t stride_p, stride_q;  // elements per matrix
+  int32_t k;                   // a multiple of 64
+  int32_t rows, cols;          // of C, multiples of 64
+  int32_t tiles_r, tiles_c;    // of C
+  int32_t per, one;            // tiles computed per matrix; whether there is one matrix
+  int32_t cut, groups;         // all `cut` tiles are cut between `groups` workgroups; or 0
+  float *parts;                // [2 groups][tile] partial sums of cut tiles
+  int32_t *arrived;            // [cut] workgroups done with a cut tile; 0 between launches
+  _Float16 *c, *ct;            // C (row length cols) and C^T (row length rows)
+  int64_t stride_c;
+  float a, b, cc;              // kPoly's coefficients
   // kLast
   uint16_t *o;
-  int64_t rows, cols, ld_o, stride_o;
-  int32_t tall;
+  int64_t out_rows, out_cols, ld_o, stride_o;
+  int32_t tall, wide;          // wide: 16 bytes of a row at a time
 };
 
 #define ZS_LDS(p) ((__attribute__((address_space(3))) void *)(p))
-#define ZS_GLOBAL(p) ((__attribute__((address_space(1))) void *)(p))
 
 // All waves of the workgroup; accesses to memory stay on their side of it.
-__device__ __forceinline__ void barrier() {
+[[maybe_unused]] __device__ __forceinline__ void barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
@@ -332,196 +338,326 @@ __device__ __forceinline__ void order() {
   }
 }
 
-// T x T tiles of C, WR x WC waves, S buffers of BK of k.  The operands go from
-// global memory straight into LDS, S - 1 buffers ahead of their use, so a
-// buffer costs one barrier; a row of BK is BK / 8 pieces of 16 bytes, piece c
-// of row r at position c ^ key(r), so the rows that one read instruction
+// How many tiles of tile row tr lie on or below the diagonal.
+__host__ __device__ inline int below(int tr, int TR, int TC, int tiles_c) {
+  const int n = ((tr + 1) * TR - 1) / TC + 1;
+  return n < tiles_c ? n : tiles_c;
+}
+
+// Tile t of a matrix, in bands of 4 tile rows, column by column within the
+// band, so that neighbours share both operands in L2; of symmetric products
+// the tiles on and below the diagonal.
+template <bool SYM, int TR, int TC>
+__device__ __forceinline__ void tile_of(int t, int tiles_r, int tiles_c, int &tr, int &tc) {
+  if constexpr (SYM) {
+    int row = 0, rows = 0, least = 0;
+    for (;; row += 4) {
+      rows = tiles_r - row < 4 ? tiles_r - row : 4;
+      least = below(row, TR, TC, tiles_c);
+      int all = 0;
+      for (int i = 0; i < rows; ++i) all += below(row + i, TR, TC, tiles_c);
+      if (t < all || row + 4 >= tiles_r) break;
+      t -= all;
+    }
+    if (t < rows * least) {
+      tc = rows == 4 ? t >> 2 : t / rows;
+      tr = row + t - tc * rows;
+      return;
+    }
+    t -= rows * least;  // the columns that only the band's later rows have
+    for (int i = 1; i < rows; ++i) {
+      const int extra = below(row + i, TR, TC, tiles_c) - least;
+      tr = row + i;
+      tc = least + t;
+      if (t < extra) return;
+      t -= extra;
+    }
+  } else {
+    const int band = t / (4 * tiles_c), in = t - band * 4 * tiles_c;
+    const int rows = tiles_r - band * 4 < 4 ? tiles_r - band * 4 : 4;
+    tc = rows == 4 ? in >> 2 : in / rows;
+    tr = band * 4 + in - tc * rows;
+  }
+}
+
+// TR x TC tiles of C, WR x WC waves, S buffers of 64 of k.  The operands go
+// from global memory straight into LDS, S - 1 buffers ahead of their use, so a
+// buffer costs one barrier; a row of 64 is eight pieces of 16 bytes, piece c
+// of row r at position c ^ (r & 7), so the rows that one read instruction
 // serves together lie in different banks.  The registers of the next 32 of k
 // are read while the matrix cores work on the present ones.
-template <int KIND, int T, int WR, int WC, int BK, int S>
+template <int KIND, bool CUT, int TR, int TC, int WR, int WC, int S>
 __global__ void __launch_bounds__(WR *WC * 64) ortho_mul_kernel(const MulArgs A) {
-  constexpr int NW = WR * WC, TM = T / WR / 16, TN = T / WC / 16;
-  constexpr int PIECES = BK / 8, RPI = 64 / PIECES;  // per row; rows per load instruction
-  constexpr int L = T / RPI / NW;  // load instructions per wave, operand and buffer
-  constexpr int PITCH = T + 8;
-  constexpr int BUF = 2 * T * BK, STAGE = S * BUF, EPI = T * PITCH;
+#ifdef __HIP_DEVICE_COMPILE__  // the buffer resources' type is known to the device pass only
+  constexpr bool SYM = KIND == kGram || KIND == kPoly;
+  constexpr int NW = WR * WC, TM = TR / WR / 16, TN = TC / WC / 16;
+  // load instructions (8 rows of 64) per wave and buffer, of P and of both;
+  // P's rows in LDS are filled up to a multiple of 8 NW
+  constexpr int LP = (TR + 8 * NW - 1) / (8 * NW), L = LP + TC / (8 * NW);
+  constexpr int PITCH = TC + 8, PITCH_T = TR + 8;  // of the tile and its transpose on their way out
+  constexpr int QAT = LP * 8 * NW * 64, BUF = QAT + TC * 64;
+  constexpr int STAGE = S * BUF, EPI = TR * PITCH > TC * PITCH_T ? TR * PITCH : TC * PITCH_T;
   __shared__ __align__(16) _Float16 lds[STAGE > EPI ? STAGE : EPI];
-  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / WC, wc = wave % WC;
+  const auto uniform = [](unsigned v) { return int(__builtin_amdgcn_readfirstlane(v)); };
 
   // Workgroups go to the 8 XCDs in turn: each gets a contiguous run of tiles.
   const unsigned total = gridDim.x, id = blockIdx.x, xcd = id & 7;
   const unsigned each = total / 8, more = total % 8;
-  const unsigned at = xcd * each + (xcd < more ? xcd : more) + id / 8;
-  const int64_t mat = at / unsigned(A.per);
-  const int t = int(at % unsigned(A.per));
-  int tr, tc;
-  if constexpr (KIND == kGram || KIND == kPoly) {
-    tr = int((sqrtf(8.0f * float(t) + 1.0f) - 1.0f) * 0.5f);
-    while (tr * (tr + 1) / 2 > t) --tr;
-    while ((tr + 1) * (tr + 2) / 2 <= t) ++tr;
-    tc = t - tr * (tr + 1) / 2;
-  } else {
-    // bands of 4 tile rows, so that neighbours share both operands in L2
-    const int band = t / (4 * A.tiles_c), in = t - band * 4 * A.tiles_c;
-    const int rows = A.tiles_r - band * 4 < 4 ? A.tiles_r - band * 4 : 4;
-    tr = band * 4 + in % rows;
-    tc = in / rows;
-  }
+  const int at = int(xcd * each + (xcd < more ? xcd : more) + id / 8);
+  const int nk = A.k / 64;
 
-  const auto key = [](int r) { return BK == 64 ? r & 7 : (r >> 1) & 3; };
-  const unsigned row0 = wave * RPI + lane / PIECES;
-  const unsigned off = row0 * unsigned(A.k) + ((lane % PIECES) ^ key(lane / PIECES)) * 8;
-  const _Float16 *pg = A.p + mat * A.stride_p + int64_t(tr) * T * A.k;
-  const _Float16 *qg = A.q + mat * A.stride_q + int64_t(tc) * T * A.k;
-  // The buffers go round: `rd` is read next and `wr_` written next (offsets
-  // into lds), `from` is the k that is loaded next; past the end the last
-  // buffer is loaded once more, so that as many loads are outstanding in
-  // every turn.
-  int rd = 0, wr_ = 0;
-  int64_t from = 0;
-  const auto load = [&](int i) {  // the i-th of a buffer's loads
-    const int at = i % L;
-    __builtin_amdgcn_global_load_lds(
-        ZS_GLOBAL((i < L ? pg : qg) + (from + at * NW * RPI * A.k) + off),
-        ZS_LDS(lds + wr_ + (i < L ? 0 : T * BK) + (at * NW + wave) * 512), 16, 0, 0);
-    if (i == 2 * L - 1) {
-      wr_ = wr_ == (S - 1) * BUF ? 0 : wr_ + BUF;
-      from = from + BK < A.k ? from + BK : from;
-    }
-  };
-  // the buffer at rd is there for all waves, and all have read the one before
-  const auto advance = [&] {
-    __builtin_amdgcn_sched_barrier(0);
-    wait_loads<(S - 2) * 2 * L>();
-    barrier();
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  half8 regs[2][TM + TN];
-  // where this lane's pieces of a buffer's first and second 32 of k are
-  int pos[BK / 32][2];
-#pragma unroll
-  for (int h = 0; h < BK / 32; ++h) {
-    const int in = (lane & 15) * BK + ((h * 4 + (lane >> 4)) ^ key(lane & 15)) * 8;
-    pos[h][0] = in + wr * TM * 16 * BK;
-    pos[h][1] = in + (T + wc * TN * 16) * BK;
+  // One whole tile, or this workgroup's share of the cut ones in 64s of k.
+  [[maybe_unused]] const unsigned steps = unsigned(A.cut) * nk, groups = A.groups;
+  int s0 = 0, s1 = nk;
+  if constexpr (CUT) {  // groups * steps < 2^32
+    s0 = uniform(at * steps / groups);
+    s1 = uniform((at + 1) * steps / groups);
   }
-  const auto fetch = [&](auto odd, int i) {  // the i-th block of the 32 of k at rd
-    constexpr int h = odd.value % (BK / 32);
-    const int at = i < TM ? pos[h][0] + i * 16 * BK : pos[h][1] + (i - TM) * 16 * BK;
-    regs[odd.value][i] = *reinterpret_cast<const half8 *>(lds + rd + at);
-    if (i == TM + TN - 1 && h == BK / 32 - 1) rd = rd == (S - 1) * BUF ? 0 : rd + BUF;
-  };
-  f32x4 acc[TM][TN] = {};
-  // 32 of k, while the next 32 are read and, in the first turn after a
-  // barrier, the loads of the buffer that it freed are issued, evenly between
-  // the matrix instructions: all loads at once fill the queue that the reads
-  // need, and the matrix cores wait.
-  const auto turn = [&](auto odd, auto loads) {
-    constexpr int G = TM + TN, N = loads.value ? 2 * L : 0;
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-#pragma unroll
-      for (int i = g * N / G; i < (g + 1) * N / G; ++i) load(i);
-      fetch(Const<1 - odd.value>{}, g);
+  do {
+    int tile = at, k0 = 0, k1 = nk;
+    if constexpr (CUT) {
+      tile = uniform(unsigned(s0) / unsigned(nk));
+      k0 = s0 - tile * nk;
+      k1 = s1 - s0 < nk - k0 ? k0 + s1 - s0 : nk;
+      s0 += k1 - k0;
     }
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-            regs[odd.value][i], regs[odd.value][TM + j], acc[i][j], 0, 0, 0);
-    constexpr int EACH = TM * TN / G > 0 ? TM * TN / G : 1;
-    order<0, G, N, EACH>();
-  };
+    // Opaque, so that no address is computed ahead of this loop and kept: the
+    // registers are full.
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63;
+    const int64_t mat = A.one ? 0 : uniform(unsigned(tile) / unsigned(A.per));
+    int tr, tc;
+    tile_of<SYM, TR, TC>(tile - int(mat) * A.per, A.tiles_r, A.tiles_c, tr, tc);
+    tr = uniform(tr);
+    tc = uniform(tc);
+    const int row0 = tr * TR, col0 = tc * TC;  // of the tile in C
 
-  // k is a multiple of 64: two turns of 32 at a time
+    // A lane's offset in bytes, below 256 rows of 2^20; loads of rows past the
+    // operand's end are dropped by the bounds of its buffer resource.
+    const int in = wave * 8 + (lane >> 3);
+    const int off = (in * A.k + ((lane & 7) ^ (lane >> 3)) * 8) * 2;
+    const auto operand = [&](const _Float16 *p, int left, int T) {
+      return __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16 *>(p), 0,
+                                               (left < T ? left : T) * A.k * 2, 0x00020000);
+    };
+    const auto pg = operand(A.p + mat * A.stride_p + int64_t(row0) * A.k, A.rows - row0, TR);
+    const auto qg = operand(A.q + mat * A.stride_q + int64_t(col0) * A.k, A.cols - col0, TC);
+    // The buffers go round: `rd` is read next and `wr_` written next (offsets
+    // into lds), `from` is the k that is loaded next; past the end the last
+    // buffer is loaded once more, so that as many loads are outstanding in
+    // every turn.
+    int rd = 0, wr_ = 0, from = k0 * 64;
+    const int end = k1 * 64;
+    const auto load = [&](int i) {  // the i-th of a buffer's loads
+      const int j = i < LP ? i : i - LP;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          i < LP ? pg : qg, ZS_LDS(lds + wr_ + (i < LP ? 0 : QAT) + (j * NW + wave) * 512), 16, off,
+          (from + j * NW * 8 * A.k) * 2, 0, 0);
+      if (i == L - 1) {
+        wr_ = wr_ == (S - 1) * BUF ? 0 : wr_ + BUF;
+        from = from + 64 < end ? from + 64 : from;
+      }
+    };
+    // the buffer at rd is there for all waves, and all have read the one before
+    const auto advance = [&] {
+      __builtin_amdgcn_sched_barrier(0);
+      wait_loads<(S - 2) * L>();
+      barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    half8 regs[2][TM + TN];
+    // where this lane's pieces of a buffer's first and second 32 of k are
+    int pos[2][2];
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s)
+    for (int h = 0; h < 2; ++h) {
+      const int piece = (lane & 15) * 64 + ((h * 4 + (lane >> 4)) ^ (lane & 7)) * 8;
+      pos[h][0] = piece + wr * TM * 1024;
+      pos[h][1] = piece + QAT + wc * TN * 1024;
+    }
+    const auto fetch = [&](auto half, int i) {  // the i-th block of that half of the buffer at rd
+      const int p = i < TM ? pos[half.value][0] + i * 1024 : pos[half.value][1] + (i - TM) * 1024;
+      regs[half.value][i] = *reinterpret_cast<const half8 *>(lds + rd + p);
+      if (half.value && i == TM + TN - 1) rd = rd == (S - 1) * BUF ? 0 : rd + BUF;
+    };
+    f32x4 acc[TM][TN] = {};
+    // 32 of k, while the next 32 are read and, in the turn after the barrier,
+    // the loads of the buffer that it freed are issued, evenly between the
+    // matrix instructions: all loads at once fill the queue that the reads
+    // need, and the matrix cores wait.
+    const auto turn = [&](auto half) {
+      constexpr int G = TM + TN, N = half.value ? L : 0;
 #pragma unroll
-    for (int i = 0; i < 2 * L; ++i) load(i);
-  advance();
+      for (int g = 0; g < G; ++g) {
 #pragma unroll
-  for (int i = 0; i < 2 * L; ++i) load(i);
+        for (int i = g * N / G; i < (g + 1) * N / G; ++i) load(i);
+        fetch(Const<1 - half.value>{}, g);
+      }
 #pragma unroll
-  for (int i = 0; i < TM + TN; ++i) fetch(Const<0>{}, i);
-  for (int64_t u = 0; u < A.k; u += 64) {
-    if constexpr (BK == 32) advance();
-    turn(Const<0>{}, Const<BK == 32>{});
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              regs[half.value][i], regs[half.value][TM + j], acc[i][j], 0, 0, 0);
+      constexpr int EACH = TM * TN / G > 0 ? TM * TN / G : 1;
+      order<0, G, N, EACH>();
+    };
+
+    if constexpr (CUT) barrier();  // the previous tile's epilogue is done with the buffers
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s)
+#pragma unroll
+      for (int i = 0; i < L; ++i) load(i);
     advance();
-    turn(Const<1>{}, Const<1>{});  // reads past the end: of some buffer, not used
-  }
-  wait_loads<0>();
+#pragma unroll
+    for (int i = 0; i < L; ++i) load(i);
+#pragma unroll
+    for (int i = 0; i < TM + TN; ++i) fetch(Const<0>{}, i);
+    for (int u = k0; u < k1; ++u) {
+      turn(Const<0>{});
+      advance();
+      turn(Const<1>{});  // after the last 64 it reads some buffer, not used
+    }
+    wait_loads<0>();
 
-  // Lane l of a 16 x 16 block holds rows 4 (l / 16) + 0..3 of column l % 16.
-  const int br = wr * TM * 16 + (lane >> 4) * 4, bc = wc * TN * 16 + (lane & 15);
-  constexpr float kBack = KIND == kLast ? 1.0f / (kScale * kScale) : 1.0f / kScale;
+    // A cut tile: the last of its workgroups to arrive adds the parts, in the
+    // order of k whoever that is, and goes on; the others have done theirs.
+    if (CUT && k1 - k0 < nk) {
+      constexpr int N = TM * TN;
+      const auto part = [&](int w, int which, int i) {
+        char *p = reinterpret_cast<char *>(A.parts + (int64_t(w) * 2 + which) * (TR * TC));
+        return reinterpret_cast<f32x4 *>(p + i * NW * 1024 + unsigned(tid) * 16);
+      };
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+      for (int i = 0; i < N; ++i) *part(at, k0 == 0, i) = acc[i / TN][i % TN];
+      const int w0 = uniform(((tile * nk + 1u) * groups - 1) / steps);
+      const int w1 = uniform(((tile + 1u) * nk * groups - 1) / steps);
+      int *flag = reinterpret_cast<int *>(lds);
+      __syncthreads();
+      if (tid == 0) {
+        const int before = __hip_atomic_fetch_add(A.arrived + tile, 1, __ATOMIC_ACQ_REL,
+                                                  __HIP_MEMORY_SCOPE_AGENT);
+        if (before == w1 - w0)
+          __hip_atomic_store(A.arrived + tile, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *flag = before == w1 - w0;
+      }
+      __syncthreads();
+      if (!uniform(*flag)) continue;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      if constexpr (KIND == kPoly) {
-        // A is symmetric: column j's four rows are four neighbours of row j
-        const int64_t r = int64_t(tr) * T + br + i * 16, c = int64_t(tc) * T + bc + j * 16;
-        const half4 s = *reinterpret_cast<const half4 *>(A.p + mat * A.stride_p + c * A.k + r);
+      for (int i = 0; i < N; ++i) acc[i / TN][i % TN] = f32x4{};
+      for (int w = w0; w <= w1; ++w) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          acc[i][j][e] = A.b * float(s[e]) + A.cc * (acc[i][j][e] * kBack);
-          if (r + e == c) acc[i][j][e] += A.a * kScale;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] *= kBack;
+        for (int i = 0; i < N; ++i) acc[i / TN][i % TN] += *part(w, w == w0, i);
       }
     }
 
-  const auto narrow = [](float v) {
-    if constexpr (KIND == kLast) return Bf16::store(v);
-    else return F16::store(v);
-  };
-  uint16_t *epi = reinterpret_cast<uint16_t *>(lds);
-  // the tile through LDS, as C (turned = false) or as its transpose
-  const auto gather = [&](bool turned) {
-    barrier();
+    // Lane l of a 16 x 16 block holds rows 4 (l / 16) + 0..3 of column l % 16.
+    const int br = wr * TM * 16 + (lane >> 4) * 4, bc = wc * TN * 16 + (lane & 15);
+    constexpr float kBack = KIND == kLast ? 1.0f / (kScale * kScale) : 1.0f / kScale;
+    const auto narrow = [](float v) -> unsigned {
+      if constexpr (KIND == kLast) return Bf16::store(v);
+      else return F16::store(v);
+    };
+    u32x2 out[TM][TN];  // a lane's four rows in 16 bits
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
+      for (int j = 0; j < TN; ++j) {
+        if constexpr (KIND == kPoly) {
+          // A is symmetric: column c's four rows are four neighbours of row c
+          const int r = row0 + br + i * 16, c = col0 + bc + j * 16;
+          half4 s = {};
+          if (r < A.rows && c < A.cols)
+            s = *reinterpret_cast<const half4 *>(A.p + mat * A.stride_p + int64_t(c) * A.k + r);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = br + i * 16 + e, c = bc + j * 16;
-          epi[turned ? c * PITCH + r : r * PITCH + c] = narrow(acc[i][j][e]);
+          for (int e = 0; e < 4; ++e) {
+            acc[i][j][e] = A.b * float(s[e]) + A.cc * (acc[i][j][e] * kBack);
+            if (r + e == c) acc[i][j][e] += A.a * kScale;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] *= kBack;
         }
-    barrier();
-  };
-  const auto put = [&](_Float16 *dst, int64_t ld, int64_t r0, int64_t c0) {
-    for (int v = threadIdx.x; v < T * T / 8; v += NW * 64) {
-      const int r = v / (T / 8), c = v % (T / 8) * 8;
-      *reinterpret_cast<u32x4 *>(dst + (r0 + r) * ld + c0 + c) =
-          *reinterpret_cast<const u32x4 *>(epi + r * PITCH + c);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          out[i][j][e] = narrow(acc[i][j][2 * e]) | narrow(acc[i][j][2 * e + 1]) << 16;
+      }
+
+    uint16_t *epi = reinterpret_cast<uint16_t *>(lds);
+    // the tile through LDS, as C (turned = false) or as its transpose
+    const auto gather = [&](bool turned) {
+      barrier();
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const int r = br + i * 16, c = bc + j * 16;
+          if (turned) {
+            *reinterpret_cast<u32x2 *>(epi + c * PITCH_T + r) = out[i][j];
+          } else {
+            // Two lanes of neighbouring columns swap a row of each pair, so
+            // that each writes two columns of two rows.
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const unsigned v = out[i][j][e];
+              const unsigned o = __builtin_amdgcn_mov_dpp(v, 0xb1, 0xf, 0xf, true);
+              const unsigned both =
+                  lane & 1 ? (o >> 16) | (v & 0xffff0000u) : (v & 0xffffu) | o << 16;
+              *reinterpret_cast<unsigned *>(epi + (r + 2 * e + (lane & 1)) * PITCH + (c & ~1)) =
+                  both;
+            }
+          }
+        }
+      barrier();
+    };
+    // Its pieces of 8 to memory, where `want` says so.
+    const auto put = [&](auto turned, auto *dst, int64_t ld, auto want) {
+      constexpr int H = turned.value ? TC : TR, W = turned.value ? TR : TC;
+      const int r0 = turned.value ? col0 : row0, c0 = turned.value ? row0 : col0;
+#pragma unroll 4
+      for (int v = tid; v < H * W / 8; v += NW * 64) {
+        const int r = v / (W / 8), c = v % (W / 8) * 8;
+        if (want(r0 + r, c0 + c))
+          *reinterpret_cast<u32x4 *>(dst + int64_t(r0 + r) * ld + c0 + c) =
+              *reinterpret_cast<const u32x4 *>(epi + r * (W + 8) + c);
+      }
+    };
+    if constexpr (KIND == kLast) {
+      uint16_t *o = A.o + mat * A.stride_o;
+      const auto inside = [&](int r, int c) { return r < A.out_rows && c < A.out_cols; };
+      gather(A.tall);
+      if (A.wide && A.tall) {
+        put(Const<1>{}, o, A.ld_o, inside);
+      } else if (A.wide) {
+        put(Const<0>{}, o, A.ld_o, inside);
+      } else {
+        const int H = A.tall ? TC : TR, W = A.tall ? TR : TC;
+        const int r0 = A.tall ? col0 : row0, c0 = A.tall ? row0 : col0;
+        for (int r = wave; r < H; r += NW)
+          for (int c = lane; c < W; c += 64)
+            if (inside(r0 + r, c0 + c))
+              o[(r0 + r) * A.ld_o + c0 + c] = epi[r * (W + 8) + c];
+      }
+    } else {
+      gather(false);
+      put(Const<0>{}, A.c + mat * A.stride_c, A.cols,
+          [&](int r, int c) { return r < A.rows && c < A.cols; });
+      if constexpr (KIND == kNext) {
+        gather(true);
+        put(Const<1>{}, A.ct + mat * A.stride_c, A.rows,
+            [&](int r, int c) { return r < A.cols && c < A.rows; });
+      } else if (TR != TC || tr != tc) {
+        // what no tile on or below the diagonal holds
+        gather(true);
+        put(Const<1>{}, A.c + mat * A.stride_c, A.rows, [&](int r, int c) {
+          return r < A.cols && c < A.rows && c / TC * TC > r / TR * TR + TR - 1;
+        });
+      }
     }
-  };
-  if constexpr (KIND == kLast) {
-    gather(A.tall);
-    const int64_t r0 = int64_t(A.tall ? tc : tr) * T, c0 = int64_t(A.tall ? tr : tc) * T;
-    uint16_t *o = A.o + mat * A.stride_o;
-    for (int v = threadIdx.x; v < T * T; v += NW * 64) {
-      const int r = v / T, c = v % T;
-      if (r0 + r < A.rows && c0 + c < A.cols) o[(r0 + r) * A.ld_o + c0 + c] = epi[r * PITCH + c];
-    }
-  } else {
-    _Float16 *c = A.c + mat * A.stride_c;
-    gather(false);
-    put(c, A.ld_c, int64_t(tr) * T, int64_t(tc) * T);
-    if constexpr (KIND == kNext) {
-      gather(true);
-      put(A.ct + mat * A.stride_c, A.ld_ct, int64_t(tc) * T, int64_t(tr) * T);
-    } else if (tr != tc) {
-      gather(true);
-      put(c, A.ld_c, int64_t(tc) * T, int64_t(tr) * T);
-    }
-  }
+  } while (CUT && s0 < s1);
+#endif
 }
 
 // ------------------------------------------------------------------- host
@@ -558,31 +694,116 @@ bool ortho_ok(const zs_ortho_desc *d) {
   return true;
 }
 
-struct Plan {
-  int64_t m, n, mp, np;
-  int tile;
-  bool tall;
-  int64_t partials, x, xt, y, yt, a, b, bytes;  // offsets into the workspace
+// The tile shapes, how many workgroups the card holds at once, and what a tile
+// costs in microseconds (measured): 64 of k when few workgroups run and when
+// the card is full of them (then the clock is lower and L2 is shared), the
+// rest of a tile, and each part of a cut one.
+// The shapes between 256 x 256 and 128 x 256 fill the last turn of the card
+// better: 5120 x 5120 is 400 tiles of 256 x 256 (two turns of 256, 279 us) or
+// 460 of 224 x 256 (253 us); its lower triangle 210 (144 us) or 251 (128 us).
+// Smaller tiles give more workgroups but read more: 4 of 1024 x 1024 take
+// 30 us as 64 tiles of 256 x 256, 16 us as 256 of 128 x 128, 21 us as 1024 of
+// 64 x 64.
+struct Shape {
+  int TR, TC, cap;
+  double alone, full, rest, part;
+};
+constexpr Shape kShapes[] = {
+    {256, 256, 256, 1.05, 1.74, 12.5, 0.0},  {224, 256, 256, 0.95, 1.49, 11.5, 0.0},
+    {192, 256, 256, 0.86, 1.29, 10.8, 0.0},  {128, 256, 256, 0.58, 0.82, 9.6, 4.2},
+    {128, 128, 256, 0.33, 0.467, 8.0, 1.15}, {64, 64, 512, 0.22, 0.39, 5.5, 1.5},
+};
+constexpr int kNumShapes = sizeof kShapes / sizeof kShapes[0];
+constexpr int kFirstCut = 3, kMostParts = 8;
+
+// How one product is spread over the card: its tile shape, and whether the
+// tiles are cut along k.
+struct Way {
+  int shape, tiles_r, tiles_c, per, grid, cut;
+  double us;
 };
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// r x c of `batch` matrices (half of it when symmetric) over k.
+Way way_with(int64_t batch, int64_t r, int64_t c, int64_t k, bool symmetric, int shape) {
+  const Shape &S = kShapes[shape];
+  Way w;
+  w.shape = shape;
+  w.tiles_r = int(up(r, S.TR) / S.TR);
+  w.tiles_c = int(up(c, S.TC) / S.TC);
+  int64_t per = 0;
+  if (symmetric)
+    for (int i = 0; i < w.tiles_r; ++i) per += below(i, S.TR, S.TC, w.tiles_c);
+  else
+    per = int64_t(w.tiles_r) * w.tiles_c;
+  const int64_t tiles = batch * per, nk = k / 64;
+  if (tiles > 0x7fffffff) {
+    w.us = INFINITY;
+    return w;
+  }
+  w.per = int(per);
+  w.grid = int(tiles);
+  w.cut = 0;
+  // n workgroups at once, each over `steps` 64s of k
+  const auto turn = [&](int64_t n, double steps) {
+    return steps * (S.alone + (S.full - S.alone) * double(n) / S.cap) + S.rest;
+  };
+  w.us = double(tiles / S.cap) * turn(S.cap, double(nk)) +
+         (tiles % S.cap ? turn(tiles % S.cap, double(nk)) : 0.0);
+  // few tiles over a long k: cut along it (larger tiles: parts cost too much)
+  for (int64_t parts = shape < kFirstCut ? kMostParts + 1 : 2; parts <= kMostParts && parts * tiles <= S.cap && parts <= nk; ++parts) {
+    const double us = turn(parts * tiles, double(nk) / double(parts)) + double(parts) * S.part;
+    if (tiles <= kCutTiles && us < w.us) {
+      w.us = us;
+      w.cut = int(tiles);
+      w.grid = int(tiles * parts);
+    }
+  }
+  return w;
+}
+
+Way way_of(int64_t batch, int64_t r, int64_t c, int64_t k, bool symmetric) {
+  Way best = way_with(batch, r, c, k, symmetric, 0);
+  for (int i = 1; i < kNumShapes; ++i) {
+    const Way w = way_with(batch, r, c, k, symmetric, i);
+    if (w.us < best.us) best = w;
+  }
+  return best;
+}
+
+struct Plan {
+  int64_t m, n, mp, np;
+  Way gram, poly, next;
+  bool tall;
+  int64_t partials, arrived, parts, x, xt, y, yt, a, b, bytes;  // offsets into the workspace
+};
 
 Plan plan_of(const zs_ortho_desc &d) {
   Plan p;
   p.tall = d.rows > d.cols;
   p.m = p.tall ? d.cols : d.rows;
   p.n = p.tall ? d.rows : d.cols;
-  const auto tiles = [&](int64_t t) { return d.batch * (up(p.m, t) / t) * (up(p.n, t) / t); };
-  p.tile = tiles(256) >= 192 ? 256 : tiles(128) >= 192 ? 128 : 64;
-  p.mp = up(p.m, p.tile);
-  p.np = up(p.n, p.tile);
+  p.mp = up(p.m, 64);
+  p.np = up(p.n, 64);
+  p.gram = way_of(d.batch, p.mp, p.mp, p.np, true);
+  p.poly = way_of(d.batch, p.mp, p.mp, p.mp, true);
+  p.next = way_of(d.batch, p.mp, p.np, p.mp, false);
   int64_t at = 0;
   const auto take = [&](int64_t bytes) {
     const int64_t was = at;
     at += up(bytes, 256);
     return was;
   };
+  const auto parts = [](const Way &w) {
+    return w.cut ? int64_t(w.grid) * 2 * kShapes[w.shape].TR * kShapes[w.shape].TC * 4 : 0;
+  };
+  int64_t most = parts(p.next);
+  if (parts(p.gram) > most) most = parts(p.gram);
+  if (parts(p.poly) > most) most = parts(p.poly);
   p.partials = take(d.batch * kNormBlocks * 8);
+  p.arrived = take(kCutTiles * 4);
+  p.parts = take(most);
   p.x = take(d.batch * p.mp * p.np * 2);
   p.xt = take(d.batch * p.mp * p.np * 2);
   p.y = take(d.batch * p.mp * p.np * 2);
@@ -593,19 +814,39 @@ Plan plan_of(const zs_ortho_desc &d) {
   return p;
 }
 
+template <int KIND, bool CUT, int I, int WR, int WC, int S>
+void launch(const MulArgs &A, int grid, hipStream_t st) {
+  hipLaunchKernelGGL((ortho_mul_kernel<KIND, CUT, kShapes[I].TR, kShapes[I].TC, WR, WC, S>), dim3(grid),
+                     dim3(WR * WC * 64), 0, st, A);
+}
+
+// C (rows x cols) = P Q^T over k.
 template <int KIND>
-int multiply(const MulArgs &A, int64_t batch, int tile, hipStream_t st) {
-  const dim3 grid(unsigned(batch * A.per));
-  switch (tile) {
-    case 256:
-      hipLaunchKernelGGL((ortho_mul_kernel<KIND, 256, 2, 4, 64, 2>), grid, dim3(512), 0, st, A);
-      break;
-    case 128:
-      hipLaunchKernelGGL((ortho_mul_kernel<KIND, 128, 2, 4, 64, 5>), grid, dim3(512), 0, st, A);
-      break;
-    default:
-      hipLaunchKernelGGL((ortho_mul_kernel<KIND, 64, 2, 2, 64, 5>), grid, dim3(256), 0, st, A);
-      break;
+int multiply(MulArgs &A, const Way &w, int64_t rows, int64_t cols, int64_t k, hipStream_t st) {
+  A.rows = int(rows);
+  A.cols = int(cols);
+  A.k = int(k);
+  A.tiles_r = w.tiles_r;
+  A.tiles_c = w.tiles_c;
+  A.per = w.per;
+  A.cut = w.cut;
+  A.groups = w.grid;
+  A.one = w.per == w.grid || (w.cut && w.per == w.cut);
+  if (w.cut) {
+    switch (w.shape) {
+      case 3: launch<KIND, true, 3, 2, 4, 3>(A, w.grid, st); break;
+      case 4: launch<KIND, true, 4, 2, 4, 5>(A, w.grid, st); break;
+      default: launch<KIND, true, 5, 2, 2, 5>(A, w.grid, st); break;
+    }
+  } else {
+    switch (w.shape) {
+      case 0: launch<KIND, false, 0, 2, 4, 2>(A, w.grid, st); break;
+      case 1: launch<KIND, false, 1, 2, 4, 2>(A, w.grid, st); break;
+      case 2: launch<KIND, false, 2, 2, 4, 2>(A, w.grid, st); break;
+      case 3: launch<KIND, false, 3, 2, 4, 3>(A, w.grid, st); break;
+      case 4: launch<KIND, false, 4, 2, 4, 5>(A, w.grid, st); break;
+      default: launch<KIND, false, 5, 2, 2, 5>(A, w.grid, st); break;
+    }
   }
   return launched();
 }
@@ -681,8 +922,8 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
   if (d->batch == 0 || d->rows == 0 || d->cols == 0) return ZS_OK;
   const Plan p = plan_of(*d);
   if (!g || !o || !workspace || workspace_bytes < p.bytes) return ZS_EINVAL;
-  if (p.mp / 64 * (p.np / 64) > 0x7fffffff ||
-      d->batch * (p.mp / p.tile) * (p.np / p.tile) > 0x7fffffff)
+  if (p.mp / 64 * (p.np / 64) > 0x7fffffff || !std::isfinite(p.gram.us) ||
+      !std::isfinite(p.next.us))
     return ZS_EINVAL;
   if (!aligned(g, dtype_size(d->dtype)) || !aligned(o, 2) || !aligned(workspace, 256))
     return ZS_EALIGN;
@@ -699,6 +940,7 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
   in.ld = ld_in;
   in.stride = d->stride_in ? d->stride_in : d->rows * ld_in;
   in.partials = reinterpret_cast<double *>(ws + p.partials);
+  in.arrived = reinterpret_cast<int32_t *>(ws + p.arrived);
   in.x = half(p.x);
   in.xt = half(p.xt);
   in.mp = p.mp;
@@ -708,41 +950,40 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
   int rc = d->dtype == ZS_F32    ? start<F32>(in, d->batch, st)
            : d->dtype == ZS_BF16 ? start<Bf16>(in, d->batch, st)
                                  : start<F16>(in, d->batch, st);
-  const int tm = int(p.mp / p.tile), tn = int(p.np / p.tile);
   _Float16 *x = half(p.x), *xt = half(p.xt), *y = half(p.y), *yt = half(p.yt);
+  MulArgs A;
+  std::memset(&A, 0, sizeof A);
+  A.parts = reinterpret_cast<float *>(ws + p.parts);
+  A.arrived = in.arrived;
+  A.o = o;
+  A.out_rows = d->rows;
+  A.out_cols = d->cols;
+  A.ld_o = ld_out;
+  A.stride_o = d->stride_out ? d->stride_out : d->rows * ld_out;
+  A.tall = p.tall;
+  A.wide = aligned(o, 16) && d->cols % 8 == 0 && ld_out % 8 == 0 && A.stride_o % 8 == 0;
   for (int s = 0; s < d->steps && !rc; ++s) {
     const float *k = d->coeffs ? d->coeffs + 3 * s : kCoeffs;
-    MulArgs A;
-    std::memset(&A, 0, sizeof A);
     A.p = A.q = x;
     A.stride_p = A.stride_q = p.mp * p.np;
-    A.k = p.np;
-    A.tiles_r = A.tiles_c = tm;
-    A.per = tm * (tm + 1) / 2;
     A.c = half(p.a);
-    A.ld_c = p.mp;
     A.stride_c = p.mp * p.mp;
-    if ((rc = multiply<kGram>(A, d->batch, p.tile, st))) break;
+    if ((rc = multiply<kGram>(A, p.gram, p.mp, p.mp, p.np, st))) break;
     A.p = A.q = half(p.a);
     A.stride_p = A.stride_q = p.mp * p.mp;
-    A.k = p.mp;
     A.c = half(p.b);
     A.a = k[0];
     A.b = k[1];
     A.cc = k[2];
-    if ((rc = multiply<kPoly>(A, d->batch, p.tile, st))) break;
+    if ((rc = multiply<kPoly>(A, p.poly, p.mp, p.mp, p.mp, st))) break;
     A.p = half(p.b);
     A.q = xt;
     A.stride_q = p.mp * p.np;
-    A.tiles_c = tn;
-    A.per = tm * tn;
     if (s + 1 < d->steps) {
       A.c = y;
       A.ct = yt;
-      A.ld_c = p.np;
-      A.ld_ct = p.mp;
       A.stride_c = p.mp * p.np;
-      rc = multiply<kNext>(A, d->batch, p.tile, st);
+      rc = multiply<kNext>(A, p.next, p.mp, p.np, p.mp, st);
       _Float16 *v = x;
       x = y;
       y = v;
@@ -750,13 +991,7 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
       xt = yt;
       yt = v;
     } else {
-      A.o = o;
-      A.rows = d->rows;
-      A.cols = d->cols;
-      A.ld_o = ld_out;
-      A.stride_o = d->stride_out ? d->stride_out : d->rows * ld_out;
-      A.tall = p.tall;
-      rc = multiply<kLast>(A, d->batch, p.tile, st);
+      rc = multiply<kLast>(A, p.next, p.mp, p.np, p.mp, st);
     }
   }
   return rc;
