@@ -198,18 +198,20 @@ __global__ void __launch_bounds__(kThreads) apply_kernel(const ApplyArgs A) {
 // --------------------------------------------------- ortho: norm and layout
 
 constexpr float kScale = 2048.0f;  // 2^11: X, A and B are held times this
-constexpr int kNormBlocks = 256;   // partial sums of squares per matrix
-constexpr int kCutTiles = kThreads; // most tiles of a product that are cut along k
-constexpr int kNormRun = 2048;     // consecutive elements a workgroup sums
+constexpr int kNormBlocks = 1024;  // most partial sums of squares per matrix
+constexpr int kNormRun = 2048;     // consecutive elements a workgroup sums at a time
+constexpr int kStrip = 256;        // columns of 64 rows that a workgroup lays out
+constexpr int kCutTiles = kThreads;  // most tiles of a product that are cut along k
 
 struct InArgs {
   const void *g;
   int64_t rows, cols, ld, stride;  // of the input, elements
-  double *partials;                // [batch][kNormBlocks]
+  double *partials;                // [batch][blocks]
   int32_t *arrived;                // [kCutTiles], zeroed
   _Float16 *x, *xt;                // [batch][mp][np] and [batch][np][mp]
   int64_t mp, np;
   double eps;
+  int32_t blocks;
   int32_t tall;  // rows > cols: X is the transpose of G
 };
 
@@ -225,55 +227,76 @@ __device__ __forceinline__ double block_sum(double v, double *lds) {
   return v;
 }
 
+// Partial sums of squares, 8 elements a thread and run.
 template <class TG>
 __global__ void __launch_bounds__(kThreads) ortho_norm_kernel(const InArgs A) {
   __shared__ double lds[kThreads / 64];
   if (blockIdx.x + blockIdx.y == 0) A.arrived[threadIdx.x] = 0;
   const typename TG::raw *g =
       static_cast<const typename TG::raw *>(A.g) + int64_t(blockIdx.y) * A.stride;
-  const int64_t runs = (A.cols + kNormRun - 1) / kNormRun;
+  const unsigned runs = unsigned((A.cols + kNormRun - 1) / kNormRun);
+  const int64_t all = A.rows * runs;
   double s = 0.0;
-  for (int64_t w = blockIdx.x; w < A.rows * runs; w += kNormBlocks) {
-    const int64_t r = w / runs, c0 = (w - r * runs) * kNormRun;
-    const int64_t c1 = c0 + kNormRun < A.cols ? c0 + kNormRun : A.cols;
-    for (int64_t c = c0 + threadIdx.x; c < c1; c += kThreads) {
-      const double v = double(TG::load(g[r * A.ld + c]));
-      s = __builtin_fma(v, v, s);
-    }
+#pragma unroll 2
+  for (int64_t w = blockIdx.x; w < all; w += A.blocks) {
+    // all < 2^20 * 2^9
+    const unsigned r = unsigned(w) / runs;
+    const int64_t c = int64_t(unsigned(w) - r * runs) * kNormRun + threadIdx.x * 8;
+    const int64_t left = A.cols - c;
+    float v[8];
+    if (left >= 8) Pack<TG, 8>::load(g + r * A.ld, c, v);
+    else Pack<TG, 8>::load_some(g + r * A.ld, c, int(left), v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = __builtin_fma(double(v[e]), double(v[e]), s);
   }
   s = block_sum(s, lds);
-  if (threadIdx.x == 0) A.partials[int64_t(blockIdx.y) * kNormBlocks + blockIdx.x] = s;
+  if (threadIdx.x == 0) A.partials[int64_t(blockIdx.y) * A.blocks + blockIdx.x] = s;
 }
 
-// 64 x 64 tiles of X and of its transpose, scaled and padded with zeros.
+// 64 x 64 tiles of X and of its transpose, scaled and padded with zeros, a
+// strip of 64 rows after another.
 template <class TG>
 __global__ void __launch_bounds__(kThreads) ortho_layout_kernel(const InArgs A) {
   __shared__ double lds[kThreads / 64];
-  __shared__ _Float16 tile[64][66];
-  static_assert(kNormBlocks == kThreads, "one partial per thread");
-  const int64_t b = blockIdx.y;
-  const double sum = block_sum(A.partials[b * kNormBlocks + threadIdx.x], lds);
+  __shared__ __align__(16) _Float16 tile[64][68];
+  const int64_t b = blockIdx.z;
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < A.blocks; i += kThreads) sum += A.partials[b * A.blocks + i];
+  sum = block_sum(sum, lds);
   const double scale = double(kScale) / (sqrt(sum) + A.eps);
   const typename TG::raw *g = static_cast<const typename TG::raw *>(A.g) + b * A.stride;
-  // the tile in the input's orientation: [r0, r0+64) x [c0, c0+64) of G
+  // in the input's orientation, padded to rp x cp
   const int64_t rp = A.tall ? A.np : A.mp, cp = A.tall ? A.mp : A.np;
-  const int64_t tc = cp / 64;
-  const int64_t r0 = int64_t(blockIdx.x) / tc * 64, c0 = int64_t(blockIdx.x) % tc * 64;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t r0 = int64_t(blockIdx.y) * 64, c1 = int64_t(blockIdx.x + 1) * kStrip;
   _Float16 *same = (A.tall ? A.xt : A.x) + b * A.mp * A.np;
   _Float16 *turned = (A.tall ? A.x : A.xt) + b * A.mp * A.np;
-#pragma unroll 4
-  for (int i = wave; i < 64; i += 4) {
-    const int64_t r = r0 + i, c = c0 + lane;
-    _Float16 v = _Float16(0.0f);
-    if (r < A.rows && c < A.cols)
-      v = _Float16(float(double(TG::load(g[r * A.ld + c])) * scale));
-    tile[i][lane] = v;
-    same[r * cp + c] = v;
+  const int row = threadIdx.x >> 3, piece = (threadIdx.x & 7) * 8;
+  for (int64_t c0 = c1 - kStrip; c0 < c1 && c0 < cp; c0 += 64) {
+    half8 out[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t r = r0 + row + i * 32, c = c0 + piece, left = r < A.rows ? A.cols - c : 0;
+      float v[8];
+      if (left >= 8) Pack<TG, 8>::load(g + r * A.ld, c, v);
+      else Pack<TG, 8>::load_some(g + r * A.ld, c, int(left), v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[i][e] = _Float16(float(double(v[e]) * scale));
+      *reinterpret_cast<half8 *>(same + r * cp + c) = out[i];
+    }
+    __syncthreads();  // the last tile has been read
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      *reinterpret_cast<half4 *>(&tile[row + i * 32][piece]) = out[i].lo;
+      *reinterpret_cast<half4 *>(&tile[row + i * 32][piece + 4]) = out[i].hi;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[i][e] = tile[piece + e][row + i * 32];
+      *reinterpret_cast<half8 *>(turned + (c0 + row + i * 32) * rp + r0 + piece) = out[i];
+    }
   }
-  __syncthreads();
-#pragma unroll 4
-  for (int i = wave; i < 64; i += 4) turned[(c0 + i) * rp + r0 + lane] = tile[lane][i];
 }
 
 // ------------------------------------------------------- ortho: products
@@ -775,6 +798,7 @@ Way way_of(int64_t batch, int64_t r, int64_t c, int64_t k, bool symmetric) {
 struct Plan {
   int64_t m, n, mp, np;
   Way gram, poly, next;
+  int blocks;  // that sum the squares of a matrix
   bool tall;
   int64_t partials, arrived, parts, x, xt, y, yt, a, b, bytes;  // offsets into the workspace
 };
@@ -801,7 +825,9 @@ Plan plan_of(const zs_ortho_desc &d) {
   int64_t most = parts(p.next);
   if (parts(p.gram) > most) most = parts(p.gram);
   if (parts(p.poly) > most) most = parts(p.poly);
-  p.partials = take(d.batch * kNormBlocks * 8);
+  const int64_t runs = d.rows * (up(d.cols, kNormRun) / kNormRun);
+  p.blocks = int(runs < kNormBlocks ? runs : kNormBlocks);
+  p.partials = take(d.batch * p.blocks * 8);
   p.arrived = take(kCutTiles * 4);
   p.parts = take(most);
   p.x = take(d.batch * p.mp * p.np * 2);
@@ -853,10 +879,12 @@ int multiply(MulArgs &A, const Way &w, int64_t rows, int64_t cols, int64_t k, hi
 
 template <class TG>
 int start(const InArgs &A, int64_t batch, hipStream_t st) {
-  hipLaunchKernelGGL(ortho_norm_kernel<TG>, dim3(kNormBlocks, unsigned(batch)), dim3(kThreads), 0,
+  hipLaunchKernelGGL(ortho_norm_kernel<TG>, dim3(A.blocks, unsigned(batch)), dim3(kThreads), 0,
                      st, A);
-  hipLaunchKernelGGL(ortho_layout_kernel<TG>, dim3(unsigned(A.mp / 64 * (A.np / 64)),
-                     unsigned(batch)), dim3(kThreads), 0, st, A);
+  const int64_t rp = A.tall ? A.np : A.mp, cp = A.tall ? A.mp : A.np;
+  hipLaunchKernelGGL(ortho_layout_kernel<TG>,
+                     dim3(unsigned(up(cp, kStrip) / kStrip), unsigned(rp / 64), unsigned(batch)),
+                     dim3(kThreads), 0, st, A);
   return launched();
 }
 
@@ -922,9 +950,7 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
   if (d->batch == 0 || d->rows == 0 || d->cols == 0) return ZS_OK;
   const Plan p = plan_of(*d);
   if (!g || !o || !workspace || workspace_bytes < p.bytes) return ZS_EINVAL;
-  if (p.mp / 64 * (p.np / 64) > 0x7fffffff || !std::isfinite(p.gram.us) ||
-      !std::isfinite(p.next.us))
-    return ZS_EINVAL;
+  if (!std::isfinite(p.gram.us) || !std::isfinite(p.next.us)) return ZS_EINVAL;
   if (!aligned(g, dtype_size(d->dtype)) || !aligned(o, 2) || !aligned(workspace, 256))
     return ZS_EALIGN;
   if (const int rc = device_is_gfx950()) return rc;
@@ -947,6 +973,7 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
   in.np = p.np;
   in.eps = double(d->eps);
   in.tall = p.tall;
+  in.blocks = p.blocks;
   int rc = d->dtype == ZS_F32    ? start<F32>(in, d->batch, st)
            : d->dtype == ZS_BF16 ? start<Bf16>(in, d->batch, st)
                                  : start<F16>(in, d->batch, st);

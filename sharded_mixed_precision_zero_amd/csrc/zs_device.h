@@ -64,6 +64,41 @@ struct F16 {
   }
 };
 
+// V consecutive elements, aligned to one element: the memory takes 16-byte
+// accesses at any address, and rows of odd widths and strides need no path of
+// their own.
+template <class T, int V>
+struct Pack {
+  using raw = typename T::raw;
+  struct __attribute__((packed, aligned(sizeof(raw)))) Vec {
+    raw e[V];
+  };
+  static __device__ __forceinline__ void load(const void *row, int64_t i, float (&out)[V]) {
+    const Vec v = *reinterpret_cast<const Vec *>(static_cast<const raw *>(row) + i);
+#pragma unroll
+    for (int e = 0; e < V; ++e) out[e] = T::load(v.e[e]);
+  }
+  static __device__ __forceinline__ void store(void *row, int64_t i, const float (&in)[V]) {
+    Vec v;
+#pragma unroll
+    for (int e = 0; e < V; ++e) v.e[e] = T::store(in[e]);
+    *reinterpret_cast<Vec *>(static_cast<raw *>(row) + i) = v;
+  }
+  // The first n < V of them, the others 0.
+  static __device__ __forceinline__ void load_some(const void *row, int64_t i, int n,
+                                                   float (&out)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      out[e] = e < n ? T::load(static_cast<const raw *>(row)[i + e]) : 0.0f;
+  }
+  static __device__ __forceinline__ void store_some(void *row, int64_t i, int n,
+                                                    const float (&in)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < n) static_cast<raw *>(row)[i + e] = T::store(in[e]);
+  }
+};
+
 }  // namespace zs_dev
 
 #endif  // ZS_DEVICE_H
