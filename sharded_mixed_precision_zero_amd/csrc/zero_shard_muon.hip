@@ -23,8 +23,18 @@
 // contiguous k: X X^T and A A^T (A is symmetric) as they stand, and B X with
 // X kept transposed as well, which each update's epilogue writes next to X.
 // A and B are symmetric, so only the tiles on and below the diagonal are
-// computed and each is stored twice: m^2 n + m^3 + 2 m^2 n multiply-adds a step
+// computed and each is stored twice: m^2 n + m^3 + 2 m^2 n operations a step
 // in place of 2 m^2 n + 2 m^3 + 2 m^2 n.
+//
+// Of a matrix much longer than wide the products with X are most of that, and
+// two steps are taken with one of each: A and the polynomials in it commute, so
+// after B the next A is B A B, and with its polynomial B' the two steps are
+// X = (B' B) X: 3 m^2 n + 6 m^3 for two steps (the three extra products are
+// symmetric) in place of 6 m^2 n + 2 m^3.  Rounding leaves A with eigenvalues a
+// little below 0 and B A B multiplies those by a^2, so it is done once and then
+// A is made anew from X: in two steps the result is as far off as before
+// (Gaussian 512 x 1382: 1.26e-3 for 1.19e-3; ill-conditioned and rank-8 ones:
+// less than before), in three it diverges where A is singular.
 // All of it is laid out padded to whole tiles with zeros, which the iteration
 // keeps zero, so the products need no bounds.
 
@@ -683,9 +693,235 @@ __global__ void __launch_bounds__(WR *WC * 64) ortho_mul_kernel(const MulArgs A)
 #endif
 }
 
+// ------------------------------------------------- ortho: small matrices
+
+// A matrix that fits in the LDS of one CU is orthogonalised by one workgroup
+// in one launch: the products are so small that a launch for each costs more
+// than the work (96 x 128: 17 launches take 67 us, this 22 us; 64 x 512 68 and 31 us).  X, X^T, A and
+// B lie in LDS, rows of k elements 8 apart more than k, so that the 16 rows one
+// read instruction serves lie in different banks.  A wave computes blocks of
+// 32 x 32.
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallWaves = kSmallThreads / 64;
+constexpr int kSmallLds = 81920;   // 16-bit elements: 160 KB
+constexpr int kSmallPacks = 5;     // of 8 elements that a thread brings in
+constexpr int kSmallBlocks = 3;    // of 32 x 32 that a wave computes
+
+struct SmallArgs {
+  const void *g;
+  uint16_t *o;
+  int64_t ld_in, stride_in, ld_o, stride_o;
+  double eps;
+  int32_t rows, cols, mp, np, tall, steps;
+  float coeffs[3 * ZS_ORTHO_MAX_STEPS];
+};
+
+__host__ __device__ inline int64_t small_lds(int64_t mp, int64_t np) {
+  return mp * (np + 8) + np * (mp + 8) + 2 * mp * (mp + 8);
+}
+
+template <class TG, int MB>
+__global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const SmallArgs A) {
+  __shared__ __align__(16) _Float16 lds[kSmallLds];
+  const int tid = threadIdx.x;
+  int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr int mp = MB * 32, pm = mp + 8;
+  const int np = A.np, pn = np + 8;
+  _Float16 *x = lds, *xt = x + mp * pn, *a = xt + np * pm, *b = a + mp * pm;
+  const typename TG::raw *g =
+      static_cast<const typename TG::raw *>(A.g) + int64_t(blockIdx.x) * A.stride_in;
+  // the input's and output's orientation
+  const int rp = A.tall ? np : mp, cp = A.tall ? mp : np, pitch = cp + 8;
+  const int per = cp / 8, packs = rp * per;
+  _Float16 *same = A.tall ? xt : x;
+  {
+    // the input in its orientation, padded with zeros
+    float v[kSmallPacks][8];
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kSmallPacks; ++i) {
+      const int p = tid + i * kSmallThreads;
+      if (p >= packs) break;
+      const int r = p / per, c = (p - r * per) * 8, left = r < A.rows ? A.cols - c : 0;
+      if (left >= 8) Pack<TG, 8>::load(g + r * A.ld_in, c, v[i]);
+      else Pack<TG, 8>::load_some(g + r * A.ld_in, c, left, v[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = __builtin_fma(double(v[i][e]), double(v[i][e]), sum);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    double *part = reinterpret_cast<double *>(b);  // mp (mp + 8) elements: room for 16
+    if (lane == 0) part[wave] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < kSmallWaves; ++w) sum += part[w];
+    const double scale = double(kScale) / (sqrt(sum) + A.eps);
+    _Float16 *turned = A.tall ? x : xt;
+#pragma unroll
+    for (int i = 0; i < kSmallPacks; ++i) {
+      const int p = tid + i * kSmallThreads;
+      if (p >= packs) break;
+      const int r = p / per, c = (p - r * per) * 8;
+      half8 h;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = _Float16(float(double(v[i][e]) * scale));
+      *reinterpret_cast<half8 *>(same + r * pitch + c) = h;
+    }
+    __syncthreads();
+    for (int p = tid; p < packs; p += kSmallThreads) {
+      const int r = p / cp * 8, c = p % cp;
+      half8 h;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = same[(r + e) * pitch + c];
+      *reinterpret_cast<half8 *>(turned + c * (rp + 8) + r) = h;
+    }
+    __syncthreads();
+  }
+
+  using Block = f32x4[2][2];
+  struct Regs {
+    half8 p[2], q[2];
+  };
+  // 32 of k of a block, at p and q (this lane's pieces), rows `pitch` apart
+  const auto read = [&](Regs &f, const _Float16 *p, const _Float16 *q, int pitch) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      f.p[e] = *reinterpret_cast<const half8 *>(p + e * 16 * pitch);
+      f.q[e] = *reinterpret_cast<const half8 *>(q + e * 16 * pitch);
+    }
+  };
+  const auto add = [&](const Regs &f, Block &acc) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        acc[e][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.p[e], f.q[h], acc[e][h], 0, 0, 0);
+  };
+  const auto mine = [&](const _Float16 *p, int i, int pitch) {
+    return p + (i * 32 + (lane & 15)) * pitch + (lane >> 4) * 8;
+  };
+  // block i, j of P Q^T over mp
+  const auto square = [&](const _Float16 *P, const _Float16 *Q, int i, int j, Block &acc) {
+    const _Float16 *p = mine(P, i, pm), *q = mine(Q, j, pm);
+    Regs f[MB];
+#pragma unroll
+    for (int k = 0; k < MB; ++k) read(f[k], p + k * 32, q + k * 32, pm);
+#pragma unroll
+    for (int k = 0; k < MB; ++k) add(f[k], acc);
+  };
+  // rows r..r+3 of column c, for each of the block's four parts
+  const auto each = [&](int i, int j, auto &acc, auto f) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        f(i * 32 + e * 16 + (lane >> 4) * 4, j * 32 + h * 16 + (lane & 15), acc[e][h]);
+  };
+  constexpr float kBack = 1.0f / kScale;
+  const auto narrow = [](const f32x4 &v) {
+    half4 h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = _Float16(v[e]);
+    return h;
+  };
+  const int nb = np / 32;
+  static_assert(MB * MB <= kSmallWaves, "a wave has one block of A and of B");
+  const int wi = wave / MB, wj = wave % MB;
+  for (int s = 0; s < A.steps; ++s) {
+    // Opaque, so that no address is computed ahead of the loop and kept.
+    asm volatile("" : "+v"(lane));
+    const float ca = A.coeffs[3 * s], cb = A.coeffs[3 * s + 1], cc = A.coeffs[3 * s + 2];
+    // A and B are symmetric: column c's rows are neighbours in row c
+    if (wave < MB * MB) {
+      Block acc = {};
+      const _Float16 *p = mine(x, wi, pn), *q = mine(x, wj, pn);
+      Regs f0, f1;
+      read(f0, p, q, pn);
+      for (int k = 1; k < nb; k += 2) {
+        read(f1, p + k * 32, q + k * 32, pn);
+        add(f0, acc);
+        const int next = k + 1 < nb ? k + 1 : k;
+        read(f0, p + next * 32, q + next * 32, pn);
+        add(f1, acc);
+      }
+      if (nb & 1) add(f0, acc);
+      each(wi, wj, acc, [&](int r, int c, f32x4 v) {
+        *reinterpret_cast<half4 *>(a + c * pm + r) = narrow(v * kBack);
+      });
+    }
+    __syncthreads();
+    if (wave < MB * MB) {
+      Block acc = {};
+      square(a, a, wi, wj, acc);
+      each(wi, wj, acc, [&](int r, int c, f32x4 v) {
+        const half4 old = *reinterpret_cast<const half4 *>(a + c * pm + r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = __builtin_fmaf(cb, float(old[e]), (cc * kBack) * v[e]);
+        if (wi == wj) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (r + e == c) v[e] += ca * kScale;
+        }
+        *reinterpret_cast<half4 *>(b + c * pm + r) = narrow(v);
+      });
+    }
+    __syncthreads();
+    Block acc[kSmallBlocks] = {};
+#pragma unroll
+    for (int u = 0; u < kSmallBlocks; ++u) {
+      const int t = wave + u * kSmallWaves;
+      if (t < MB * nb) square(b, xt, t % MB, t / MB, acc[u]);
+    }
+    const bool last = s + 1 == A.steps;
+    __syncthreads();  // X^T has been read
+#pragma unroll
+    for (int u = 0; u < kSmallBlocks; ++u) {
+      const int t = wave + u * kSmallWaves;
+      if (t < MB * nb)
+        each(t % MB, t / MB, acc[u], [&](int r, int c, f32x4 v) {
+          half4 h;
+          if (last) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              h[e] = __builtin_bit_cast(_Float16, Bf16::store(v[e] * (kBack * kBack)));
+          } else {
+            h = narrow(v * kBack);
+          }
+          if (!last || A.tall) *reinterpret_cast<half4 *>(xt + c * pm + r) = h;
+          if (!last || !A.tall) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[(r + e) * pn + c] = h[e];
+          }
+        });
+    }
+    __syncthreads();
+  }
+  uint16_t *o = A.o + int64_t(blockIdx.x) * A.stride_o;
+  struct __attribute__((packed, aligned(2))) Vec {
+    half8 h;
+  };
+  for (int p = tid; p < packs; p += kSmallThreads) {
+    const int r = p / per, c = (p - r * per) * 8;
+    if (r >= A.rows) break;
+    uint16_t *to = o + r * A.ld_o + c;
+    const half8 h = *reinterpret_cast<const half8 *>(same + r * pitch + c);
+    if (c + 8 <= A.cols) {
+      reinterpret_cast<Vec *>(to)->h = h;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < A.cols) to[e] = reinterpret_cast<const uint16_t *>(same + r * pitch + c)[e];
+    }
+  }
+}
+
 // ------------------------------------------------------------------- host
 
 constexpr float kCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
+constexpr float kPairMost = 16.0f;  // of the product of a pair's first coefficients
 constexpr int64_t kMaxSide = INT64_C(1) << 20;
 
 bool muon_ok(const zs_muon_desc *d) {
@@ -798,9 +1034,11 @@ Way way_of(int64_t batch, int64_t r, int64_t c, int64_t k, bool symmetric) {
 struct Plan {
   int64_t m, n, mp, np;
   Way gram, poly, next;
-  int blocks;  // that sum the squares of a matrix
+  int blocks;   // that sum the squares of a matrix
+  bool small;   // one workgroup per matrix, padded to 32
+  bool paired;  // two steps at a time where the coefficients allow it
   bool tall;
-  int64_t partials, arrived, parts, x, xt, y, yt, a, b, bytes;  // offsets into the workspace
+  int64_t partials, arrived, parts, x, xt, y, yt, a, b, c, bytes;  // offsets into the workspace
 };
 
 Plan plan_of(const zs_ortho_desc &d) {
@@ -808,11 +1046,19 @@ Plan plan_of(const zs_ortho_desc &d) {
   p.tall = d.rows > d.cols;
   p.m = p.tall ? d.cols : d.rows;
   p.n = p.tall ? d.rows : d.cols;
+  p.mp = up(p.m, 32);
+  p.np = up(p.n, 32);
+  p.small = small_lds(p.mp, p.np) <= kSmallLds;
+  if (p.small) {
+    p.bytes = 256;  // not used: every plan asks for a workspace
+    return p;
+  }
   p.mp = up(p.m, 64);
   p.np = up(p.n, 64);
   p.gram = way_of(d.batch, p.mp, p.mp, p.np, true);
   p.poly = way_of(d.batch, p.mp, p.mp, p.mp, true);
   p.next = way_of(d.batch, p.mp, p.np, p.mp, false);
+  p.paired = d.steps > 1 && 3 * p.poly.us < p.gram.us + p.next.us;
   int64_t at = 0;
   const auto take = [&](int64_t bytes) {
     const int64_t was = at;
@@ -836,6 +1082,7 @@ Plan plan_of(const zs_ortho_desc &d) {
   p.yt = take(d.batch * p.mp * p.np * 2);
   p.a = take(d.batch * p.mp * p.mp * 2);
   p.b = take(d.batch * p.mp * p.mp * 2);
+  p.c = p.paired ? take(d.batch * p.mp * p.mp * 2) : 0;
   p.bytes = at;
   return p;
 }
@@ -885,6 +1132,18 @@ int start(const InArgs &A, int64_t batch, hipStream_t st) {
   hipLaunchKernelGGL(ortho_layout_kernel<TG>,
                      dim3(unsigned(up(cp, kStrip) / kStrip), unsigned(rp / 64), unsigned(batch)),
                      dim3(kThreads), 0, st, A);
+  return launched();
+}
+
+template <class TG>
+int small(const SmallArgs &A, int64_t batch, hipStream_t st) {
+  const dim3 grid{unsigned(batch)}, block{kSmallThreads};
+  switch (A.mp / 32) {
+    case 1: hipLaunchKernelGGL((ortho_small_kernel<TG, 1>), grid, block, 0, st, A); break;
+    case 2: hipLaunchKernelGGL((ortho_small_kernel<TG, 2>), grid, block, 0, st, A); break;
+    case 3: hipLaunchKernelGGL((ortho_small_kernel<TG, 3>), grid, block, 0, st, A); break;
+    default: hipLaunchKernelGGL((ortho_small_kernel<TG, 4>), grid, block, 0, st, A); break;
+  }
   return launched();
 }
 
@@ -950,7 +1209,7 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
   if (d->batch == 0 || d->rows == 0 || d->cols == 0) return ZS_OK;
   const Plan p = plan_of(*d);
   if (!g || !o || !workspace || workspace_bytes < p.bytes) return ZS_EINVAL;
-  if (!std::isfinite(p.gram.us) || !std::isfinite(p.next.us)) return ZS_EINVAL;
+  if (!p.small && (!std::isfinite(p.gram.us) || !std::isfinite(p.next.us))) return ZS_EINVAL;
   if (!aligned(g, dtype_size(d->dtype)) || !aligned(o, 2) || !aligned(workspace, 256))
     return ZS_EALIGN;
   if (const int rc = device_is_gfx950()) return rc;
@@ -958,6 +1217,27 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
   char *ws = static_cast<char *>(workspace);
   const auto half = [&](int64_t off) { return reinterpret_cast<_Float16 *>(ws + off); };
   const int64_t ld_in = d->ld_in ? d->ld_in : d->cols, ld_out = d->ld_out ? d->ld_out : d->cols;
+  if (p.small) {
+    SmallArgs A;
+    std::memset(&A, 0, sizeof A);
+    A.g = g;
+    A.o = o;
+    A.ld_in = ld_in;
+    A.stride_in = d->stride_in ? d->stride_in : d->rows * ld_in;
+    A.ld_o = ld_out;
+    A.stride_o = d->stride_out ? d->stride_out : d->rows * ld_out;
+    A.eps = double(d->eps);
+    A.rows = int32_t(d->rows);
+    A.cols = int32_t(d->cols);
+    A.mp = int32_t(p.mp);
+    A.np = int32_t(p.np);
+    A.tall = p.tall;
+    A.steps = d->steps;
+    for (int i = 0; i < 3 * d->steps; ++i) A.coeffs[i] = d->coeffs ? d->coeffs[i] : kCoeffs[i % 3];
+    return d->dtype == ZS_F32    ? small<F32>(A, d->batch, st)
+           : d->dtype == ZS_BF16 ? small<Bf16>(A, d->batch, st)
+                                 : small<F16>(A, d->batch, st);
+  }
   InArgs in;
   std::memset(&in, 0, sizeof in);
   in.g = g;
@@ -989,27 +1269,49 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
   A.stride_o = d->stride_out ? d->stride_out : d->rows * ld_out;
   A.tall = p.tall;
   A.wide = aligned(o, 16) && d->cols % 8 == 0 && ld_out % 8 == 0 && A.stride_o % 8 == 0;
-  for (int s = 0; s < d->steps && !rc; ++s) {
-    const float *k = d->coeffs ? d->coeffs + 3 * s : kCoeffs;
-    A.p = A.q = x;
-    A.stride_p = A.stride_q = p.mp * p.np;
-    A.c = half(p.a);
-    A.stride_c = p.mp * p.mp;
-    if ((rc = multiply<kGram>(A, p.gram, p.mp, p.mp, p.np, st))) break;
-    A.p = A.q = half(p.a);
-    A.stride_p = A.stride_q = p.mp * p.mp;
-    A.c = half(p.b);
+  const int64_t square = p.mp * p.mp, whole = p.mp * p.np;
+  // C = P Q^T of m x m matrices that commute, and poly's combination
+  const auto small = [&](auto kind, const _Float16 *pp, const _Float16 *qq, _Float16 *cc) {
+    A.p = pp;
+    A.q = qq;
+    A.stride_p = A.stride_q = A.stride_c = square;
+    A.c = cc;
+    return multiply<kind.value>(A, p.poly, p.mp, p.mp, p.mp, st);
+  };
+  const auto poly = [&](const float *k, const _Float16 *from, _Float16 *to) {
     A.a = k[0];
     A.b = k[1];
     A.cc = k[2];
-    if ((rc = multiply<kPoly>(A, p.poly, p.mp, p.mp, p.mp, st))) break;
-    A.p = half(p.b);
+    return small(Const<kPoly>{}, from, from, to);
+  };
+  _Float16 *a = half(p.a), *b = half(p.b), *c = half(p.c);
+  for (int s = 0; s < d->steps && !rc;) {
+    const float *k = d->coeffs ? d->coeffs + 3 * s : kCoeffs;
+    const float *k2 = d->coeffs ? k + 3 : kCoeffs;
+    A.p = A.q = x;
+    A.stride_p = A.stride_q = whole;
+    A.c = a;
+    A.stride_c = square;
+    if ((rc = multiply<kGram>(A, p.gram, p.mp, p.mp, p.np, st))) break;
+    if ((rc = poly(k, a, b))) break;
+    const _Float16 *by = b;
+    ++s;
+    if (p.paired && s < d->steps && k[0] * k2[0] > 0.0f && k[0] * k2[0] <= kPairMost) {
+      // A of the next step is B A B; its B times this one's is applied to X
+      if ((rc = small(Const<kGram>{}, b, a, c)) || (rc = small(Const<kGram>{}, c, b, a)) ||
+          (rc = poly(k2, a, c)) || (rc = small(Const<kGram>{}, c, b, a)))
+        break;
+      by = a;
+      ++s;
+    }
+    A.p = by;
+    A.stride_p = square;
     A.q = xt;
-    A.stride_q = p.mp * p.np;
-    if (s + 1 < d->steps) {
+    A.stride_q = whole;
+    if (s < d->steps) {
       A.c = y;
       A.ct = yt;
-      A.stride_c = p.mp * p.np;
+      A.stride_c = whole;
       rc = multiply<kNext>(A, p.next, p.mp, p.np, p.mp, st);
       _Float16 *v = x;
       x = y;
