@@ -233,6 +233,10 @@ def _ptr(t) -> int | None:
     return int(t.data_ptr())
 
 
+def _ptrs(*tensors) -> list:
+    return [None if t is None else t.data_ptr() for t in tensors]
+
+
 def contrib_table(contrib) -> ctypes.Array | None:
     """Host array of device pointers: a list of 1-D tensors (or None), or the
     rows of a 2-D tensor (row k = rank k's contribution, codes or scales)."""
@@ -452,8 +456,8 @@ def layernorm_desc(*, rows: int, cols: int, dtype=torch.bfloat16, param_dtype=No
 
 def zero_shard_layernorm(desc: zs_layernorm_desc, x, residual, gamma, beta, sum_out, y, mean,
                          rstd) -> int:
-    return _lib.zero_shard_layernorm(ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(gamma),
-                                     _ptr(beta), _ptr(sum_out), _ptr(y), _ptr(mean), _ptr(rstd))
+    return _lib.zero_shard_layernorm(ctypes.byref(desc),
+                                     *_ptrs(x, residual, gamma, beta, sum_out, y, mean, rstd))
 
 
 def zero_shard_layernorm_workspace(desc: zs_layernorm_desc) -> int:
@@ -465,8 +469,8 @@ def zero_shard_layernorm_bwd(desc: zs_layernorm_desc, dy, x, gamma, mean, rstd, 
     """workspace: a contiguous device tensor (its size in bytes is passed on)
     or None."""
     return _lib.zero_shard_layernorm_bwd(
-        ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd), _ptr(dsum),
-        _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), _nbytes(workspace))
+        ctypes.byref(desc), *_ptrs(dy, x, gamma, mean, rstd, dsum, dx, dgamma, dbeta, workspace),
+        _nbytes(workspace))
 
 
 def _nbytes(t) -> int:
@@ -635,7 +639,8 @@ class ZeroLayerNorm:
         self._stream = torch.cuda.current_stream() if stream is None else stream
         self.desc = layernorm_desc(rows=rows, cols=cols, dtype=dtype, param_dtype=param_dtype,
                                    eps=eps, stream=self._stream)
-        size = zero_shard_layernorm_workspace(self.desc)
+        self._ref = ctypes.byref(self.desc)
+        self._workspace_bytes = size = zero_shard_layernorm_workspace(self.desc)
         _require(size >= 0, "layer norm's sizes")
         with torch.cuda.stream(self._stream):
             self.mean = torch.empty(rows, device="cuda", dtype=torch.float32)
@@ -646,14 +651,17 @@ class ZeroLayerNorm:
         """Row stride of a (rows, cols) tensor; 0 for None."""
         if t is None:
             return 0
-        _require(t.shape == self.shape and t.dtype == self.dtype and t.is_cuda
-                 and (t.stride(1) == 1 or self.shape[1] == 1), what)
-        return t.stride(0) if self.shape[0] > 1 else 0
+        if t.shape != self.shape or t.dtype is not self.dtype or not t.is_cuda:
+            raise ZeroShardError(ZS_EINVAL, what)
+        ld, unit = t.stride()
+        if unit != 1 and self.shape[1] != 1:
+            raise ZeroShardError(ZS_EINVAL, what)
+        return ld if self.shape[0] > 1 else 0
 
     def _param(self, t, what: str) -> None:
-        if t is not None:
-            _require(t.shape == self.shape[1:] and t.dtype == self.param_dtype and t.is_cuda
-                     and t.is_contiguous(), what)
+        if (t.shape != self.shape[1:] or t.dtype is not self.param_dtype or not t.is_cuda
+                or not t.is_contiguous()):
+            raise ZeroShardError(ZS_EINVAL, what)
 
     def forward(self, x, y, *, gamma=None, beta=None, residual=None, sum_out=None) -> None:
         """y = LN(x), or LN(sum_out) with sum_out = x + residual; keeps the
@@ -661,10 +669,14 @@ class ZeroLayerNorm:
         d = self.desc
         d.ld_x, d.ld_y = self._row(x, "x"), self._row(y, "y")
         d.ld_residual, d.ld_sum = self._row(residual, "residual"), self._row(sum_out, "sum_out")
-        self._param(gamma, "gamma")
-        self._param(beta, "beta")
-        _check(zero_shard_layernorm(d, x, residual, gamma, beta, sum_out, y, self.mean,
-                                    self.rstd), "zero_shard_layernorm")
+        if gamma is not None:
+            self._param(gamma, "gamma")
+        if beta is not None:
+            self._param(beta, "beta")
+        rc = _lib.zero_shard_layernorm(self._ref, *_ptrs(x, residual, gamma, beta, sum_out, y,
+                                                         self.mean, self.rstd))
+        if rc:
+            _check(rc, "zero_shard_layernorm")
 
     def backward(self, dy, x, dx, *, gamma=None, dgamma=None, dbeta=None, dsum=None, mean=None,
                  rstd=None) -> None:
@@ -673,15 +685,18 @@ class ZeroLayerNorm:
         d = self.desc
         d.ld_dy, d.ld_x = self._row(dy, "dy"), self._row(x, "x")
         d.ld_dx, d.ld_dsum = self._row(dx, "dx"), self._row(dsum, "dsum")
-        self._param(gamma, "gamma")
-        self._param(dgamma, "dgamma")
-        self._param(dbeta, "dbeta")
+        for t, what in ((gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta")):
+            if t is not None:
+                self._param(t, what)
         for t in (mean, rstd):
-            _require(t is None or (t.shape == self.shape[:1] and t.dtype == torch.float32
+            _require(t is None or (t.shape == self.shape[:1] and t.dtype is torch.float32
                                    and t.is_cuda and t.is_contiguous()), "mean, rstd")
-        _check(zero_shard_layernorm_bwd(d, dy, x, gamma, self.mean if mean is None else mean,
-                                        self.rstd if rstd is None else rstd, dsum, dx, dgamma,
-                                        dbeta, self.workspace), "zero_shard_layernorm_bwd")
+        rc = _lib.zero_shard_layernorm_bwd(
+            self._ref, *_ptrs(dy, x, gamma, self.mean if mean is None else mean,
+                              self.rstd if rstd is None else rstd, dsum, dx, dgamma, dbeta,
+                              self.workspace), self._workspace_bytes)
+        if rc:
+            _check(rc, "zero_shard_layernorm_bwd")
 
 
 class ZeroOrtho:

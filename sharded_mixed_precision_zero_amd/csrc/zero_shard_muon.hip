@@ -252,12 +252,10 @@ __global__ void __launch_bounds__(kThreads) ortho_norm_kernel(const InArgs A) {
     // all < 2^20 * 2^9
     const unsigned r = unsigned(w) / runs;
     const int64_t c = int64_t(unsigned(w) - r * runs) * kNormRun + threadIdx.x * 8;
-    const int64_t left = A.cols - c;
-    float v[8];
-    if (left >= 8) Pack<TG, 8>::load(g + r * A.ld, c, v);
-    else Pack<TG, 8>::load_some(g + r * A.ld, c, int(left), v);
+    Eight<TG> v;
+    v.load(g + r * A.ld, c, A.cols - c);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s = __builtin_fma(double(v[e]), double(v[e]), s);
+    for (int e = 0; e < 8; ++e) s = __builtin_fma(double(v.get(e)), double(v.get(e)), s);
   }
   s = block_sum(s, lds);
   if (threadIdx.x == 0) A.partials[int64_t(blockIdx.y) * A.blocks + blockIdx.x] = s;
@@ -286,11 +284,10 @@ __global__ void __launch_bounds__(kThreads) ortho_layout_kernel(const InArgs A) 
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int64_t r = r0 + row + i * 32, c = c0 + piece, left = r < A.rows ? A.cols - c : 0;
-      float v[8];
-      if (left >= 8) Pack<TG, 8>::load(g + r * A.ld, c, v);
-      else Pack<TG, 8>::load_some(g + r * A.ld, c, int(left), v);
+      Eight<TG> v;
+      v.load(g + r * A.ld, c, left);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) out[i][e] = _Float16(float(double(v[e]) * scale));
+      for (int e = 0; e < 8; ++e) out[i][e] = _Float16(float(double(v.get(e)) * scale));
       *reinterpret_cast<half8 *>(same + r * cp + c) = out[i];
     }
     __syncthreads();  // the last tile has been read
@@ -737,17 +734,17 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const SmallA
   _Float16 *same = A.tall ? xt : x;
   {
     // the input in its orientation, padded with zeros
-    float v[kSmallPacks][8];
+    Eight<TG> v[kSmallPacks];
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < kSmallPacks; ++i) {
       const int p = tid + i * kSmallThreads;
       if (p >= packs) break;
       const int r = p / per, c = (p - r * per) * 8, left = r < A.rows ? A.cols - c : 0;
-      if (left >= 8) Pack<TG, 8>::load(g + r * A.ld_in, c, v[i]);
-      else Pack<TG, 8>::load_some(g + r * A.ld_in, c, left, v[i]);
+      v[i].load(g + r * A.ld_in, c, left);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum = __builtin_fma(double(v[i][e]), double(v[i][e]), sum);
+      for (int e = 0; e < 8; ++e)
+        sum = __builtin_fma(double(v[i].get(e)), double(v[i].get(e)), sum);
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
@@ -766,7 +763,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const SmallA
       const int r = p / per, c = (p - r * per) * 8;
       half8 h;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = _Float16(float(double(v[i][e]) * scale));
+      for (int e = 0; e < 8; ++e) h[e] = _Float16(float(double(v[i].get(e)) * scale));
       *reinterpret_cast<half8 *>(same + r * pitch + c) = h;
     }
     __syncthreads();

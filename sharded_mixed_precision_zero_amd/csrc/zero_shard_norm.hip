@@ -9,12 +9,14 @@
 //             dgamma = sum_rows dy h;  dbeta = sum_rows dy
 //
 // Everything is binary32 inside, each output rounded once.  Both directions
-// are HBM-bound, so a row is read once and stays in registers: one wave per
-// row up to 2048 columns, a workgroup per row up to 16384, and the variance is
-// the centred sum of squares over the registers.  The backward pass keeps
-// dgamma and dbeta of the rows it walks in registers too, one partial row of
-// each per workgroup, and a second launch adds the partials in a fixed order:
-// no atomics, so the same inputs give the same bits.
+// are HBM-bound, so a row is read once and stays in registers as it lay in
+// memory, eight elements a thread (sixteen above 8192 columns), and the
+// variance is the centred sum of squares over them.  A workgroup takes several
+// rows at a time: their loads are in flight together and their sums cross the
+// waves together, and it goes on to further rows with gamma and beta (and the
+// gradients' sums) in its registers.  The backward pass leaves one partial row
+// of dgamma and dbeta per workgroup, and a second launch adds the partials in a
+// fixed order: no atomics, so the same inputs give the same bits.
 
 #include <hip/hip_runtime.h>
 
@@ -32,58 +34,67 @@ using namespace zs_dev;
 constexpr int kThreads = 256;
 constexpr int kLongThreads = 1024;
 constexpr int kMaxRegCols = 16384;  // rows up to here stay in registers
-constexpr int kMaxParts = 512;      // partial rows of dgamma / dbeta
+constexpr int kCus = 256;
+constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr int kMaxParts = 256;      // partial rows of dgamma / dbeta
 
-// V consecutive elements of a row: one access of V * sizeof(raw) bytes.
-template <class T, int V>
-struct Pack {
-  using raw = typename T::raw;
-  static constexpr int kBytes = V * int(sizeof(raw));
-  struct alignas(kBytes < 16 ? kBytes : 16) Vec {
-    raw e[V];
-  };
-  static __device__ __forceinline__ void load(const void *row, int64_t i, float (&out)[V]) {
-    const Vec v = *reinterpret_cast<const Vec *>(static_cast<const raw *>(row) + i);
-#pragma unroll
-    for (int e = 0; e < V; ++e) out[e] = T::load(v.e[e]);
-  }
-  static __device__ __forceinline__ void store(void *row, int64_t i, const float (&in)[V]) {
-    Vec v;
-#pragma unroll
-    for (int e = 0; e < V; ++e) v.e[e] = T::store(in[e]);
-    *reinterpret_cast<Vec *>(static_cast<raw *>(row) + i) = v;
-  }
-};
-
-template <class T>
-__device__ __forceinline__ float rounded(float v) {
-  return T::load(T::store(v));
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, ROWS, 0xf, false));
 }
 
-// Sum of a and b over the TPR threads of a row, in every one of them.
-template <int TPR>
-__device__ __forceinline__ void row_sum2(float &a, float &b, float (*lds)[2]) {
+// Sum over each 16 lanes, in all of them.
+__device__ __forceinline__ float sum16(float v) {
+  v += dpp<0xb1>(v);   // lanes 1 apart
+  v += dpp<0x4e>(v);   // 2 apart
+  v += dpp<0x141>(v);  // half row mirrored
+  return v + dpp<0x140>(v);  // row mirrored
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+
+// Sum over the wave, uniform.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = sum16(v);
+  v += dpp<0x142, 0xa>(v);  // rows 1 and 3: with the row before
+  v += dpp<0x143, 0xc>(v);  // rows 2 and 3: with the first half
+  return lane_value(v, 63);
+}
+
+// Sums over the waves of a row group, M of them at once, uniform.  One barrier
+// each: two buffers take turns, so a buffer is written again only after all
+// have passed the next sum's barrier.
+struct Sums {
+  float (*lds)[16][8];  // [2][wave of the workgroup][sum]
+  int first, waves;     // of this row group
+  int turn = 0;
+  template <int M>
+  __device__ __forceinline__ void add(float (&v)[M]) {
+    static_assert(M <= 8, "a buffer's row");
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    a += __shfl_xor(a, o, 64);
-    b += __shfl_xor(b, o, 64);
-  }
-  if constexpr (TPR > 64) {
-    constexpr int W = TPR / 64;
-    __syncthreads();  // the previous sum's readers are done
-    if ((threadIdx.x & 63) == 0) {
-      lds[threadIdx.x >> 6][0] = a;
-      lds[threadIdx.x >> 6][1] = b;
+    for (int m = 0; m < M; ++m) v[m] = wave_sum(v[m]);
+    if (waves == 1) return;
+    const int lane = threadIdx.x & 63;
+    float (*buf)[8] = lds[turn];
+    turn ^= 1;
+    if (lane == 0) {
+#pragma unroll
+      for (int m = 0; m < M; ++m) buf[threadIdx.x >> 6][m] = v[m];
     }
     __syncthreads();
-    a = b = 0.0f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      a += lds[w][0];
-      b += lds[w][1];
+    for (int m = 0; m < M; m += 4) {
+      const int at = m + (lane >> 4), w = lane & 15;
+      float s = w < waves && at < M ? buf[first + w][at] : 0.0f;
+      s = sum16(s);
+#pragma unroll
+      for (int k = m; k < m + 4 && k < M; ++k) v[k] = lane_value(s, (k - m) * 16);
     }
   }
-}
+};
 
 // The statistics after the centred sweep: off = the sum of (s - mean), zero
 // but for the rounding of the mean, becomes what the mean is off by (a row
@@ -103,6 +114,7 @@ struct FwdArgs {
   void *sum, *y;
   float *mean, *rstd;
   float eps;
+  int32_t per;  // threads of a row
 };
 
 template <class T>
@@ -114,151 +126,196 @@ __device__ __forceinline__ void *row_of(void *p, int64_t r, int64_t ld) {
   return static_cast<typename T::raw *>(p) + r * ld;
 }
 
-template <int TPR>
-constexpr int kBlock = TPR < kThreads ? kThreads : TPR;
+// A thread's columns: N times eight, `per` threads apart.
+template <int N>
+struct Columns {
+  unsigned i[N];
+  int left[N];
+  __device__ __forceinline__ Columns(int t, int per, int cols) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      i[n] = (n * per + t) * 8;
+      left[n] = cols - int(i[n]);
+    }
+  }
+};
 
-// One row per TPR threads, E elements of it in each thread's registers.
-template <class TX, class TP, int TPR, int E, int V>
-__global__ void __launch_bounds__(kBlock<TPR>) ln_fwd_kernel(const FwdArgs A) {
-  constexpr int N = E / V, RPB = kBlock<TPR> / TPR;
-  __shared__ float lds[TPR > 64 ? TPR / 64 : 1][2];
-  const int t = threadIdx.x % TPR;
+// gamma or beta at these columns (`none` where the caller gave none)
+template <bool TAIL, class TP, int N>
+__device__ __forceinline__ void load_params(Eight<TP> (&v)[N], const void *p, float none,
+                                            const Columns<N> &c) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    if (p) {
+      v[n].template load<TAIL>(p, c.i[n], c.left[n]);
+    } else {
+      const float all[8] = {none, none, none, none, none, none, none, none};
+      v[n].set(all);
+    }
+  }
+}
+
+// R rows at a time, each over `per` threads (a multiple of 64) of the
+// workgroup's blockDim.x / per row groups.  TAIL: the columns are no multiple of 8.
+template <class TX, class TP, int N, int R, bool TAIL>
+__global__ void __launch_bounds__(1024) ln_fwd_kernel(const FwdArgs A) {
+  __shared__ float lds[2][16][8];
+  const int per = A.per, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / per);
+  const int t = threadIdx.x - sub * per, subs = blockDim.x / per;
+  Sums sums{lds, sub * per / 64, per / 64};
+  const Columns<N> c(t, per, int(A.cols));
+  Eight<TP> gamma[N], beta[N];
+  load_params<TAIL>(gamma, A.gamma, 1.0f, c);
+  load_params<TAIL>(beta, A.beta, 0.0f, c);
   const float inv = 1.0f / float(A.cols);
-  for (int64_t r = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR; r < A.rows;
-       r += int64_t(gridDim.x) * RPB) {
-    float s[N][V];
-    const void *xr = row_of<TX>(A.x, r, A.ld_x);
-    float total = 0.0f, sq = 0.0f;
+  const int64_t step = int64_t(gridDim.x) * subs * R;
+  for (int64_t first = int64_t(blockIdx.x) * subs * R; first < A.rows; first += step) {
+    const int64_t r0 = first + sub * R;
+    Eight<TX> x[R][N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int64_t i = int64_t(j * TPR + t) * V;
-      if (i < A.cols) {
-        Pack<TX, V>::load(xr, i, s[j]);
-      } else {
+    for (int k = 0; k < R; ++k)
 #pragma unroll
-        for (int e = 0; e < V; ++e) s[j][e] = 0.0f;
-      }
-    }
+      for (int n = 0; n < N; ++n)
+        x[k][n].template load<TAIL, true>(row_of<TX>(A.x, r0 + k, A.ld_x), c.i[n], r0 + k < A.rows ? c.left[n] : 0);
     if (A.residual) {
-      const void *rr = row_of<TX>(A.residual, r, A.ld_r);
-      void *sr = row_of<TX>(A.sum, r, A.ld_s);
+      Eight<TX> q[R][N];
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int64_t i = int64_t(j * TPR + t) * V;
-        if (i < A.cols) {
-          float q[V];
-          Pack<TX, V>::load(rr, i, q);
+      for (int k = 0; k < R; ++k)
 #pragma unroll
-          for (int e = 0; e < V; ++e) s[j][e] = rounded<TX>(s[j][e] + q[e]);
-          Pack<TX, V>::store(sr, i, s[j]);
+        for (int n = 0; n < N; ++n)
+          q[k][n].template load<TAIL, true>(row_of<TX>(A.residual, r0 + k, A.ld_r), c.i[n],
+                       r0 + k < A.rows ? c.left[n] : 0);
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          float s[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[e] = x[k][n].get(e) + q[k][n].get(e);
+          x[k][n].set(s);
+          if (r0 + k < A.rows)
+            x[k][n].template store<TAIL>(row_of<TX>(A.sum, r0 + k, A.ld_s), c.i[n], c.left[n]);
         }
-      }
     }
+    float mean[R], both[2 * R];
 #pragma unroll
-    for (int j = 0; j < N; ++j)
+    for (int k = 0; k < R; ++k) {
+      mean[k] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < V; ++e) total += s[j][e];
-    row_sum2<TPR>(total, sq, lds);
-    float mean = total * inv, off = 0.0f;
+      for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int64_t i = int64_t(j * TPR + t) * V;
-      if (i < A.cols) {
+        for (int e = 0; e < 8; ++e) mean[k] += x[k][n].get(e);
+    }
+    sums.add(mean);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          s[j][e] -= mean;
-          sq = __builtin_fmaf(s[j][e], s[j][e], sq);
-          off += s[j][e];
+    for (int k = 0; k < R; ++k) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) x[k][n].forget();
+      mean[k] *= inv;
+      float sq = 0.0f, off = 0.0f;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = (TAIL ? e : 0) < c.left[n] ? x[k][n].get(e) - mean[k] : 0.0f;
+          sq = __builtin_fmaf(d, d, sq);
+          off += d;
         }
-      }
+      both[2 * k] = sq;
+      both[2 * k + 1] = off;
     }
-    row_sum2<TPR>(sq, off, lds);
-    const float rstd = finish(sq, off, inv, A.eps, mean);
-    void *yr = row_of<TX>(A.y, r, A.ld_y);
+    sums.add(both);
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int64_t i = int64_t(j * TPR + t) * V;
-      if (i < A.cols) {
-        float g[V], b[V];
-        if (A.gamma) Pack<TP, V>::load(A.gamma, i, g);
-        if (A.beta) Pack<TP, V>::load(A.beta, i, b);
+    for (int k = 0; k < R; ++k) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          float h = (s[j][e] - off) * rstd;
-          if (A.gamma) h *= g[e];
-          if (A.beta) h += b[e];
-          s[j][e] = h;
+      for (int n = 0; n < N; ++n) x[k][n].forget();
+      const float rough = mean[k];
+      float off = both[2 * k + 1];
+      const float rstd = finish(both[2 * k], off, inv, A.eps, mean[k]);
+      if (r0 + k >= A.rows) break;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float h = ((x[k][n].get(e) - rough) - off) * rstd;
+          y[e] = h * gamma[n].get(e) + beta[n].get(e);
         }
-        Pack<TX, V>::store(yr, i, s[j]);
+        x[k][n].set(y);
+        x[k][n].template store<TAIL>(row_of<TX>(A.y, r0 + k, A.ld_y), c.i[n], c.left[n]);
       }
-    }
-    if (t == 0) {
-      if (A.mean) A.mean[r] = mean;
-      if (A.rstd) A.rstd[r] = rstd;
+      if (t == 0) {
+        if (A.mean) A.mean[r0 + k] = mean[k];
+        if (A.rstd) A.rstd[r0 + k] = rstd;
+      }
     }
   }
 }
 
 // Rows too long for registers: three sweeps, each thread over its own
 // elements (which also makes the sum it wrote the sum it reads back).
-template <class TX, class TP, int V>
+template <class TX, class TP>
 __global__ void __launch_bounds__(kLongThreads) ln_fwd_long_kernel(const FwdArgs A) {
-  __shared__ float lds[kLongThreads / 64][2];
+  __shared__ float lds[2][16][8];
+  Sums sums{lds, 0, kLongThreads / 64};
   const float inv = 1.0f / float(A.cols);
+  const int64_t i0 = int64_t(threadIdx.x) * 8, step = int64_t(kLongThreads) * 8;
   for (int64_t r = blockIdx.x; r < A.rows; r += gridDim.x) {
-    const void *xr = row_of<TX>(A.x, r, A.ld_x);
-    const void *src = xr;
-    float total = 0.0f, sq = 0.0f, none = 0.0f, s[V];
+    const void *src = row_of<TX>(A.x, r, A.ld_x);
+    float total[1] = {0.0f}, both[2] = {0.0f, 0.0f};
+    Eight<TX> x, q;
     if (A.residual) {
       const void *rr = row_of<TX>(A.residual, r, A.ld_r);
       void *sr = row_of<TX>(A.sum, r, A.ld_s);
-      for (int64_t i = int64_t(threadIdx.x) * V; i < A.cols; i += int64_t(kLongThreads) * V) {
-        float q[V];
-        Pack<TX, V>::load(xr, i, s);
-        Pack<TX, V>::load(rr, i, q);
+      for (int64_t i = i0; i < A.cols; i += step) {
+        float s[8];
+        x.load(src, i, A.cols - i);
+        q.load(rr, i, A.cols - i);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          s[e] = rounded<TX>(s[e] + q[e]);
-          total += s[e];
-        }
-        Pack<TX, V>::store(sr, i, s);
+        for (int e = 0; e < 8; ++e) s[e] = x.get(e) + q.get(e);
+        x.set(s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) total[0] += x.get(e);
+        x.store(sr, i, A.cols - i);
       }
       src = sr;
     } else {
-      for (int64_t i = int64_t(threadIdx.x) * V; i < A.cols; i += int64_t(kLongThreads) * V) {
-        Pack<TX, V>::load(src, i, s);
+      for (int64_t i = i0; i < A.cols; i += step) {
+        x.load(src, i, A.cols - i);
 #pragma unroll
-        for (int e = 0; e < V; ++e) total += s[e];
+        for (int e = 0; e < 8; ++e) total[0] += x.get(e);
       }
     }
-    row_sum2<kLongThreads>(total, none, lds);
-    float mean = total * inv, off = 0.0f;
+    sums.add(total);
+    float mean = total[0] * inv;
     const float first = mean;
-    for (int64_t i = int64_t(threadIdx.x) * V; i < A.cols; i += int64_t(kLongThreads) * V) {
-      Pack<TX, V>::load(src, i, s);
+    for (int64_t i = i0; i < A.cols; i += step) {
+      x.load(src, i, A.cols - i);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float c = s[e] - first;
-        sq = __builtin_fmaf(c, c, sq);
-        off += c;
+      for (int e = 0; e < 8; ++e) {
+        const float d = e < A.cols - i ? x.get(e) - first : 0.0f;
+        both[0] = __builtin_fmaf(d, d, both[0]);
+        both[1] += d;
       }
     }
-    row_sum2<kLongThreads>(sq, off, lds);
-    const float rstd = finish(sq, off, inv, A.eps, mean);
+    sums.add(both);
+    float off = both[1];
+    const float rstd = finish(both[0], off, inv, A.eps, mean);
     void *yr = row_of<TX>(A.y, r, A.ld_y);
-    for (int64_t i = int64_t(threadIdx.x) * V; i < A.cols; i += int64_t(kLongThreads) * V) {
-      float g[V], b[V];
-      Pack<TX, V>::load(src, i, s);
-      if (A.gamma) Pack<TP, V>::load(A.gamma, i, g);
-      if (A.beta) Pack<TP, V>::load(A.beta, i, b);
+    for (int64_t i = i0; i < A.cols; i += step) {
+      float y[8];
+      Eight<TP> g, b;
+      x.load(src, i, A.cols - i);
+      if (A.gamma) g.load(A.gamma, i, A.cols - i);
+      if (A.beta) b.load(A.beta, i, A.cols - i);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float h = (s[e] - first - off) * rstd;
-        if (A.gamma) h *= g[e];
-        if (A.beta) h += b[e];
-        s[e] = h;
+      for (int e = 0; e < 8; ++e) {
+        y[e] = (x.get(e) - first - off) * rstd;
+        if (A.gamma) y[e] *= g.get(e);
+        if (A.beta) y[e] += b.get(e);
       }
-      Pack<TX, V>::store(yr, i, s);
+      x.set(y);
+      x.store(yr, i, A.cols - i);
     }
     if (threadIdx.x == 0) {
       if (A.mean) A.mean[r] = mean;
@@ -275,101 +332,104 @@ struct BwdArgs {
   void *dx, *dgamma, *dbeta;
   float *part;    // [parts][cols] of dgamma, then of dbeta
   int32_t parts;  // 0: no rows (the gradients are zero)
+  int32_t per;    // threads of a row
 };
 
-template <class TX, class TP, int TPR, int E, int V>
-__global__ void __launch_bounds__(kBlock<TPR>) ln_bwd_kernel(const BwdArgs A) {
-  constexpr int N = E / V, RPB = kBlock<TPR> / TPR;
-  __shared__ float lds[TPR > 64 ? TPR / 64 : 1][2];
-  __shared__ float join[RPB > 1 ? (RPB - 1) * TPR * E : 1];
-  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+template <class TX, class TP, int N, int R, bool TAIL>
+__global__ void __launch_bounds__(1024) ln_bwd_kernel(const BwdArgs A) {
+  __shared__ float lds[2][16][8];
+  __shared__ float join[1024 * 8];
+  const int per = A.per, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / per);
+  const int t = threadIdx.x - sub * per, subs = blockDim.x / per;
+  Sums sums{lds, sub * per / 64, per / 64};
+  const Columns<N> c(t, per, int(A.cols));
+  Eight<TP> gamma[N];
+  load_params<TAIL>(gamma, A.gamma, 1.0f, c);
   const float inv = 1.0f / float(A.cols);
-  float dg[N][V], db[N][V];
+  float dg[N][8] = {}, db[N][8] = {};
+  const int64_t step = int64_t(gridDim.x) * subs * R;
+  for (int64_t first = int64_t(blockIdx.x) * subs * R; first < A.rows; first += step) {
+    const int64_t r0 = first + sub * R;
+    Eight<TX> x[R][N], dy[R][N], ds[R][N];
+    float mean[R], rstd[R], both[2 * R];
 #pragma unroll
-  for (int j = 0; j < N; ++j)
+    for (int k = 0; k < R; ++k) {
+      const bool in = r0 + k < A.rows;
+      mean[k] = in ? A.mean[r0 + k] : 0.0f;
+      rstd[k] = in ? A.rstd[r0 + k] : 0.0f;
 #pragma unroll
-    for (int e = 0; e < V; ++e) dg[j][e] = db[j][e] = 0.0f;
-  for (int64_t r = int64_t(blockIdx.x) * RPB + sub; r < A.rows; r += int64_t(gridDim.x) * RPB) {
-    const void *xr = row_of<TX>(A.x, r, A.ld_x), *dyr = row_of<TX>(A.dy, r, A.ld_dy);
-    const float mean = A.mean[r], rstd = A.rstd[r];
-    float h[N][V], g[N][V];
-    float c1 = 0.0f, c2 = 0.0f;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int64_t i = int64_t(j * TPR + t) * V;
-      if (i < A.cols) {
-        Pack<TX, V>::load(xr, i, h[j]);
-        Pack<TX, V>::load(dyr, i, g[j]);
+      for (int n = 0; n < N; ++n) {
+        const int left = in ? c.left[n] : 0;
+        x[k][n].template load<TAIL, true>(row_of<TX>(A.x, r0 + k, A.ld_x), c.i[n], left);
+        dy[k][n].template load<TAIL, true>(row_of<TX>(A.dy, r0 + k, A.ld_dy), c.i[n], left);
+        if (A.dsum) ds[k][n].template load<TAIL, true>(row_of<TX>(A.dsum, r0 + k, A.ld_ds), c.i[n], left);
       }
     }
+    // past a row's end dy is 0, and so is all that it is a factor of
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int64_t i = int64_t(j * TPR + t) * V;
-      if (i < A.cols) {
-        float w[V];
-        if (A.gamma) Pack<TP, V>::load(A.gamma, i, w);
+    for (int k = 0; k < R; ++k) {
+      float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          h[j][e] = (h[j][e] - mean) * rstd;
-          dg[j][e] = __builtin_fmaf(g[j][e], h[j][e], dg[j][e]);
-          db[j][e] += g[j][e];
-          if (A.gamma) g[j][e] *= w[e];
-          c1 += g[j][e];
-          c2 = __builtin_fmaf(g[j][e], h[j][e], c2);
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float h = (x[k][n].get(e) - mean[k]) * rstd[k], d = dy[k][n].get(e);
+          dg[n][e] = __builtin_fmaf(d, h, dg[n][e]);
+          db[n][e] += d;
+          const float g = d * gamma[n].get(e);
+          c1 += g;
+          c2 = __builtin_fmaf(g, h, c2);
         }
-      }
+      both[2 * k] = c1;
+      both[2 * k + 1] = c2;
+      __builtin_amdgcn_sched_barrier(0);  // one row's values at a time
     }
-    row_sum2<TPR>(c1, c2, lds);
-    c1 *= inv;
-    c2 *= inv;
-    void *dxr = row_of<TX>(A.dx, r, A.ld_dx);
+    sums.add(both);
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int64_t i = int64_t(j * TPR + t) * V;
-      if (i < A.cols) {
-        float d[V];
-        if (A.dsum) Pack<TX, V>::load(row_of<TX>(A.dsum, r, A.ld_ds), i, d);
+    for (int k = 0; k < R; ++k) {
+      if (r0 + k >= A.rows) break;
+      const float c1 = both[2 * k] * inv, c2 = both[2 * k + 1] * inv;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          float v = rstd * (g[j][e] - c1 - h[j][e] * c2);
-          if (A.dsum) v += d[e];
-          h[j][e] = v;
+      for (int n = 0; n < N; ++n) {
+        float v[8];
+        x[k][n].forget();
+        dy[k][n].forget();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float h = (x[k][n].get(e) - mean[k]) * rstd[k];
+          v[e] = rstd[k] * (dy[k][n].get(e) * gamma[n].get(e) - c1 - h * c2);
+          if (A.dsum) v[e] += ds[k][n].get(e);
         }
-        Pack<TX, V>::store(dxr, i, h[j]);
+        x[k][n].set(v);
+        x[k][n].template store<TAIL>(row_of<TX>(A.dx, r0 + k, A.ld_dx), c.i[n], c.left[n]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
   if (!A.part) return;
-  // the rows that the workgroup's waves walked side by side, then its partial
+  // the row groups' sums, then the workgroup's partial row
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    float (&acc)[N][V] = which ? db : dg;
+    float (&acc)[N][8] = which ? db : dg;
     if (which ? !A.dbeta : !A.dgamma) continue;
-    if constexpr (RPB > 1) {
-      __syncthreads();
-      if (sub > 0) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-#pragma unroll
-          for (int e = 0; e < V; ++e) join[((sub - 1) * E + j * V + e) * TPR + t] = acc[j][e];
-      }
-      __syncthreads();
-      if (sub > 0) continue;
-#pragma unroll
-      for (int w = 0; w < RPB - 1; ++w)
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-#pragma unroll
-          for (int e = 0; e < V; ++e) acc[j][e] += join[(w * E + j * V + e) * TPR + t];
-    }
     float *out = A.part + (int64_t(which) * A.parts + blockIdx.x) * A.cols;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int64_t i = int64_t(j * TPR + t) * V;
-      if (i < A.cols) {
+    for (int n = 0; n < N; ++n) {
+      if (subs > 1) {
+        __syncthreads();
+        if (sub > 0) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) out[i + e] = acc[j][e];
+          for (int e = 0; e < 8; ++e) join[((sub - 1) * 8 + e) * per + t] = acc[n][e];
+        }
+        __syncthreads();
+        if (sub > 0) continue;
+        for (int w = 0; w < subs - 1; ++w)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[n][e] += join[(w * 8 + e) * per + t];
       }
+      Eight<F32> v;
+      v.set(acc[n]);
+      v.template store<TAIL>(out, c.i[n], c.left[n]);
     }
   }
 }
@@ -391,67 +451,87 @@ __global__ void __launch_bounds__(kThreads) ln_bwd_long_cols_kernel(const BwdArg
   A.part[(int64_t(A.parts) + blockIdx.y) * A.cols + c] = db;
 }
 
-template <class TX, class TP, int V>
+template <class TX, class TP>
 __global__ void __launch_bounds__(kLongThreads) ln_bwd_long_dx_kernel(const BwdArgs A) {
-  __shared__ float lds[kLongThreads / 64][2];
+  __shared__ float lds[2][16][8];
+  Sums sums{lds, 0, kLongThreads / 64};
   const float inv = 1.0f / float(A.cols);
+  const int64_t i0 = int64_t(threadIdx.x) * 8, step = int64_t(kLongThreads) * 8;
   for (int64_t r = blockIdx.x; r < A.rows; r += gridDim.x) {
     const void *xr = row_of<TX>(A.x, r, A.ld_x), *dyr = row_of<TX>(A.dy, r, A.ld_dy);
     const float mean = A.mean[r], rstd = A.rstd[r];
-    float c1 = 0.0f, c2 = 0.0f, h[V], g[V], w[V];
-    for (int64_t i = int64_t(threadIdx.x) * V; i < A.cols; i += int64_t(kLongThreads) * V) {
-      Pack<TX, V>::load(xr, i, h);
-      Pack<TX, V>::load(dyr, i, g);
-      if (A.gamma) Pack<TP, V>::load(A.gamma, i, w);
+    float both[2] = {0.0f, 0.0f};
+    Eight<TX> x, dy, ds;
+    Eight<TP> w;
+    for (int64_t i = i0; i < A.cols; i += step) {
+      x.load(xr, i, A.cols - i);
+      dy.load(dyr, i, A.cols - i);
+      if (A.gamma) w.load(A.gamma, i, A.cols - i);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (A.gamma) g[e] *= w[e];
-        c1 += g[e];
-        c2 = __builtin_fmaf(g[e], (h[e] - mean) * rstd, c2);
+      for (int e = 0; e < 8; ++e) {
+        const float g = A.gamma ? dy.get(e) * w.get(e) : dy.get(e);
+        both[0] += g;
+        both[1] = __builtin_fmaf(g, (x.get(e) - mean) * rstd, both[1]);
       }
     }
-    row_sum2<kLongThreads>(c1, c2, lds);
-    c1 *= inv;
-    c2 *= inv;
+    sums.add(both);
+    const float c1 = both[0] * inv, c2 = both[1] * inv;
     void *dxr = row_of<TX>(A.dx, r, A.ld_dx);
-    for (int64_t i = int64_t(threadIdx.x) * V; i < A.cols; i += int64_t(kLongThreads) * V) {
-      float d[V];
-      Pack<TX, V>::load(xr, i, h);
-      Pack<TX, V>::load(dyr, i, g);
-      if (A.gamma) Pack<TP, V>::load(A.gamma, i, w);
-      if (A.dsum) Pack<TX, V>::load(row_of<TX>(A.dsum, r, A.ld_ds), i, d);
+    for (int64_t i = i0; i < A.cols; i += step) {
+      float v[8];
+      x.load(xr, i, A.cols - i);
+      dy.load(dyr, i, A.cols - i);
+      if (A.gamma) w.load(A.gamma, i, A.cols - i);
+      if (A.dsum) ds.load(row_of<TX>(A.dsum, r, A.ld_ds), i, A.cols - i);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (A.gamma) g[e] *= w[e];
-        float v = rstd * (g[e] - c1 - (h[e] - mean) * rstd * c2);
-        if (A.dsum) v += d[e];
-        h[e] = v;
+      for (int e = 0; e < 8; ++e) {
+        const float g = A.gamma ? dy.get(e) * w.get(e) : dy.get(e);
+        v[e] = rstd * (g - c1 - (x.get(e) - mean) * rstd * c2);
+        if (A.dsum) v[e] += ds.get(e);
       }
-      Pack<TX, V>::store(dxr, i, h);
+      x.set(v);
+      x.store(dxr, i, A.cols - i);
     }
   }
 }
 
 // dgamma / dbeta = the sum of the partial rows, in the partials' order within
-// each of kSplit interleaved groups, the groups then in order.
-constexpr int kSplit = 16;
+// each of kSplit interleaved groups, the groups then in order.  Four columns a
+// thread.
+constexpr int kSplit = 64;
 template <class TP>
-__global__ void __launch_bounds__(64 * kSplit) ln_bwd_join_kernel(const BwdArgs A) {
-  __shared__ float lds[kSplit][64];
-  const int64_t c = int64_t(blockIdx.x) * 64 + threadIdx.x;
+__global__ void __launch_bounds__(16 * kSplit) ln_bwd_join_kernel(const BwdArgs A) {
+  __shared__ float lds[kSplit][68];
+  struct __attribute__((packed, aligned(4))) Four {
+    float e[4];
+  };
+  const int64_t c = int64_t(blockIdx.x) * 64 + threadIdx.x * 4;
   void *out = blockIdx.y ? A.dbeta : A.dgamma;
   if (!out) return;
-  const float *p = A.part + int64_t(blockIdx.y) * A.parts * A.cols;
-  float s = 0.0f;
-  if (c < A.cols)
-    for (int k = threadIdx.y; k < A.parts; k += kSplit) s += p[int64_t(k) * A.cols + c];
-  lds[threadIdx.y][threadIdx.x] = s;
-  __syncthreads();
-  if (threadIdx.y || c >= A.cols) return;
-  s = 0.0f;
+  const float *p = A.part + int64_t(blockIdx.y) * A.parts * A.cols + c;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c + 4 <= A.cols) {
+#pragma unroll 8
+    for (int k = threadIdx.y; k < A.parts; k += kSplit) {
+      const Four v = *reinterpret_cast<const Four *>(p + k * A.cols);
 #pragma unroll
-  for (int k = 0; k < kSplit; ++k) s += lds[k][threadIdx.x];
-  static_cast<typename TP::raw *>(out)[c] = TP::store(s);
+      for (int e = 0; e < 4; ++e) s[e] += v.e[e];
+    }
+  } else {
+    for (int k = threadIdx.y; k < A.parts; k += kSplit)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < A.cols) s[e] += p[k * A.cols + e];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) lds[threadIdx.y][threadIdx.x * 4 + e] = s[e];
+  __syncthreads();
+  const int t = threadIdx.y * 16 + threadIdx.x;
+  if (t >= 64 || int64_t(blockIdx.x) * 64 + t >= A.cols) return;
+  float sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kSplit; ++k) sum += lds[k][t];
+  static_cast<typename TP::raw *>(out)[int64_t(blockIdx.x) * 64 + t] = TP::store(sum);
 }
 
 // ------------------------------------------------------------------- host
@@ -469,20 +549,46 @@ bool desc_ok(const zs_layernorm_desc *d) {
   return true;
 }
 
-// Threads per row and elements per thread of the register kernels.
-template <int TPR_, int E_>
-struct Shape {
-  static constexpr int TPR = TPR_, E = E_;
+// How the register kernels take the rows: N times eight columns a thread, R
+// rows at a time, `per` threads a row, `subs` row groups a workgroup.
+struct Way {
+  int n, r, per, subs;
+  bool tail;
+  int64_t groups;  // of R rows, workgroups
 };
 
-template <class F>
-int by_shape(int64_t cols, F f) {
-  if (cols <= 512) return f(Shape<64, 8>{});
-  if (cols <= 1024) return f(Shape<64, 16>{});
-  if (cols <= 2048) return f(Shape<64, 32>{});
-  if (cols <= 4096) return f(Shape<256, 16>{});
-  if (cols <= 8192) return f(Shape<256, 32>{});
-  return f(Shape<1024, 16>{});
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+Way way_of(const zs_layernorm_desc &d, bool forward) {
+  Way w;
+  w.n = d.cols <= kMaxRegCols / 2 ? 1 : 2;
+  w.per = int(up(up(d.cols, 8 * w.n) / (8 * w.n), 64));
+  // a workgroup's partial row costs as much whatever it covers
+  const int threads = forward ? kThreads : 1024;
+  w.subs = w.per < threads ? threads / w.per : 1;
+  // few rows: a workgroup for each
+  if (d.rows < int64_t(kCus) * w.subs) w.subs = int((d.rows + kCus - 1) / kCus);
+  if (w.subs < 1) w.subs = 1;
+  w.tail = d.cols % 8 != 0;
+  // two rows at a time once every CU has some, where the registers hold them
+  w.r = d.rows >= 4 * kCus && w.n == 1 && (forward || d.dtype != ZS_F32) ? 2 : 1;
+  const int64_t rows = int64_t(w.subs) * w.r;
+  w.groups = (d.rows + rows - 1) / rows;
+  return w;
+}
+
+template <bool PAIRS, class F>
+int by_way(const Way &w, F f) {
+  using std::integral_constant;
+  const auto rows = [&](auto n, auto tail) {
+    if constexpr (PAIRS && n.value == 1)
+      if (w.r == 2) return f(n, integral_constant<int, 2>{}, tail);
+    return f(n, integral_constant<int, 1>{}, tail);
+  };
+  const auto cols = [&](auto n) {
+    return w.tail ? rows(n, std::true_type{}) : rows(n, std::false_type{});
+  };
+  return w.n == 1 ? cols(integral_constant<int, 1>{}) : cols(integral_constant<int, 2>{});
 }
 
 template <class F>
@@ -493,26 +599,10 @@ int by_type(const zs_layernorm_desc &d, F f) {
   return d.param_dtype == ZS_F32 ? f(F16{}, F32{}) : f(F16{}, F16{});
 }
 
-template <class F>
-int by_vector(bool vec, F f) {
-  if (!vec) return f(std::integral_constant<int, 1>{});
-  return f(std::integral_constant<int, 8>{});
-}
-
-int64_t row_blocks(int64_t rows, int per) {
-  const int64_t b = (rows + per - 1) / per;
-  return b < 0x7fffffff ? b : 0x7fffffff;
-}
-
+// Workgroups of the backward pass, each of which leaves a partial row.
 int64_t parts_of(const zs_layernorm_desc &d) {
-  const int rpb = d.cols <= 2048 ? 4 : 1;
-  const int64_t b = row_blocks(d.rows, rpb);
+  const int64_t b = d.cols > kMaxRegCols ? (d.rows + 3) / 4 : way_of(d, false).groups;
   return b < kMaxParts ? b : kMaxParts;
-}
-
-// Every row of p starts on a 16-byte boundary (or p is absent).
-bool rows_aligned(const void *p, int64_t ld, int size) {
-  return !p || (aligned(p, 16) && ld * size % 16 == 0);
 }
 
 }  // namespace
@@ -532,28 +622,26 @@ int zero_shard_layernorm(const zs_layernorm_desc *d, const void *x, const void *
   if (const int rc = device_is_gfx950()) return rc;
   const auto ld = [&](int64_t v) { return v ? v : d->cols; };
   FwdArgs A{d->rows, d->cols, ld(d->ld_x), ld(d->ld_residual), ld(d->ld_sum), ld(d->ld_y),
-            x, residual, gamma, beta, sum, y, mean, rstd, d->eps};
-  const bool vec = d->cols % 8 == 0 && rows_aligned(x, A.ld_x, size) &&
-                   rows_aligned(residual, A.ld_r, size) && rows_aligned(sum, A.ld_s, size) &&
-                   rows_aligned(y, A.ld_y, size) && aligned(gamma, 16) && aligned(beta, 16);
+            x, residual, gamma, beta, sum, y, mean, rstd, d->eps, 0};
   const hipStream_t st = static_cast<hipStream_t>(d->stream);
   return by_type(*d, [&](auto tx, auto tp) {
     using TX = decltype(tx);
     using TP = decltype(tp);
-    return by_vector(vec, [&](auto v) {
-      constexpr int V = decltype(v)::value;
-      if (A.cols > kMaxRegCols) {
-        hipLaunchKernelGGL((ln_fwd_long_kernel<TX, TP, V>), dim3(unsigned(row_blocks(A.rows, 1))),
-                           dim3(kLongThreads), 0, st, A);
-        return launched();
-      }
-      return by_shape(A.cols, [&](auto s) {
-        constexpr int TPR = decltype(s)::TPR, E = decltype(s)::E;
-        constexpr int B = kBlock<TPR>;
-        hipLaunchKernelGGL((ln_fwd_kernel<TX, TP, TPR, E, V>),
-                           dim3(unsigned(row_blocks(A.rows, B / TPR))), dim3(B), 0, st, A);
-        return launched();
-      });
+    if (A.cols > kMaxRegCols) {
+      hipLaunchKernelGGL((ln_fwd_long_kernel<TX, TP>),
+                         dim3(unsigned(A.rows < kMaxGrid ? A.rows : kMaxGrid)),
+                         dim3(kLongThreads), 0, st, A);
+      return launched();
+    }
+    const Way w = way_of(*d, true);
+    A.per = w.per;
+    const int threads = w.per * w.subs;
+    const int64_t most = int64_t(kCus) * (2048 / threads);
+    return by_way<true>(w, [&](auto n, auto r, auto tail) {
+      hipLaunchKernelGGL((ln_fwd_kernel<TX, TP, n.value, r.value, tail.value>),
+                         dim3(unsigned(w.groups < most ? w.groups : most)), dim3(threads), 0, st,
+                         A);
+      return launched();
     });
   });
 }
@@ -584,39 +672,33 @@ int zero_shard_layernorm_bwd(const zs_layernorm_desc *d, const void *dy, const v
   const auto ld = [&](int64_t v) { return v ? v : d->cols; };
   BwdArgs A{d->rows, d->cols, ld(d->ld_dy), ld(d->ld_x), ld(d->ld_dsum), ld(d->ld_dx),
             dy, x, gamma, dsum, mean, rstd, dx, dgamma, dbeta,
-            params ? static_cast<float *>(workspace) : nullptr, int32_t(parts_of(*d))};
-  const bool vec = d->cols % 8 == 0 && rows_aligned(dy, A.ld_dy, size) &&
-                   rows_aligned(x, A.ld_x, size) && rows_aligned(dsum, A.ld_ds, size) &&
-                   rows_aligned(dx, A.ld_dx, size) && aligned(gamma, 16);
+            params ? static_cast<float *>(workspace) : nullptr, int32_t(parts_of(*d)), 0};
   const hipStream_t st = static_cast<hipStream_t>(d->stream);
   return by_type(*d, [&](auto tx, auto tp) {
     using TX = decltype(tx);
     using TP = decltype(tp);
     int rc = ZS_OK;
-    if (A.rows > 0) {
-      rc = by_vector(vec, [&](auto v) {
-        constexpr int V = decltype(v)::value;
-        if (A.cols > kMaxRegCols) {
-          if (A.part)
-            hipLaunchKernelGGL((ln_bwd_long_cols_kernel<TX>),
-                               dim3(unsigned((A.cols + kThreads - 1) / kThreads),
-                                    unsigned(A.parts)),
-                               dim3(kThreads), 0, st, A);
-          hipLaunchKernelGGL((ln_bwd_long_dx_kernel<TX, TP, V>),
-                             dim3(unsigned(row_blocks(A.rows, 1))), dim3(kLongThreads), 0, st, A);
-          return launched();
-        }
-        return by_shape(A.cols, [&](auto s) {
-          constexpr int TPR = decltype(s)::TPR, E = decltype(s)::E;
-          hipLaunchKernelGGL((ln_bwd_kernel<TX, TP, TPR, E, V>), dim3(unsigned(A.parts)),
-                             dim3(kBlock<TPR>), 0, st, A);
-          return launched();
-        });
+    if (A.rows > 0 && A.cols > kMaxRegCols) {
+      if (A.part)
+        hipLaunchKernelGGL((ln_bwd_long_cols_kernel<TX>),
+                           dim3(unsigned((A.cols + kThreads - 1) / kThreads), unsigned(A.parts)),
+                           dim3(kThreads), 0, st, A);
+      hipLaunchKernelGGL((ln_bwd_long_dx_kernel<TX, TP>),
+                         dim3(unsigned(A.rows < kMaxGrid ? A.rows : kMaxGrid)),
+                         dim3(kLongThreads), 0, st, A);
+      rc = launched();
+    } else if (A.rows > 0) {
+      const Way w = way_of(*d, false);
+      A.per = w.per;
+      rc = by_way<!std::is_same_v<TX, F32>>(w, [&](auto n, auto r, auto tail) {
+        hipLaunchKernelGGL((ln_bwd_kernel<TX, TP, n.value, r.value, tail.value>), dim3(unsigned(A.parts)),
+                           dim3(w.per * w.subs), 0, st, A);
+        return launched();
       });
     }
     if (rc || !params) return rc;
     hipLaunchKernelGGL((ln_bwd_join_kernel<TP>), dim3(unsigned((A.cols + 63) / 64), 2),
-                       dim3(64, kSplit), 0, st, A);
+                       dim3(16, kSplit), 0, st, A);
     return launched();
   });
 }

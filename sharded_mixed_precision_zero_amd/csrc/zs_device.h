@@ -64,38 +64,82 @@ struct F16 {
   }
 };
 
-// V consecutive elements, aligned to one element: the memory takes 16-byte
-// accesses at any address, and rows of odd widths and strides need no path of
-// their own.
-template <class T, int V>
-struct Pack {
+// Eight consecutive elements as they lie in memory, aligned to one element:
+// the memory takes 16-byte accesses at any address, and rows of odd widths and
+// strides need no path of their own.
+template <class T>
+struct Eight {
   using raw = typename T::raw;
-  struct __attribute__((packed, aligned(sizeof(raw)))) Vec {
-    raw e[V];
+  static constexpr int kWords = int(sizeof(raw)) * 2;
+  struct __attribute__((packed, aligned(sizeof(raw)))) Words {
+    unsigned w[kWords];
   };
-  static __device__ __forceinline__ void load(const void *row, int64_t i, float (&out)[V]) {
-    const Vec v = *reinterpret_cast<const Vec *>(static_cast<const raw *>(row) + i);
-#pragma unroll
-    for (int e = 0; e < V; ++e) out[e] = T::load(v.e[e]);
+  using Four = unsigned __attribute__((ext_vector_type(4), aligned(sizeof(raw))));
+  unsigned w[kWords];
+
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (sizeof(raw) == 4) return T::load(__uint_as_float(w[e]));
+    else return T::load(raw(w[e / 2] >> (e % 2 * 16)));
   }
-  static __device__ __forceinline__ void store(void *row, int64_t i, const float (&in)[V]) {
-    Vec v;
+  __device__ __forceinline__ void get(float (&out)[8]) const {
 #pragma unroll
-    for (int e = 0; e < V; ++e) v.e[e] = T::store(in[e]);
-    *reinterpret_cast<Vec *>(static_cast<raw *>(row) + i) = v;
+    for (int e = 0; e < 8; ++e) out[e] = get(e);
   }
-  // The first n < V of them, the others 0.
-  static __device__ __forceinline__ void load_some(const void *row, int64_t i, int n,
-                                                   float (&out)[V]) {
+  __device__ __forceinline__ void set(const float (&in)[8]) {
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      out[e] = e < n ? T::load(static_cast<const raw *>(row)[i + e]) : 0.0f;
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(raw) == 4) w[i] = __float_as_uint(in[i]);
+      else w[i] = unsigned(T::store(in[2 * i])) | unsigned(T::store(in[2 * i + 1])) << 16;
+    }
   }
-  static __device__ __forceinline__ void store_some(void *row, int64_t i, int n,
-                                                    const float (&in)[V]) {
+  // Values taken from here on are converted anew, not kept in registers.
+  __device__ __forceinline__ void forget() {
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (e < n) static_cast<raw *>(row)[i + e] = T::store(in[e]);
+    for (int i = 0; i < kWords; ++i) asm volatile("" : "+v"(w[i]));
+  }
+  // Elements i.. of a row, the first `left` of them (8 or more: all), others
+  // 0.  TAIL: `left` may also be between 0 and 8.  A 32-bit index (of a row
+  // below 2^32 bytes) is added to the row's address by the access itself.
+  // ONCE: no cache need keep it.
+  template <bool TAIL = true, bool ONCE = false, class I, class L>
+  __device__ __forceinline__ void load(const void *row, I i, L left) {
+    const raw *p =
+        reinterpret_cast<const raw *>(static_cast<const char *>(row) + I(i * I(sizeof(raw))));
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) w[k] = 0;
+    if (left >= 8) {
+#pragma unroll
+      for (int k = 0; k < kWords; k += 4) {
+        const Four *from = reinterpret_cast<const Four *>(p) + k / 4;
+        const Four v = ONCE ? __builtin_nontemporal_load(from) : *from;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[k + q] = v[q];
+      }
+    } else if (TAIL && left > 0) {
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (e < left) {
+          if constexpr (sizeof(raw) == 4) w[e] = __float_as_uint(p[e]);
+          else w[e / 2] |= unsigned(p[e]) << (e % 2 * 16);
+        }
+    }
+  }
+  template <bool TAIL = true, class I, class L>
+  __device__ __forceinline__ void store(void *row, I i, L left) const {
+    raw *p = reinterpret_cast<raw *>(static_cast<char *>(row) + I(i * I(sizeof(raw))));
+    if (left >= 8) {
+      Words v;
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) v.w[k] = w[k];
+      *reinterpret_cast<Words *>(p) = v;
+    } else if (TAIL && left > 0) {
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (e < left) {
+          if constexpr (sizeof(raw) == 4) p[e] = __uint_as_float(w[e]);
+          else p[e] = raw(w[e / 2] >> (e % 2 * 16));
+        }
+    }
   }
 };
 
