@@ -690,19 +690,229 @@ __global__ void __launch_bounds__(WR *WC * 64) ortho_mul_kernel(const MulArgs A)
 #endif
 }
 
-// ------------------------------------------------- ortho: small matrices
+// ---------------------------------------------- ortho: matrices of up to 128
 
-// A matrix that fits in the LDS of one CU is orthogonalised by one workgroup
-// in one launch: the products are so small that a launch for each costs more
-// than the work (96 x 128: 17 launches take 67 us, this 22 us; 64 x 512 68 and 31 us).  X, X^T, A and
-// B lie in LDS, rows of k elements 8 apart more than k, so that the 16 rows one
-// read instruction serves lie in different banks.  A wave computes blocks of
-// 32 x 32.
+// Short matrices are worked on in the LDS of a CU, 16 waves of 32 x 32 blocks:
+// at up to 128 rows the products are so small that a launch for each costs more
+// than the work.  Rows of k elements lie k + 8 apart, so that the 16 rows one
+// read instruction serves lie in different banks.
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallWaves = kSmallThreads / 64;
 constexpr int kSmallLds = 81920;   // 16-bit elements: 160 KB
 constexpr int kSmallPacks = 5;     // of 8 elements that a thread brings in
 constexpr int kSmallBlocks = 3;    // of 32 x 32 that a wave computes
+constexpr float kBack1 = 1.0f / kScale, kBack2 = kBack1 * kBack1;
+
+using Block = f32x4[2][2];
+
+struct BlockRegs {
+  half8 p[2], q[2];
+  // 32 of k at p and q (this lane's pieces)
+  __device__ __forceinline__ void read(const _Float16 *pp, const _Float16 *qq, int pitch) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      p[e] = *reinterpret_cast<const half8 *>(pp + e * 16 * pitch);
+      q[e] = *reinterpret_cast<const half8 *>(qq + e * 16 * pitch);
+    }
+  }
+  __device__ __forceinline__ void add(Block &acc) const {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        acc[e][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(p[e], q[h], acc[e][h], 0, 0, 0);
+  }
+};
+
+__device__ __forceinline__ const _Float16 *block_at(const _Float16 *p, int i, int pitch, int lane) {
+  return p + (i * 32 + (lane & 15)) * pitch + (lane >> 4) * 8;
+}
+
+// Block i, j of P Q^T over K 32s of k.
+template <int K>
+__device__ __forceinline__ void block_mul(const _Float16 *P, const _Float16 *Q, int i, int j,
+                                          int lane, Block &acc) {
+  constexpr int pitch = K * 32 + 8;
+  const _Float16 *p = block_at(P, i, pitch, lane), *q = block_at(Q, j, pitch, lane);
+  BlockRegs f[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) f[k].read(p + k * 32, q + k * 32, pitch);
+#pragma unroll
+  for (int k = 0; k < K; ++k) f[k].add(acc);
+}
+
+// f(r, c, rows r..r+3 of column c), for each of the block's four parts
+template <class F>
+__device__ __forceinline__ void block_each(int i, int j, int lane, const Block &acc, F f) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      f(i * 32 + e * 16 + (lane >> 4) * 4, j * 32 + h * 16 + (lane & 15), acc[e][h]);
+}
+
+__device__ __forceinline__ half4 narrow4(const f32x4 &v) {
+  half4 h;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = _Float16(v[e]);
+  return h;
+}
+
+// C = P Q of symmetric matrices that commute: column c's rows are neighbours
+// in row c.  All waves; a barrier follows.
+template <int MB>
+__device__ __forceinline__ void short_mul(const _Float16 *P, const _Float16 *Q, _Float16 *C,
+                                          int wave, int lane) {
+  static_assert(MB * MB <= kSmallWaves, "a wave has one block");
+  constexpr int pm = MB * 32 + 8;
+  if (wave < MB * MB) {
+    Block acc = {};
+    block_mul<MB>(P, Q, wave / MB, wave % MB, lane, acc);
+    block_each(wave / MB, wave % MB, lane, acc, [&](int r, int c, f32x4 v) {
+      *reinterpret_cast<half4 *>(C + c * pm + r) = narrow4(v * kBack1);
+    });
+  }
+  __syncthreads();
+}
+
+// B = a I + b A + c A A.
+template <int MB>
+__device__ __forceinline__ void short_poly(const float *k, const _Float16 *A, _Float16 *B, int wave,
+                                           int lane) {
+  constexpr int pm = MB * 32 + 8;
+  if (wave < MB * MB) {
+    const int i = wave / MB, j = wave % MB;
+    Block acc = {};
+    block_mul<MB>(A, A, i, j, lane, acc);
+    block_each(i, j, lane, acc, [&](int r, int c, f32x4 v) {
+      const half4 old = *reinterpret_cast<const half4 *>(A + c * pm + r);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = __builtin_fmaf(k[1], float(old[e]), (k[2] * kBack1) * v[e]);
+      if (i == j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (r + e == c) v[e] += k[0] * kScale;
+      }
+      *reinterpret_cast<half4 *>(B + c * pm + r) = narrow4(v);
+    });
+  }
+  __syncthreads();
+}
+
+// A matrix's (or a strip's) rp x cp elements in LDS, in the caller's
+// orientation, and from there turned; rows of the caller's matrix past `rows`
+// and columns past `cols` are zeros.  A barrier follows.
+template <class TG>
+struct Brought {
+  Eight<TG> v[kSmallPacks];
+  int per, packs;
+  __device__ __forceinline__ void load(const typename TG::raw *g, int64_t ld, int rp, int cp,
+                                       int rows, int cols) {
+    per = cp / 8;
+    packs = rp * per;
+#pragma unroll
+    for (int i = 0; i < kSmallPacks; ++i) {
+      const int p = int(threadIdx.x) + i * kSmallThreads;
+      if (p >= packs) break;
+      const int r = p / per, c = (p - r * per) * 8;
+      v[i].load(g + r * ld, c, r < rows ? cols - c : 0);
+    }
+  }
+  __device__ __forceinline__ double squares() const {
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kSmallPacks; ++i) {
+      if (int(threadIdx.x) + i * kSmallThreads >= packs) break;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = __builtin_fma(double(v[i].get(e)), double(v[i].get(e)), sum);
+    }
+    return sum;
+  }
+  __device__ __forceinline__ void place(double scale, _Float16 *same, _Float16 *turned) const {
+    const int cp = per * 8, rp = packs / per;
+#pragma unroll
+    for (int i = 0; i < kSmallPacks; ++i) {
+      const int p = int(threadIdx.x) + i * kSmallThreads;
+      if (p >= packs) break;
+      const int r = p / per, c = (p - r * per) * 8;
+      half8 h;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = _Float16(float(double(v[i].get(e)) * scale));
+      *reinterpret_cast<half8 *>(same + r * (cp + 8) + c) = h;
+    }
+    __syncthreads();
+    for (int p = threadIdx.x; p < packs; p += kSmallThreads) {
+      const int r = p / cp * 8, c = p % cp;
+      half8 h;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = same[(r + e) * (cp + 8) + c];
+      *reinterpret_cast<half8 *>(turned + c * (rp + 8) + r) = h;
+    }
+    __syncthreads();
+  }
+};
+
+// Sum over the workgroup's 1024 threads, in all of them.
+__device__ __forceinline__ double small_sum(double v, double *lds) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = 0.0;
+#pragma unroll
+  for (int w = 0; w < kSmallWaves; ++w) v += lds[w];
+  return v;
+}
+
+// What an update leaves: X or X^T (whichever are given) from the blocks of B X,
+// in binary16, or the result in bf16.
+template <int MB, bool LAST>
+__device__ __forceinline__ void short_put(const Block *acc, int blocks, _Float16 *x, int pn,
+                                          _Float16 *xt, int wave, int lane) {
+  constexpr int pm = MB * 32 + 8;
+#pragma unroll
+  for (int u = 0; u < kSmallBlocks; ++u) {
+    const int t = wave + u * kSmallWaves;
+    if (t < blocks)
+      block_each(t % MB, t / MB, lane, acc[u], [&](int r, int c, f32x4 v) {
+        half4 h;
+        if constexpr (LAST) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = __builtin_bit_cast(_Float16, Bf16::store(v[e] * kBack2));
+        } else {
+          h = narrow4(v * kBack1);
+        }
+        if (xt) *reinterpret_cast<half4 *>(xt + c * pm + r) = h;
+        if (x) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[(r + e) * pn + c] = h[e];
+        }
+      });
+  }
+}
+
+// The bf16 result from LDS, rp x cp of pitch cp + 8, to rows x cols of o.
+__device__ __forceinline__ void short_out(const _Float16 *from, int rp, int cp, uint16_t *o,
+                                          int64_t ld, int rows, int cols) {
+  struct __attribute__((packed, aligned(2))) Vec {
+    half8 h;
+  };
+  const int per = cp / 8;
+  for (int p = threadIdx.x; p < rp * per; p += kSmallThreads) {
+    const int r = p / per, c = (p - r * per) * 8;
+    if (r >= rows) break;
+    uint16_t *to = o + r * ld + c;
+    const _Float16 *h = from + r * (cp + 8) + c;
+    if (c + 8 <= cols) {
+      reinterpret_cast<Vec *>(to)->h = *reinterpret_cast<const half8 *>(h);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < cols) to[e] = reinterpret_cast<const uint16_t *>(h)[e];
+    }
+  }
+}
 
 struct SmallArgs {
   const void *g;
@@ -713,212 +923,217 @@ struct SmallArgs {
   float coeffs[3 * ZS_ORTHO_MAX_STEPS];
 };
 
-__host__ __device__ inline int64_t small_lds(int64_t mp, int64_t np) {
+int64_t small_lds(int64_t mp, int64_t np) {
   return mp * (np + 8) + np * (mp + 8) + 2 * mp * (mp + 8);
 }
 
+// A matrix whose X, X^T, A and B fit in the LDS of one CU: one workgroup, one
+// launch (96 x 128: 17 launches take 67 us, this 22 us; 64 x 512 68 and 31 us).
 template <class TG, int MB>
 __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const SmallArgs A) {
   __shared__ __align__(16) _Float16 lds[kSmallLds];
-  const int tid = threadIdx.x;
-  int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int mp = MB * 32, pm = mp + 8;
-  const int np = A.np, pn = np + 8;
+  const int np = A.np, pn = np + 8, nb = np / 32;
   _Float16 *x = lds, *xt = x + mp * pn, *a = xt + np * pm, *b = a + mp * pm;
-  const typename TG::raw *g =
-      static_cast<const typename TG::raw *>(A.g) + int64_t(blockIdx.x) * A.stride_in;
   // the input's and output's orientation
-  const int rp = A.tall ? np : mp, cp = A.tall ? mp : np, pitch = cp + 8;
-  const int per = cp / 8, packs = rp * per;
-  _Float16 *same = A.tall ? xt : x;
+  const int rp = A.tall ? np : mp, cp = A.tall ? mp : np;
+  _Float16 *same = A.tall ? xt : x, *turned = A.tall ? x : xt;
   {
-    // the input in its orientation, padded with zeros
-    Eight<TG> v[kSmallPacks];
-    double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < kSmallPacks; ++i) {
-      const int p = tid + i * kSmallThreads;
-      if (p >= packs) break;
-      const int r = p / per, c = (p - r * per) * 8, left = r < A.rows ? A.cols - c : 0;
-      v[i].load(g + r * A.ld_in, c, left);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        sum = __builtin_fma(double(v[i].get(e)), double(v[i].get(e)), sum);
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-    double *part = reinterpret_cast<double *>(b);  // mp (mp + 8) elements: room for 16
-    if (lane == 0) part[wave] = sum;
-    __syncthreads();
-    sum = 0.0;
-#pragma unroll
-    for (int w = 0; w < kSmallWaves; ++w) sum += part[w];
-    const double scale = double(kScale) / (sqrt(sum) + A.eps);
-    _Float16 *turned = A.tall ? x : xt;
-#pragma unroll
-    for (int i = 0; i < kSmallPacks; ++i) {
-      const int p = tid + i * kSmallThreads;
-      if (p >= packs) break;
-      const int r = p / per, c = (p - r * per) * 8;
-      half8 h;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = _Float16(float(double(v[i].get(e)) * scale));
-      *reinterpret_cast<half8 *>(same + r * pitch + c) = h;
-    }
-    __syncthreads();
-    for (int p = tid; p < packs; p += kSmallThreads) {
-      const int r = p / cp * 8, c = p % cp;
-      half8 h;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = same[(r + e) * pitch + c];
-      *reinterpret_cast<half8 *>(turned + c * (rp + 8) + r) = h;
-    }
-    __syncthreads();
+    Brought<TG> in;
+    in.load(static_cast<const typename TG::raw *>(A.g) + int64_t(blockIdx.x) * A.stride_in, A.ld_in,
+            rp, cp, A.rows, A.cols);
+    // the sums' places are B's
+    const double sum = small_sum(in.squares(), reinterpret_cast<double *>(b));
+    in.place(double(kScale) / (sqrt(sum) + A.eps), same, turned);
   }
-
-  using Block = f32x4[2][2];
-  struct Regs {
-    half8 p[2], q[2];
-  };
-  // 32 of k of a block, at p and q (this lane's pieces), rows `pitch` apart
-  const auto read = [&](Regs &f, const _Float16 *p, const _Float16 *q, int pitch) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      f.p[e] = *reinterpret_cast<const half8 *>(p + e * 16 * pitch);
-      f.q[e] = *reinterpret_cast<const half8 *>(q + e * 16 * pitch);
-    }
-  };
-  const auto add = [&](const Regs &f, Block &acc) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        acc[e][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.p[e], f.q[h], acc[e][h], 0, 0, 0);
-  };
-  const auto mine = [&](const _Float16 *p, int i, int pitch) {
-    return p + (i * 32 + (lane & 15)) * pitch + (lane >> 4) * 8;
-  };
-  // block i, j of P Q^T over mp
-  const auto square = [&](const _Float16 *P, const _Float16 *Q, int i, int j, Block &acc) {
-    const _Float16 *p = mine(P, i, pm), *q = mine(Q, j, pm);
-    Regs f[MB];
-#pragma unroll
-    for (int k = 0; k < MB; ++k) read(f[k], p + k * 32, q + k * 32, pm);
-#pragma unroll
-    for (int k = 0; k < MB; ++k) add(f[k], acc);
-  };
-  // rows r..r+3 of column c, for each of the block's four parts
-  const auto each = [&](int i, int j, auto &acc, auto f) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        f(i * 32 + e * 16 + (lane >> 4) * 4, j * 32 + h * 16 + (lane & 15), acc[e][h]);
-  };
-  constexpr float kBack = 1.0f / kScale;
-  const auto narrow = [](const f32x4 &v) {
-    half4 h;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = _Float16(v[e]);
-    return h;
-  };
-  const int nb = np / 32;
-  static_assert(MB * MB <= kSmallWaves, "a wave has one block of A and of B");
-  const int wi = wave / MB, wj = wave % MB;
   for (int s = 0; s < A.steps; ++s) {
     // Opaque, so that no address is computed ahead of the loop and kept.
     asm volatile("" : "+v"(lane));
-    const float ca = A.coeffs[3 * s], cb = A.coeffs[3 * s + 1], cc = A.coeffs[3 * s + 2];
-    // A and B are symmetric: column c's rows are neighbours in row c
     if (wave < MB * MB) {
+      const int wi = wave / MB, wj = wave % MB;
       Block acc = {};
-      const _Float16 *p = mine(x, wi, pn), *q = mine(x, wj, pn);
-      Regs f0, f1;
-      read(f0, p, q, pn);
+      const _Float16 *p = block_at(x, wi, pn, lane), *q = block_at(x, wj, pn, lane);
+      BlockRegs f0, f1;
+      f0.read(p, q, pn);
       for (int k = 1; k < nb; k += 2) {
-        read(f1, p + k * 32, q + k * 32, pn);
-        add(f0, acc);
+        f1.read(p + k * 32, q + k * 32, pn);
+        f0.add(acc);
         const int next = k + 1 < nb ? k + 1 : k;
-        read(f0, p + next * 32, q + next * 32, pn);
-        add(f1, acc);
+        f0.read(p + next * 32, q + next * 32, pn);
+        f1.add(acc);
       }
-      if (nb & 1) add(f0, acc);
-      each(wi, wj, acc, [&](int r, int c, f32x4 v) {
-        *reinterpret_cast<half4 *>(a + c * pm + r) = narrow(v * kBack);
+      if (nb & 1) f0.add(acc);
+      block_each(wi, wj, lane, acc, [&](int r, int c, f32x4 v) {
+        *reinterpret_cast<half4 *>(a + c * pm + r) = narrow4(v * kBack1);
       });
     }
     __syncthreads();
-    if (wave < MB * MB) {
-      Block acc = {};
-      square(a, a, wi, wj, acc);
-      each(wi, wj, acc, [&](int r, int c, f32x4 v) {
-        const half4 old = *reinterpret_cast<const half4 *>(a + c * pm + r);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          v[e] = __builtin_fmaf(cb, float(old[e]), (cc * kBack) * v[e]);
-        if (wi == wj) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (r + e == c) v[e] += ca * kScale;
-        }
-        *reinterpret_cast<half4 *>(b + c * pm + r) = narrow(v);
-      });
-    }
-    __syncthreads();
+    short_poly<MB>(A.coeffs + 3 * s, a, b, wave, lane);
     Block acc[kSmallBlocks] = {};
 #pragma unroll
     for (int u = 0; u < kSmallBlocks; ++u) {
       const int t = wave + u * kSmallWaves;
-      if (t < MB * nb) square(b, xt, t % MB, t / MB, acc[u]);
+      if (t < MB * nb) block_mul<MB>(b, xt, t % MB, t / MB, lane, acc[u]);
     }
-    const bool last = s + 1 == A.steps;
     __syncthreads();  // X^T has been read
-#pragma unroll
-    for (int u = 0; u < kSmallBlocks; ++u) {
-      const int t = wave + u * kSmallWaves;
-      if (t < MB * nb)
-        each(t % MB, t / MB, acc[u], [&](int r, int c, f32x4 v) {
-          half4 h;
-          if (last) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              h[e] = __builtin_bit_cast(_Float16, Bf16::store(v[e] * (kBack * kBack)));
-          } else {
-            h = narrow(v * kBack);
-          }
-          if (!last || A.tall) *reinterpret_cast<half4 *>(xt + c * pm + r) = h;
-          if (!last || !A.tall) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[(r + e) * pn + c] = h[e];
-          }
-        });
-    }
+    if (s + 1 < A.steps)
+      short_put<MB, false>(acc, MB * nb, x, pn, xt, wave, lane);
+    else
+      short_put<MB, true>(acc, MB * nb, A.tall ? nullptr : x, pn, A.tall ? xt : nullptr, wave, lane);
     __syncthreads();
   }
-  uint16_t *o = A.o + int64_t(blockIdx.x) * A.stride_o;
-  struct __attribute__((packed, aligned(2))) Vec {
-    half8 h;
-  };
-  for (int p = tid; p < packs; p += kSmallThreads) {
-    const int r = p / per, c = (p - r * per) * 8;
-    if (r >= A.rows) break;
-    uint16_t *to = o + r * A.ld_o + c;
-    const half8 h = *reinterpret_cast<const half8 *>(same + r * pitch + c);
-    if (c + 8 <= A.cols) {
-      reinterpret_cast<Vec *>(to)->h = h;
-    } else {
+  short_out(same, rp, cp, A.o + int64_t(blockIdx.x) * A.stride_o, A.ld_o, A.rows, A.cols);
+}
+
+// Longer ones in strips of 128 columns of X, a workgroup each.  Between two
+// updates of X only A is needed of all strips together: each leaves its part of
+// X X^T, one launch adds them, and the next update's workgroups all work out
+// the polynomials in A again, two steps of them where the coefficients allow
+// it, and apply them to their strip.  64 x 13824: 8 launches, XXX us, in place
+// of 19, 105 us.
+constexpr int kStripCols = 128, kStripRows = 128;
+
+struct StripArgs {
+  const void *g;
+  uint16_t *o;
+  int64_t ld_in, stride_in, ld_o, stride_o;
+  const double *partials;  // of the norm, [batch][blocks]
+  double eps;
+  _Float16 *xt;   // [batch][strips * kStripCols][mp]
+  float *parts;   // [batch][strips][mp][mp] of X X^T, times 2^22
+  _Float16 *a;    // [batch][mp][mp]
+  int32_t blocks, rows, cols, tall, strips, pair;
+  float k[6];     // this update's coefficients
+};
+
+// This strip's part of X X^T, and its X^T for the next update.
+template <int MB>
+__device__ __forceinline__ void strip_leave(const StripArgs &A, const _Float16 *x,
+                                            const _Float16 *xt, int wave, int lane) {
+  constexpr int mp = MB * 32, pm = mp + 8;
+  const int64_t strip = int64_t(blockIdx.y) * A.strips + blockIdx.x;
+  if (wave < MB * MB) {
+    Block acc = {};
+    block_mul<kStripCols / 32>(x, x, wave / MB, wave % MB, lane, acc);
+    float *out = A.parts + strip * (mp * mp);
+    block_each(wave / MB, wave % MB, lane, acc, [&](int r, int c, f32x4 v) {
+      *reinterpret_cast<f32x4 *>(out + c * mp + r) = v;
+    });
+  }
+  _Float16 *to = A.xt + strip * (kStripCols * mp);
+  for (int p = threadIdx.x; p < kStripCols * mp / 8; p += kSmallThreads) {
+    const int r = p / (mp / 8), c = p % (mp / 8) * 8;
+    *reinterpret_cast<half8 *>(to + p * 8) = *reinterpret_cast<const half8 *>(xt + r * pm + c);
+  }
+}
+
+template <class TG, int MB>
+__global__ void __launch_bounds__(kSmallThreads) ortho_strip_in_kernel(const StripArgs A) {
+  constexpr int mp = MB * 32, pm = mp + 8, W = kStripCols;
+  __shared__ __align__(16) _Float16 lds[mp * (W + 8) + W * pm];
+  __shared__ double sums[kSmallWaves];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  _Float16 *x = lds, *xt = lds + mp * (W + 8);
+  const int64_t first = int64_t(blockIdx.x) * W;  // column of X
+  const typename TG::raw *g = static_cast<const typename TG::raw *>(A.g) +
+                              blockIdx.y * A.stride_in + first * (A.tall ? A.ld_in : 1);
+  const int rows = A.tall ? int(A.rows - first) : A.rows;
+  const int cols = A.tall ? A.cols : int(A.cols - first);
+  Brought<TG> in;
+  in.load(g, A.ld_in, A.tall ? W : mp, A.tall ? mp : W, rows, cols);
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < A.blocks; i += kSmallThreads)
+    sum += A.partials[int64_t(blockIdx.y) * A.blocks + i];
+  sum = small_sum(sum, sums);
+  in.place(double(kScale) / (sqrt(sum) + A.eps), A.tall ? xt : x, A.tall ? x : xt);
+  strip_leave<MB>(A, x, xt, wave, lane);
+}
+
+// A from the strips' parts, in their order within each of 64 interleaved
+// groups, the groups then in order.
+__global__ void __launch_bounds__(1024) ortho_strip_sum_kernel(const StripArgs A, int square) {
+  __shared__ float lds[64][68];
+  const int64_t b = blockIdx.y, at = int64_t(blockIdx.x) * 64;
+  const float *p = A.parts + b * A.strips * square + at + threadIdx.x * 4;
+  f32x4 s = {};
+#pragma unroll 4
+  for (int k = threadIdx.y; k < A.strips; k += 64)
+    s += *reinterpret_cast<const f32x4 *>(p + int64_t(k) * square);
+  *reinterpret_cast<f32x4 *>(&lds[threadIdx.y][threadIdx.x * 4]) = s;
+  __syncthreads();
+  const int t = threadIdx.y * 16 + threadIdx.x;
+  if (t >= 64) return;
+  float sum = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (c + e < A.cols) to[e] = reinterpret_cast<const uint16_t *>(same + r * pitch + c)[e];
-    }
+  for (int k = 0; k < 64; ++k) sum += lds[k][t];
+  A.a[b * square + at + t] = _Float16(sum * kBack1);
+}
+
+template <int MB, bool LAST>
+__global__ void __launch_bounds__(kSmallThreads) ortho_strip_step_kernel(const StripArgs A) {
+  constexpr int mp = MB * 32, pm = mp + 8, W = kStripCols, square = mp * pm;
+  // X lies over B and C, which are done with by then, where LDS is full
+  constexpr int xat = MB == 4 ? square : 3 * square;
+  static_assert(MB < 4 || mp * (W + 8) <= 2 * square, "X in B and C's place");
+  __shared__ __align__(16) _Float16 lds[W * pm + (MB == 4 ? 3 * square : 3 * square + mp * (W + 8))];
+  int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  _Float16 *xt = lds, *a = xt + W * pm, *b = a + square, *c = b + square, *x = a + xat;
+  const int64_t strip = int64_t(blockIdx.y) * A.strips + blockIdx.x;
+  const auto bring = [&](const _Float16 *from, int n, _Float16 *to) {  // rows of mp
+    for (int p = threadIdx.x; p < n * mp / 8; p += kSmallThreads)
+      *reinterpret_cast<half8 *>(to + p / (mp / 8) * pm + p % (mp / 8) * 8) =
+          *reinterpret_cast<const half8 *>(from + p * 8);
+  };
+  bring(A.a + int64_t(blockIdx.y) * mp * mp, mp, a);
+  bring(A.xt + strip * (W * mp), W, xt);
+  __syncthreads();
+  short_poly<MB>(A.k, a, b, wave, lane);
+  const _Float16 *by = b;
+  if (A.pair) {
+    // A of the next step is B A B; its B times this one's is applied to X
+    short_mul<MB>(b, a, c, wave, lane);
+    short_mul<MB>(c, b, a, wave, lane);
+    short_poly<MB>(A.k + 3, a, c, wave, lane);
+    short_mul<MB>(c, b, a, wave, lane);
+    by = a;
+  }
+  constexpr int blocks = MB * W / 32;
+  static_assert(blocks <= kSmallWaves * kSmallBlocks, "a wave's blocks");
+  Block acc[kSmallBlocks] = {};
+#pragma unroll
+  for (int u = 0; u < kSmallBlocks; ++u) {
+    const int t = wave + u * kSmallWaves;
+    if (t < blocks) block_mul<MB>(by, xt, t % MB, t / MB, lane, acc[u]);
+  }
+  __syncthreads();  // X^T, B and C have been read
+  short_put<MB, LAST>(acc, blocks, LAST && A.tall ? nullptr : x, W + 8,
+                      LAST && !A.tall ? nullptr : xt, wave, lane);
+  __syncthreads();
+  if constexpr (LAST) {
+    const int64_t first = int64_t(blockIdx.x) * W;
+    uint16_t *o = A.o + blockIdx.y * A.stride_o + first * (A.tall ? A.ld_o : 1);
+    if (A.tall) short_out(xt, W, mp, o, A.ld_o, int(A.rows - first), A.cols);
+    else short_out(x, mp, W, o, A.ld_o, A.rows, int(A.cols - first));
+  } else {
+    strip_leave<MB>(A, x, xt, wave, lane);
   }
 }
 
 // ------------------------------------------------------------------- host
 
 constexpr float kCoeffs[3] = {3.4445f, -4.7750f, 2.0315f};
-constexpr float kPairMost = 16.0f;  // of the product of a pair's first coefficients
+constexpr float kPairMost = 16.0f;
+
+// Whether two steps may be taken together: rounding in A comes out of the pair
+// a a' times as large.
+bool pairs(const float *k, const float *k2) {
+  return k[0] * k2[0] > 0.0f && k[0] * k2[0] <= kPairMost;
+}
+
 constexpr int64_t kMaxSide = INT64_C(1) << 20;
 
 bool muon_ok(const zs_muon_desc *d) {
@@ -1033,13 +1248,14 @@ struct Plan {
   Way gram, poly, next;
   int blocks;   // that sum the squares of a matrix
   bool small;   // one workgroup per matrix, padded to 32
+  int strips;   // of kStripCols columns of X, a workgroup each, padded to 32 rows; or 0
   bool paired;  // two steps at a time where the coefficients allow it
   bool tall;
   int64_t partials, arrived, parts, x, xt, y, yt, a, b, c, bytes;  // offsets into the workspace
 };
 
 Plan plan_of(const zs_ortho_desc &d) {
-  Plan p;
+  Plan p = {};
   p.tall = d.rows > d.cols;
   p.m = p.tall ? d.cols : d.rows;
   p.n = p.tall ? d.rows : d.cols;
@@ -1050,28 +1266,37 @@ Plan plan_of(const zs_ortho_desc &d) {
     p.bytes = 256;  // not used: every plan asks for a workspace
     return p;
   }
-  p.mp = up(p.m, 64);
-  p.np = up(p.n, 64);
-  p.gram = way_of(d.batch, p.mp, p.mp, p.np, true);
-  p.poly = way_of(d.batch, p.mp, p.mp, p.mp, true);
-  p.next = way_of(d.batch, p.mp, p.np, p.mp, false);
-  p.paired = d.steps > 1 && 3 * p.poly.us < p.gram.us + p.next.us;
+  const int64_t runs = d.rows * (up(d.cols, kNormRun) / kNormRun);
+  p.blocks = int(runs < kNormBlocks ? runs : kNormBlocks);
   int64_t at = 0;
   const auto take = [&](int64_t bytes) {
     const int64_t was = at;
     at += up(bytes, 256);
     return was;
   };
+  p.partials = take(d.batch * p.blocks * 8);
+  p.arrived = take(kCutTiles * 4);
+  p.strips = p.mp <= kStripRows ? int(up(p.n, kStripCols) / kStripCols) : 0;
+  if (p.strips) {
+    p.np = int64_t(p.strips) * kStripCols;
+    p.xt = take(d.batch * p.np * p.mp * 2);
+    p.parts = take(d.batch * p.strips * p.mp * p.mp * 4);
+    p.a = take(d.batch * p.mp * p.mp * 2);
+    p.bytes = at;
+    return p;
+  }
+  p.mp = up(p.m, 64);
+  p.np = up(p.n, 64);
+  p.gram = way_of(d.batch, p.mp, p.mp, p.np, true);
+  p.poly = way_of(d.batch, p.mp, p.mp, p.mp, true);
+  p.next = way_of(d.batch, p.mp, p.np, p.mp, false);
+  p.paired = d.steps > 1 && 3 * p.poly.us < p.gram.us + p.next.us;
   const auto parts = [](const Way &w) {
     return w.cut ? int64_t(w.grid) * 2 * kShapes[w.shape].TR * kShapes[w.shape].TC * 4 : 0;
   };
   int64_t most = parts(p.next);
   if (parts(p.gram) > most) most = parts(p.gram);
   if (parts(p.poly) > most) most = parts(p.poly);
-  const int64_t runs = d.rows * (up(d.cols, kNormRun) / kNormRun);
-  p.blocks = int(runs < kNormBlocks ? runs : kNormBlocks);
-  p.partials = take(d.batch * p.blocks * 8);
-  p.arrived = take(kCutTiles * 4);
   p.parts = take(most);
   p.x = take(d.batch * p.mp * p.np * 2);
   p.xt = take(d.batch * p.mp * p.np * 2);
@@ -1122,14 +1347,55 @@ int multiply(MulArgs &A, const Way &w, int64_t rows, int64_t cols, int64_t k, hi
 }
 
 template <class TG>
-int start(const InArgs &A, int64_t batch, hipStream_t st) {
+int norm(const InArgs &A, int64_t batch, hipStream_t st) {
   hipLaunchKernelGGL(ortho_norm_kernel<TG>, dim3(A.blocks, unsigned(batch)), dim3(kThreads), 0,
                      st, A);
+  return launched();
+}
+
+template <class TG>
+int start(const InArgs &A, int64_t batch, hipStream_t st) {
+  if (const int rc = norm<TG>(A, batch, st)) return rc;
   const int64_t rp = A.tall ? A.np : A.mp, cp = A.tall ? A.mp : A.np;
   hipLaunchKernelGGL(ortho_layout_kernel<TG>,
                      dim3(unsigned(up(cp, kStrip) / kStrip), unsigned(rp / 64), unsigned(batch)),
                      dim3(kThreads), 0, st, A);
   return launched();
+}
+
+// `steps` steps in strips.
+template <class TG, int MB>
+int strips_of(StripArgs &A, const zs_ortho_desc &d, hipStream_t st) {
+  const dim3 grid{unsigned(A.strips), unsigned(d.batch)}, block{kSmallThreads};
+  hipLaunchKernelGGL((ortho_strip_in_kernel<TG, MB>), grid, block, 0, st, A);
+  int rc = launched();
+  for (int s = 0; s < d.steps && !rc; s += A.pair + 1) {
+    const float *k = d.coeffs ? d.coeffs + 3 * s : kCoeffs;
+    const float *k2 = d.coeffs ? k + 3 : kCoeffs;
+    A.pair = s + 1 < d.steps && pairs(k, k2);
+    for (int i = 0; i < 3; ++i) {
+      A.k[i] = k[i];
+      A.k[i + 3] = A.pair ? k2[i] : 0.0f;
+    }
+    hipLaunchKernelGGL(ortho_strip_sum_kernel, dim3(MB * MB * 16, unsigned(d.batch)), dim3(16, 64),
+                       0, st, A, MB * MB * 1024);
+    if (s + A.pair + 1 < d.steps)
+      hipLaunchKernelGGL((ortho_strip_step_kernel<MB, false>), grid, block, 0, st, A);
+    else
+      hipLaunchKernelGGL((ortho_strip_step_kernel<MB, true>), grid, block, 0, st, A);
+    rc = launched();
+  }
+  return rc;
+}
+
+template <class TG>
+int strips(StripArgs &A, int64_t mp, const zs_ortho_desc &d, hipStream_t st) {
+  switch (mp / 32) {
+    case 1: return strips_of<TG, 1>(A, d, st);
+    case 2: return strips_of<TG, 2>(A, d, st);
+    case 3: return strips_of<TG, 3>(A, d, st);
+    default: return strips_of<TG, 4>(A, d, st);
+  }
 }
 
 template <class TG>
@@ -1206,7 +1472,8 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
   if (d->batch == 0 || d->rows == 0 || d->cols == 0) return ZS_OK;
   const Plan p = plan_of(*d);
   if (!g || !o || !workspace || workspace_bytes < p.bytes) return ZS_EINVAL;
-  if (!p.small && (!std::isfinite(p.gram.us) || !std::isfinite(p.next.us))) return ZS_EINVAL;
+  if (!p.small && !p.strips && (!std::isfinite(p.gram.us) || !std::isfinite(p.next.us)))
+    return ZS_EINVAL;
   if (!aligned(g, dtype_size(d->dtype)) || !aligned(o, 2) || !aligned(workspace, 256))
     return ZS_EALIGN;
   if (const int rc = device_is_gfx950()) return rc;
@@ -1251,6 +1518,32 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
   in.eps = double(d->eps);
   in.tall = p.tall;
   in.blocks = p.blocks;
+  if (p.strips) {
+    StripArgs A;
+    std::memset(&A, 0, sizeof A);
+    A.g = g;
+    A.o = o;
+    A.ld_in = ld_in;
+    A.stride_in = in.stride;
+    A.ld_o = ld_out;
+    A.stride_o = d->stride_out ? d->stride_out : d->rows * ld_out;
+    A.partials = in.partials;
+    A.eps = in.eps;
+    A.xt = half(p.xt);
+    A.parts = reinterpret_cast<float *>(ws + p.parts);
+    A.a = half(p.a);
+    A.blocks = p.blocks;
+    A.rows = int32_t(d->rows);
+    A.cols = int32_t(d->cols);
+    A.tall = p.tall;
+    A.strips = p.strips;
+    const auto all = [&](auto t) {
+      using TG = decltype(t);
+      const int rc = norm<TG>(in, d->batch, st);
+      return rc ? rc : strips<TG>(A, p.mp, *d, st);
+    };
+    return d->dtype == ZS_F32 ? all(F32{}) : d->dtype == ZS_BF16 ? all(Bf16{}) : all(F16{});
+  }
   int rc = d->dtype == ZS_F32    ? start<F32>(in, d->batch, st)
            : d->dtype == ZS_BF16 ? start<Bf16>(in, d->batch, st)
                                  : start<F16>(in, d->batch, st);
@@ -1293,7 +1586,7 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
     if ((rc = poly(k, a, b))) break;
     const _Float16 *by = b;
     ++s;
-    if (p.paired && s < d->steps && k[0] * k2[0] > 0.0f && k[0] * k2[0] <= kPairMost) {
+    if (p.paired && s < d->steps && pairs(k, k2)) {
       // A of the next step is B A B; its B times this one's is applied to X
       if ((rc = small(Const<kGram>{}, b, a, c)) || (rc = small(Const<kGram>{}, c, b, a)) ||
           (rc = poly(k2, a, c)) || (rc = small(Const<kGram>{}, c, b, a)))
