@@ -758,19 +758,41 @@ __device__ __forceinline__ half4 narrow4(const f32x4 &v) {
   return h;
 }
 
-// C = P Q of symmetric matrices that commute: column c's rows are neighbours
-// in row c.  All waves; a barrier follows.
+// The wave's block of a symmetric MB x MB one.  Of the larger ones, which the
+// reading of LDS bounds, those on and below the diagonal are computed and
+// written twice (128 x 128: 31.0 -> 28.2 us); of the smaller all, which the
+// latency bounds (64 x 512: 31.3 us, with half of them 31.9).
+template <int MB>
+struct Lower {
+  static constexpr bool kHalf = MB > 2;
+  static constexpr int kBlocks = kHalf ? MB * (MB + 1) / 2 : MB * MB;
+  static_assert(kBlocks <= kSmallWaves, "a wave has one block");
+  int i, j;
+  __device__ __forceinline__ explicit Lower(int wave)
+      : i(!kHalf ? wave / MB : wave < 1 ? 0 : wave < 3 ? 1 : wave < 6 ? 2 : 3),
+        j(kHalf ? wave - i * (i + 1) / 2 : wave % MB) {}
+  // rows r..r+3 of column c, which are neighbours in row c too
+  __device__ __forceinline__ void put(_Float16 *C, int r, int c, const f32x4 &v) const {
+    constexpr int pm = MB * 32 + 8;
+    const half4 h = narrow4(v);
+    *reinterpret_cast<half4 *>(C + c * pm + r) = h;
+    if (kHalf && i != j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) C[(r + e) * pm + c] = h[e];
+    }
+  }
+};
+
+// C = P Q of symmetric matrices that commute.  All waves; a barrier follows.
 template <int MB>
 __device__ __forceinline__ void short_mul(const _Float16 *P, const _Float16 *Q, _Float16 *C,
                                           int wave, int lane) {
-  static_assert(MB * MB <= kSmallWaves, "a wave has one block");
-  constexpr int pm = MB * 32 + 8;
-  if (wave < MB * MB) {
+  if (wave < Lower<MB>::kBlocks) {
+    const Lower<MB> at(wave);
     Block acc = {};
-    block_mul<MB>(P, Q, wave / MB, wave % MB, lane, acc);
-    block_each(wave / MB, wave % MB, lane, acc, [&](int r, int c, f32x4 v) {
-      *reinterpret_cast<half4 *>(C + c * pm + r) = narrow4(v * kBack1);
-    });
+    block_mul<MB>(P, Q, at.i, at.j, lane, acc);
+    block_each(at.i, at.j, lane, acc,
+               [&](int r, int c, const f32x4 &v) { at.put(C, r, c, v * kBack1); });
   }
   __syncthreads();
 }
@@ -780,21 +802,21 @@ template <int MB>
 __device__ __forceinline__ void short_poly(const float *k, const _Float16 *A, _Float16 *B, int wave,
                                            int lane) {
   constexpr int pm = MB * 32 + 8;
-  if (wave < MB * MB) {
-    const int i = wave / MB, j = wave % MB;
+  if (wave < Lower<MB>::kBlocks) {
+    const Lower<MB> at(wave);
     Block acc = {};
-    block_mul<MB>(A, A, i, j, lane, acc);
-    block_each(i, j, lane, acc, [&](int r, int c, f32x4 v) {
+    block_mul<MB>(A, A, at.i, at.j, lane, acc);
+    block_each(at.i, at.j, lane, acc, [&](int r, int c, f32x4 v) {
       const half4 old = *reinterpret_cast<const half4 *>(A + c * pm + r);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         v[e] = __builtin_fmaf(k[1], float(old[e]), (k[2] * kBack1) * v[e]);
-      if (i == j) {
+      if (at.i == at.j) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (r + e == c) v[e] += k[0] * kScale;
       }
-      *reinterpret_cast<half4 *>(B + c * pm + r) = narrow4(v);
+      at.put(B, r, c, v);
     });
   }
   __syncthreads();
@@ -951,10 +973,10 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const SmallA
   for (int s = 0; s < A.steps; ++s) {
     // Opaque, so that no address is computed ahead of the loop and kept.
     asm volatile("" : "+v"(lane));
-    if (wave < MB * MB) {
-      const int wi = wave / MB, wj = wave % MB;
+    if (wave < Lower<MB>::kBlocks) {
+      const Lower<MB> at(wave);
       Block acc = {};
-      const _Float16 *p = block_at(x, wi, pn, lane), *q = block_at(x, wj, pn, lane);
+      const _Float16 *p = block_at(x, at.i, pn, lane), *q = block_at(x, at.j, pn, lane);
       BlockRegs f0, f1;
       f0.read(p, q, pn);
       for (int k = 1; k < nb; k += 2) {
@@ -965,9 +987,8 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const SmallA
         f1.add(acc);
       }
       if (nb & 1) f0.add(acc);
-      block_each(wi, wj, lane, acc, [&](int r, int c, f32x4 v) {
-        *reinterpret_cast<half4 *>(a + c * pm + r) = narrow4(v * kBack1);
-      });
+      block_each(at.i, at.j, lane, acc,
+                 [&](int r, int c, const f32x4 &v) { at.put(a, r, c, v * kBack1); });
     }
     __syncthreads();
     short_poly<MB>(A.coeffs + 3 * s, a, b, wave, lane);
