@@ -61,7 +61,7 @@ constexpr int kThreads = 256;
 // ------------------------------------------------- momentum and apply
 
 struct Rows {
-  const u32x4 *p[ZS_MAX_ND];
+  const uint16_t *p[ZS_MAX_ND];
 };
 
 struct MomentumArgs {
@@ -75,78 +75,73 @@ struct MomentumArgs {
 };
 
 // 8 elements per lane: one 16-byte load per contribution row, eight rows in
-// flight while the binary64 sum keeps the rank order.
+// flight while the binary64 sum keeps the rank order.  16 rows of 5120 x 5120:
+// 171-195 us, 5.9-6.4 TB/s (the card's best for such a mix); 64 rows of 8192
+// elements 7.4 us, the latency of eight batches (with 32 rows in flight 10.5).
+// The last n % 8 elements have a lane each: one lane for all of them would load
+// element by element (63 rows of 3001: 14.4 us, this 9.3).
+template <class T>  // of a row: Eight<Bf16>, or one element
+__device__ __forceinline__ T row_at(const uint16_t *row, int64_t e0) {
+  T v;
+  if constexpr (sizeof(T) == 2) v = row[e0];
+  else v.template load<false, true>(row, e0, 8);
+  return v;
+}
+
+template <int N, class T, class F>
+__device__ __forceinline__ void sum_rows(const MomentumArgs &A, int64_t e0, double (&s)[N], F get) {
+  const auto batch = [&](int k, int n) {
+    T r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) r[i] = row_at<T>(A.rows.p[k + i], e0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[e] += double(get(r[i], e));
+      }
+  };
+  int k = 0;
+  for (; k + 8 <= A.n_d; k += 8) batch(k, 8);
+  if (k < A.n_d) batch(k, A.n_d - k);
+}
+
+// g = the average; the new momentum; the update
+__device__ __forceinline__ void momentum_of(const MomentumArgs &A, double sum, float &m, float &u) {
+  const float g = float(sum / double(A.n_d));
+  const double mm = A.mu * double(m) + double(g);
+  m = float(mm);
+  u = A.nesterov ? float(double(g) + A.mu * mm) : float(mm);
+}
+
 template <class TU>
 __global__ void __launch_bounds__(kThreads) momentum_kernel(const MomentumArgs A) {
-  const int64_t vec = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t e0 = vec * 8;
-  if (e0 >= A.n) return;
-  const int nvalid = A.n - e0 < 8 ? int(A.n - e0) : 8;
-  double s[8] = {};
-  float m[8], g[8], u[8];
-  if (nvalid == 8) {
-    const f32x4 ma = reinterpret_cast<const f32x4 *>(A.m_in)[2 * vec];
-    const f32x4 mb = reinterpret_cast<const f32x4 *>(A.m_in)[2 * vec + 1];
+  const int64_t at = int64_t(blockIdx.x) * kThreads + threadIdx.x, whole = A.n / 8;
+  if (at < whole) {
+    const int64_t e0 = at * 8;
+    Eight<F32> m;
+    m.load<false>(A.m_in, e0, 8);
+    double s[8] = {};
+    sum_rows<8, Eight<Bf16>>(A, e0, s, [](const Eight<Bf16> &r, int e) { return r.get(e); });
+    float mv[8], u[8];
+    m.get(mv);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      m[e] = ma[e];
-      m[e + 4] = mb[e];
-    }
-    int k = 0;
-    for (; k + 8 <= A.n_d; k += 8) {
-      u32x4 r[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = __builtin_nontemporal_load(A.rows.p[k + i] + vec);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[2 * e] += double(__uint_as_float(r[i][e] << 16));
-          s[2 * e + 1] += double(__uint_as_float(r[i][e] & 0xffff0000u));
-        }
-    }
-    for (; k < A.n_d; ++k) {
-      const u32x4 r = __builtin_nontemporal_load(A.rows.p[k] + vec);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[2 * e] += double(__uint_as_float(r[e] << 16));
-        s[2 * e + 1] += double(__uint_as_float(r[e] & 0xffff0000u));
-      }
-    }
+    for (int e = 0; e < 8; ++e) momentum_of(A, s[e], mv[e], u[e]);
+    m.set(mv);
+    m.store<false>(A.m_out, e0, 8);
+    Eight<TU> out;
+    out.set(u);
+    out.template store<false>(A.update, e0, 8);
   } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      m[e] = e < nvalid ? A.m_in[e0 + e] : 0.0f;
-      if (e < nvalid)
-        for (int k = 0; k < A.n_d; ++k)
-          s[e] += double(Bf16::load(reinterpret_cast<const uint16_t *>(A.rows.p[k])[e0 + e]));
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    g[e] = float(s[e] / double(A.n_d));
-    const double mm = A.mu * double(m[e]) + double(g[e]);
-    m[e] = float(mm);
-    u[e] = A.nesterov ? float(double(g[e]) + A.mu * mm) : float(mm);
-  }
-  typename TU::raw *up = static_cast<typename TU::raw *>(A.update) + e0;
-  if (nvalid == 8) {
-    f32x4 *mo = reinterpret_cast<f32x4 *>(A.m_out) + 2 * vec;
-    mo[0] = f32x4{m[0], m[1], m[2], m[3]};
-    mo[1] = f32x4{m[4], m[5], m[6], m[7]};
-    struct alignas(16) Out {
-      typename TU::raw e[8];
-    } o;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o.e[e] = TU::store(u[e]);
-    *reinterpret_cast<Out *>(up) = o;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < nvalid) {
-        A.m_out[e0 + e] = m[e];
-        up[e] = TU::store(u[e]);
-      }
+    const int64_t e0 = whole * 8 + (at - whole);
+    if (e0 >= A.n) return;
+    float m = A.m_in[e0], u;
+    double s[1] = {};
+    sum_rows<1, uint16_t>(A, e0, s, [](uint16_t r, int) { return Bf16::load(r); });
+    momentum_of(A, s[0], m, u);
+    A.m_out[e0] = m;
+    static_cast<typename TU::raw *>(A.update)[e0] = TU::store(u);
   }
 }
 
@@ -1445,7 +1440,7 @@ int zero_shard_muon_momentum(const zs_muon_desc *d, const zs_bf16 *const *contri
   for (int k = 0; k < d->n_d; ++k) {
     if (!contrib[k]) return ZS_EINVAL;
     if (!aligned(contrib[k], 16)) return ZS_EALIGN;
-    A.rows.p[k] = reinterpret_cast<const u32x4 *>(contrib[k]);
+    A.rows.p[k] = contrib[k];
   }
   if (!aligned(m_in, 16) || !aligned(m_out, 16) || !aligned(update, 16)) return ZS_EALIGN;
   if (const int rc = device_is_gfx950()) return rc;
@@ -1456,7 +1451,7 @@ int zero_shard_muon_momentum(const zs_muon_desc *d, const zs_bf16 *const *contri
   A.m_in = m_in;
   A.m_out = m_out;
   A.update = update;
-  const dim3 grid(unsigned((d->n + kThreads * 8 - 1) / (kThreads * 8)));
+  const dim3 grid(unsigned((d->n / 8 + d->n % 8 + kThreads - 1) / kThreads));
   const hipStream_t st = static_cast<hipStream_t>(d->stream);
   if (d->dtype == ZS_F32)
     hipLaunchKernelGGL(momentum_kernel<F32>, grid, dim3(kThreads), 0, st, A);
