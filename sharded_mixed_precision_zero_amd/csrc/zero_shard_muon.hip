@@ -57,6 +57,7 @@ using half8 = _Float16 __attribute__((ext_vector_type(8)));
 using half4 = _Float16 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
+constexpr unsigned kFew = 256;  // workgroups: one a CU, too few for HBM to bound them
 
 // ------------------------------------------------- momentum and apply
 
@@ -75,11 +76,12 @@ struct MomentumArgs {
 };
 
 // 8 elements per lane: one 16-byte load per contribution row, eight rows in
-// flight while the binary64 sum keeps the rank order.  16 rows of 5120 x 5120:
-// 171-195 us, 5.9-6.4 TB/s (the card's best for such a mix); 64 rows of 8192
-// elements 7.4 us, the latency of eight batches (with 32 rows in flight 10.5).
-// The last n % 8 elements have a lane each: one lane for all of them would load
-// element by element (63 rows of 3001: 14.4 us, this 9.3).
+// flight while the binary64 sum keeps the rank order, of short ranges two times
+// eight.  16 rows of 5120 x 5120: 171 us, 6.4 TB/s (220 us out of no cache);
+// 64 rows of 8192 elements 6.3 us, the latency of the batches (7.5 with eight
+// rows in flight, 10.5 with 32 at once).  The last n % 8 elements have a lane
+// each: one lane for all of them would load element by element (63 rows of
+// 3001: 14.4 us, this 8.1).
 template <class T>  // of a row: Eight<Bf16>, or one element
 __device__ __forceinline__ T row_at(const uint16_t *row, int64_t e0) {
   T v;
@@ -88,23 +90,66 @@ __device__ __forceinline__ T row_at(const uint16_t *row, int64_t e0) {
   return v;
 }
 
-template <int N, class T, class F>
+// DEEP: the next eight rows' loads are issued before these are added.
+template <bool DEEP, int N, class T, class F>
 __device__ __forceinline__ void sum_rows(const MomentumArgs &A, int64_t e0, double (&s)[N], F get) {
-  const auto batch = [&](int k, int n) {
-    T r[8];
+  const auto load = [&](T (&r)[8], int k) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) r[i] = row_at<T>(A.rows.p[k + i], e0);
+      if (k + i < A.n_d) r[i] = row_at<T>(A.rows.p[k + i], e0);
+  };
+  const auto add = [&](const T (&r)[8], int k) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) {
+      if (k + i < A.n_d) {
 #pragma unroll
         for (int e = 0; e < N; ++e) s[e] += double(get(r[i], e));
       }
   };
+  const auto load8 = [&](T (&r)[8], int k) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = row_at<T>(A.rows.p[k + i], e0);
+  };
+  const auto add8 = [&](const T (&r)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < N; ++e) s[e] += double(get(r[i], e));
+  };
+  T r[8], q[8];
   int k = 0;
-  for (; k + 8 <= A.n_d; k += 8) batch(k, 8);
-  if (k < A.n_d) batch(k, A.n_d - k);
+  if constexpr (DEEP) {
+    if (A.n_d >= 8) load8(r, 0);
+    for (; k + 24 <= A.n_d; k += 16) {
+      load8(q, k + 8);
+      add8(r);
+      load8(r, k + 16);
+      add8(q);
+    }
+    if (k + 16 <= A.n_d) {
+      load8(q, k + 8);
+      add8(r);
+      load(r, k + 16);
+      add8(q);
+      add(r, k + 16);
+    } else if (k + 8 <= A.n_d) {
+      load(q, k + 8);
+      add8(r);
+      add(q, k + 8);
+    } else {
+      load(q, k);
+      add(q, k);
+    }
+  } else {
+    for (; k + 8 <= A.n_d; k += 8) {
+      load8(r, k);
+      add8(r);
+    }
+    if (k < A.n_d) {
+      load(q, k);
+      add(q, k);
+    }
+  }
 }
 
 // g = the average; the new momentum; the update
@@ -115,7 +160,7 @@ __device__ __forceinline__ void momentum_of(const MomentumArgs &A, double sum, f
   u = A.nesterov ? float(double(g) + A.mu * mm) : float(mm);
 }
 
-template <class TU>
+template <class TU, bool DEEP>
 __global__ void __launch_bounds__(kThreads) momentum_kernel(const MomentumArgs A) {
   const int64_t at = int64_t(blockIdx.x) * kThreads + threadIdx.x, whole = A.n / 8;
   if (at < whole) {
@@ -123,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) momentum_kernel(const MomentumArgs A
     Eight<F32> m;
     m.load<false>(A.m_in, e0, 8);
     double s[8] = {};
-    sum_rows<8, Eight<Bf16>>(A, e0, s, [](const Eight<Bf16> &r, int e) { return r.get(e); });
+    sum_rows<DEEP, 8, Eight<Bf16>>(A, e0, s, [](const Eight<Bf16> &r, int e) { return r.get(e); });
     float mv[8], u[8];
     m.get(mv);
 #pragma unroll
@@ -138,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) momentum_kernel(const MomentumArgs A
     if (e0 >= A.n) return;
     float m = A.m_in[e0], u;
     double s[1] = {};
-    sum_rows<1, uint16_t>(A, e0, s, [](uint16_t r, int) { return Bf16::load(r); });
+    sum_rows<true, 1, uint16_t>(A, e0, s, [](uint16_t r, int) { return Bf16::load(r); });
     momentum_of(A, s[0], m, u);
     A.m_out[e0] = m;
     static_cast<typename TU::raw *>(A.update)[e0] = TU::store(u);
@@ -1453,11 +1498,15 @@ int zero_shard_muon_momentum(const zs_muon_desc *d, const zs_bf16 *const *contri
   A.update = update;
   const dim3 grid(unsigned((d->n / 8 + d->n % 8 + kThreads - 1) / kThreads));
   const hipStream_t st = static_cast<hipStream_t>(d->stream);
-  if (d->dtype == ZS_F32)
-    hipLaunchKernelGGL(momentum_kernel<F32>, grid, dim3(kThreads), 0, st, A);
-  else
-    hipLaunchKernelGGL(momentum_kernel<Bf16>, grid, dim3(kThreads), 0, st, A);
-  return launched();
+  const auto launch = [&](auto t) {
+    using TU = decltype(t);
+    if (grid.x <= kFew)
+      hipLaunchKernelGGL((momentum_kernel<TU, true>), grid, dim3(kThreads), 0, st, A);
+    else
+      hipLaunchKernelGGL((momentum_kernel<TU, false>), grid, dim3(kThreads), 0, st, A);
+    return launched();
+  };
+  return d->dtype == ZS_F32 ? launch(F32{}) : launch(Bf16{});
 }
 
 int zero_shard_muon_apply(const zs_muon_desc *d, const zs_bf16 *o, float lr, float scale,
