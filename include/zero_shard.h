@@ -464,12 +464,15 @@ int64_t zero_shard_ortho_workspace(const zs_ortho_desc *d);
 /* Per matrix: X = G / (|G|_F + eps) (the norm in binary64), then `steps` times
  *   A = X X^T;  X = a X + (b A + c A A) X
  * (X^T X and products from the right when rows > cols); o = bf16(X).
- * Products are summed in binary32; X, A and a I + b A + c A A are rounded to
- * binary16 times 2^-11 between products, so their entries must stay below 32
- * (coefficients that bring singular values in [0, 1] towards 1 keep them
- * below 4), and entries of X under 2^-36 vanish: a matrix whose norm is far
- * below eps gives zeros.  A zero matrix gives zeros (eps > 0; NaN with eps = 0);
- * a matrix that holds an infinity or NaN gives NaN in that matrix only.
+ * Products are summed in binary32; X, A and B = a I + b A + c A A are rounded
+ * to binary16 times 2^-11 between products.  Of a matrix much longer than wide
+ * two steps whose a have a product in (0, 16] are taken together: the second A
+ * is B A B and X becomes (B' B) X, the same products in another order; B A and
+ * B' B are rounded likewise.  The entries of all of them must stay below 32
+ * (coefficients that bring singular values in [0, 1] towards 1 keep them below
+ * 16), and entries of X under 2^-36 vanish: a matrix whose norm is far below eps
+ * gives zeros.  A zero matrix gives zeros (eps > 0; NaN with eps = 0); a matrix
+ * that holds an infinity or NaN gives NaN in that matrix only.
  * g: input; o: bf16 output, overlapping nothing else; workspace: device,
  * 256-byte aligned, at least zero_shard_ortho_workspace(d) bytes.
  * Errors: ZS_EINVAL, ZS_EALIGN, ZS_EDEVICE, ZS_EHIP. */

@@ -35,8 +35,16 @@
 // A is made anew from X: in two steps the result is as far off as before
 // (Gaussian 512 x 1382: 1.26e-3 for 1.19e-3; ill-conditioned and rank-8 ones:
 // less than before), in three it diverges where A is singular.
-// All of it is laid out padded to whole tiles with zeros, which the iteration
-// keeps zero, so the products need no bounds.
+//
+// What bounds the large ones is the card's power: with the operands' bits at
+// random the clock falls to 2.0-2.2 GHz at 60% of the matrix cores' cycles, and
+// a variant that needs fewer cycles (32 x 32 x 16 instructions: 10% fewer) takes
+// the same time.  5120 x 5120 in five steps: 2.4 ms, 1.1 PFLOP/s of the
+// operations counted above, where a library product of that size reaches 1.0
+// and of 8192 1.4; 13824 x 5120 4.2 ms, 1.4 PFLOP/s of the single steps' count.
+// X is laid out padded to multiples of 64 with zeros, which the iteration keeps
+// zero; tiles reach past that, loads there are dropped by the hardware's bounds
+// and stores checked.  Matrices of up to 128 rows take ways of their own.
 
 #include <hip/hip_runtime.h>
 
@@ -1052,8 +1060,10 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const SmallA
 // updates of X only A is needed of all strips together: each leaves its part of
 // X X^T, one launch adds them, and the next update's workgroups all work out
 // the polynomials in A again, two steps of them where the coefficients allow
-// it, and apply them to their strip.  64 x 13824: 8 launches, XXX us, in place
-// of 19, 105 us.
+// it, and apply them to their strip.  64 x 13824: 8 launches, 33 us, in place of
+// 19, 105 us; 128 x 4000 50 and 101 us.  What is left is launches and the latency
+// of LDS: at 128 rows a product of 128^3 takes 1.5 us, of which one CU's matrix
+// cores work 0.2.
 constexpr int kStripCols = 128, kStripRows = 128;
 
 struct StripArgs {
@@ -1233,6 +1243,8 @@ bool ortho_ok(const zs_ortho_desc *d) {
 // The shapes between 256 x 256 and 128 x 256 fill the last turn of the card
 // better: 5120 x 5120 is 400 tiles of 256 x 256 (two turns of 256, 279 us) or
 // 460 of 224 x 256 (253 us); its lower triangle 210 (144 us) or 251 (128 us).
+// (Over many products, when the clock has fallen, idle CUs leave it higher and
+// the two differ by 1%.)
 // Smaller tiles give more workgroups but read more: 4 of 1024 x 1024 take
 // 30 us as 64 tiles of 256 x 256, 16 us as 256 of 128 x 128, 21 us as 1024 of
 // 64 x 64.
