@@ -83,18 +83,33 @@ struct MomentumArgs {
   void *update;
 };
 
-// 8 elements per lane: one 16-byte load per contribution row, eight rows in
-// flight while the binary64 sum keeps the rank order, of short ranges two times
-// eight.  16 rows of 5120 x 5120: 171 us, 6.4 TB/s (220 us out of no cache);
-// 64 rows of 8192 elements 6.3 us, the latency of the batches (7.5 with eight
-// rows in flight, 10.5 with 32 at once).  The last n % 8 elements have a lane
-// each: one lane for all of them would load element by element (63 rows of
-// 3001: 14.4 us, this 8.1).
-template <class T>  // of a row: Eight<Bf16>, or one element
+// A wave takes 512 elements, a lane two fours of them 256 apart, so that each
+// access of the wave covers one stretch; rows and momentum are used once a step
+// and go past the caches, the update is what the orthogonalisation reads next.
+// Eight rows are in flight while the binary64 sum keeps the rank order, of short
+// ranges two times eight.  Out of no cache: 16 rows of 5120 x 5120 201 us, 5.5
+// TB/s, 3 rows of 9.4 million 29 us (eight consecutive elements a lane, momentum
+// through the caches: 220 and 37 us); 64 rows of 40000 11 us (14 with eight rows
+// in flight).  The last n % 512 elements have a lane each (60 rows of 3001: 11
+// us; one lane for eight of them, element by element, 20).
+struct Fours {
+  u32x2 w[2];
+  __device__ __forceinline__ float get(int e) const {
+    const unsigned v = w[e / 4][e % 4 / 2];
+    return __uint_as_float(e % 2 ? v & 0xffff0000u : v << 16);
+  }
+};
+
+template <class T>  // of a row: Fours, or one element
 __device__ __forceinline__ T row_at(const uint16_t *row, int64_t e0) {
   T v;
-  if constexpr (sizeof(T) == 2) v = row[e0];
-  else v.template load<false, true>(row, e0, 8);
+  if constexpr (sizeof(T) == 2) {
+    v = row[e0];
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      v.w[h] = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(row + e0 + h * 256));
+  }
   return v;
 }
 
@@ -170,24 +185,33 @@ __device__ __forceinline__ void momentum_of(const MomentumArgs &A, double sum, f
 
 template <class TU, bool DEEP>
 __global__ void __launch_bounds__(kThreads) momentum_kernel(const MomentumArgs A) {
-  const int64_t at = int64_t(blockIdx.x) * kThreads + threadIdx.x, whole = A.n / 8;
-  if (at < whole) {
-    const int64_t e0 = at * 8;
-    Eight<F32> m;
-    m.load<false>(A.m_in, e0, 8);
-    double s[8] = {};
-    sum_rows<DEEP, 8, Eight<Bf16>>(A, e0, s, [](const Eight<Bf16> &r, int e) { return r.get(e); });
-    float mv[8], u[8];
-    m.get(mv);
+  const int64_t at = int64_t(blockIdx.x) * kThreads + threadIdx.x, whole = A.n / 512 * 512;
+  if (at < whole / 8) {
+    const int64_t e0 = at / 64 * 512 + at % 64 * 4;
+    f32x4 m[2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) momentum_of(A, s[e], mv[e], u[e]);
-    m.set(mv);
-    m.store<false>(A.m_out, e0, 8);
-    Eight<TU> out;
-    out.set(u);
-    out.template store<false>(A.update, e0, 8);
+    for (int h = 0; h < 2; ++h)
+      m[h] = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(A.m_in + e0 + h * 256));
+    double s[8] = {};
+    sum_rows<DEEP, 8, Fours>(A, e0, s, [](const Fours &r, int e) { return r.get(e); });
+    struct alignas(sizeof(typename TU::raw) * 4) Out {
+      typename TU::raw e[4];
+    };
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      Out out;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v = m[h][e], u;
+        momentum_of(A, s[h * 4 + e], v, u);
+        m[h][e] = v;
+        out.e[e] = TU::store(u);
+      }
+      __builtin_nontemporal_store(m[h], reinterpret_cast<f32x4 *>(A.m_out + e0 + h * 256));
+      *reinterpret_cast<Out *>(static_cast<typename TU::raw *>(A.update) + e0 + h * 256) = out;
+    }
   } else {
-    const int64_t e0 = whole * 8 + (at - whole);
+    const int64_t e0 = whole + (at - whole / 8);
     if (e0 >= A.n) return;
     float m = A.m_in[e0], u;
     double s[1] = {};
@@ -1509,7 +1533,7 @@ int zero_shard_muon_momentum(const zs_muon_desc *d, const zs_bf16 *const *contri
   A.m_in = m_in;
   A.m_out = m_out;
   A.update = update;
-  const dim3 grid(unsigned((d->n / 8 + d->n % 8 + kThreads - 1) / kThreads));
+  const dim3 grid(unsigned((d->n / 512 * 64 + d->n % 512 + kThreads - 1) / kThreads));
   const hipStream_t st = static_cast<hipStream_t>(d->stream);
   const auto launch = [&](auto t) {
     using TU = decltype(t);
