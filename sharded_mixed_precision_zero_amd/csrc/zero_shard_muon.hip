@@ -84,11 +84,11 @@ struct MomentumArgs {
 };
 
 // A wave takes 512 elements, a lane two fours of them 256 apart, so that each
-// access of the wave covers one stretch; rows and momentum are used once a step
-// and go past the caches, the update is what the orthogonalisation reads next.
-// Eight rows are in flight while the binary64 sum keeps the rank order, of short
-// ranges two times eight.  Out of no cache: 16 rows of 5120 x 5120 201 us, 5.5
-// TB/s, 3 rows of 9.4 million 29 us (eight consecutive elements a lane, momentum
+// access of the wave covers one stretch; all of them go past the caches (the
+// whole Muon step takes the same time with the update kept there).  Eight rows
+// are in flight while the binary64 sum keeps the rank order, of short ranges two
+// times eight.  Out of no cache: 16 rows of 5120 x 5120 190 us, 5.8 TB/s, 3 rows
+// of 9.4 million 29 us (eight consecutive elements a lane, momentum and update
 // through the caches: 220 and 37 us); 64 rows of 40000 11 us (14 with eight rows
 // in flight).  The last n % 512 elements have a lane each (60 rows of 3001: 11
 // us; one lane for eight of them, element by element, 20).
@@ -194,9 +194,10 @@ __global__ void __launch_bounds__(kThreads) momentum_kernel(const MomentumArgs A
       m[h] = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(A.m_in + e0 + h * 256));
     double s[8] = {};
     sum_rows<DEEP, 8, Fours>(A, e0, s, [](const Fours &r, int e) { return r.get(e); });
-    struct alignas(sizeof(typename TU::raw) * 4) Out {
+    struct Out {
       typename TU::raw e[4];
     };
+    using Words = std::conditional_t<sizeof(Out) == 16, u32x4, u32x2>;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       Out out;
@@ -208,7 +209,9 @@ __global__ void __launch_bounds__(kThreads) momentum_kernel(const MomentumArgs A
         out.e[e] = TU::store(u);
       }
       __builtin_nontemporal_store(m[h], reinterpret_cast<f32x4 *>(A.m_out + e0 + h * 256));
-      *reinterpret_cast<Out *>(static_cast<typename TU::raw *>(A.update) + e0 + h * 256) = out;
+      __builtin_nontemporal_store(
+          __builtin_bit_cast(Words, out),
+          reinterpret_cast<Words *>(static_cast<typename TU::raw *>(A.update) + e0 + h * 256));
     }
   } else {
     const int64_t e0 = whole + (at - whole / 8);
