@@ -37,11 +37,11 @@
 // less than before), in three it diverges where A is singular.
 //
 // What bounds the large ones is the card's power: with the operands' bits at
-// random the clock falls to 2.0-2.2 GHz at 60% of the matrix cores' cycles, and
+// random the clock falls to 1.9-2.1 GHz at 60% of the matrix cores' cycles, and
 // a variant that needs fewer cycles (32 x 32 x 16 instructions: 10% fewer) takes
 // the same time.  5120 x 5120 in five steps: 2.4 ms, 1.1 PFLOP/s of the
 // operations counted above, where a library product of that size reaches 1.0
-// and of 8192 1.4; 13824 x 5120 4.2 ms, 1.4 PFLOP/s of the single steps' count.
+// and of 8192 1.4; 13824 x 5120 4.1 ms, 1.5 PFLOP/s of the single steps' count.
 // X is laid out padded to multiples of 64 with zeros, which the iteration keeps
 // zero; tiles reach past that, loads there are dropped by the hardware's bounds
 // and stores checked.  Matrices of up to 128 rows take ways of their own.
