@@ -84,7 +84,10 @@ struct Sums {
 #pragma unroll
       for (int m = 0; m < M; ++m) buf[threadIdx.x >> 6][m] = v[m];
     }
-    __syncthreads();
+    // all of LDS is there; loads from memory stay in flight
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 #pragma unroll
     for (int m = 0; m < M; m += 4) {
       const int at = m + (lane >> 4), w = lane & 15;
@@ -168,30 +171,48 @@ __global__ void __launch_bounds__(1024) ln_fwd_kernel(const FwdArgs A) {
   load_params<TAIL>(gamma, A.gamma, 1.0f, c);
   load_params<TAIL>(beta, A.beta, 0.0f, c);
   const float inv = 1.0f / float(A.cols);
+  // Past the caches where a lane's accesses are 16 bytes side by side; others
+  // leave parts of lines, which should stay (8192 x 4096 fp32: 103 us for 108;
+  // 16384 x 511 bf16: 23 for 29; but 8192 x 5120 bf16: 71 for 74).
+  constexpr bool kOnce = N == 1 && !TAIL && sizeof(typename TX::raw) == 2;
   const int64_t step = int64_t(gridDim.x) * subs * R;
-  for (int64_t first = int64_t(blockIdx.x) * subs * R; first < A.rows; first += step) {
-    const int64_t r0 = first + sub * R;
-    Eight<TX> x[R][N];
+  struct Rows {
+    Eight<TX> x[R][N], q[R][N];
+  };
+  const auto load = [&](Rows &v, int64_t r0) {
 #pragma unroll
     for (int k = 0; k < R; ++k)
 #pragma unroll
-      for (int n = 0; n < N; ++n)
-        x[k][n].template load<TAIL, true>(row_of<TX>(A.x, r0 + k, A.ld_x), c.i[n], r0 + k < A.rows ? c.left[n] : 0);
+      for (int n = 0; n < N; ++n) {
+        const int left = r0 + k < A.rows ? c.left[n] : 0;
+        v.x[k][n].template load<TAIL, kOnce>(row_of<TX>(A.x, r0 + k, A.ld_x), c.i[n], left);
+        if (A.residual)
+          v.q[k][n].template load<TAIL, kOnce>(row_of<TX>(A.residual, r0 + k, A.ld_r), c.i[n], left);
+      }
+  };
+  // The next rows are on their way while these are worked on, where the
+  // registers hold both.
+  constexpr bool kAhead = N == 1;
+  Rows ahead;
+  if constexpr (kAhead) load(ahead, (int64_t(blockIdx.x) * subs + sub) * R);
+  for (int64_t first = int64_t(blockIdx.x) * subs * R; first < A.rows; first += step) {
+    const int64_t r0 = first + sub * R;
+    Rows now;
+    if constexpr (kAhead) {
+      now = ahead;
+      if (first + step < A.rows) load(ahead, r0 + step);
+    } else {
+      load(now, r0);
+    }
+    auto &x = now.x;
     if (A.residual) {
-      Eight<TX> q[R][N];
-#pragma unroll
-      for (int k = 0; k < R; ++k)
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-          q[k][n].template load<TAIL, true>(row_of<TX>(A.residual, r0 + k, A.ld_r), c.i[n],
-                       r0 + k < A.rows ? c.left[n] : 0);
 #pragma unroll
       for (int k = 0; k < R; ++k)
 #pragma unroll
         for (int n = 0; n < N; ++n) {
           float s[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s[e] = x[k][n].get(e) + q[k][n].get(e);
+          for (int e = 0; e < 8; ++e) s[e] = x[k][n].get(e) + now.q[k][n].get(e);
           x[k][n].set(s);
           if (r0 + k < A.rows)
             x[k][n].template store<TAIL>(row_of<TX>(A.sum, r0 + k, A.ld_s), c.i[n], c.left[n]);
@@ -207,6 +228,9 @@ __global__ void __launch_bounds__(1024) ln_fwd_kernel(const FwdArgs A) {
         for (int e = 0; e < 8; ++e) mean[k] += x[k][n].get(e);
     }
     sums.add(mean);
+    // the deviations; where registers are short, anew from x each time
+    constexpr bool kKeep = N == 1;
+    float dev[kKeep ? R : 1][kKeep ? N : 1][8];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
 #pragma unroll
@@ -220,6 +244,7 @@ __global__ void __launch_bounds__(1024) ln_fwd_kernel(const FwdArgs A) {
           const float d = (TAIL ? e : 0) < c.left[n] ? x[k][n].get(e) - mean[k] : 0.0f;
           sq = __builtin_fmaf(d, d, sq);
           off += d;
+          if constexpr (kKeep) dev[k][n][e] = d;
         }
       both[2 * k] = sq;
       both[2 * k + 1] = off;
@@ -227,8 +252,6 @@ __global__ void __launch_bounds__(1024) ln_fwd_kernel(const FwdArgs A) {
     sums.add(both);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-#pragma unroll
-      for (int n = 0; n < N; ++n) x[k][n].forget();
       const float rough = mean[k];
       float off = both[2 * k + 1];
       const float rstd = finish(both[2 * k], off, inv, A.eps, mean[k]);
@@ -236,10 +259,13 @@ __global__ void __launch_bounds__(1024) ln_fwd_kernel(const FwdArgs A) {
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         float y[8];
+        if constexpr (!kKeep) x[k][n].forget();
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float h = ((x[k][n].get(e) - rough) - off) * rstd;
-          y[e] = h * gamma[n].get(e) + beta[n].get(e);
+          float d;
+          if constexpr (kKeep) d = dev[k][n][e];
+          else d = x[k][n].get(e) - rough;
+          y[e] = __builtin_fmaf((d - off) * rstd, gamma[n].get(e), beta[n].get(e));
         }
         x[k][n].set(y);
         x[k][n].template store<TAIL>(row_of<TX>(A.y, r0 + k, A.ld_y), c.i[n], c.left[n]);
@@ -347,24 +373,46 @@ __global__ void __launch_bounds__(1024) ln_bwd_kernel(const BwdArgs A) {
   load_params<TAIL>(gamma, A.gamma, 1.0f, c);
   const float inv = 1.0f / float(A.cols);
   float dg[N][8] = {}, db[N][8] = {};
+  // Past the caches where a lane's accesses are 16 bytes side by side; others
+  // leave parts of lines, which should stay (8192 x 4096 fp32: 103 us for 108;
+  // 16384 x 511 bf16: 23 for 29; but 8192 x 5120 bf16: 71 for 74).
+  constexpr bool kOnce = N == 1 && !TAIL && sizeof(typename TX::raw) == 2;
   const int64_t step = int64_t(gridDim.x) * subs * R;
-  for (int64_t first = int64_t(blockIdx.x) * subs * R; first < A.rows; first += step) {
-    const int64_t r0 = first + sub * R;
+  struct Rows {
     Eight<TX> x[R][N], dy[R][N], ds[R][N];
-    float mean[R], rstd[R], both[2 * R];
+    float mean[R], rstd[R];
+  };
+  const auto load = [&](Rows &v, int64_t r0) {
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       const bool in = r0 + k < A.rows;
-      mean[k] = in ? A.mean[r0 + k] : 0.0f;
-      rstd[k] = in ? A.rstd[r0 + k] : 0.0f;
+      v.mean[k] = in ? A.mean[r0 + k] : 0.0f;
+      v.rstd[k] = in ? A.rstd[r0 + k] : 0.0f;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         const int left = in ? c.left[n] : 0;
-        x[k][n].template load<TAIL, true>(row_of<TX>(A.x, r0 + k, A.ld_x), c.i[n], left);
-        dy[k][n].template load<TAIL, true>(row_of<TX>(A.dy, r0 + k, A.ld_dy), c.i[n], left);
-        if (A.dsum) ds[k][n].template load<TAIL, true>(row_of<TX>(A.dsum, r0 + k, A.ld_ds), c.i[n], left);
+        v.x[k][n].template load<TAIL, kOnce>(row_of<TX>(A.x, r0 + k, A.ld_x), c.i[n], left);
+        v.dy[k][n].template load<TAIL, kOnce>(row_of<TX>(A.dy, r0 + k, A.ld_dy), c.i[n], left);
+        if (A.dsum)
+          v.ds[k][n].template load<TAIL, kOnce>(row_of<TX>(A.dsum, r0 + k, A.ld_ds), c.i[n], left);
       }
     }
+  };
+  constexpr bool kAhead = N == 1;  // as in the forward pass
+  Rows ahead;
+  if constexpr (kAhead) load(ahead, (int64_t(blockIdx.x) * subs + sub) * R);
+  for (int64_t first = int64_t(blockIdx.x) * subs * R; first < A.rows; first += step) {
+    const int64_t r0 = first + sub * R;
+    Rows now;
+    if constexpr (kAhead) {
+      now = ahead;
+      if (first + step < A.rows) load(ahead, r0 + step);
+    } else {
+      load(now, r0);
+    }
+    auto &x = now.x, &dy = now.dy, &ds = now.ds;
+    auto &mean = now.mean, &rstd = now.rstd;
+    float both[2 * R];
     // past a row's end dy is 0, and so is all that it is a factor of
 #pragma unroll
     for (int k = 0; k < R; ++k) {
@@ -397,7 +445,8 @@ __global__ void __launch_bounds__(1024) ln_bwd_kernel(const BwdArgs A) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float h = (x[k][n].get(e) - mean[k]) * rstd[k];
-          v[e] = rstd[k] * (dy[k][n].get(e) * gamma[n].get(e) - c1 - h * c2);
+          const float g = dy[k][n].get(e) * gamma[n].get(e) - c1;
+          v[e] = rstd[k] * __builtin_fmaf(-h, c2, g);
           if (A.dsum) v[e] += ds[k][n].get(e);
         }
         x[k][n].set(v);
@@ -559,7 +608,8 @@ struct Way {
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-Way way_of(const zs_layernorm_desc &d, bool forward) {
+// `even`: all rows start on 16-byte boundaries.
+Way way_of(const zs_layernorm_desc &d, bool forward, bool even = true) {
   Way w;
   w.n = d.cols <= kMaxRegCols / 2 ? 1 : 2;
   w.per = int(up(up(d.cols, 8 * w.n) / (8 * w.n), 64));
@@ -569,7 +619,7 @@ Way way_of(const zs_layernorm_desc &d, bool forward) {
   // few rows: a workgroup for each
   if (d.rows < int64_t(kCus) * w.subs) w.subs = int((d.rows + kCus - 1) / kCus);
   if (w.subs < 1) w.subs = 1;
-  w.tail = d.cols % 8 != 0;
+  w.tail = d.cols % 8 != 0 || !even;
   // two rows at a time once every CU has some, where the registers hold them
   w.r = d.rows >= 4 * kCus && w.n == 1 && (forward || d.dtype != ZS_F32) ? 2 : 1;
   const int64_t rows = int64_t(w.subs) * w.r;
@@ -599,6 +649,11 @@ int by_type(const zs_layernorm_desc &d, F f) {
   return d.param_dtype == ZS_F32 ? f(F16{}, F32{}) : f(F16{}, F16{});
 }
 
+// Every row of p starts on a 16-byte boundary (or p is absent).
+bool rows_even(const void *p, int64_t ld, int size) {
+  return !p || (aligned(p, 16) && ld * size % 16 == 0);
+}
+
 // Workgroups of the backward pass, each of which leaves a partial row.
 int64_t parts_of(const zs_layernorm_desc &d) {
   const int64_t b = d.cols > kMaxRegCols ? (d.rows + 3) / 4 : way_of(d, false).groups;
@@ -623,6 +678,8 @@ int zero_shard_layernorm(const zs_layernorm_desc *d, const void *x, const void *
   const auto ld = [&](int64_t v) { return v ? v : d->cols; };
   FwdArgs A{d->rows, d->cols, ld(d->ld_x), ld(d->ld_residual), ld(d->ld_sum), ld(d->ld_y),
             x, residual, gamma, beta, sum, y, mean, rstd, d->eps, 0};
+  const bool even = rows_even(x, A.ld_x, size) && rows_even(residual, A.ld_r, size) &&
+                    rows_even(sum, A.ld_s, size) && rows_even(y, A.ld_y, size);
   const hipStream_t st = static_cast<hipStream_t>(d->stream);
   return by_type(*d, [&](auto tx, auto tp) {
     using TX = decltype(tx);
@@ -633,7 +690,7 @@ int zero_shard_layernorm(const zs_layernorm_desc *d, const void *x, const void *
                          dim3(kLongThreads), 0, st, A);
       return launched();
     }
-    const Way w = way_of(*d, true);
+    const Way w = way_of(*d, true, even);
     A.per = w.per;
     const int threads = w.per * w.subs;
     const int64_t most = int64_t(kCus) * (2048 / threads);
@@ -673,6 +730,8 @@ int zero_shard_layernorm_bwd(const zs_layernorm_desc *d, const void *dy, const v
   BwdArgs A{d->rows, d->cols, ld(d->ld_dy), ld(d->ld_x), ld(d->ld_dsum), ld(d->ld_dx),
             dy, x, gamma, dsum, mean, rstd, dx, dgamma, dbeta,
             params ? static_cast<float *>(workspace) : nullptr, int32_t(parts_of(*d)), 0};
+  const bool even = rows_even(dy, A.ld_dy, size) && rows_even(x, A.ld_x, size) &&
+                    rows_even(dsum, A.ld_ds, size) && rows_even(dx, A.ld_dx, size);
   const hipStream_t st = static_cast<hipStream_t>(d->stream);
   return by_type(*d, [&](auto tx, auto tp) {
     using TX = decltype(tx);
@@ -688,7 +747,7 @@ int zero_shard_layernorm_bwd(const zs_layernorm_desc *d, const void *dy, const v
                          dim3(kLongThreads), 0, st, A);
       rc = launched();
     } else if (A.rows > 0) {
-      const Way w = way_of(*d, false);
+      const Way w = way_of(*d, false, even);
       A.per = w.per;
       rc = by_way<!std::is_same_v<TX, F32>>(w, [&](auto n, auto r, auto tail) {
         hipLaunchKernelGGL((ln_bwd_kernel<TX, TP, n.value, r.value, tail.value>), dim3(unsigned(A.parts)),
