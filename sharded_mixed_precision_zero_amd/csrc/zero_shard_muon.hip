@@ -833,10 +833,58 @@ __device__ __forceinline__ half4 narrow4(const f32x4 &v) {
   return h;
 }
 
+// A symmetric matrix of mp rows in LDS is followed by `rest`, what rounding took
+// off its diagonal.  The diagonals of A and B are much the largest elements
+// there and much alike, so their rounding scales whole rows of X and, where the
+// singular values lie together on a steep part of the polynomial, the next steps
+// make that larger: without the rests the result of a random 32 x 13824 is 2.3
+// times as far off as the rounding of a right one to bf16, with them 1.03; 96 x
+// 128 takes 22.9 us, without them 21.9.
+constexpr int short_size(int mp) { return mp * (mp + 8) + 2 * mp; }
+
+template <int MB>
+__device__ __forceinline__ float *rest_of(_Float16 *M) {
+  return reinterpret_cast<float *>(M + MB * 32 * (MB * 32 + 8));
+}
+template <int MB>
+__device__ __forceinline__ const float *rest_of(const _Float16 *M) {
+  return rest_of<MB>(const_cast<_Float16 *>(M));
+}
+
+// v + f * x
+__device__ __forceinline__ f32x4 add4(f32x4 v, const f32x4 &f, const half4 &x) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f[e], float(x[e]), v[e]);
+  return v;
+}
+
+// What the rests add to a block of a product, where its sums start: added at
+// their end, behind the matrix instructions, 96 x 128 takes 1.5 us more.  Rows
+// r..r+3 of column c of the second factor by the first's rest (`rows`), and of
+// the first by the second's (`cols`).
+template <int MB>
+__device__ __forceinline__ void block_start(const float *rows, const _Float16 *Q, const float *cols,
+                                            const _Float16 *P, int i, int j, int lane, Block &acc) {
+  constexpr int pm = MB * 32 + 8;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = i * 32 + e * 16 + (lane >> 4) * 4;
+    const f32x4 d = *reinterpret_cast<const f32x4 *>(rows + r);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = j * 32 + h * 16 + (lane & 15);
+      acc[e][h] = add4(f32x4{}, d, *reinterpret_cast<const half4 *>(Q + c * pm + r));
+      if (cols)
+        acc[e][h] = add4(acc[e][h], f32x4{} + cols[c],
+                         *reinterpret_cast<const half4 *>(P + c * pm + r));
+    }
+  }
+}
+
 // The wave's block of a symmetric MB x MB one.  Of the larger ones, which the
 // reading of LDS bounds, those on and below the diagonal are computed and
-// written twice (128 x 128: 31.0 -> 28.2 us); of the smaller all, which the
-// latency bounds (64 x 512: 31.3 us, with half of them 31.9).
+// written twice (128 x 128, without the rests: 31.0 -> 28.2 us); of the smaller
+// all, which the latency bounds (64 x 512: 31.3 us, with half of them 31.9).
 template <int MB>
 struct Lower {
   static constexpr bool kHalf = MB > 2;
@@ -846,14 +894,33 @@ struct Lower {
   __device__ __forceinline__ explicit Lower(int wave)
       : i(!kHalf ? wave / MB : wave < 1 ? 0 : wave < 3 ? 1 : wave < 6 ? 2 : 3),
         j(kHalf ? wave - i * (i + 1) / 2 : wave % MB) {}
-  // rows r..r+3 of column c, which are neighbours in row c too
-  __device__ __forceinline__ void put(_Float16 *C, int r, int c, const f32x4 &v) const {
+  // f(r, c, rows r..r+3 of column c) to C.  They are neighbours in row c too.
+  template <class F>
+  __device__ __forceinline__ void put(_Float16 *C, int lane, const Block &acc, F f) const {
     constexpr int pm = MB * 32 + 8;
-    const half4 h = narrow4(v);
-    *reinterpret_cast<half4 *>(C + c * pm + r) = h;
-    if (kHalf && i != j) {
+    // Of the two parts on the diagonal a lane in four holds an element each.
+    float rest[2];
+    const int at = (lane & 15) - (lane >> 4) * 4;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) C[(r + e) * pm + c] = h[e];
+    for (int p = 0; p < 4; ++p) {
+      const int r = i * 32 + p / 2 * 16 + (lane >> 4) * 4, c = j * 32 + p % 2 * 16 + (lane & 15);
+      const f32x4 v = f(r, c, acc[p / 2][p % 2]);
+      const half4 h = narrow4(v);
+      *reinterpret_cast<half4 *>(C + c * pm + r) = h;
+      if (kHalf && i != j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) C[(r + e) * pm + c] = h[e];
+      }
+      if (p / 2 == p % 2) {
+        rest[p / 2] = v[0] - float(h[0]);
+#pragma unroll
+        for (int e = 1; e < 4; ++e) rest[p / 2] = at == e ? v[e] - float(h[e]) : rest[p / 2];
+      }
+    }
+    if (i == j && at >= 0 && at < 4) {
+      float *to = rest_of<MB>(C) + i * 32 + (lane & 15);
+      to[0] = rest[0];
+      to[16] = rest[1];
     }
   }
 };
@@ -864,10 +931,10 @@ __device__ __forceinline__ void short_mul(const _Float16 *P, const _Float16 *Q, 
                                           int wave, int lane) {
   if (wave < Lower<MB>::kBlocks) {
     const Lower<MB> at(wave);
-    Block acc = {};
+    Block acc;
+    block_start<MB>(rest_of<MB>(P), Q, rest_of<MB>(Q), P, at.i, at.j, lane, acc);
     block_mul<MB>(P, Q, at.i, at.j, lane, acc);
-    block_each(at.i, at.j, lane, acc,
-               [&](int r, int c, const f32x4 &v) { at.put(C, r, c, v * kBack1); });
+    at.put(C, lane, acc, [](int, int, const f32x4 &v) { return v * kBack1; });
   }
   __syncthreads();
 }
@@ -879,22 +946,30 @@ __device__ __forceinline__ void short_poly(const float *k, const _Float16 *A, _F
   constexpr int pm = MB * 32 + 8;
   if (wave < Lower<MB>::kBlocks) {
     const Lower<MB> at(wave);
-    Block acc = {};
+    const float *d = rest_of<MB>(A);
+    Block acc;
+    block_start<MB>(d, A, d, A, at.i, at.j, lane, acc);
     block_mul<MB>(A, A, at.i, at.j, lane, acc);
-    block_each(at.i, at.j, lane, acc, [&](int r, int c, f32x4 v) {
-      const half4 old = *reinterpret_cast<const half4 *>(A + c * pm + r);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        v[e] = __builtin_fmaf(k[1], float(old[e]), (k[2] * kBack1) * v[e]);
+    at.put(B, lane, acc, [&](int r, int c, f32x4 v) {
+      v = add4(v * (k[2] * kBack1), f32x4{} + k[1],
+               *reinterpret_cast<const half4 *>(A + c * pm + r));
       if (at.i == at.j) {
+        const float more = k[0] * kScale + k[1] * d[c];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (r + e == c) v[e] += k[0] * kScale;
+        for (int e = 0; e < 4; ++e) v[e] += r + e == c ? more : 0.0f;
       }
-      at.put(B, r, c, v);
+      return v;
     });
   }
   __syncthreads();
+}
+
+// Block i, j of B X.
+template <int MB>
+__device__ __forceinline__ void times(const _Float16 *B, const _Float16 *xt, int i, int j, int lane,
+                                      Block &acc) {
+  block_start<MB>(rest_of<MB>(B), xt, nullptr, nullptr, i, j, lane, acc);
+  block_mul<MB>(B, xt, i, j, lane, acc);
 }
 
 // A matrix's (or a strip's) rp x cp elements in LDS, in the caller's
@@ -1021,11 +1096,11 @@ struct SmallArgs {
 };
 
 int64_t small_lds(int64_t mp, int64_t np) {
-  return mp * (np + 8) + np * (mp + 8) + 2 * mp * (mp + 8);
+  return mp * (np + 8) + np * (mp + 8) + 2 * short_size(int(mp));
 }
 
 // A matrix whose X, X^T, A and B fit in the LDS of one CU: one workgroup, one
-// launch (96 x 128: 17 launches take 67 us, this 22 us; 64 x 512 68 and 31 us).
+// launch (96 x 128: 17 launches take 67 us, this 23 us; 64 x 512 68 and 34 us).
 template <class TG, int MB>
 __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const SmallArgs A) {
   __shared__ __align__(16) _Float16 lds[kSmallLds];
@@ -1033,7 +1108,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const SmallA
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int mp = MB * 32, pm = mp + 8;
   const int np = A.np, pn = np + 8, nb = np / 32;
-  _Float16 *x = lds, *xt = x + mp * pn, *a = xt + np * pm, *b = a + mp * pm;
+  _Float16 *x = lds, *xt = x + mp * pn, *a = xt + np * pm, *b = a + short_size(mp);
   // the input's and output's orientation
   const int rp = A.tall ? np : mp, cp = A.tall ? mp : np;
   _Float16 *same = A.tall ? xt : x, *turned = A.tall ? x : xt;
@@ -1062,16 +1137,15 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const SmallA
         f1.add(acc);
       }
       if (nb & 1) f0.add(acc);
-      block_each(at.i, at.j, lane, acc,
-                 [&](int r, int c, const f32x4 &v) { at.put(a, r, c, v * kBack1); });
+      at.put(a, lane, acc, [](int, int, const f32x4 &v) { return v * kBack1; });
     }
     __syncthreads();
     short_poly<MB>(A.coeffs + 3 * s, a, b, wave, lane);
-    Block acc[kSmallBlocks] = {};
+    Block acc[kSmallBlocks];
 #pragma unroll
     for (int u = 0; u < kSmallBlocks; ++u) {
       const int t = wave + u * kSmallWaves;
-      if (t < MB * nb) block_mul<MB>(b, xt, t % MB, t / MB, lane, acc[u]);
+      if (t < MB * nb) times<MB>(b, xt, t % MB, t / MB, lane, acc[u]);
     }
     __syncthreads();  // X^T has been read
     if (s + 1 < A.steps)
@@ -1087,8 +1161,8 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const SmallA
 // updates of X only A is needed of all strips together: each leaves its part of
 // X X^T, one launch adds them, and the next update's workgroups all work out
 // the polynomials in A again, two steps of them where the coefficients allow
-// it, and apply them to their strip.  64 x 13824: 8 launches, 33 us, in place of
-// 19, 105 us; 128 x 4000 50 and 101 us.  What is left is launches and the latency
+// it, and apply them to their strip.  64 x 13824: 8 launches, 37 us, in place of
+// 19, 105 us.  What is left is launches and the latency
 // of LDS: at 128 rows a product of 128^3 takes 1.5 us, of which one CU's matrix
 // cores work 0.2.
 constexpr int kStripCols = 128, kStripRows = 128;
@@ -1101,7 +1175,7 @@ struct StripArgs {
   double eps;
   _Float16 *xt;   // [batch][strips * kStripCols][mp]
   float *parts;   // [batch][strips][mp][mp] of X X^T, times 2^22
-  _Float16 *a;    // [batch][mp][mp]
+  _Float16 *a;    // [batch][short_size(mp)], as it lies in LDS
   int32_t blocks, rows, cols, tall, strips, pair;
   float k[6];     // this update's coefficients
 };
@@ -1152,9 +1226,10 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_strip_in_kernel(const Str
 
 // A from the strips' parts, in their order within each of 64 interleaved
 // groups, the groups then in order.
-__global__ void __launch_bounds__(1024) ortho_strip_sum_kernel(const StripArgs A, int square) {
+__global__ void __launch_bounds__(1024) ortho_strip_sum_kernel(const StripArgs A, int mp) {
   __shared__ float lds[64][68];
-  const int64_t b = blockIdx.y, at = int64_t(blockIdx.x) * 64;
+  const int64_t b = blockIdx.y, square = mp * mp;
+  const int at = blockIdx.x * 64;
   const float *p = A.parts + b * A.strips * square + at + threadIdx.x * 4;
   f32x4 s = {};
 #pragma unroll 4
@@ -1167,12 +1242,16 @@ __global__ void __launch_bounds__(1024) ortho_strip_sum_kernel(const StripArgs A
   float sum = 0.0f;
 #pragma unroll
   for (int k = 0; k < 64; ++k) sum += lds[k][t];
-  A.a[b * square + at + t] = _Float16(sum * kBack1);
+  const int r = (at + t) / mp, c = (at + t) - r * mp;
+  _Float16 *to = A.a + b * short_size(mp);
+  const _Float16 h = _Float16(sum * kBack1);
+  to[r * (mp + 8) + c] = h;
+  if (r == c) reinterpret_cast<float *>(to + mp * (mp + 8))[r] = sum * kBack1 - float(h);
 }
 
 template <int MB, bool LAST>
 __global__ void __launch_bounds__(kSmallThreads) ortho_strip_step_kernel(const StripArgs A) {
-  constexpr int mp = MB * 32, pm = mp + 8, W = kStripCols, square = mp * pm;
+  constexpr int mp = MB * 32, pm = mp + 8, W = kStripCols, square = short_size(mp);
   // X lies over B and C, which are done with by then, where LDS is full
   constexpr int xat = MB == 4 ? square : 3 * square;
   static_assert(MB < 4 || mp * (W + 8) <= 2 * square, "X in B and C's place");
@@ -1181,13 +1260,12 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_strip_step_kernel(const S
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   _Float16 *xt = lds, *a = xt + W * pm, *b = a + square, *c = b + square, *x = a + xat;
   const int64_t strip = int64_t(blockIdx.y) * A.strips + blockIdx.x;
-  const auto bring = [&](const _Float16 *from, int n, _Float16 *to) {  // rows of mp
-    for (int p = threadIdx.x; p < n * mp / 8; p += kSmallThreads)
-      *reinterpret_cast<half8 *>(to + p / (mp / 8) * pm + p % (mp / 8) * 8) =
-          *reinterpret_cast<const half8 *>(from + p * 8);
-  };
-  bring(A.a + int64_t(blockIdx.y) * mp * mp, mp, a);
-  bring(A.xt + strip * (W * mp), W, xt);
+  for (int p = threadIdx.x; p < square / 8; p += kSmallThreads)
+    reinterpret_cast<half8 *>(a)[p] =
+        reinterpret_cast<const half8 *>(A.a + int64_t(blockIdx.y) * square)[p];
+  for (int p = threadIdx.x; p < W * mp / 8; p += kSmallThreads)
+    *reinterpret_cast<half8 *>(xt + p / (mp / 8) * pm + p % (mp / 8) * 8) =
+        *reinterpret_cast<const half8 *>(A.xt + strip * (W * mp) + p * 8);
   __syncthreads();
   short_poly<MB>(A.k, a, b, wave, lane);
   const _Float16 *by = b;
@@ -1201,11 +1279,11 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_strip_step_kernel(const S
   }
   constexpr int blocks = MB * W / 32;
   static_assert(blocks <= kSmallWaves * kSmallBlocks, "a wave's blocks");
-  Block acc[kSmallBlocks] = {};
+  Block acc[kSmallBlocks];
 #pragma unroll
   for (int u = 0; u < kSmallBlocks; ++u) {
     const int t = wave + u * kSmallWaves;
-    if (t < blocks) block_mul<MB>(by, xt, t % MB, t / MB, lane, acc[u]);
+    if (t < blocks) times<MB>(by, xt, t % MB, t / MB, lane, acc[u]);
   }
   __syncthreads();  // X^T, B and C have been read
   short_put<MB, LAST>(acc, blocks, LAST && A.tall ? nullptr : x, W + 8,
@@ -1382,7 +1460,7 @@ Plan plan_of(const zs_ortho_desc &d) {
     p.np = int64_t(p.strips) * kStripCols;
     p.xt = take(d.batch * p.np * p.mp * 2);
     p.parts = take(d.batch * p.strips * p.mp * p.mp * 4);
-    p.a = take(d.batch * p.mp * p.mp * 2);
+    p.a = take(d.batch * short_size(int(p.mp)) * 2);
     p.bytes = at;
     return p;
   }
@@ -1479,7 +1557,7 @@ int strips_of(StripArgs &A, const zs_ortho_desc &d, hipStream_t st) {
       A.k[i + 3] = A.pair ? k2[i] : 0.0f;
     }
     hipLaunchKernelGGL(ortho_strip_sum_kernel, dim3(MB * MB * 16, unsigned(d.batch)), dim3(16, 64),
-                       0, st, A, MB * MB * 1024);
+                       0, st, A, MB * 32);
     if (s + A.pair + 1 < d.steps)
       hipLaunchKernelGGL((ortho_strip_step_kernel<MB, false>), grid, block, 0, st, A);
     else
