@@ -33,8 +33,8 @@
 // symmetric) in place of 6 m^2 n + 2 m^3.  Rounding leaves A with eigenvalues a
 // little below 0 and B A B multiplies those by a^2, so it is done once and then
 // A is made anew from X: in two steps the result is as far off as before
-// (Gaussian 512 x 1382: 1.26e-3 for 1.19e-3; ill-conditioned and rank-8 ones:
-// less than before), in three it diverges where A is singular.
+// (Gaussian 512 x 1382, without the rests of the diagonals: 1.26e-3 for 1.19e-3;
+// ill-conditioned and rank-8 ones: less than before), in three it diverges where A is singular.
 //
 // What bounds the large ones is the card's power: with the operands' bits at
 // random the clock falls to 1.9-2.1 GHz at 60% of the matrix cores' cycles, and
@@ -397,6 +397,10 @@ struct MulArgs {
   int32_t *arrived;            // [cut] workgroups done with a cut tile; 0 between launches
   _Float16 *c, *ct;            // C (row length cols) and C^T (row length rows)
   int64_t stride_c;
+  // The rests of P's, Q's and C's diagonals, [batch][rows], where they are no X;
+  // or null
+  const float *rest_p, *rest_q;
+  float *rest_c;
   float a, b, cc;              // kPoly's coefficients
   int32_t past;                // C^T goes past the caches
   // kLast
@@ -404,6 +408,23 @@ struct MulArgs {
   int64_t out_rows, out_cols, ld_o, stride_o;
   int32_t tall, wide;          // wide: 16 bytes of a row at a time
 };
+
+// What rounding to binary16 took off an element v of a diagonal, relative to
+// what is left.  The diagonals of A and B are much the largest elements there
+// and much alike, so their rounding scales whole rows of X; where the singular
+// values lie together on a steep part of the polynomial, the next steps make
+// that larger: the result of a random 32 x 13824 came out 2.3 times as far off as
+// the rounding of a right one to bf16, 430 x 13824 1.7, 256 x 256 1.26 times.  So
+// it is kept.  Rows of B X are multiplied by 1 + rest, which is right for the
+// diagonal's share and for the others no more than their own rounding; in
+// products of A and B it is made good on the diagonal alone.  With it those are
+// 1.03, 1.03 and 1.17 times; it costs 0.5% at 5120 x 13824, 3% at 300 x 700.
+// Below binary16's normal range nothing is kept, so that the rest is never more
+// than 2^-11.
+__device__ __forceinline__ float rest_in(float v) {
+  const float h = float(_Float16(v));
+  return __builtin_fabsf(h) < 0x1p-14f ? 0.0f : (v - h) * __builtin_amdgcn_rcpf(h);
+}
 
 #define ZS_LDS(p) ((__attribute__((address_space(3))) void *)(p))
 
@@ -649,8 +670,14 @@ __global__ void __launch_bounds__(WR *WC * 64) ortho_mul_kernel(const MulArgs A)
 #pragma unroll
       for (int i = 0; i < N; ++i) acc[i / TN][i % TN] = f32x4{};
       for (int w = w0; w <= w1; ++w) {
+        // all under way at once: one after the other A of 1000 x 13000 takes 48 us
+        // for 41
+        f32x4 got[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i / TN][i % TN] += *part(w, w == w0, i);
+        for (int i = 0; i < N; ++i) got[i] = *part(w, w == w0, i);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i / TN][i % TN] += got[i];
       }
     }
 
@@ -661,14 +688,17 @@ __global__ void __launch_bounds__(WR *WC * 64) ortho_mul_kernel(const MulArgs A)
       if constexpr (KIND == kLast) return Bf16::store(v);
       else return F16::store(v);
     };
-    u32x2 out[TM][TN];  // a lane's four rows in 16 bits
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < TM; ++i) {
+      const int r = row0 + br + i * 16;
+      f32x4 row = f32x4{} + kBack;  // of B X
+      if (!SYM && r < A.rows)
+        row += kBack * *reinterpret_cast<const f32x4 *>(A.rest_p + mat * A.rows + r);
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
         if constexpr (KIND == kPoly) {
           // A is symmetric: column c's four rows are four neighbours of row c
-          const int r = row0 + br + i * 16, c = col0 + bc + j * 16;
+          const int c = col0 + bc + j * 16;
           half4 s = {};
           if (r < A.rows && c < A.cols)
             s = *reinterpret_cast<const half4 *>(A.p + mat * A.stride_p + int64_t(c) * A.k + r);
@@ -679,12 +709,50 @@ __global__ void __launch_bounds__(WR *WC * 64) ortho_mul_kernel(const MulArgs A)
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] *= kBack;
+          for (int e = 0; e < 4; ++e) acc[i][j][e] *= row[e];
         }
+      }
+    }
+    // On the diagonal, of which a lane in four holds an element of a 16 x 16
+    // block: what the rests add, and the rest of this one.  All is read first.
+    const int wr0 = row0 + wr * TM * 16, wc0 = col0 + wc * TN * 16;
+    if (SYM && wr0 < wc0 + TN * 16 && wc0 < wr0 + TM * 16) {
+      const int e0 = (lane & 15) - (lane >> 4) * 4;
+      float more[TM] = {};
+      if (A.rest_p) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          const int d = wr0 + i * 16 + (lane & 15), c = d < A.cols ? d : 0;
+          const int64_t at_c = int64_t(c) * A.k + c, rest = mat * A.rows + c;
+          const float p = float(A.p[mat * A.stride_p + at_c]), dp = A.rest_p[rest];
+          const float q = float(A.q[mat * A.stride_q + at_c]), dq = A.rest_q[rest];
+          more[i] = (dp + dq) * p * q * kBack;
+          if (KIND == kPoly) more[i] = A.cc * more[i] + A.b * dp * p;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const int c = wc0 + j * 16 + (lane & 15);
+          if (wr0 + i * 16 != wc0 + j * 16 || unsigned(e0) >= 4 || c >= A.cols) continue;
+          float v = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[i][j][e] += e0 == e ? more[i] : 0.0f;
+            v = e0 == e ? acc[i][j][e] : v;
+          }
+          A.rest_c[mat * A.rows + c] = rest_in(v);
+        }
+    }
+    u32x2 out[TM][TN];  // a lane's four rows in 16 bits
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           out[i][j][e] = narrow(acc[i][j][2 * e]) | narrow(acc[i][j][2 * e + 1]) << 16;
-      }
 
     uint16_t *epi = reinterpret_cast<uint16_t *>(lds);
     // the tile through LDS, as C (turned = false) or as its transpose
@@ -833,13 +901,8 @@ __device__ __forceinline__ half4 narrow4(const f32x4 &v) {
   return h;
 }
 
-// A symmetric matrix of mp rows in LDS is followed by `rest`, what rounding took
-// off its diagonal.  The diagonals of A and B are much the largest elements
-// there and much alike, so their rounding scales whole rows of X and, where the
-// singular values lie together on a steep part of the polynomial, the next steps
-// make that larger: without the rests the result of a random 32 x 13824 is 2.3
-// times as far off as the rounding of a right one to bf16, with them 1.03; 96 x
-// 128 takes 22.9 us, without them 21.9.
+// A symmetric matrix of mp rows in LDS is followed by the rests of its diagonal
+// (96 x 128: 22.3 us, without them 21.8; 64 x 13824 36 and 33).
 constexpr int short_size(int mp) { return mp * (mp + 8) + 2 * mp; }
 
 template <int MB>
@@ -851,33 +914,22 @@ __device__ __forceinline__ const float *rest_of(const _Float16 *M) {
   return rest_of<MB>(const_cast<_Float16 *>(M));
 }
 
-// v + f * x
-__device__ __forceinline__ f32x4 add4(f32x4 v, const f32x4 &f, const half4 &x) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f[e], float(x[e]), v[e]);
-  return v;
-}
-
-// What the rests add to a block of a product, where its sums start: added at
-// their end, behind the matrix instructions, 96 x 128 takes 1.5 us more.  Rows
-// r..r+3 of column c of the second factor by the first's rest (`rows`), and of
-// the first by the second's (`cols`).
+// What the rests add to a block of a symmetric product, where its sums start: to
+// the diagonal's elements, of which a lane in four holds one in each of two parts.
 template <int MB>
-__device__ __forceinline__ void block_start(const float *rows, const _Float16 *Q, const float *cols,
-                                            const _Float16 *P, int i, int j, int lane, Block &acc) {
-  constexpr int pm = MB * 32 + 8;
+__device__ __forceinline__ void block_start(const _Float16 *P, const _Float16 *Q, int i, int j,
+                                            int lane, Block &acc) {
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = i * 32 + e * 16 + (lane >> 4) * 4;
-    const f32x4 d = *reinterpret_cast<const f32x4 *>(rows + r);
+  for (int p = 0; p < 4; ++p) acc[p / 2][p % 2] = f32x4{};
+  if (i != j) return;
+  const float *dp = rest_of<MB>(P), *dq = rest_of<MB>(Q);
+  const int at = (lane & 15) - (lane >> 4) * 4;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = j * 32 + h * 16 + (lane & 15);
-      acc[e][h] = add4(f32x4{}, d, *reinterpret_cast<const half4 *>(Q + c * pm + r));
-      if (cols)
-        acc[e][h] = add4(acc[e][h], f32x4{} + cols[c],
-                         *reinterpret_cast<const half4 *>(P + c * pm + r));
-    }
+  for (int t = 0; t < 2; ++t) {
+    const int c = i * 32 + t * 16 + (lane & 15), to = c * (MB * 32 + 8) + c;
+    const float more = (dp[c] + dq[c]) * float(P[to]) * float(Q[to]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[t][t][e] = at == e ? more : 0.0f;
   }
 }
 
@@ -912,15 +964,15 @@ struct Lower {
         for (int e = 0; e < 4; ++e) C[(r + e) * pm + c] = h[e];
       }
       if (p / 2 == p % 2) {
-        rest[p / 2] = v[0] - float(h[0]);
+        rest[p / 2] = v[0];
 #pragma unroll
-        for (int e = 1; e < 4; ++e) rest[p / 2] = at == e ? v[e] - float(h[e]) : rest[p / 2];
+        for (int e = 1; e < 4; ++e) rest[p / 2] = at == e ? v[e] : rest[p / 2];
       }
     }
     if (i == j && at >= 0 && at < 4) {
       float *to = rest_of<MB>(C) + i * 32 + (lane & 15);
-      to[0] = rest[0];
-      to[16] = rest[1];
+      to[0] = rest_in(rest[0]);
+      to[16] = rest_in(rest[1]);
     }
   }
 };
@@ -932,7 +984,7 @@ __device__ __forceinline__ void short_mul(const _Float16 *P, const _Float16 *Q, 
   if (wave < Lower<MB>::kBlocks) {
     const Lower<MB> at(wave);
     Block acc;
-    block_start<MB>(rest_of<MB>(P), Q, rest_of<MB>(Q), P, at.i, at.j, lane, acc);
+    block_start<MB>(P, Q, at.i, at.j, lane, acc);
     block_mul<MB>(P, Q, at.i, at.j, lane, acc);
     at.put(C, lane, acc, [](int, int, const f32x4 &v) { return v * kBack1; });
   }
@@ -948,13 +1000,15 @@ __device__ __forceinline__ void short_poly(const float *k, const _Float16 *A, _F
     const Lower<MB> at(wave);
     const float *d = rest_of<MB>(A);
     Block acc;
-    block_start<MB>(d, A, d, A, at.i, at.j, lane, acc);
+    block_start<MB>(A, A, at.i, at.j, lane, acc);
     block_mul<MB>(A, A, at.i, at.j, lane, acc);
     at.put(B, lane, acc, [&](int r, int c, f32x4 v) {
-      v = add4(v * (k[2] * kBack1), f32x4{} + k[1],
-               *reinterpret_cast<const half4 *>(A + c * pm + r));
+      const half4 old = *reinterpret_cast<const half4 *>(A + c * pm + r);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = __builtin_fmaf(k[1], float(old[e]), (k[2] * kBack1) * v[e]);
       if (at.i == at.j) {
-        const float more = k[0] * kScale + k[1] * d[c];
+        const float more = k[0] * kScale + k[1] * d[c] * float(A[c * pm + c]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] += r + e == c ? more : 0.0f;
       }
@@ -968,8 +1022,16 @@ __device__ __forceinline__ void short_poly(const float *k, const _Float16 *A, _F
 template <int MB>
 __device__ __forceinline__ void times(const _Float16 *B, const _Float16 *xt, int i, int j, int lane,
                                       Block &acc) {
-  block_start<MB>(rest_of<MB>(B), xt, nullptr, nullptr, i, j, lane, acc);
+  const float *rest = rest_of<MB>(B) + i * 32 + (lane >> 4) * 4;
+  f32x4 d[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) d[e] = *reinterpret_cast<const f32x4 *>(rest + e * 16) + 1.0f;
+  acc[0][0] = acc[0][1] = acc[1][0] = acc[1][1] = f32x4{};
   block_mul<MB>(B, xt, i, j, lane, acc);
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+#pragma unroll
+    for (int n = 0; n < 4; ++n) acc[p / 2][p % 2][n] *= d[p / 2][n];
 }
 
 // A matrix's (or a strip's) rp x cp elements in LDS, in the caller's
@@ -1100,7 +1162,7 @@ int64_t small_lds(int64_t mp, int64_t np) {
 }
 
 // A matrix whose X, X^T, A and B fit in the LDS of one CU: one workgroup, one
-// launch (96 x 128: 17 launches take 67 us, this 23 us; 64 x 512 68 and 34 us).
+// launch (96 x 128: 17 launches take 67 us, this 22 us; 64 x 512 68 and 32 us).
 template <class TG, int MB>
 __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const SmallArgs A) {
   __shared__ __align__(16) _Float16 lds[kSmallLds];
@@ -1161,7 +1223,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const SmallA
 // updates of X only A is needed of all strips together: each leaves its part of
 // X X^T, one launch adds them, and the next update's workgroups all work out
 // the polynomials in A again, two steps of them where the coefficients allow
-// it, and apply them to their strip.  64 x 13824: 8 launches, 37 us, in place of
+// it, and apply them to their strip.  64 x 13824: 8 launches, 36 us, in place of
 // 19, 105 us.  What is left is launches and the latency
 // of LDS: at 128 rows a product of 128^3 takes 1.5 us, of which one CU's matrix
 // cores work 0.2.
@@ -1244,9 +1306,8 @@ __global__ void __launch_bounds__(1024) ortho_strip_sum_kernel(const StripArgs A
   for (int k = 0; k < 64; ++k) sum += lds[k][t];
   const int r = (at + t) / mp, c = (at + t) - r * mp;
   _Float16 *to = A.a + b * short_size(mp);
-  const _Float16 h = _Float16(sum * kBack1);
-  to[r * (mp + 8) + c] = h;
-  if (r == c) reinterpret_cast<float *>(to + mp * (mp + 8))[r] = sum * kBack1 - float(h);
+  to[r * (mp + 8) + c] = _Float16(sum * kBack1);
+  if (r == c) reinterpret_cast<float *>(to + mp * (mp + 8))[r] = rest_in(sum * kBack1);
 }
 
 template <int MB, bool LAST>
@@ -1430,7 +1491,7 @@ struct Plan {
   int strips;   // of kStripCols columns of X, a workgroup each, padded to 32 rows; or 0
   bool paired;  // two steps at a time where the coefficients allow it
   bool tall;
-  int64_t partials, arrived, parts, x, xt, y, yt, a, b, c, bytes;  // offsets into the workspace
+  int64_t partials, arrived, parts, x, xt, y, yt, a, b, c, rests, bytes;  // offsets into the workspace
 };
 
 Plan plan_of(const zs_ortho_desc &d) {
@@ -1484,6 +1545,7 @@ Plan plan_of(const zs_ortho_desc &d) {
   p.a = take(d.batch * p.mp * p.mp * 2);
   p.b = take(d.batch * p.mp * p.mp * 2);
   p.c = p.paired ? take(d.batch * p.mp * p.mp * 2) : 0;
+  p.rests = take(3 * d.batch * p.mp * 4);
   p.bytes = at;
   return p;
 }
@@ -1743,10 +1805,18 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
   A.tall = p.tall;
   A.wide = aligned(o, 16) && d->cols % 8 == 0 && ld_out % 8 == 0 && A.stride_o % 8 == 0;
   const int64_t square = p.mp * p.mp, whole = p.mp * p.np;
+  _Float16 *a = half(p.a), *b = half(p.b), *c = half(p.c);
+  const auto rest_of = [&](const _Float16 *of) {
+    return reinterpret_cast<float *>(ws + p.rests) +
+           (of == a ? 0 : of == b ? 1 : 2) * d->batch * p.mp;
+  };
   // C = P Q^T of m x m matrices that commute, and poly's combination
   const auto small = [&](auto kind, const _Float16 *pp, const _Float16 *qq, _Float16 *cc) {
     A.p = pp;
     A.q = qq;
+    A.rest_p = rest_of(pp);
+    A.rest_q = rest_of(qq);
+    A.rest_c = rest_of(cc);
     A.stride_p = A.stride_q = A.stride_c = square;
     A.c = cc;
     return multiply<kind.value>(A, p.poly, p.mp, p.mp, p.mp, st);
@@ -1761,11 +1831,12 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
   // reads, should be, and X^T not take its place (13824 x 5120: 4.16 -> 4.09 ms;
   // 5120 x 5120, which fits: the same either way, with X past them too +4%).
   A.past = 4 * d->batch * whole > kCacheBytes;
-  _Float16 *a = half(p.a), *b = half(p.b), *c = half(p.c);
   for (int s = 0; s < d->steps && !rc;) {
     const float *k = d->coeffs ? d->coeffs + 3 * s : kCoeffs;
     const float *k2 = d->coeffs ? k + 3 : kCoeffs;
     A.p = A.q = x;
+    A.rest_p = A.rest_q = nullptr;
+    A.rest_c = rest_of(a);
     A.stride_p = A.stride_q = whole;
     A.c = a;
     A.stride_c = square;
@@ -1782,6 +1853,7 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
       ++s;
     }
     A.p = by;
+    A.rest_p = rest_of(by);
     A.stride_p = square;
     A.q = xt;
     A.stride_q = whole;

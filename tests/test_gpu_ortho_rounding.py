@@ -49,3 +49,31 @@ def test_short_equal(rows, cols):
     gen = torch.Generator(device="cuda").manual_seed(4)
     q = torch.linalg.qr(torch.randn(cols, rows, device="cuda", generator=gen))[0]
     assert _off(q.T.contiguous()) < BOUND
+
+
+# products of tiles, cut and not, one step at a time and two
+@pytest.mark.parametrize("rows,cols", [(136, 136), (256, 300), (400, 13824), (13824, 430),
+                                       (480, 9000), (1000, 1000)])
+def test_long(rows, cols):
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    assert _off(torch.randn(rows, cols, device="cuda", generator=gen)) < BOUND
+
+
+@pytest.mark.parametrize("rows,cols", [(150, 700), (300, 400), (1024, 1500)])
+def test_long_equal(rows, cols):
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    q = torch.linalg.qr(torch.randn(cols, rows, device="cuda", generator=gen))[0]
+    assert _off(q.T.contiguous()) < BOUND
+
+
+@pytest.mark.parametrize("rows,cols", [(40, 320), (48, 5000), (200, 210), (430, 5000)])
+def test_batch(rows, cols):
+    """Each matrix has the rests of its own diagonals."""
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    g = torch.randn(3, rows, cols, device="cuda", generator=gen)
+    g[1] = torch.linalg.qr(g[1].T)[0].T
+    o = torch.empty_like(g, dtype=torch.bfloat16)
+    Z.ZeroOrtho(batch=3, rows=rows, cols=cols, dtype=g.dtype)(g, o)
+    for i in range(3):
+        ref = R.ortho_ref(g[i], [R.COEFFS] * 5, 1e-7)
+        assert float((o[i].double() - ref).norm() / ref.norm()) < BOUND
