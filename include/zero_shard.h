@@ -465,7 +465,8 @@ int64_t zero_shard_ortho_workspace(const zs_ortho_desc *d);
  *   A = X X^T;  X = a X + (b A + c A A) X
  * (X^T X and products from the right when rows > cols); o = bf16(X).
  * Products are summed in binary32; X, A and B = a I + b A + c A A are rounded
- * to binary16 times 2^-11 between products.  Of a matrix much longer than wide
+ * to binary16 times 2^-11 between products, and what that takes off A's and B's
+ * diagonals is kept in binary32 and made good.  Of a matrix much longer than wide
  * two steps whose a have a product in (0, 16] are taken together: the second A
  * is B A B and X becomes (B' B) X, the same products in another order; B A and
  * B' B are rounded likewise.  The entries of all of them must stay below 32
