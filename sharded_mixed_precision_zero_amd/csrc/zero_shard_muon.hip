@@ -435,7 +435,7 @@ __device__ __forceinline__ float rest_in(float v) {
   asm volatile("" ::: "memory");
 }
 
-// At most N of this wave's loads outstanding.
+// At most N of this wave's loads and stores outstanding.
 template <int N>
 __device__ __forceinline__ void wait_loads() {
   static_assert(N < 64, "vmcnt has 6 bits");
@@ -654,6 +654,10 @@ __global__ void __launch_bounds__(WR *WC * 64) ortho_mul_kernel(const MulArgs A)
       };
 #pragma unroll
       for (int i = 0; i < N; ++i) *part(at, k0 == 0, i) = acc[i / TN][i % TN];
+      // Each wave waits for its own stores: the barrier waits for LDS only and the
+      // release below for the stores of the first wave.  They are in this XCD's L2
+      // then, which the release writes back.
+      wait_loads<0>();
       const int w0 = uniform(((tile * nk + 1u) * groups - 1) / steps);
       const int w1 = uniform(((tile + 1u) * nk * groups - 1) / steps);
       int *flag = reinterpret_cast<int *>(lds);
