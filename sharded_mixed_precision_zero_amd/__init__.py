@@ -627,10 +627,11 @@ class ZeroLayerNorm:
     saved statistics and the workspace of the gradient reduction.
 
     All tensors are on the current device; x, residual, sum_out, y, dy, dsum
-    and dx are (rows, cols) of ``dtype`` with column stride 1, the parameters
-    and their gradients contiguous (cols,) of ``param_dtype`` (default:
-    dtype).  ``stream`` is a torch stream (default: the current one at
-    construction)."""
+    and dx are (rows, cols) of ``dtype`` with column stride 1 and rows that do
+    not overlap (an expanded tensor, such as autograd's gradient of ``y.sum(0)``,
+    needs ``.contiguous()`` first), the parameters and their gradients contiguous
+    (cols,) of ``param_dtype`` (default: dtype).  ``stream`` is a torch stream
+    (default: the current one at construction)."""
 
     def __init__(self, *, rows: int, cols: int, dtype=torch.bfloat16, param_dtype=None,
                  eps: float = 1e-5, stream=None):
@@ -648,15 +649,18 @@ class ZeroLayerNorm:
             self.workspace = torch.empty(size, device="cuda", dtype=torch.uint8)
 
     def _row(self, t, what: str) -> int:
-        """Row stride of a (rows, cols) tensor; 0 for None."""
+        """Row stride of a (rows, cols) tensor; 0 for None and a single row.
+        Rows that share memory (expanded tensors have row stride 0, which the
+        descriptor takes for cols) are refused."""
         if t is None:
             return 0
+        rows, cols = self.shape
         if t.shape != self.shape or t.dtype is not self.dtype or not t.is_cuda:
             raise ZeroShardError(ZS_EINVAL, what)
         ld, unit = t.stride()
-        if unit != 1 and self.shape[1] != 1:
+        if (unit != 1 and cols != 1) or (rows > 1 and ld < cols):
             raise ZeroShardError(ZS_EINVAL, what)
-        return ld if self.shape[0] > 1 else 0
+        return ld if rows > 1 else 0
 
     def _param(self, t, what: str) -> None:
         if (t.shape != self.shape[1:] or t.dtype is not self.param_dtype or not t.is_cuda

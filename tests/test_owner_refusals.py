@@ -1,0 +1,84 @@
+"""What the owner objects of layer norm and Muon refuse before anything is
+queued.  On the CPU stand-ins take the place of device tensors, whose memory the
+checks do not touch."""
+
+from __future__ import annotations
+
+import pytest
+import torch
+
+import sharded_mixed_precision_zero_amd as Z
+
+BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+class OnDevice(torch.Tensor):
+    """A CPU tensor that says it is on the GPU."""
+
+    @property
+    def is_cuda(self):
+        return True
+
+
+def on_device(t):
+    return t.as_subclass(OnDevice)
+
+
+def _norm(rows, cols, dtype=BF):
+    ln = object.__new__(Z.ZeroLayerNorm)
+    ln.shape, ln.dtype = (rows, cols), dtype
+    return ln
+
+
+EXPANDED_ROWS = [lambda r, c: torch.zeros(c, dtype=BF).expand(r, c),
+                 lambda r, c: torch.zeros((), dtype=BF).expand(r, c),
+                 lambda r, c: torch.zeros(r * c, dtype=BF).as_strided((r, c), (c // 2, 1))]
+
+
+@pytest.mark.parametrize("make", EXPANDED_ROWS)
+@pytest.mark.parametrize("rows,cols", [(2, 2), (8, 5120)])
+def test_layernorm_refuses_rows_that_share_memory(make, rows, cols):
+    with pytest.raises(Z.ZeroShardError):
+        _norm(rows, cols)._row(on_device(make(rows, cols)), "dy")
+
+
+def test_layernorm_refuses_a_single_column_expanded():
+    with pytest.raises(Z.ZeroShardError):
+        _norm(4, 1)._row(on_device(torch.zeros(1, 1, dtype=BF).expand(4, 1)), "dy")
+
+
+def test_layernorm_takes_single_rows_and_padded_ones():
+    row = _norm(1, 64)._row(on_device(torch.zeros(64, dtype=BF).expand(1, 64)), "x")
+    assert row == 0  # one row: whatever its stride
+    wide = on_device(torch.zeros(4, 80, dtype=BF)[:, :64])
+    assert _norm(4, 64)._row(wide, "x") == 80
+    assert _norm(4, 64)._row(on_device(torch.zeros(4, 64, dtype=BF)), "x") == 64
+    column = on_device(torch.zeros(4, 7, dtype=BF)[:, 3:4])
+    assert _norm(4, 1)._row(column, "x") == 7
+    assert _norm(4, 64)._row(None, "x") == 0
+
+
+@pytest.mark.gpu
+def test_layernorm_refuses_expanded_operands():
+    """Every operand, before anything is queued."""
+    ln = Z.ZeroLayerNorm(rows=4, cols=64, dtype=BF)
+    new = lambda: torch.full((4, 64), 3.0, device="cuda", dtype=BF)
+    bad = torch.zeros(64, device="cuda", dtype=BF).expand(4, 64)
+    out = new()
+    for kw in (dict(x=bad), dict(y=bad), dict(residual=bad, sum_out=new()),
+               dict(residual=new(), sum_out=bad)):
+        with pytest.raises(Z.ZeroShardError):
+            ln.forward(**{"x": new(), "y": out, **kw})
+    for kw in (dict(dy=bad), dict(x=bad), dict(dx=bad), dict(dsum=bad)):
+        with pytest.raises(Z.ZeroShardError):
+            ln.backward(**{"dy": new(), "x": new(), "dx": out, **kw})
+    torch.cuda.synchronize()
+    assert (out == 3.0).all()
+    # what autograd hands back for y.sum(0) is such a tensor
+    y = new().requires_grad_()
+    grad, = torch.autograd.grad(y.sum(0), y, torch.ones(64, device="cuda", dtype=BF))
+    assert grad.stride() == (0, 1)
+    with pytest.raises(Z.ZeroShardError):
+        ln.backward(grad, new(), out)
+    ln.forward(new(), out)
+    ln.backward(grad.contiguous(), new(), out)
