@@ -706,7 +706,8 @@ class ZeroLayerNorm:
 class ZeroOrtho:
     """Newton-Schulz orthogonalisation of (batch, rows, cols) tensors of
     ``dtype`` into bf16 ones, with its workspace; a 2-D tensor is a batch of
-    one.  Column stride 1; ``stream`` as for ZeroLayerNorm."""
+    one.  Column stride 1, no expanded rows or matrices; ``stream`` as for
+    ZeroLayerNorm."""
 
     def __init__(self, *, batch: int = 1, rows: int, cols: int, dtype=torch.bfloat16,
                  steps: int = 5, coeffs=None, eps: float = 1e-7, stream=None):
@@ -720,11 +721,15 @@ class ZeroOrtho:
             self.workspace = torch.empty(size, device="cuda", dtype=torch.uint8)
 
     def _strides(self, t, dtype, what: str) -> tuple[int, int]:
+        """Row and matrix strides.  Expanded tensors are refused: their strides of
+        0 are the dense ones to the descriptor."""
         b, r, c = self.shape
         _require((t.shape == self.shape or (b == 1 and t.shape == self.shape[1:]))
                  and t.dtype == dtype and t.is_cuda and (t.stride(-1) == 1 or c == 1), what)
         ld = t.stride(-2) if r > 1 else c
-        return ld, t.stride(0) if b > 1 else r * ld
+        each = t.stride(0) if b > 1 else r * ld
+        _require(t.numel() == 0 or (ld > 0 and each > 0), what)
+        return ld, each
 
     def __call__(self, g, o) -> None:
         """o = the orthogonalised g."""

@@ -82,3 +82,55 @@ def test_layernorm_refuses_expanded_operands():
         ln.backward(grad, new(), out)
     ln.forward(new(), out)
     ln.backward(grad.contiguous(), new(), out)
+
+
+def _ortho(b, r, c):
+    orth = object.__new__(Z.ZeroOrtho)
+    orth.shape, orth.dtype = (b, r, c), F32
+    return orth
+
+
+@pytest.mark.parametrize("make", [
+    lambda: torch.zeros(8, 16).expand(4, 8, 16), lambda: torch.zeros(4, 1, 16).expand(4, 8, 16),
+    lambda: torch.zeros(16).expand(4, 8, 16)])
+def test_ortho_refuses_matrices_that_share_memory(make):
+    with pytest.raises(Z.ZeroShardError):
+        _ortho(4, 8, 16)._strides(on_device(make()), F32, "g")
+
+
+@pytest.mark.parametrize("b,r,c", [(3, 1, 9), (3, 5, 1), (1, 5, 9)])
+def test_ortho_refuses_expanded_rows_columns_and_batches(b, r, c):
+    t = torch.zeros(1, 1, c).expand(b, r, c)
+    with pytest.raises(Z.ZeroShardError):
+        _ortho(b, r, c)._strides(on_device(t), F32, "g")
+    if b == 1:
+        with pytest.raises(Z.ZeroShardError):
+            _ortho(b, r, c)._strides(on_device(t[0]), F32, "g")
+
+
+def test_ortho_takes_what_does_not_share_memory():
+    strides = lambda b, r, c, t: _ortho(b, r, c)._strides(on_device(t), F32, "g")
+    assert strides(4, 8, 16, torch.zeros(4, 9, 20)[:, :8, :16]) == (20, 180)
+    assert strides(4, 8, 16, torch.zeros(8, 4, 16).transpose(0, 1)) == (64, 16)  # between each other
+    assert strides(1, 8, 16, torch.zeros(1, 8, 16).expand(1, 8, 16)) == (16, 128)
+    assert strides(1, 1, 16, torch.zeros(16).expand(1, 16)) == (16, 16)
+    strides(4, 0, 16, torch.zeros(0, 16).expand(4, 0, 16))  # empty: nothing is read
+
+
+@pytest.mark.gpu
+def test_ortho_refuses_expanded_operands():
+    orth = Z.ZeroOrtho(batch=4, rows=8, cols=16, dtype=F32)
+    g = torch.randn(4, 8, 16, device="cuda")
+    o = torch.full((4, 8, 16), 3.0, device="cuda", dtype=BF)
+    for bad in (g[0].expand(4, 8, 16), g[:, :1].expand(4, 8, 16)):
+        with pytest.raises(Z.ZeroShardError):
+            orth(bad, o)
+        with pytest.raises(Z.ZeroShardError):
+            orth(g, bad.to(BF)[:1].expand(4, 8, 16))
+    torch.cuda.synchronize()
+    assert (o == 3.0).all()
+    between = torch.randn(8, 4, 16, device="cuda").transpose(0, 1)
+    orth(between, o)
+    again = torch.empty_like(o)
+    orth(between.contiguous(), again)
+    assert torch.equal(o, again)
