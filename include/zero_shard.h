@@ -379,7 +379,9 @@ typedef struct zs_layernorm_desc {
  *   y = (s - mean) rstd gamma + beta.
  * gamma and beta (cols elements) may each be NULL (1 and 0); mean and rstd
  * (fp32[rows]) may each be NULL when no backward pass follows.  A row that
- * holds an infinity or NaN gives NaN in that row only.  sum may be x's or
+ * holds an infinity or NaN gives NaN in that row only, as does one whose sum is
+ * beyond binary32; a constant row gives beta up to rounding (eps > 0; with eps =
+ * 0 it has no value).  sum may be x's or
  * residual's own buffer with the same row stride, y may be x's (or
  * residual's) unless sum is; otherwise outputs overlap nothing.
  * Errors: ZS_EINVAL, ZS_EALIGN (a pointer not aligned to its element),

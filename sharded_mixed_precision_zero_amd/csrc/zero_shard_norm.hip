@@ -102,12 +102,14 @@ struct Sums {
 // The statistics after the centred sweep: off = the sum of (s - mean), zero
 // but for the rounding of the mean, becomes what the mean is off by (a row
 // far from zero would show it in y); returns rstd.  An infinite row keeps
-// its mean.
+// its mean.  Of a constant row the variance is a difference of two equal values
+// up to rounding, which may fall below 0 by more than eps; a NaN stays one.
 __device__ __forceinline__ float finish(float sq, float &off, float inv, float eps, float &mean) {
   off *= inv;
   if (!(fabsf(off) < INFINITY)) off = 0.0f;
   mean += off;
-  return 1.0f / sqrtf((sq * inv - off * off) + eps);
+  const float var = sq * inv - off * off;
+  return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps);
 }
 
 struct FwdArgs {
