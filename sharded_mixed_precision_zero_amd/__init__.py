@@ -485,8 +485,11 @@ def muon_desc(*, n: int, n_d: int = 1, mu: float = 0.95, nesterov: bool = True,
 
 
 def zero_shard_muon_momentum(desc: zs_muon_desc, contrib, m_in, m_out, update) -> int:
-    return _lib.zero_shard_muon_momentum(ctypes.byref(desc), contrib_table(contrib), _ptr(m_in),
-                                         _ptr(m_out), _ptr(update))
+    table = contrib_table(contrib)
+    if table is not None and len(table) < desc.n_d:
+        return ZS_EINVAL
+    return _lib.zero_shard_muon_momentum(ctypes.byref(desc), table, _ptr(m_in), _ptr(m_out),
+                                         _ptr(update))
 
 
 def zero_shard_muon_apply(desc: zs_muon_desc, o, lr: float, scale: float, master_in, master_out,
@@ -739,24 +742,27 @@ class ZeroOrtho:
         _check(zero_shard_ortho(d, g, o, self.workspace), "zero_shard_ortho")
 
 
+_BF16_LIKE = (torch.bfloat16, torch.int16, torch.uint16)  # bf16 or its patterns
+
+
 class ZeroMuon:
     """One rank's Muon step over ``batch`` matrices of rows x cols that lie one
     after another in caller-owned torch tensors.
 
-    master, momentum: float32[n]; param_out: bf16 (or 16-bit) [n], n = batch *
-    rows * cols, 16-byte aligned.  ``update_dtype``: of the momentum's update
-    matrix (bf16 or float32).  ``scale``: the update's scale (default
-    0.2 sqrt(max(rows, cols)), which matches an Adam update's size)."""
+    master, momentum: float32[n]; param_out: bf16[n] (or its patterns as int16
+    or uint16), n = batch * rows * cols, 16-byte aligned.  ``update_dtype``: of the
+    momentum's update matrix (bf16 or float32).  ``scale``: the update's scale
+    (default 0.2 sqrt(max(rows, cols)), which matches an Adam update's size)."""
 
     def __init__(self, *, n_d: int, rows: int, cols: int, master, momentum, param_out,
                  batch: int = 1, mu: float = 0.95, nesterov: bool = True,
                  weight_decay: float = 0.0, steps: int = 5, coeffs=None, eps: float = 1e-7,
                  scale: float | None = None, update_dtype=torch.bfloat16, stream=None):
         n = int(batch) * int(rows) * int(cols)
-        for t, size, what in ((master, 4, "master"), (momentum, 4, "momentum"),
-                              (param_out, 2, "param_out")):
-            _require(t.numel() == n and t.element_size() == size and t.is_contiguous()
-                     and t.is_cuda, what)
+        for t, types, what in ((master, (torch.float32,), "master"),
+                               (momentum, (torch.float32,), "momentum"),
+                               (param_out, _BF16_LIKE, "param_out")):
+            _require(t.numel() == n and t.dtype in types and t.is_contiguous() and t.is_cuda, what)
         self._stream = torch.cuda.current_stream() if stream is None else stream
         self.master, self.momentum, self.param_out = master, momentum, param_out
         self.scale = 0.2 * max(rows, cols) ** 0.5 if scale is None else float(scale)
@@ -768,10 +774,26 @@ class ZeroMuon:
             self.update = torch.empty(batch, rows, cols, device="cuda", dtype=update_dtype)
             self.o = torch.empty(batch, rows, cols, device="cuda", dtype=torch.bfloat16)
 
+    def _table(self, contrib):
+        """The table of n_d contributions, each n contiguous bf16 elements."""
+        n, n_d = self.desc.n, self.desc.n_d
+        if isinstance(contrib, ctypes.Array):  # kept by the caller
+            _require(len(contrib) == n_d, "contrib")
+            return contrib
+        rows = list(contrib)  # also of a 2-D tensor
+        _require(len(rows) == n_d, "contrib")
+        for r in rows:
+            _require(r is not None and r.numel() == n and r.dtype in _BF16_LIKE
+                     and r.is_contiguous() and r.is_cuda, "contrib")
+        return contrib_table(rows)
+
     def step(self, contrib, lr: float) -> None:
         """Momentum over the mean of the contributions, its orthogonalisation,
-        and the weight update; param_out holds the bf16 weights."""
-        _check(zero_shard_muon_momentum(self.desc, contrib, self.momentum, self.momentum,
+        and the weight update; param_out holds the bf16 weights.  contrib: n_d
+        bf16[n] tensors (or their patterns), the rows of an (n_d, n) one, or a
+        table of theirs (contrib_table)."""
+        table = self._table(contrib)
+        _check(zero_shard_muon_momentum(self.desc, table, self.momentum, self.momentum,
                                         self.update), "zero_shard_muon_momentum")
         self.ortho(self.update, self.o)
         _check(zero_shard_muon_apply(self.desc, self.o, lr, self.scale, self.master, self.master,

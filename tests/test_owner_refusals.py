@@ -134,3 +134,67 @@ def test_ortho_refuses_expanded_operands():
     again = torch.empty_like(o)
     orth(between.contiguous(), again)
     assert torch.equal(o, again)
+
+
+def _muon(n, n_d):
+    muon = object.__new__(Z.ZeroMuon)
+    muon.desc = Z.zs_muon_desc(n=n, n_d=n_d, mu=0.95)
+    muon.momentum = muon.update = torch.zeros(n)
+    return muon
+
+
+GOOD = lambda: on_device(torch.zeros(32, dtype=BF))
+
+
+@pytest.mark.parametrize("contrib", [
+    lambda: [GOOD()] * 2, lambda: [GOOD()] * 4, lambda: [], lambda: [GOOD(), None, GOOD()],
+    lambda: [GOOD(), GOOD(), on_device(torch.zeros(32))],             # fp32
+    lambda: [GOOD(), GOOD(), on_device(torch.zeros(32, dtype=F16))],
+    lambda: [GOOD(), on_device(torch.zeros(31, dtype=BF)), GOOD()],   # short
+    lambda: [GOOD(), on_device(torch.zeros(64, dtype=BF))[::2], GOOD()],
+    lambda: [GOOD(), on_device(torch.zeros(1, dtype=BF)).expand(32), GOOD()],
+    lambda: [GOOD(), torch.zeros(32, dtype=BF), GOOD()],              # on the host
+    lambda: on_device(torch.zeros(2, 32, dtype=BF)), lambda: on_device(torch.zeros(3, 30, dtype=BF)),
+    lambda: on_device(torch.zeros(32, 3, dtype=BF)).T,
+    lambda: Z.contrib_table([GOOD()] * 2)])
+def test_muon_refuses_wrong_contributions(contrib):
+    with pytest.raises(Z.ZeroShardError, match="contrib"):
+        _muon(32, 3).step(contrib(), 0.1)
+
+
+@pytest.mark.parametrize("contrib", [
+    lambda: [GOOD()] * 3, lambda: iter([GOOD()] * 3), lambda: tuple([GOOD().view(4, 8)] * 3),
+    lambda: on_device(torch.zeros(3, 40, dtype=BF))[:, :32],
+    lambda: [GOOD().view(torch.int16), GOOD().view(torch.uint16), GOOD()],
+    lambda: Z.contrib_table([GOOD()] * 3)])
+def test_muon_takes_contributions(contrib):
+    assert len(_muon(32, 3)._table(contrib())) == 3
+
+
+def test_momentum_refuses_a_short_table():
+    d = Z.zs_muon_desc(n=32, n_d=3, nesterov=1, dtype=Z.ZS_BF16, mu=0.95)
+    t = [torch.zeros(32, dtype=BF)] * 2
+    assert Z.zero_shard_muon_momentum(d, t, None, None, None) == Z.ZS_EINVAL
+    assert Z.zero_shard_muon_momentum(d, Z.contrib_table(t), t[0], t[0], t[0]) == Z.ZS_EINVAL
+
+
+@pytest.mark.gpu
+def test_muon_refuses_state_of_another_type():
+    n = 32 * 16
+    new = lambda t: torch.zeros(n, device="cuda", dtype=t)
+    good = dict(n_d=2, rows=32, cols=16, master=new(F32), momentum=new(F32), param_out=new(BF))
+    for kw in (dict(master=new(torch.int32)), dict(momentum=new(torch.int32)),
+               dict(param_out=new(F16)), dict(param_out=new(F32)), dict(master=new(BF))):
+        with pytest.raises(Z.ZeroShardError):
+            Z.ZeroMuon(**{**good, **kw})
+    muon = Z.ZeroMuon(**{**good, "param_out": new(torch.int16)})
+    rows = [torch.ones(n, device="cuda", dtype=BF) for _ in range(2)]
+    for bad in (rows[:1], rows + rows[:1], [rows[0], rows[1].float()], [rows[0], rows[1][:-1]]):
+        with pytest.raises(Z.ZeroShardError):
+            muon.step(bad, 0.1)
+    torch.cuda.synchronize()
+    assert not muon.momentum.any() and not muon.master.any()
+    muon.step(rows, 0.1)
+    muon.step(Z.contrib_table(rows), 0.1)
+    muon.step(torch.stack(rows), 0.1)
+    assert torch.isfinite(muon.master).all() and muon.master.any()
