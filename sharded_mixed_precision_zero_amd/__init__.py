@@ -763,11 +763,14 @@ class ZeroMuon:
                                (momentum, (torch.float32,), "momentum"),
                                (param_out, _BF16_LIKE, "param_out")):
             _require(t.numel() == n and t.dtype in types and t.is_contiguous() and t.is_cuda, what)
+            if t.data_ptr() % 16:
+                raise ZeroShardError(ZS_EALIGN, what)
         self._stream = torch.cuda.current_stream() if stream is None else stream
         self.master, self.momentum, self.param_out = master, momentum, param_out
         self.scale = 0.2 * max(rows, cols) ** 0.5 if scale is None else float(scale)
         self.desc = muon_desc(n=n, n_d=n_d, mu=mu, nesterov=nesterov, dtype=update_dtype,
                               weight_decay=weight_decay, stream=self._stream)
+        self._no_elements = muon_desc(n=0, weight_decay=weight_decay, stream=self._stream)
         self.ortho = ZeroOrtho(batch=batch, rows=rows, cols=cols, dtype=update_dtype, steps=steps,
                                coeffs=coeffs, eps=eps, stream=self._stream)
         with torch.cuda.stream(self._stream):
@@ -793,6 +796,10 @@ class ZeroMuon:
         bf16[n] tensors (or their patterns), the rows of an (n_d, n) one, or a
         table of theirs (contrib_table)."""
         table = self._table(contrib)
+        # the rate is refused before the momentum moves on: the weight update of
+        # no elements checks it and does nothing else
+        _check(zero_shard_muon_apply(self._no_elements, None, lr, self.scale, None, None, None),
+               "lr, scale")
         _check(zero_shard_muon_momentum(self.desc, table, self.momentum, self.momentum,
                                         self.update), "zero_shard_muon_momentum")
         self.ortho(self.update, self.o)

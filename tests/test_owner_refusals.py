@@ -138,6 +138,7 @@ def test_ortho_refuses_expanded_operands():
 
 def _muon(n, n_d):
     muon = object.__new__(Z.ZeroMuon)
+    muon._no_elements, muon.scale = Z.zs_muon_desc(n=0, n_d=1), 1.0
     muon.desc = Z.zs_muon_desc(n=n, n_d=n_d, mu=0.95)
     muon.momentum = muon.update = torch.zeros(n)
     return muon
@@ -198,3 +199,37 @@ def test_muon_refuses_state_of_another_type():
     muon.step(Z.contrib_table(rows), 0.1)
     muon.step(torch.stack(rows), 0.1)
     assert torch.isfinite(muon.master).all() and muon.master.any()
+
+
+def test_a_refused_rate_queues_nothing(monkeypatch):
+    """The momentum does not move on when the weight update would be refused."""
+    called = []
+    monkeypatch.setattr(Z, "zero_shard_muon_momentum", lambda *a: called.append(a) or Z.ZS_OK)
+    muon = _muon(32, 3)
+    for lr in (-1.0, float("nan"), float("inf")):
+        with pytest.raises(Z.ZeroShardError):
+            muon.step([GOOD()] * 3, lr)
+    muon.scale = float("nan")
+    with pytest.raises(Z.ZeroShardError):
+        muon.step([GOOD()] * 3, 0.1)
+    assert not called
+
+
+@pytest.mark.gpu
+def test_muon_refuses_before_the_state_moves():
+    n = 32 * 16
+    new = lambda t=F32, k=n: torch.zeros(k, device="cuda", dtype=t)
+    good = dict(n_d=1, rows=32, cols=16, master=new(), momentum=new(), param_out=new(BF))
+    for kw in (dict(master=new(k=n + 1)[1:]), dict(momentum=new(k=n + 1)[1:]),
+               dict(param_out=new(BF, n + 4)[4:])):
+        with pytest.raises(Z.ZeroShardError):
+            Z.ZeroMuon(**{**good, **kw})
+    muon = Z.ZeroMuon(**good)
+    rows = [torch.ones(n, device="cuda", dtype=BF)]
+    for lr in (-1.0, float("nan")):
+        with pytest.raises(Z.ZeroShardError):
+            muon.step(rows, lr)
+    torch.cuda.synchronize()
+    assert not muon.momentum.any()
+    muon.step(rows, 0.1)
+    assert muon.momentum.any()
