@@ -907,7 +907,7 @@ __device__ __forceinline__ half4 narrow4(const f32x4 &v) {
 
 // A symmetric matrix of mp rows in LDS is followed by the rests of its diagonal
 // (96 x 128: 22.3 us, without them 21.8; 64 x 13824 36 and 33).
-constexpr int short_size(int mp) { return mp * (mp + 8) + 2 * mp; }
+constexpr int64_t short_size(int64_t mp) { return mp * (mp + 8) + 2 * mp; }
 
 template <int MB>
 __device__ __forceinline__ float *rest_of(_Float16 *M) {
@@ -1162,7 +1162,7 @@ struct SmallArgs {
 };
 
 int64_t small_lds(int64_t mp, int64_t np) {
-  return mp * (np + 8) + np * (mp + 8) + 2 * short_size(int(mp));
+  return mp * (np + 8) + np * (mp + 8) + 2 * short_size(mp);
 }
 
 // A matrix whose X, X^T, A and B fit in the LDS of one CU: one workgroup, one
@@ -1525,7 +1525,7 @@ Plan plan_of(const zs_ortho_desc &d) {
     p.np = int64_t(p.strips) * kStripCols;
     p.xt = take(d.batch * p.np * p.mp * 2);
     p.parts = take(d.batch * p.strips * p.mp * p.mp * 4);
-    p.a = take(d.batch * short_size(int(p.mp)) * 2);
+    p.a = take(d.batch * short_size(p.mp) * 2);
     p.bytes = at;
     return p;
   }
