@@ -460,7 +460,8 @@ typedef struct zs_ortho_desc {
 } zs_ortho_desc;
 
 /* Bytes of workspace that zero_shard_ortho needs for d, or -1 for an invalid
- * descriptor. */
+ * descriptor, among them one with a product of 2^23 or more tiles of 256 x 256,
+ * which no launch takes (and no card holds). */
 int64_t zero_shard_ortho_workspace(const zs_ortho_desc *d);
 
 /* Per matrix: X = G / (|G|_F + eps) (the norm in binary64), then `steps` times

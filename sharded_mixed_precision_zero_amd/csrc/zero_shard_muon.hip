@@ -1430,6 +1430,7 @@ constexpr Shape kShapes[] = {
 };
 constexpr int kNumShapes = sizeof kShapes / sizeof kShapes[0];
 constexpr int kFirstCut = 3, kMostParts = 8;
+constexpr int64_t kMostTiles = 0xffffffff / 512;  // of a launch: it takes below 2^32 threads
 
 // How one product is spread over the card: its tile shape, and whether the
 // tiles are cut along k.
@@ -1443,7 +1444,7 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 // r x c of `batch` matrices (half of it when symmetric) over k.
 Way way_with(int64_t batch, int64_t r, int64_t c, int64_t k, bool symmetric, int shape) {
   const Shape &S = kShapes[shape];
-  Way w;
+  Way w = {};
   w.shape = shape;
   w.tiles_r = int(up(r, S.TR) / S.TR);
   w.tiles_c = int(up(c, S.TC) / S.TC);
@@ -1453,13 +1454,12 @@ Way way_with(int64_t batch, int64_t r, int64_t c, int64_t k, bool symmetric, int
   else
     per = int64_t(w.tiles_r) * w.tiles_c;
   const int64_t tiles = batch * per, nk = k / 64;
-  if (tiles > 0x7fffffff) {
+  if (tiles > kMostTiles) {
     w.us = INFINITY;
     return w;
   }
   w.per = int(per);
   w.grid = int(tiles);
-  w.cut = 0;
   // n workgroups at once, each over `steps` 64s of k
   const auto turn = [&](int64_t n, double steps) {
     return steps * (S.alone + (S.full - S.alone) * double(n) / S.cap) + S.rest;
@@ -1534,6 +1534,10 @@ Plan plan_of(const zs_ortho_desc &d) {
   p.gram = way_of(d.batch, p.mp, p.mp, p.np, true);
   p.poly = way_of(d.batch, p.mp, p.mp, p.mp, true);
   p.next = way_of(d.batch, p.mp, p.np, p.mp, false);
+  if (!std::isfinite(p.gram.us) || !std::isfinite(p.next.us)) {
+    p.bytes = -1;
+    return p;
+  }
   p.paired = d.steps > 1 && 3 * p.poly.us < p.gram.us + p.next.us;
   const auto parts = [](const Way &w) {
     return w.cut ? int64_t(w.grid) * 2 * kShapes[w.shape].TR * kShapes[w.shape].TC * 4 : 0;
@@ -1720,9 +1724,7 @@ int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *wo
   if (!ortho_ok(d)) return ZS_EINVAL;
   if (d->batch == 0 || d->rows == 0 || d->cols == 0) return ZS_OK;
   const Plan p = plan_of(*d);
-  if (!g || !o || !workspace || workspace_bytes < p.bytes) return ZS_EINVAL;
-  if (!p.small && !p.strips && (!std::isfinite(p.gram.us) || !std::isfinite(p.next.us)))
-    return ZS_EINVAL;
+  if (!g || !o || !workspace || p.bytes < 0 || workspace_bytes < p.bytes) return ZS_EINVAL;
   if (!aligned(g, dtype_size(d->dtype)) || !aligned(o, 2) || !aligned(workspace, 256))
     return ZS_EALIGN;
   if (const int rc = device_is_gfx950()) return rc;

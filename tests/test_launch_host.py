@@ -73,6 +73,20 @@ def test_ordinary_sizes(call):
 
 def test_ortho_sides_of_every_power_of_two(call):
     sides = [1 << k for k in range(21)]
-    lines = [f"ortho 1 {r} {c} 0 5" for r in sides for c in sides]
+    lines = [f"ortho 1 {r} {c} 0 5" for r in sides for c in sides if r * c <= 1 << 38]
     for line, (need, _, _) in zip(lines, call(*lines)):
         assert need > 0, line
+
+
+def test_ortho_refuses_what_no_launch_takes(call):
+    """Products of more tiles than a launch takes: no workspace and no launch; up
+    to there every call is queued, whatever shape its tiles would take alone."""
+    huge = ["ortho 65535 65536 65536 0 5", "ortho 65535 1048576 200 1 5", "ortho 1 1048576 1048576 0 1",
+            "ortho 600 32768 32768 0 5"]
+    for line, (need, rc, launches) in zip(huge, call(*huge)):
+        assert (need, rc, launches) == (-1, Z.ZS_EINVAL, 0), line
+    sides = [1 << k for k in range(5, 21)]
+    lines = [f"ortho {b} {r} {c} 0 5" for b in (1, 1000, 65535) for r in sides for c in sides]
+    for line, (need, rc, launches) in zip(lines, call(*lines)):
+        assert (rc == Z.ZS_OK and need > 0 and launches > 0) or (
+            rc == Z.ZS_EINVAL and need == -1 and launches == 0), line
