@@ -35,7 +35,7 @@ constexpr int kThreads = 256;
 constexpr int kLongThreads = 1024;
 constexpr int kMaxRegCols = 16384;  // rows up to here stay in registers
 constexpr int kCus = 256;
-constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr int64_t kMaxGrid = 0xffffffff / kLongThreads;  // a launch takes below 2^32 threads
 constexpr int kMaxParts = 256;      // partial rows of dgamma / dbeta
 
 template <int CTRL, int ROWS = 0xf>

@@ -90,3 +90,11 @@ def test_ortho_refuses_what_no_launch_takes(call):
     for line, (need, rc, launches) in zip(lines, call(*lines)):
         assert (rc == Z.ZS_OK and need > 0 and launches > 0) or (
             rc == Z.ZS_EINVAL and need == -1 and launches == 0), line
+
+
+def test_layernorm_of_any_number_of_rows_is_queued(call):
+    lines = [f"{op} {rows} {cols} {t}" for op in ("norm", "norm_grad") for t in (0, 1)
+             for rows in (1, 4194303, 4194304, 1 << 31, 1 << 40)
+             for cols in (1, 512, 8192, 16384, 16385, 1 << 31)]
+    for line, (need, rc, launches) in zip(lines, call(*lines)):
+        assert need > 0 and rc == Z.ZS_OK and launches > 0, line
