@@ -66,6 +66,9 @@ using half4 = _Float16 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
 constexpr unsigned kFew = 256;  // workgroups: one a CU, too few for HBM to bound them
+// Elements of a launch of momentum or apply, a thread for eight: it takes below
+// 2^32 threads.
+constexpr int64_t kPiece = INT64_C(1) << 34;
 
 // ------------------------------------------------- momentum and apply
 
@@ -1673,26 +1676,29 @@ int zero_shard_muon_momentum(const zs_muon_desc *d, const zs_bf16 *const *contri
   for (int k = 0; k < d->n_d; ++k) {
     if (!contrib[k]) return ZS_EINVAL;
     if (!aligned(contrib[k], 16)) return ZS_EALIGN;
-    A.rows.p[k] = contrib[k];
   }
   if (!aligned(m_in, 16) || !aligned(m_out, 16) || !aligned(update, 16)) return ZS_EALIGN;
   if (const int rc = device_is_gfx950()) return rc;
-  A.n = d->n;
   A.n_d = d->n_d;
   A.nesterov = d->nesterov;
   A.mu = double(d->mu);
-  A.m_in = m_in;
-  A.m_out = m_out;
-  A.update = update;
-  const dim3 grid(unsigned((d->n / 512 * 64 + d->n % 512 + kThreads - 1) / kThreads));
   const hipStream_t st = static_cast<hipStream_t>(d->stream);
   const auto launch = [&](auto t) {
     using TU = decltype(t);
-    if (grid.x <= kFew)
-      hipLaunchKernelGGL((momentum_kernel<TU, true>), grid, dim3(kThreads), 0, st, A);
-    else
-      hipLaunchKernelGGL((momentum_kernel<TU, false>), grid, dim3(kThreads), 0, st, A);
-    return launched();
+    for (int64_t from = 0; from < d->n; from += kPiece) {
+      A.n = d->n - from < kPiece ? d->n - from : kPiece;
+      for (int k = 0; k < d->n_d; ++k) A.rows.p[k] = contrib[k] + from;
+      A.m_in = m_in + from;
+      A.m_out = m_out + from;
+      A.update = static_cast<typename TU::raw *>(update) + from;
+      const dim3 grid(unsigned((A.n / 512 * 64 + A.n % 512 + kThreads - 1) / kThreads));
+      if (grid.x <= kFew)
+        hipLaunchKernelGGL((momentum_kernel<TU, true>), grid, dim3(kThreads), 0, st, A);
+      else
+        hipLaunchKernelGGL((momentum_kernel<TU, false>), grid, dim3(kThreads), 0, st, A);
+      if (const int rc = launched()) return rc;
+    }
+    return int(ZS_OK);
   };
   return d->dtype == ZS_F32 ? launch(F32{}) : launch(Bf16{});
 }
@@ -1706,11 +1712,15 @@ int zero_shard_muon_apply(const zs_muon_desc *d, const zs_bf16 *o, float lr, flo
       !aligned(param_out, 16))
     return ZS_EALIGN;
   if (const int rc = device_is_gfx950()) return rc;
-  const ApplyArgs A{d->n, o, master_in, master_out, param_out,
-                    double(lr) * double(d->weight_decay), double(lr) * double(scale)};
-  hipLaunchKernelGGL(apply_kernel, dim3(unsigned((d->n + kThreads * 8 - 1) / (kThreads * 8))),
-                     dim3(kThreads), 0, static_cast<hipStream_t>(d->stream), A);
-  return launched();
+  for (int64_t from = 0; from < d->n; from += kPiece) {
+    const int64_t n = d->n - from < kPiece ? d->n - from : kPiece;
+    const ApplyArgs A{n, o + from, master_in + from, master_out + from, param_out + from,
+                      double(lr) * double(d->weight_decay), double(lr) * double(scale)};
+    hipLaunchKernelGGL(apply_kernel, dim3(unsigned((n + kThreads * 8 - 1) / (kThreads * 8))),
+                       dim3(kThreads), 0, static_cast<hipStream_t>(d->stream), A);
+    if (const int rc = launched()) return rc;
+  }
+  return ZS_OK;
 }
 
 int64_t zero_shard_ortho_workspace(const zs_ortho_desc *d) {

@@ -98,3 +98,12 @@ def test_layernorm_of_any_number_of_rows_is_queued(call):
              for cols in (1, 512, 8192, 16384, 16385, 1 << 31)]
     for line, (need, rc, launches) in zip(lines, call(*lines)):
         assert need > 0 and rc == Z.ZS_OK and launches > 0, line
+
+
+def test_muon_passes_of_any_length_are_queued(call):
+    sizes = [1, (1 << 34) - 1, 1 << 34, (1 << 34) + 1, (1 << 35) - 1, 1 << 35, (1 << 35) + 5,
+             1 << 38]
+    lines = [f"momentum {n} {k} {t}" for n in sizes for k in (1, 64) for t in (0, 1)]
+    lines += [f"apply {n}" for n in sizes]
+    for line, (_, rc, launches) in zip(lines, call(*lines)):
+        assert rc == Z.ZS_OK and launches >= 1, line
