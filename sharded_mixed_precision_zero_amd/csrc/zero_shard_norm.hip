@@ -415,7 +415,8 @@ __global__ void __launch_bounds__(1024) ln_bwd_kernel(const BwdArgs A) {
     auto &x = now.x, &dy = now.dy, &ds = now.ds;
     auto &mean = now.mean, &rstd = now.rstd;
     float both[2 * R];
-    // past a row's end dy is 0, and so is all that it is a factor of
+    // Past a row's end dy is 0, and so is all that it is a factor of: rstd is taken
+    // as 0 there, since -mean rstd may be beyond binary32.
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       float c1 = 0.0f, c2 = 0.0f;
@@ -423,7 +424,8 @@ __global__ void __launch_bounds__(1024) ln_bwd_kernel(const BwdArgs A) {
       for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float h = (x[k][n].get(e) - mean[k]) * rstd[k], d = dy[k][n].get(e);
+          const float scale = (TAIL ? e : 0) < c.left[n] ? rstd[k] : 0.0f;
+          const float h = (x[k][n].get(e) - mean[k]) * scale, d = dy[k][n].get(e);
           dg[n][e] = __builtin_fmaf(d, h, dg[n][e]);
           db[n][e] += d;
           const float g = d * gamma[n].get(e);
@@ -522,7 +524,8 @@ __global__ void __launch_bounds__(kLongThreads) ln_bwd_long_dx_kernel(const BwdA
       for (int e = 0; e < 8; ++e) {
         const float g = A.gamma ? dy.get(e) * w.get(e) : dy.get(e);
         both[0] += g;
-        both[1] = __builtin_fmaf(g, (x.get(e) - mean) * rstd, both[1]);
+        // past the row's end: as in the register kernel
+        both[1] = __builtin_fmaf(g, (x.get(e) - mean) * (e < A.cols - i ? rstd : 0.0f), both[1]);
       }
     }
     sums.add(both);
