@@ -426,7 +426,8 @@ typedef struct zs_muon_desc {
 
 /* gbar as in the shard step (binary64 sum in rank order, averaged, rounded to
  * binary32);  M' = mu M + gbar;  u = gbar + mu M' (nesterov) or M'; binary64
- * from binary32 values, M' rounded to binary32 and u to its type once each.
+ * from binary32 values, M' and u rounded to binary32 once each.  A bf16 u is the
+ * bf16 of that binary32 value (as the bf16 weights are of the master's).
  * contrib: HOST array of n_d device pointers to bf16[n]; m_in, m_out: fp32[n],
  * may be the same buffer; update: u.
  * Errors: ZS_EINVAL, ZS_EALIGN, ZS_EDEVICE, ZS_EHIP. */

@@ -4,7 +4,9 @@
 // include/zero_shard.h).
 //
 // momentum and apply are HBM-bound elementwise passes over a flat range, in
-// binary64 with one rounding per stored value, as the shard step's update.
+// binary64 with one rounding to binary32 per value, as the shard step's update;
+// bf16 values (the update matrix, the weights' copy) are rounded from those, so
+// that they are the same whether the binary32 value is stored as well or not.
 //
 // ortho: with m = min(rows, cols), n = max(rows, cols) and X the m x n matrix
 // (the transpose of a tall one), X0 = G / (|G|_F + eps) and, `steps` times,
