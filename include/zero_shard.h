@@ -380,8 +380,8 @@ typedef struct zs_layernorm_desc {
  * gamma and beta (cols elements) may each be NULL (1 and 0); mean and rstd
  * (fp32[rows]) may each be NULL when no backward pass follows.  A row that
  * holds an infinity or NaN gives NaN in that row only, as does one whose sum is
- * beyond binary32; a constant row gives beta up to rounding (eps > 0; with eps =
- * 0 it has no value).  sum may be x's or
+ * beyond binary32; where the deviations' squares are, rstd is 0.  A constant row
+ * gives beta up to rounding (eps > 0; with eps = 0 it has no value).  sum may be x's or
  * residual's own buffer with the same row stride, y may be x's (or
  * residual's) unless sum is; otherwise outputs overlap nothing.
  * Errors: ZS_EINVAL, ZS_EALIGN (a pointer not aligned to its element),
@@ -438,7 +438,8 @@ int zero_shard_muon_momentum(const zs_muon_desc *d, const zs_bf16 *const *contri
  * bf16 values, rounded once; p = bf16(theta').  o: bf16[n], the
  * orthogonalised update; scale: the caller's adjustment for the matrix's
  * shape, e.g. 0.2 sqrt(max(rows, cols)); master_in, master_out: fp32[n], may be
- * the same buffer; param_out: bf16[n], the buffer the all-gather sends.
+ * the same buffer; param_out: bf16[n], the buffer the all-gather sends.  lr and
+ * scale are taken at the call: a captured graph keeps those of its capture.
  * Errors: ZS_EINVAL (lr negative or not finite, ...), ZS_EALIGN, ZS_EDEVICE,
  * ZS_EHIP. */
 int zero_shard_muon_apply(const zs_muon_desc *d, const zs_bf16 *o, float lr, float scale,

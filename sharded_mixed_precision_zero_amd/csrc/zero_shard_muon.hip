@@ -679,8 +679,8 @@ __global__ void __launch_bounds__(WR *WC * 64) ortho_mul_kernel(const MulArgs A)
 #pragma unroll
       for (int i = 0; i < N; ++i) acc[i / TN][i % TN] = f32x4{};
       for (int w = w0; w <= w1; ++w) {
-        // all under way at once: one after the other A of 1000 x 13000 takes 48 us
-        // for 41
+        // all under way at once: one after the other A of 1000 x 13000 took 48 us
+        // for 41 (38 on another card)
         f32x4 got[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) got[i] = *part(w, w == w0, i);
@@ -1233,9 +1233,10 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(const SmallA
 // X X^T, one launch adds them, and the next update's workgroups all work out
 // the polynomials in A again, two steps of them where the coefficients allow
 // it, and apply them to their strip.  64 x 13824: 8 launches, 36 us, in place of
-// 19, 105 us.  What is left is launches and the latency
-// of LDS: at 128 rows a product of 128^3 takes 1.5 us, of which one CU's matrix
-// cores work 0.2.
+// 19, 105 us.  What is left is launches and waiting: at 128 rows a product of 128^3
+// takes 1.5 us, of which one CU's matrix cores work 0.2.  (Of the one-workgroup
+// kernel's time, 96 x 128 to 128 x 160, the LDS is busy 43-57%, a third of that with
+// bank conflicts, the matrix cores 11-18%; its waves wait 49-63%.)
 constexpr int kStripCols = 128, kStripRows = 128;
 
 struct StripArgs {

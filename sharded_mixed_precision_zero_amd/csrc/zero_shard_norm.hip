@@ -173,9 +173,10 @@ __global__ void __launch_bounds__(1024) ln_fwd_kernel(const FwdArgs A) {
   load_params<TAIL>(gamma, A.gamma, 1.0f, c);
   load_params<TAIL>(beta, A.beta, 0.0f, c);
   const float inv = 1.0f / float(A.cols);
-  // Past the caches where a lane's accesses are 16 bytes side by side; others
-  // leave parts of lines, which should stay (8192 x 4096 fp32: 103 us for 108;
-  // 16384 x 511 bf16: 23 for 29; but 8192 x 5120 bf16: 71 for 74).
+  // Past the caches where a lane's accesses are 16 bytes side by side (8192 x 5120
+  // bf16 with a residual: 58 us for 67 through them); others leave parts of lines,
+  // which should stay (16384 x 511 bf16: 15.4 us for 18.1 past them, 2048 x 1601
+  // fp32 11.1 for 14.5; only even rows of fp32 lose by it, 8192 x 4096 102 for 98).
   constexpr bool kOnce = N == 1 && !TAIL && sizeof(typename TX::raw) == 2;
   const int64_t step = int64_t(gridDim.x) * subs * R;
   struct Rows {
@@ -375,9 +376,9 @@ __global__ void __launch_bounds__(1024) ln_bwd_kernel(const BwdArgs A) {
   load_params<TAIL>(gamma, A.gamma, 1.0f, c);
   const float inv = 1.0f / float(A.cols);
   float dg[N][8] = {}, db[N][8] = {};
-  // Past the caches where a lane's accesses are 16 bytes side by side; others
-  // leave parts of lines, which should stay (8192 x 4096 fp32: 103 us for 108;
-  // 16384 x 511 bf16: 23 for 29; but 8192 x 5120 bf16: 71 for 74).
+  // Past the caches as in the forward pass (8192 x 5120 bf16 with a residual: 66 us
+  // for 72 through them; 16384 x 511 bf16 through them 29 for 34, 2048 x 1601 fp32
+  // 17.7 for 19.7, and 8192 x 4096 fp32 105 for 98).
   constexpr bool kOnce = N == 1 && !TAIL && sizeof(typename TX::raw) == 2;
   const int64_t step = int64_t(gridDim.x) * subs * R;
   struct Rows {
