@@ -486,7 +486,7 @@ def muon_desc(*, n: int, n_d: int = 1, mu: float = 0.95, nesterov: bool = True,
 
 def zero_shard_muon_momentum(desc: zs_muon_desc, contrib, m_in, m_out, update) -> int:
     table = contrib_table(contrib)
-    if table is not None and len(table) < desc.n_d:
+    if table is not None and len(table) < desc.n_d and desc.n > 0:
         return ZS_EINVAL
     return _lib.zero_shard_muon_momentum(ctypes.byref(desc), table, _ptr(m_in), _ptr(m_out),
                                          _ptr(update))
@@ -778,7 +778,8 @@ class ZeroMuon:
             self.o = torch.empty(batch, rows, cols, device="cuda", dtype=torch.bfloat16)
 
     def _table(self, contrib):
-        """The table of n_d contributions, each n contiguous bf16 elements."""
+        """The table of n_d contributions, each n contiguous bf16 elements or more
+        (a row may be padded at its end)."""
         n, n_d = self.desc.n, self.desc.n_d
         if isinstance(contrib, ctypes.Array):  # kept by the caller
             _require(len(contrib) == n_d, "contrib")
@@ -786,15 +787,15 @@ class ZeroMuon:
         rows = list(contrib)  # also of a 2-D tensor
         _require(len(rows) == n_d, "contrib")
         for r in rows:
-            _require(r is not None and r.numel() == n and r.dtype in _BF16_LIKE
+            _require(r is not None and r.numel() >= n and r.dtype in _BF16_LIKE
                      and r.is_contiguous() and r.is_cuda, "contrib")
         return contrib_table(rows)
 
     def step(self, contrib, lr: float) -> None:
         """Momentum over the mean of the contributions, its orthogonalisation,
         and the weight update; param_out holds the bf16 weights.  contrib: n_d
-        bf16[n] tensors (or their patterns), the rows of an (n_d, n) one, or a
-        table of theirs (contrib_table)."""
+        bf16[n] tensors (or their patterns; longer ones are read up to n), the rows
+        of an (n_d, n) one, or a table of theirs (contrib_table)."""
         table = self._table(contrib)
         # the rate is refused before the momentum moves on: the weight update of
         # no elements checks it and does nothing else

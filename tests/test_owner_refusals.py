@@ -166,6 +166,7 @@ def test_muon_refuses_wrong_contributions(contrib):
 @pytest.mark.parametrize("contrib", [
     lambda: [GOOD()] * 3, lambda: iter([GOOD()] * 3), lambda: tuple([GOOD().view(4, 8)] * 3),
     lambda: on_device(torch.zeros(3, 40, dtype=BF))[:, :32],
+    lambda: on_device(torch.zeros(3, 40, dtype=BF)),                  # padded at the rows' ends
     lambda: [GOOD().view(torch.int16), GOOD().view(torch.uint16), GOOD()],
     lambda: Z.contrib_table([GOOD()] * 3)])
 def test_muon_takes_contributions(contrib):
@@ -177,6 +178,8 @@ def test_momentum_refuses_a_short_table():
     t = [torch.zeros(32, dtype=BF)] * 2
     assert Z.zero_shard_muon_momentum(d, t, None, None, None) == Z.ZS_EINVAL
     assert Z.zero_shard_muon_momentum(d, Z.contrib_table(t), t[0], t[0], t[0]) == Z.ZS_EINVAL
+    d.n = 0  # nothing is read
+    assert Z.zero_shard_muon_momentum(d, [], None, None, None) == Z.ZS_OK
 
 
 @pytest.mark.gpu
