@@ -485,6 +485,89 @@ int64_t zero_shard_ortho_workspace(const zs_ortho_desc *d);
 int zero_shard_ortho(const zs_ortho_desc *d, const void *g, zs_bf16 *o, void *workspace,
                      int64_t workspace_bytes);
 
+/* ---------------------------------------------------------------------------
+ * The seam between two blocks of a network: the norm of a block's output, its
+ * gate, the scaled residual sum, and the norm before the next block.  No
+ * handle; launches only, as for layer norm.
+ *
+ * Rows of `cols` elements, column stride 1, row strides ld_* in elements (0:
+ * cols).  Sums, statistics and products are binary32, each output is rounded once to
+ * its type (nearest even). */
+#define ZS_BLOCKNORM_MAX_COLS 16384
+typedef enum zs_norm_kind { ZS_NORM_LAYER = 0, ZS_NORM_RMS = 1 } zs_norm_kind;
+typedef enum zs_gate {
+  ZS_GATE_NONE = 0,
+  ZS_GATE_COLUMN = 1, /* a factor for each column: param_dtype, cols elements  */
+  ZS_GATE_SIGMOID = 2 /* sigmoid(z) for each element: z is dtype, rows x cols  */
+} zs_gate;
+
+typedef struct zs_blocknorm_desc {
+  int64_t rows, cols;  /* rows >= 0, 1 <= cols <= ZS_BLOCKNORM_MAX_COLS       */
+  int32_t dtype;       /* zs_dtype of x, block, sum, y, their gradients, and z */
+  int32_t param_dtype; /* of gains, biases, column gates: ZS_F32 or dtype     */
+  int32_t kind;        /* zs_norm_kind of both norms                          */
+  int32_t post;        /* 1: the block's output is normalised; 0: it is not   */
+  int32_t gate;        /* zs_gate                                             */
+  float eps;           /* >= 0, finite                                        */
+  float residual_scale;  /* finite                                            */
+  int64_t ld_x, ld_block, ld_gate, ld_sum, ld_y;      /* ld_gate: of z        */
+  int64_t ld_dy, ld_dsum, ld_dx, ld_dblock, ld_dgate; /* ld_dgate: of z's     */
+  void *stream;        /* hipStream_t, NULL = null stream                     */
+} zs_blocknorm_desc;
+
+/* Forward:
+ *   n = N(block) gamma_post + beta_post  (post)  or  block
+ *   s = round(residual_scale x + g n),  g = 1, the column's gate or sigmoid(z)
+ *   y = N(s) gamma + beta
+ * N(a) = (a - mean) rstd for layer norm, as zero_shard_layernorm; for RMS norm
+ * N(a) = a rstd, rstd = 1 / sqrt(sum_c a^2 / cols + eps).  Gains and biases may each be
+ * NULL (1 and 0; gamma_post and beta_post have to be without post), gate is NULL iff
+ * the descriptor has none.  s is stored to sum.  stats (may be NULL when no
+ * backward pass follows): fp32[4][rows] (layer) or fp32[2][rows] (RMS), the rows'
+ * rstd of the first norm, rstd of the second, mean of the first, mean of the
+ * second; those of the first are not written without post.
+ * block and sum may both be NULL: then s = x and y = N(x) gamma + beta, with post 0,
+ * no gate and residual_scale 1.
+ * An infinity or NaN stays in its row: a layer norm's row is NaN, an RMS norm's
+ * too for a NaN; where an RMS norm's sum of squares is beyond binary32, rstd is 0
+ * (an infinity itself gives NaN).  A row of zeros gives beta (eps > 0).
+ * sum may be x's or block's own buffer with the same row stride, y may be
+ * x's, block's or z's unless sum is; otherwise outputs overlap nothing.
+ * Errors: ZS_EINVAL, ZS_EALIGN (a pointer not aligned to its element),
+ * ZS_EDEVICE, ZS_EHIP. */
+int zero_shard_blocknorm(const zs_blocknorm_desc *d, const void *x, const void *block,
+                         const void *gate, const void *gamma_post, const void *beta_post,
+                         const void *gamma, const void *beta, void *sum, void *y, float *stats);
+
+/* Bytes of workspace that zero_shard_blocknorm_bwd needs for d when a gradient of
+ * columns is asked for, or -1 for an invalid descriptor. */
+int64_t zero_shard_blocknorm_workspace(const zs_blocknorm_desc *d);
+
+/* Backward, from dy and dsum (the gradient that reaches sum from elsewhere; may
+ * be NULL), with the forward pass's sum, block and stats.  h0, h1: N(block) (block
+ * itself without post) and N(sum):
+ *   D = N'(dy gamma) + dsum;  dx = residual_scale D;  dn = g D
+ *   dblock = N'(dn gamma_post)  (post)  or  dn
+ *   N'(u) = rstd (u - sum_c u / cols - h sum_c (u h) / cols), RMS without the first sum
+ *   dgamma = sum_rows dy h1;  dbeta = sum_rows dy
+ *   dgamma_post = sum_rows dn h0;  dbeta_post = sum_rows dn
+ *   dgate = sum_rows D n  (column)  or the gradient of z, D n g (1 - g)
+ * The five parameters' gradients may each be NULL (not computed; those of what the
+ * descriptor lacks have to be); they are written, not added to.  Without a block
+ * (as in the forward pass) sum is x and dblock is NULL.  Of no rows the columns'
+ * gradients are zeros.
+ * dx and dblock may each be dy's, dsum's, sum's or block's own buffer with the same
+ * row stride, and dgate z's; otherwise outputs overlap nothing.  workspace: device,
+ * 16-byte aligned, at least zero_shard_blocknorm_workspace(d) bytes (may be NULL when
+ * no gradient of columns is asked for).
+ * Errors: ZS_EINVAL, ZS_EALIGN, ZS_EDEVICE, ZS_EHIP. */
+int zero_shard_blocknorm_bwd(const zs_blocknorm_desc *d, const void *dy, const void *dsum,
+                             const void *sum, const void *block, const void *gate,
+                             const void *gamma_post, const void *beta_post, const void *gamma,
+                             const float *stats, void *dx, void *dblock, void *dgate,
+                             void *dgamma_post, void *dbeta_post, void *dgamma, void *dbeta,
+                             void *workspace, int64_t workspace_bytes);
+
 /* Wait for the handle's stream, release its scratch and the handle.
  * Passing NULL is a no-op returning ZS_OK. */
 int zero_shard_free(zs_handle *h);

@@ -22,6 +22,9 @@ ZS_OK, ZS_EINVAL, ZS_EALIGN, ZS_ENOMEM, ZS_EHIP, ZS_EDEVICE, ZS_ESTATE, ZS_ETOOB
 ZS_MAX_ND = 64
 ZS_F32, ZS_BF16, ZS_F16 = 0, 1, 2
 ZS_ORTHO_MAX_STEPS = 32
+ZS_NORM_LAYER, ZS_NORM_RMS = 0, 1
+ZS_GATE_NONE, ZS_GATE_COLUMN, ZS_GATE_SIGMOID = 0, 1, 2
+ZS_BLOCKNORM_MAX_COLS = 16384
 # how a call's work is split into kernel launches (zero_shard.h)
 ZS_NORM_LAUNCH_LEN = 1 << 26
 ZS_WIDE_LAUNCH_LEN = 1 << 25
@@ -113,6 +116,31 @@ class zs_ortho_desc(ctypes.Structure):  # noqa: N801
     ]
 
 
+class zs_blocknorm_desc(ctypes.Structure):  # noqa: N801
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("param_dtype", ctypes.c_int32),
+        ("kind", ctypes.c_int32),
+        ("post", ctypes.c_int32),
+        ("gate", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("residual_scale", ctypes.c_float),
+        ("ld_x", ctypes.c_int64),
+        ("ld_block", ctypes.c_int64),
+        ("ld_gate", ctypes.c_int64),
+        ("ld_sum", ctypes.c_int64),
+        ("ld_y", ctypes.c_int64),
+        ("ld_dy", ctypes.c_int64),
+        ("ld_dsum", ctypes.c_int64),
+        ("ld_dx", ctypes.c_int64),
+        ("ld_dblock", ctypes.c_int64),
+        ("ld_dgate", ctypes.c_int64),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _handle_p = ctypes.c_void_p
 _lib.zero_shard_init.restype = ctypes.c_int
 _lib.zero_shard_init.argtypes = [ctypes.POINTER(zs_desc), ctypes.POINTER(_handle_p)]
@@ -191,6 +219,13 @@ _lib.zero_shard_ortho_workspace.argtypes = [ctypes.POINTER(zs_ortho_desc)]
 _lib.zero_shard_ortho.restype = ctypes.c_int
 _lib.zero_shard_ortho.argtypes = [ctypes.POINTER(zs_ortho_desc), ctypes.c_void_p, ctypes.c_void_p,
                                   ctypes.c_void_p, ctypes.c_int64]
+_lib.zero_shard_blocknorm.restype = ctypes.c_int
+_lib.zero_shard_blocknorm.argtypes = [ctypes.POINTER(zs_blocknorm_desc)] + [ctypes.c_void_p] * 10
+_lib.zero_shard_blocknorm_workspace.restype = ctypes.c_int64
+_lib.zero_shard_blocknorm_workspace.argtypes = [ctypes.POINTER(zs_blocknorm_desc)]
+_lib.zero_shard_blocknorm_bwd.restype = ctypes.c_int
+_lib.zero_shard_blocknorm_bwd.argtypes = ([ctypes.POINTER(zs_blocknorm_desc)]
+                                          + [ctypes.c_void_p] * 17 + [ctypes.c_int64])
 _lib.zero_shard_free.restype = ctypes.c_int
 _lib.zero_shard_free.argtypes = [_handle_p]
 _lib.zero_shard_strerror.restype = ctypes.c_char_p
@@ -208,7 +243,8 @@ EXPORTS = ("zero_shard_init", "zero_shard_gnorm", "zero_shard_gnorm_noalloc", "z
            "zero_shard_offload_params", "zero_shard_offload_wait", "zero_shard_offload_free",
            "zero_shard_layernorm", "zero_shard_layernorm_workspace", "zero_shard_layernorm_bwd",
            "zero_shard_muon_momentum", "zero_shard_muon_apply", "zero_shard_ortho_workspace",
-           "zero_shard_ortho", "zero_shard_free", "zero_shard_strerror", "zero_shard_len")
+           "zero_shard_ortho", "zero_shard_blocknorm", "zero_shard_blocknorm_workspace",
+           "zero_shard_blocknorm_bwd", "zero_shard_free", "zero_shard_strerror", "zero_shard_len")
 
 
 class ZeroShardError(RuntimeError):
@@ -524,6 +560,46 @@ def zero_shard_ortho(desc: zs_ortho_desc, g, o, workspace) -> int:
                                  _nbytes(workspace))
 
 
+_KINDS = {"layer": ZS_NORM_LAYER, "rms": ZS_NORM_RMS}
+_GATES = {"none": ZS_GATE_NONE, "column": ZS_GATE_COLUMN, "sigmoid": ZS_GATE_SIGMOID}
+
+
+def blocknorm_desc(*, rows: int, cols: int, dtype=torch.bfloat16, param_dtype=None,
+                   kind: str = "rms", post: bool = True, gate: str = "none", eps: float = 1e-5,
+                   residual_scale: float = 1.0, stream=None, **ld: int) -> zs_blocknorm_desc:
+    """kind: "layer" or "rms"; gate: "none", "column" or "sigmoid"; the rest as
+    for layernorm_desc."""
+    if kind not in _KINDS or gate not in _GATES:
+        raise ZeroShardError(ZS_EINVAL, f"kind {kind!r}, gate {gate!r}")
+    return zs_blocknorm_desc(
+        rows=int(rows), cols=int(cols), dtype=dtype_code(dtype),
+        param_dtype=dtype_code(dtype if param_dtype is None else param_dtype),
+        kind=_KINDS[kind], post=int(bool(post)), gate=_GATES[gate], eps=eps,
+        residual_scale=residual_scale, stream=_stream(stream), **ld)
+
+
+def zero_shard_blocknorm(desc: zs_blocknorm_desc, x, block, gate, gamma_post, beta_post, gamma,
+                         beta, sum_out, y, stats) -> int:
+    return _lib.zero_shard_blocknorm(ctypes.byref(desc),
+                                     *_ptrs(x, block, gate, gamma_post, beta_post, gamma, beta,
+                                            sum_out, y, stats))
+
+
+def zero_shard_blocknorm_workspace(desc: zs_blocknorm_desc) -> int:
+    return int(_lib.zero_shard_blocknorm_workspace(ctypes.byref(desc)))
+
+
+def zero_shard_blocknorm_bwd(desc: zs_blocknorm_desc, dy, dsum, total, block, gate, gamma_post,
+                             beta_post, gamma, stats, dx, dblock, dgate, dgamma_post, dbeta_post,
+                             dgamma, dbeta, workspace) -> int:
+    """workspace: a contiguous device tensor (its size in bytes is passed on)
+    or None."""
+    return _lib.zero_shard_blocknorm_bwd(
+        ctypes.byref(desc),
+        *_ptrs(dy, dsum, total, block, gate, gamma_post, beta_post, gamma, stats, dx, dblock,
+               dgate, dgamma_post, dbeta_post, dgamma, dbeta, workspace), _nbytes(workspace))
+
+
 # ------------------------------------------------------------ owner objects
 
 class ZeroShard:
@@ -704,6 +780,89 @@ class ZeroLayerNorm:
                               self.workspace), self._workspace_bytes)
         if rc:
             _check(rc, "zero_shard_layernorm_bwd")
+
+
+class ZeroBlockNorm:
+    """The seam between two blocks: the norm of a block's output (``post``), its
+    gate, the scaled residual sum and the norm before the next block, forward
+    and backward, with the saved statistics and the workspace of the gradients'
+    reduction.
+
+    ``kind``: "rms" or "layer", of both norms; ``gate``: "none", "column" (a
+    (cols,) parameter) or "sigmoid" (a (rows, cols) tensor z, of which the
+    sigmoid is taken).  Tensors, parameters and ``stream`` as for ZeroLayerNorm."""
+
+    def __init__(self, *, rows: int, cols: int, dtype=torch.bfloat16, param_dtype=None,
+                 kind: str = "rms", post: bool = True, gate: str = "none", eps: float = 1e-5,
+                 residual_scale: float = 1.0, stream=None):
+        self.dtype, self.param_dtype = dtype, dtype if param_dtype is None else param_dtype
+        self.shape, self.gate = (int(rows), int(cols)), gate
+        self._stream = torch.cuda.current_stream() if stream is None else stream
+        self.desc = blocknorm_desc(rows=rows, cols=cols, dtype=dtype, param_dtype=param_dtype,
+                                   kind=kind, post=post, gate=gate, eps=eps,
+                                   residual_scale=residual_scale, stream=self._stream)
+        self._ref = ctypes.byref(self.desc)
+        self._workspace_bytes = size = zero_shard_blocknorm_workspace(self.desc)
+        _require(size >= 0, "block norm's sizes")
+        with torch.cuda.stream(self._stream):
+            # rstd of the first norm and the second, then (layer) their means
+            self.stats = torch.zeros(4 if kind == "layer" else 2, rows, device="cuda")
+            self.workspace = torch.empty(size, device="cuda", dtype=torch.uint8)
+
+    _row = ZeroLayerNorm._row
+    _param = ZeroLayerNorm._param
+
+    def _gate(self, t, what: str) -> int:
+        """Row stride of an element gate or its gradient; 0 for other gates."""
+        if t is None or self.gate == "sigmoid":
+            return self._row(t, what)
+        self._param(t, what)
+        return 0
+
+    def forward(self, x, block, sum_out, y, *, gate=None, gamma_post=None, beta_post=None,
+                gamma=None, beta=None) -> None:
+        """sum_out = residual_scale x + gate N(block), y = N(sum_out); keeps the
+        rows' statistics for backward.  block and sum_out None: y = N(x)."""
+        d = self.desc
+        d.ld_x, d.ld_block = self._row(x, "x"), self._row(block, "block")
+        d.ld_sum, d.ld_y = self._row(sum_out, "sum_out"), self._row(y, "y")
+        d.ld_gate = self._gate(gate, "gate")
+        for t, what in ((gamma_post, "gamma_post"), (beta_post, "beta_post"), (gamma, "gamma"),
+                        (beta, "beta")):
+            if t is not None:
+                self._param(t, what)
+        rc = _lib.zero_shard_blocknorm(self._ref, *_ptrs(x, block, gate, gamma_post, beta_post,
+                                                         gamma, beta, sum_out, y, self.stats))
+        if rc:
+            _check(rc, "zero_shard_blocknorm")
+
+    def backward(self, dy, total, block, dx, dblock, *, dsum=None, gate=None, gamma_post=None,
+                 beta_post=None, gamma=None, dgate=None, dgamma_post=None, dbeta_post=None,
+                 dgamma=None, dbeta=None, stats=None) -> None:
+        """total: the forward pass's sum_out (x without a block); dsum: the
+        gradient that reaches it from elsewhere; stats: the saved statistics
+        (default: those of the last forward)."""
+        d = self.desc
+        d.ld_dy, d.ld_sum = self._row(dy, "dy"), self._row(total, "total")
+        d.ld_block, d.ld_dsum = self._row(block, "block"), self._row(dsum, "dsum")
+        d.ld_dx, d.ld_dblock = self._row(dx, "dx"), self._row(dblock, "dblock")
+        d.ld_gate, d.ld_dgate = self._gate(gate, "gate"), self._gate(dgate, "dgate")
+        for t, what in ((gamma_post, "gamma_post"), (beta_post, "beta_post"), (gamma, "gamma"),
+                        (dgamma_post, "dgamma_post"), (dbeta_post, "dbeta_post"),
+                        (dgamma, "dgamma"), (dbeta, "dbeta")):
+            if t is not None:
+                self._param(t, what)
+        if stats is None:
+            stats = self.stats
+        else:
+            _require(stats.shape == self.stats.shape and stats.dtype is torch.float32
+                     and stats.is_cuda and stats.is_contiguous(), "stats")
+        rc = _lib.zero_shard_blocknorm_bwd(
+            self._ref, *_ptrs(dy, dsum, total, block, gate, gamma_post, beta_post, gamma, stats,
+                              dx, dblock, dgate, dgamma_post, dbeta_post, dgamma, dbeta,
+                              self.workspace), self._workspace_bytes)
+        if rc:
+            _check(rc, "zero_shard_blocknorm_bwd")
 
 
 class ZeroOrtho:

@@ -1,0 +1,644 @@
+// zero_shard_seam.hip -- the seam between two blocks of a network, forward and
+// backward, on MI355X (gfx950) (declarations and the contract:
+// include/zero_shard.h).
+//
+//   forward   n = N0(block) gamma0 + beta0;  s = round(a x + gate n);
+//             y = N1(s) gamma + beta
+//   backward  D = N1'(dy gamma) + dsum;  dx = a D;  dn = gate D;
+//             dblock = N0'(dn gamma0);  the columns' sums of dy h1, dy, dn h0, dn
+//
+// N0 and N1 are layer or RMS norms (h: their values before gain and bias), N'
+// their transposed derivatives: rstd (g - mean(g) - h mean(g h)), without
+// mean(g) for RMS.  Everything is binary32 inside, each output rounded once.
+//
+// Both directions are HBM-bound: a row is read once, stays in registers between
+// its two norms (eight columns a thread, sixteen above 8192), and the next row
+// is loaded before this one is worked on.  A gate that is one number per column
+// factors out of the backward pass's sums: with E = D (or D times the
+// element's gate) every gradient of the first norm and the gate follows from
+// sum(E h0) and sum(E), so a thread carries four sums a column, whatever is asked
+// for.  A workgroup leaves one partial row of each, and a second launch adds them
+// in a fixed order: no atomics, so the same inputs give the same bits.
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "zero_shard.h"
+#include "zs_rows.h"
+
+namespace {
+
+using namespace zs_dev;
+
+constexpr int kThreads = 256;
+constexpr int kMaxCols = ZS_BLOCKNORM_MAX_COLS;  // sixteen columns of 1024 threads
+constexpr int kCus = 256;
+constexpr int kMaxParts = 256;  // partial rows of the columns' sums
+
+// sigmoid and its derivative; exp of a negative number only, so neither
+// overflows and 1 - sigmoid loses nothing
+__device__ __forceinline__ float sigmoid(float z, float &slope) {
+  const float t = expf(-fabsf(z)), inv = 1.0f / (1.0f + t);
+  slope = t * inv * inv;
+  return z < 0.0f ? t * inv : inv;  // of a NaN: a NaN
+}
+
+struct FwdArgs {
+  int64_t rows, cols;
+  int64_t ld_x, ld_b, ld_z, ld_s, ld_y;  // elements
+  const void *x, *block, *z;             // z: gates of elements (before the sigmoid)
+  const void *gate, *gamma0, *beta0, *gamma, *beta;
+  void *sum, *y;
+  float *stats;
+  float eps, scale;
+  int32_t center, post;
+  int32_t per;  // threads of a row
+};
+
+// R rows at a time, each over `per` threads (a multiple of 64) of the
+// workgroup's blockDim.x / per row groups.  TAIL: the columns are no multiple of 8,
+// or rows start anywhere.  WIDE: a gate for each element.
+template <class TX, class TP, int N, int R, bool TAIL, bool WIDE>
+__global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
+  __shared__ float lds[2][16][8];
+  const int per = A.per, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / per);
+  const int t = threadIdx.x - sub * per, subs = blockDim.x / per;
+  Sums sums{lds, sub * per / 64, per / 64};
+  const Columns<N> c(t, per, int(A.cols));
+  Eight<TP> gate[N], gamma0[N], beta0[N], gamma[N], beta[N];
+  load_params<TAIL>(gate, A.gate, 1.0f, c);
+  load_params<TAIL>(gamma0, A.gamma0, 1.0f, c);
+  load_params<TAIL>(beta0, A.beta0, 0.0f, c);
+  load_params<TAIL>(gamma, A.gamma, 1.0f, c);
+  load_params<TAIL>(beta, A.beta, 0.0f, c);
+  const float inv = 1.0f / float(A.cols);
+  const auto live = [&](int n, int e) { return (TAIL ? e : 0) < c.left[n]; };
+  constexpr bool kOnce = N == 1 && !TAIL && sizeof(typename TX::raw) == 2;
+  const int64_t step = int64_t(gridDim.x) * subs * R;
+  struct Rows {
+    Eight<TX> x[R][N], b[R][N], z[WIDE ? R : 1][WIDE ? N : 1];
+  };
+  const auto load = [&](Rows &v, int64_t r0) {
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int left = r0 + k < A.rows ? c.left[n] : 0;
+        v.x[k][n].template load<TAIL, kOnce>(row_of<TX>(A.x, r0 + k, A.ld_x), c.i[n], left);
+        v.b[k][n].template load<TAIL, kOnce>(row_of<TX>(A.block, r0 + k, A.ld_b), c.i[n],
+                                             A.block ? left : 0);
+        if constexpr (WIDE)
+          v.z[k][n].template load<TAIL, kOnce>(row_of<TX>(A.z, r0 + k, A.ld_z), c.i[n], left);
+      }
+  };
+  // Rows of values (zeros past their ends) to their normalised ones.
+  float v[R][N][8], mean[R], rstd[R];
+  const auto normalise = [&]() {
+    if (A.center) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        mean[k] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mean[k] += v[k][n][e];
+      }
+      sums.add(mean);
+      float both[2 * R];
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        mean[k] *= inv;
+        float sq = 0.0f, off = 0.0f;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float d = live(n, e) ? v[k][n][e] - mean[k] : 0.0f;
+            sq = __builtin_fmaf(d, d, sq);
+            off += d;
+            v[k][n][e] = d;
+          }
+        both[2 * k] = sq;
+        both[2 * k + 1] = off;
+      }
+      sums.add(both);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        float off = both[2 * k + 1];
+        rstd[k] = finish(both[2 * k], off, inv, A.eps, mean[k]);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[k][n][e] = (v[k][n][e] - off) * rstd[k];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        rstd[k] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) rstd[k] = __builtin_fmaf(v[k][n][e], v[k][n][e], rstd[k]);
+      }
+      sums.add(rstd);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        rstd[k] = 1.0f / sqrtf(rstd[k] * inv + A.eps);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[k][n][e] *= rstd[k];
+      }
+    }
+  };
+  const auto keep = [&](int64_t r0, int which) {
+    if (t != 0 || !A.stats) return;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (r0 + k < A.rows) {
+        A.stats[which * A.rows + r0 + k] = rstd[k];
+        if (A.center) A.stats[(which + 2) * A.rows + r0 + k] = mean[k];
+      }
+  };
+  // The next rows are on their way while these are worked on, where the
+  // registers hold both.
+  constexpr bool kAhead = N == 1;
+  Rows ahead;
+  if constexpr (kAhead) load(ahead, (int64_t(blockIdx.x) * subs + sub) * R);
+  for (int64_t first = int64_t(blockIdx.x) * subs * R; first < A.rows; first += step) {
+    const int64_t r0 = first + sub * R;
+    Rows now;
+    if constexpr (kAhead) {
+      now = ahead;
+      if (first + step < A.rows) load(ahead, r0 + step);
+    } else {
+      load(now, r0);
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int n = 0; n < N; ++n) now.b[k][n].get(v[k][n]);
+    if (A.post) {
+      normalise();
+      keep(r0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float g = v[k][n][e];
+          if (A.post) g = __builtin_fmaf(g, gamma0[n].get(e), beta0[n].get(e));
+          if constexpr (WIDE) {
+            float slope;
+            g *= sigmoid(now.z[k][n].get(e), slope);
+          } else {
+            g *= gate[n].get(e);
+          }
+          g = __builtin_fmaf(A.scale, now.x[k][n].get(e), g);
+          v[k][n][e] = live(n, e) ? g : 0.0f;
+        }
+        if (A.block) {
+          now.x[k][n].set(v[k][n]);
+          if (r0 + k < A.rows)
+            now.x[k][n].template store<TAIL>(row_of<TX>(A.sum, r0 + k, A.ld_s), c.i[n], c.left[n]);
+        }
+        now.x[k][n].get(v[k][n]);  // as it was rounded
+      }
+    normalise();
+    keep(r0, 1);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (r0 + k >= A.rows) break;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          v[k][n][e] = __builtin_fmaf(v[k][n][e], gamma[n].get(e), beta[n].get(e));
+        now.x[k][n].set(v[k][n]);
+        now.x[k][n].template store<TAIL>(row_of<TX>(A.y, r0 + k, A.ld_y), c.i[n], c.left[n]);
+      }
+    }
+  }
+}
+
+struct BwdArgs {
+  int64_t rows, cols;
+  int64_t ld_dy, ld_ds, ld_s, ld_b, ld_z, ld_dx, ld_db, ld_dz;  // elements
+  const void *dy, *dsum, *sum, *block, *z;
+  const void *gate, *gamma0, *beta0, *gamma;
+  const float *stats;
+  void *dx, *dblock, *dz;
+  void *dgate, *dgamma0, *dbeta0, *dgamma, *dbeta;  // of the columns
+  float *part;  // [4][parts][cols]: sums of dy h1, dy, E h0, E
+  float scale;
+  int32_t center, post;
+  int32_t want;   // 1: the sums of dy h1 and dy, 2: of E h0 and E
+  int32_t parts;  // 0: no rows (the gradients are zero)
+  int32_t per;    // threads of a row
+};
+
+template <class TX, class TP, int N, bool TAIL, bool WIDE>
+__global__ void __launch_bounds__(1024) seam_bwd_kernel(const BwdArgs A) {
+  __shared__ float lds[2][16][8];
+  __shared__ float join[1024 * 8];
+  const int per = A.per, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / per);
+  const int t = threadIdx.x - sub * per, subs = blockDim.x / per;
+  Sums sums{lds, sub * per / 64, per / 64};
+  const Columns<N> c(t, per, int(A.cols));
+  Eight<TP> gate[N], gamma0[N], beta0[N], gamma[N];
+  load_params<TAIL>(gate, A.gate, 1.0f, c);
+  load_params<TAIL>(gamma0, A.gamma0, 1.0f, c);
+  if constexpr (WIDE) load_params<TAIL>(beta0, A.beta0, 0.0f, c);
+  load_params<TAIL>(gamma, A.gamma, 1.0f, c);
+  const float inv = 1.0f / float(A.cols);
+  const auto live = [&](int n, int e) { return (TAIL ? e : 0) < c.left[n]; };
+  float acc[4][N][8] = {};
+  constexpr bool kOnce = N == 1 && !TAIL && sizeof(typename TX::raw) == 2;
+  const int64_t step = int64_t(gridDim.x) * subs;
+  struct Rows {
+    Eight<TX> dy[N], ds[N], s[N], b[N], z[WIDE ? N : 1];
+    float r0, r1, m0, m1;
+  };
+  const auto load = [&](Rows &v, int64_t r) {
+    const bool in = r < A.rows;
+    // a block that is not normalised is its own h0
+    v.r0 = !in ? 0.0f : A.post ? A.stats[r] : 1.0f;
+    v.r1 = in ? A.stats[A.rows + r] : 0.0f;
+    v.m0 = in && A.post && A.center ? A.stats[2 * A.rows + r] : 0.0f;
+    v.m1 = in && A.center ? A.stats[3 * A.rows + r] : 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int left = in ? c.left[n] : 0;
+      v.dy[n].template load<TAIL, kOnce>(row_of<TX>(A.dy, r, A.ld_dy), c.i[n], left);
+      v.s[n].template load<TAIL, kOnce>(row_of<TX>(A.sum, r, A.ld_s), c.i[n], left);
+      v.ds[n].template load<TAIL, kOnce>(row_of<TX>(A.dsum, r, A.ld_ds), c.i[n],
+                                         A.dsum ? left : 0);
+      v.b[n].template load<TAIL, kOnce>(row_of<TX>(A.block, r, A.ld_b), c.i[n],
+                                        A.block ? left : 0);
+      if constexpr (WIDE)
+        v.z[n].template load<TAIL, kOnce>(row_of<TX>(A.z, r, A.ld_z), c.i[n], left);
+    }
+  };
+  constexpr bool kAhead = N == 1;  // as in the forward pass
+  Rows ahead;
+  if constexpr (kAhead) load(ahead, int64_t(blockIdx.x) * subs + sub);
+  for (int64_t first = int64_t(blockIdx.x) * subs; first < A.rows; first += step) {
+    const int64_t r = first + sub;
+    Rows now;
+    if constexpr (kAhead) {
+      now = ahead;
+      if (first + step < A.rows) load(ahead, r + step);
+    } else {
+      load(now, r);
+    }
+    // Past a row's end the gradients are 0 and so are the factors they meet: rstd is
+    // taken as 0 there, since mean rstd may be beyond binary32.
+    const auto h1 = [&](int n, int e) {
+      return (now.s[n].get(e) - now.m1) * (live(n, e) ? now.r1 : 0.0f);
+    };
+    const auto h0 = [&](int n, int e) {
+      return (now.b[n].get(e) - now.m0) * (live(n, e) ? now.r0 : 0.0f);
+    };
+    float both[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float h = h1(n, e), d = now.dy[n].get(e), g = d * gamma[n].get(e);
+        acc[0][n][e] = __builtin_fmaf(d, h, acc[0][n][e]);
+        acc[1][n][e] += d;
+        both[0] += g;
+        both[1] = __builtin_fmaf(g, h, both[1]);
+      }
+    sums.add(both);
+    float c1 = A.center ? both[0] * inv : 0.0f, c2 = both[1] * inv;
+    float D[N][8];  // then, normalised through the gate, the gradient of h0
+    both[0] = both[1] = 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      now.dy[n].forget();
+      now.s[n].forget();
+      float out[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float g = now.dy[n].get(e) * gamma[n].get(e) - c1;
+        const float d = now.r1 * __builtin_fmaf(-h1(n, e), c2, g) + now.ds[n].get(e);
+        D[n][e] = live(n, e) ? d : 0.0f;
+        out[e] = A.scale * d;
+      }
+      now.dy[n].set(out);
+      if (r < A.rows)
+        now.dy[n].template store<TAIL>(row_of<TX>(A.dx, r, A.ld_dx), c.i[n], c.left[n]);
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float slope;
+          const float gain = sigmoid(now.z[n].get(e), slope);
+          float v = h0(n, e);
+          if (A.post) v = __builtin_fmaf(v, gamma0[n].get(e), beta0[n].get(e));
+          out[e] = D[n][e] * v * slope;
+          D[n][e] = live(n, e) ? D[n][e] * gain : 0.0f;
+        }
+        now.z[n].set(out);
+        if (r < A.rows && A.dz)
+          now.z[n].template store<TAIL>(row_of<TX>(A.dz, r, A.ld_dz), c.i[n], c.left[n]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float h = h0(n, e);
+        acc[2][n][e] = __builtin_fmaf(D[n][e], h, acc[2][n][e]);
+        acc[3][n][e] += D[n][e];
+        D[n][e] *= WIDE ? gamma0[n].get(e) : gamma0[n].get(e) * gate[n].get(e);
+        both[0] += D[n][e];
+        both[1] = __builtin_fmaf(D[n][e], h, both[1]);
+      }
+    }
+    if (!A.block) continue;
+    c1 = c2 = 0.0f;
+    if (A.post) {
+      sums.add(both);
+      c1 = A.center ? both[0] * inv : 0.0f;
+      c2 = both[1] * inv;
+    }
+    if (r >= A.rows) continue;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      now.b[n].forget();
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        D[n][e] = now.r0 * __builtin_fmaf(-h0(n, e), c2, D[n][e] - c1);
+      now.b[n].set(D[n]);
+      now.b[n].template store<TAIL>(row_of<TX>(A.dblock, r, A.ld_db), c.i[n], c.left[n]);
+    }
+  }
+  if (!A.part) return;
+  // the row groups' sums, then the workgroup's partial rows
+#pragma unroll
+  for (int which = 0; which < 4; ++which) {
+    if (!(A.want & (which < 2 ? 1 : 2))) continue;
+    float *out = A.part + (int64_t(which) * A.parts + blockIdx.x) * A.cols;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if (subs > 1) {
+        __syncthreads();
+        if (sub > 0) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) join[((sub - 1) * 8 + e) * per + t] = acc[which][n][e];
+        }
+        __syncthreads();
+        if (sub > 0) continue;
+        for (int w = 0; w < subs - 1; ++w)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[which][n][e] += join[(w * 8 + e) * per + t];
+      }
+      Eight<F32> v;
+      v.set(acc[which][n]);
+      v.template store<TAIL>(out, c.i[n], c.left[n]);
+    }
+  }
+}
+
+// The columns' gradients from the sums of the partial rows, which are added in
+// the partials' order within each of kSplit interleaved groups, the groups then in
+// order.  Four columns a thread; blockIdx.y 0: the second norm's, 1: the
+// first's and the gate's:
+//   dgamma0 = gate sum(E h0);  dbeta0 = gate sum(E);
+//   dgate = sum(D n) = gamma0 sum(E h0) + beta0 sum(E)   (one gate a column)
+constexpr int kSplit = 64;
+template <class TP>
+__global__ void __launch_bounds__(16 * kSplit) seam_join_kernel(const BwdArgs A) {
+  __shared__ float lds[2][kSplit][68];
+  struct __attribute__((packed, aligned(4))) Four {
+    float e[4];
+  };
+  const int first = blockIdx.y * 2;
+  if (!(A.want & (first ? 2 : 1))) return;
+  const int64_t c = int64_t(blockIdx.x) * 64 + threadIdx.x * 4;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float *p = A.part + int64_t(first + j) * A.parts * A.cols + c;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c + 4 <= A.cols) {
+#pragma unroll 8
+      for (int k = threadIdx.y; k < A.parts; k += kSplit) {
+        const Four v = *reinterpret_cast<const Four *>(p + k * A.cols);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += v.e[e];
+      }
+    } else {
+      for (int k = threadIdx.y; k < A.parts; k += kSplit)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < A.cols) s[e] += p[k * A.cols + e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) lds[j][threadIdx.y][threadIdx.x * 4 + e] = s[e];
+  }
+  __syncthreads();
+  const int t = threadIdx.y * 16 + threadIdx.x;
+  const int64_t col = int64_t(blockIdx.x) * 64 + t;
+  if (t >= 64 || col >= A.cols) return;
+  float sh = 0.0f, s1 = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kSplit; ++k) {
+    sh += lds[0][k][t];
+    s1 += lds[1][k][t];
+  }
+  const auto param = [&](const void *p, float none) {
+    return p ? TP::load(static_cast<const typename TP::raw *>(p)[col]) : none;
+  };
+  const auto put = [&](void *p, float v) {
+    if (p) static_cast<typename TP::raw *>(p)[col] = TP::store(v);
+  };
+  if (first == 0) {
+    put(A.dgamma, sh);
+    put(A.dbeta, s1);
+  } else {
+    const float gate = param(A.gate, 1.0f);
+    put(A.dgamma0, gate * sh);
+    put(A.dbeta0, gate * s1);
+    put(A.dgate, __builtin_fmaf(param(A.gamma0, 1.0f), sh, param(A.beta0, 0.0f) * s1));
+  }
+}
+
+// ------------------------------------------------------------------- host
+
+bool desc_ok(const zs_blocknorm_desc *d) {
+  if (!d || d->rows < 0 || d->cols < 1 || d->cols > kMaxCols) return false;
+  if (d->rows > (INT64_C(1) << 40)) return false;
+  if (!dtype_size(d->dtype)) return false;
+  if (d->param_dtype != ZS_F32 && d->param_dtype != d->dtype) return false;
+  if (d->kind != ZS_NORM_LAYER && d->kind != ZS_NORM_RMS) return false;
+  if (d->gate < ZS_GATE_NONE || d->gate > ZS_GATE_SIGMOID || d->post < 0 || d->post > 1)
+    return false;
+  if (!(d->eps >= 0.0f) || !std::isfinite(d->eps) || !std::isfinite(d->residual_scale))
+    return false;
+  const int64_t lds[] = {d->ld_x, d->ld_block, d->ld_gate, d->ld_sum, d->ld_y, d->ld_dy,
+                         d->ld_dsum, d->ld_dx, d->ld_dblock, d->ld_dgate};
+  for (int64_t ld : lds)
+    if (ld != 0 && (ld < d->cols || ld > (INT64_C(1) << 40))) return false;
+  return true;
+}
+
+// A row's threads, and the row groups of a workgroup; a workgroup for each row
+// where there are few.
+struct Way {
+  int n, per, subs;
+};
+Way way_of(const zs_blocknorm_desc &d, int threads) {
+  Way w;
+  w.n = d.cols <= kMaxCols / 2 ? 1 : 2;
+  w.per = int(up(up(d.cols, 8 * w.n) / (8 * w.n), 64));
+  w.subs = w.per < threads ? threads / w.per : 1;
+  if (d.rows < int64_t(kCus) * w.subs) w.subs = int((d.rows + kCus - 1) / kCus);
+  if (w.subs < 1) w.subs = 1;
+  return w;
+}
+
+int64_t parts_of(const zs_blocknorm_desc &d) {
+  const Way w = way_of(d, 1024);
+  const int64_t b = (d.rows + w.subs - 1) / w.subs;
+  return b < kMaxParts ? b : kMaxParts;
+}
+
+template <class F>
+int by_type(const zs_blocknorm_desc &d, F f) {
+  if (d.dtype == ZS_F32) return f(F32{}, F32{});
+  if (d.dtype == ZS_BF16)
+    return d.param_dtype == ZS_F32 ? f(Bf16{}, F32{}) : f(Bf16{}, Bf16{});
+  return d.param_dtype == ZS_F32 ? f(F16{}, F32{}) : f(F16{}, F16{});
+}
+
+template <class F>
+int by_way(int n, bool tail, bool wide, F f) {
+  using std::integral_constant;
+  const auto gates = [&](auto nn, auto tt) {
+    return wide ? f(nn, tt, std::true_type{}) : f(nn, tt, std::false_type{});
+  };
+  const auto tails = [&](auto nn) {
+    return tail ? gates(nn, std::true_type{}) : gates(nn, std::false_type{});
+  };
+  return n == 1 ? tails(integral_constant<int, 1>{}) : tails(integral_constant<int, 2>{});
+}
+
+// Without a block the seam is the second norm of x alone.
+bool no_block_ok(const zs_blocknorm_desc &d) {
+  return !d.post && d.gate == ZS_GATE_NONE && d.residual_scale == 1.0f;
+}
+
+}  // namespace
+
+extern "C" {
+
+int zero_shard_blocknorm(const zs_blocknorm_desc *d, const void *x, const void *block,
+                         const void *gate, const void *gamma_post, const void *beta_post,
+                         const void *gamma, const void *beta, void *sum, void *y, float *stats) {
+  if (!desc_ok(d)) return ZS_EINVAL;
+  if (d->rows == 0) return ZS_OK;
+  if (!x || !y || !block != !sum || y == sum || !gate != (d->gate == ZS_GATE_NONE))
+    return ZS_EINVAL;
+  if (!block && !no_block_ok(*d)) return ZS_EINVAL;
+  if (!d->post && (gamma_post || beta_post)) return ZS_EINVAL;
+  const int size = dtype_size(d->dtype), psize = dtype_size(d->param_dtype);
+  const bool wide = d->gate == ZS_GATE_SIGMOID;
+  if (!aligned(x, size) || !aligned(block, size) || !aligned(gate, wide ? size : psize) ||
+      !aligned(gamma_post, psize) || !aligned(beta_post, psize) || !aligned(gamma, psize) ||
+      !aligned(beta, psize) || !aligned(sum, size) || !aligned(y, size) || !aligned(stats, 4))
+    return ZS_EALIGN;
+  if (const int rc = device_is_gfx950()) return rc;
+  const auto ld = [&](int64_t v) { return v ? v : d->cols; };
+  const Way w = way_of(*d, kThreads);
+  const FwdArgs A{d->rows, d->cols, ld(d->ld_x), ld(d->ld_block), ld(d->ld_gate), ld(d->ld_sum),
+                  ld(d->ld_y), x, block, wide ? gate : nullptr, wide ? nullptr : gate, gamma_post,
+                  beta_post, gamma, beta, sum, y, stats, d->eps, d->residual_scale,
+                  d->kind == ZS_NORM_LAYER, d->post, w.per};
+  const bool even = rows_even(x, A.ld_x, size) && rows_even(block, A.ld_b, size) &&
+                    rows_even(A.z, A.ld_z, size) && rows_even(sum, A.ld_s, size) &&
+                    rows_even(y, A.ld_y, size);
+  const int threads = w.per * w.subs;
+  const int64_t groups = (A.rows + w.subs - 1) / w.subs;
+  const int64_t most = int64_t(kCus) * (2048 / threads);
+  return by_type(*d, [&](auto tx, auto tp) {
+    using TX = decltype(tx);
+    using TP = decltype(tp);
+    return by_way(w.n, d->cols % 8 != 0 || !even, wide, [&](auto n, auto tail, auto wd) {
+      hipLaunchKernelGGL((seam_fwd_kernel<TX, TP, n.value, 1, tail.value, wd.value>),
+                         dim3(unsigned(groups < most ? groups : most)), dim3(threads), 0,
+                         static_cast<hipStream_t>(d->stream), A);
+      return launched();
+    });
+  });
+}
+
+int64_t zero_shard_blocknorm_workspace(const zs_blocknorm_desc *d) {
+  if (!desc_ok(d)) return -1;
+  return 4 * parts_of(*d) * d->cols * int64_t(sizeof(float));
+}
+
+int zero_shard_blocknorm_bwd(const zs_blocknorm_desc *d, const void *dy, const void *dsum,
+                             const void *sum, const void *block, const void *gate,
+                             const void *gamma_post, const void *beta_post, const void *gamma,
+                             const float *stats, void *dx, void *dblock, void *dgate,
+                             void *dgamma_post, void *dbeta_post, void *dgamma, void *dbeta,
+                             void *workspace, int64_t workspace_bytes) {
+  if (!desc_ok(d)) return ZS_EINVAL;
+  const int size = dtype_size(d->dtype), psize = dtype_size(d->param_dtype);
+  const bool wide = d->gate == ZS_GATE_SIGMOID, column = d->gate == ZS_GATE_COLUMN;
+  const int want = (dgamma || dbeta ? 1 : 0) |
+                   (dgamma_post || dbeta_post || (column && dgate) ? 2 : 0);
+  if (!d->post && (gamma_post || beta_post || dgamma_post || dbeta_post)) return ZS_EINVAL;
+  if (d->gate == ZS_GATE_NONE && dgate) return ZS_EINVAL;
+  if (d->rows > 0) {
+    if (!dy || !sum || !stats || !dx || !block != !dblock || dx == dblock) return ZS_EINVAL;
+    if (!gate != (d->gate == ZS_GATE_NONE) || (!block && !no_block_ok(*d))) return ZS_EINVAL;
+    if (want && (!workspace || workspace_bytes < zero_shard_blocknorm_workspace(d)))
+      return ZS_EINVAL;
+  }
+  const int gsize = wide ? size : psize;
+  if (!aligned(dy, size) || !aligned(dsum, size) || !aligned(sum, size) || !aligned(block, size) ||
+      !aligned(gate, gsize) || !aligned(gamma_post, psize) || !aligned(beta_post, psize) ||
+      !aligned(gamma, psize) || !aligned(stats, 4) || !aligned(dx, size) ||
+      !aligned(dblock, size) || !aligned(dgate, gsize) || !aligned(dgamma_post, psize) ||
+      !aligned(dbeta_post, psize) || !aligned(dgamma, psize) || !aligned(dbeta, psize) ||
+      !aligned(workspace, 16))
+    return ZS_EALIGN;
+  if (d->rows == 0 && !want) return ZS_OK;
+  if (const int rc = device_is_gfx950()) return rc;
+  const auto ld = [&](int64_t v) { return v ? v : d->cols; };
+  const Way w = way_of(*d, 1024);
+  const BwdArgs A{d->rows, d->cols, ld(d->ld_dy), ld(d->ld_dsum), ld(d->ld_sum), ld(d->ld_block),
+                  ld(d->ld_gate), ld(d->ld_dx), ld(d->ld_dblock), ld(d->ld_dgate),
+                  dy, dsum, sum, block, wide ? gate : nullptr,
+                  wide ? nullptr : gate, gamma_post, beta_post, gamma, stats,
+                  dx, dblock, wide ? dgate : nullptr, column ? dgate : nullptr, dgamma_post,
+                  dbeta_post, dgamma, dbeta, want ? static_cast<float *>(workspace) : nullptr,
+                  d->residual_scale, d->kind == ZS_NORM_LAYER, d->post, want,
+                  int32_t(parts_of(*d)), w.per};
+  const bool even = rows_even(dy, A.ld_dy, size) && rows_even(dsum, A.ld_ds, size) &&
+                    rows_even(sum, A.ld_s, size) && rows_even(block, A.ld_b, size) &&
+                    rows_even(A.z, A.ld_z, size) && rows_even(dx, A.ld_dx, size) &&
+                    rows_even(dblock, A.ld_db, size) && rows_even(A.dz, A.ld_dz, size);
+  const hipStream_t st = static_cast<hipStream_t>(d->stream);
+  return by_type(*d, [&](auto tx, auto tp) {
+    using TX = decltype(tx);
+    using TP = decltype(tp);
+    int rc = ZS_OK;
+    if (A.rows > 0)
+      rc = by_way(w.n, d->cols % 8 != 0 || !even, wide, [&](auto n, auto tail, auto wd) {
+        hipLaunchKernelGGL((seam_bwd_kernel<TX, TP, n.value, tail.value, wd.value>),
+                           dim3(unsigned(A.parts)), dim3(w.per * w.subs), 0, st, A);
+        return launched();
+      });
+    if (rc || !want) return rc;
+    hipLaunchKernelGGL((seam_join_kernel<TP>), dim3(unsigned((A.cols + 63) / 64), 2),
+                       dim3(16, kSplit), 0, st, A);
+    return launched();
+  });
+}
+
+}  // extern "C"
