@@ -568,6 +568,50 @@ int zero_shard_blocknorm_bwd(const zs_blocknorm_desc *d, const void *dy, const v
                              void *dgamma_post, void *dbeta_post, void *dgamma, void *dbeta,
                              void *workspace, int64_t workspace_bytes);
 
+/* ---------------------------------------------------------------------------
+ * The embedding of tokens, and the gradient of its table.  No handle; launches
+ * only, as for layer norm.  The table may be a rank's part of a larger one: its
+ * rows stand for the ids first, first + 1, ..; other ids (negative ones too)
+ * belong to other ranks, give rows of zeros and no gradient, so that the ranks'
+ * outputs add up to the whole table's. */
+#define ZS_EMBEDDING_MAX_TOKENS (INT64_C(1) << 27)
+#define ZS_EMBEDDING_MAX_VOCAB INT64_C(0x7fffffff)
+typedef struct zs_embedding_desc {
+  int64_t tokens;      /* 0 .. ZS_EMBEDDING_MAX_TOKENS                        */
+  int64_t vocab;       /* rows of the table, 1 .. ZS_EMBEDDING_MAX_VOCAB      */
+  int64_t cols;        /* 1 .. 2^20                                           */
+  int64_t first;       /* the id of the table's first row; the last row's has to fit */
+  int64_t padding;     /* an id whose tokens give no gradient                 */
+  int32_t pad_set;     /* 1: padding counts; 0: there is none                 */
+  int32_t id_bytes;    /* 4 or 8: ids are int32_t or int64_t                  */
+  int32_t dtype;       /* zs_dtype of y and dy                                */
+  int32_t table_dtype; /* of table: ZS_F32 or dtype                           */
+  int32_t grad_dtype;  /* of dtable: ZS_F32 or dtype                          */
+  int32_t accumulate;  /* 1: dtable is added to; 0: it is written             */
+  float scale;         /* finite                                              */
+  int64_t ld_table, ld_y, ld_dy, ld_dtable; /* row strides in elements (0: cols) */
+  void *stream;        /* hipStream_t, NULL = null stream                     */
+} zs_embedding_desc;
+
+/* y[t] = scale table[ids[t] - first] (binary32, rounded once), zeros where that is
+ * no row of the table.  ids: tokens of them; table: vocab x cols; y: tokens x
+ * cols, overlapping nothing.  Errors: ZS_EINVAL, ZS_EALIGN (a pointer not aligned to
+ * its element), ZS_EDEVICE, ZS_EHIP. */
+int zero_shard_embedding(const zs_embedding_desc *d, const void *ids, const void *table, void *y);
+
+/* Bytes of workspace that zero_shard_embedding_bwd needs for d, or -1 for an
+ * invalid descriptor. */
+int64_t zero_shard_embedding_workspace(const zs_embedding_desc *d);
+
+/* dtable[v] = scale sum dy[t] over the tokens t of row v, in binary32 and in the
+ * order of t: runs of 32 tokens of the row each, the runs then in order (eight stretches
+ * of runs side by side); rounded once.  accumulate: dtable[v] + that, rounded
+ * once; rows without tokens are left as they are.  Otherwise they become zeros.
+ * dtable overlaps nothing; workspace: device, 256-byte aligned, at least
+ * zero_shard_embedding_workspace(d) bytes.  Errors: as above. */
+int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const void *dy,
+                             void *dtable, void *workspace, int64_t workspace_bytes);
+
 /* Wait for the handle's stream, release its scratch and the handle.
  * Passing NULL is a no-op returning ZS_OK. */
 int zero_shard_free(zs_handle *h);

@@ -25,6 +25,7 @@ ZS_ORTHO_MAX_STEPS = 32
 ZS_NORM_LAYER, ZS_NORM_RMS = 0, 1
 ZS_GATE_NONE, ZS_GATE_COLUMN, ZS_GATE_SIGMOID = 0, 1, 2
 ZS_BLOCKNORM_MAX_COLS = 16384
+ZS_EMBEDDING_MAX_TOKENS, ZS_EMBEDDING_MAX_VOCAB = 1 << 27, (1 << 31) - 1
 # how a call's work is split into kernel launches (zero_shard.h)
 ZS_NORM_LAUNCH_LEN = 1 << 26
 ZS_WIDE_LAUNCH_LEN = 1 << 25
@@ -141,6 +142,28 @@ class zs_blocknorm_desc(ctypes.Structure):  # noqa: N801
     ]
 
 
+class zs_embedding_desc(ctypes.Structure):  # noqa: N801
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("vocab", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("first", ctypes.c_int64),
+        ("padding", ctypes.c_int64),
+        ("pad_set", ctypes.c_int32),
+        ("id_bytes", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("table_dtype", ctypes.c_int32),
+        ("grad_dtype", ctypes.c_int32),
+        ("accumulate", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("ld_table", ctypes.c_int64),
+        ("ld_y", ctypes.c_int64),
+        ("ld_dy", ctypes.c_int64),
+        ("ld_dtable", ctypes.c_int64),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _handle_p = ctypes.c_void_p
 _lib.zero_shard_init.restype = ctypes.c_int
 _lib.zero_shard_init.argtypes = [ctypes.POINTER(zs_desc), ctypes.POINTER(_handle_p)]
@@ -226,6 +249,13 @@ _lib.zero_shard_blocknorm_workspace.argtypes = [ctypes.POINTER(zs_blocknorm_desc
 _lib.zero_shard_blocknorm_bwd.restype = ctypes.c_int
 _lib.zero_shard_blocknorm_bwd.argtypes = ([ctypes.POINTER(zs_blocknorm_desc)]
                                           + [ctypes.c_void_p] * 17 + [ctypes.c_int64])
+_lib.zero_shard_embedding.restype = ctypes.c_int
+_lib.zero_shard_embedding.argtypes = [ctypes.POINTER(zs_embedding_desc)] + [ctypes.c_void_p] * 3
+_lib.zero_shard_embedding_workspace.restype = ctypes.c_int64
+_lib.zero_shard_embedding_workspace.argtypes = [ctypes.POINTER(zs_embedding_desc)]
+_lib.zero_shard_embedding_bwd.restype = ctypes.c_int
+_lib.zero_shard_embedding_bwd.argtypes = ([ctypes.POINTER(zs_embedding_desc)]
+                                          + [ctypes.c_void_p] * 4 + [ctypes.c_int64])
 _lib.zero_shard_free.restype = ctypes.c_int
 _lib.zero_shard_free.argtypes = [_handle_p]
 _lib.zero_shard_strerror.restype = ctypes.c_char_p
@@ -244,7 +274,8 @@ EXPORTS = ("zero_shard_init", "zero_shard_gnorm", "zero_shard_gnorm_noalloc", "z
            "zero_shard_layernorm", "zero_shard_layernorm_workspace", "zero_shard_layernorm_bwd",
            "zero_shard_muon_momentum", "zero_shard_muon_apply", "zero_shard_ortho_workspace",
            "zero_shard_ortho", "zero_shard_blocknorm", "zero_shard_blocknorm_workspace",
-           "zero_shard_blocknorm_bwd", "zero_shard_free", "zero_shard_strerror", "zero_shard_len")
+           "zero_shard_blocknorm_bwd", "zero_shard_embedding", "zero_shard_embedding_workspace",
+           "zero_shard_embedding_bwd", "zero_shard_free", "zero_shard_strerror", "zero_shard_len")
 
 
 class ZeroShardError(RuntimeError):
@@ -600,6 +631,41 @@ def zero_shard_blocknorm_bwd(desc: zs_blocknorm_desc, dy, dsum, total, block, ga
                dgate, dgamma_post, dbeta_post, dgamma, dbeta, workspace), _nbytes(workspace))
 
 
+def embedding_desc(*, tokens: int, vocab: int, cols: int, dtype=torch.bfloat16, table_dtype=None,
+                   grad_dtype=None, scale: float = 1.0, first: int = 0, padding: int | None = None,
+                   id_dtype=torch.int64, accumulate: bool = False, stream=None,
+                   **ld: int) -> zs_embedding_desc:
+    """table_dtype, grad_dtype: of the table and its gradient (default: dtype);
+    padding: the id that gives no gradient; id_dtype: torch.int64 or torch.int32;
+    ld: the row strides ld_table, ... that are not cols."""
+    if id_dtype not in _ID_BYTES:
+        raise ZeroShardError(ZS_EINVAL, f"id_dtype {id_dtype}")
+    return zs_embedding_desc(
+        tokens=int(tokens), vocab=int(vocab), cols=int(cols), first=int(first),
+        padding=0 if padding is None else int(padding), pad_set=int(padding is not None),
+        id_bytes=_ID_BYTES[id_dtype], dtype=dtype_code(dtype),
+        table_dtype=dtype_code(dtype if table_dtype is None else table_dtype),
+        grad_dtype=dtype_code(dtype if grad_dtype is None else grad_dtype),
+        accumulate=int(bool(accumulate)), scale=scale, stream=_stream(stream), **ld)
+
+
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def zero_shard_embedding(desc: zs_embedding_desc, ids, table, y) -> int:
+    return _lib.zero_shard_embedding(ctypes.byref(desc), *_ptrs(ids, table, y))
+
+
+def zero_shard_embedding_workspace(desc: zs_embedding_desc) -> int:
+    return int(_lib.zero_shard_embedding_workspace(ctypes.byref(desc)))
+
+
+def zero_shard_embedding_bwd(desc: zs_embedding_desc, ids, dy, dtable, workspace) -> int:
+    """workspace: a contiguous device tensor (its size in bytes is passed on)."""
+    return _lib.zero_shard_embedding_bwd(ctypes.byref(desc), *_ptrs(ids, dy, dtable, workspace),
+                                         _nbytes(workspace))
+
+
 # ------------------------------------------------------------ owner objects
 
 class ZeroShard:
@@ -863,6 +929,82 @@ class ZeroBlockNorm:
                               self.workspace), self._workspace_bytes)
         if rc:
             _check(rc, "zero_shard_blocknorm_bwd")
+
+
+class ZeroEmbedding:
+    """The embedding of tokens out of a (vocab, cols) table, scaled, and the
+    gradient of the table, with its workspace.
+
+    The table's rows stand for the ids ``first``, ``first`` + 1, ...; other ids
+    give rows of zeros and no gradient (a table split over ranks); tokens of the id
+    ``padding`` give no gradient.  ids: contiguous, ``tokens`` of them in any shape;
+    y and dy: (tokens, cols) of ``dtype``; the table and its gradient of
+    ``table_dtype`` and ``grad_dtype`` (default: dtype).  Column stride 1, no
+    rows that overlap; ``stream`` as for ZeroLayerNorm."""
+
+    def __init__(self, *, tokens: int, vocab: int, cols: int, dtype=torch.bfloat16,
+                 table_dtype=None, grad_dtype=None, scale: float = 1.0, first: int = 0,
+                 padding: int | None = None, id_dtype=torch.int64, stream=None):
+        self.dtype, self.id_dtype = dtype, id_dtype
+        self.table_dtype = dtype if table_dtype is None else table_dtype
+        self.grad_dtype = dtype if grad_dtype is None else grad_dtype
+        self.rows, self.shape = (int(vocab), int(cols)), (int(tokens), int(cols))
+        self._stream = torch.cuda.current_stream() if stream is None else stream
+        self.desc = embedding_desc(tokens=tokens, vocab=vocab, cols=cols, dtype=dtype,
+                                   table_dtype=table_dtype, grad_dtype=grad_dtype, scale=scale,
+                                   first=first, padding=padding, id_dtype=id_dtype,
+                                   stream=self._stream)
+        self._ref = ctypes.byref(self.desc)
+        self._workspace_bytes = size = zero_shard_embedding_workspace(self.desc)
+        _require(size >= 0, "embedding's sizes")
+        self._workspace = None
+
+    @property
+    def workspace(self):
+        """Of the backward pass, from its first call on."""
+        if self._workspace is None:
+            with torch.cuda.stream(self._stream):
+                self._workspace = torch.empty(self._workspace_bytes, device="cuda",
+                                              dtype=torch.uint8)
+        return self._workspace
+
+    def _ids(self, ids) -> None:
+        if (ids.numel() != self.shape[0] or ids.dtype is not self.id_dtype or not ids.is_cuda
+                or not ids.is_contiguous()):
+            raise ZeroShardError(ZS_EINVAL, "ids")
+
+    @staticmethod
+    def _matrix(t, shape, dtype, what: str) -> int:
+        """Row stride of a matrix; 0 for a single row."""
+        if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
+            raise ZeroShardError(ZS_EINVAL, what)
+        (rows, cols), (ld, unit) = shape, t.stride()
+        if (unit != 1 and cols != 1) or (rows > 1 and ld < cols):
+            raise ZeroShardError(ZS_EINVAL, what)
+        return ld if rows > 1 else 0
+
+    def forward(self, ids, table, y) -> None:
+        """y = scale table[ids - first]."""
+        d = self.desc
+        self._ids(ids)
+        d.ld_table = self._matrix(table, self.rows, self.table_dtype, "table")
+        d.ld_y = self._matrix(y, self.shape, self.dtype, "y")
+        rc = _lib.zero_shard_embedding(self._ref, *_ptrs(ids, table, y))
+        if rc:
+            _check(rc, "zero_shard_embedding")
+
+    def backward(self, ids, dy, dtable, accumulate: bool = False) -> None:
+        """dtable = the table's gradient (all of its rows), or, with
+        ``accumulate``, dtable + that."""
+        d = self.desc
+        self._ids(ids)
+        d.ld_dy = self._matrix(dy, self.shape, self.dtype, "dy")
+        d.ld_dtable = self._matrix(dtable, self.rows, self.grad_dtype, "dtable")
+        d.accumulate = 1 if accumulate else 0
+        rc = _lib.zero_shard_embedding_bwd(self._ref, *_ptrs(ids, dy, dtable, self.workspace),
+                                           self._workspace_bytes)
+        if rc:
+            _check(rc, "zero_shard_embedding_bwd")
 
 
 class ZeroOrtho:
