@@ -612,6 +612,109 @@ int64_t zero_shard_embedding_workspace(const zs_embedding_desc *d);
 int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const void *dy,
                              void *dtable, void *workspace, int64_t workspace_bytes);
 
+/* ---------------------------------------------------------------------------
+ * AdamW over many tensors at once: what Muon leaves, or whole models.  Each
+ * tensor has its own length, weight decay and learning-rate factor, gradients of
+ * its own type, and moments in 32 or in 8 bits.  One launch takes up to 440
+ * tensors (further ones follow in launches of their own).
+ *
+ * A plan of the tensors is filled on the host, and copied to device memory by the
+ * caller, once; the calls take both copies.  They queue kernel launches only, so
+ * they can be captured in a HIP graph (with the gradients' addresses of the
+ * capture).  Calls of one plan must not overlap.  Same inputs => same bits.
+ *
+ * Arithmetic, element i of a tensor, gradient g:
+ *   g'  = coef g, coef as in zero_shard_step (1 without clipping)
+ *   m'  = b1 m + (1-b1) g'      v' = b2 v + (1-b2) g'^2
+ *   theta' = theta - (lr f wd) theta - lr f (m'/bc1) / (sqrt(v'/bc2) + eps)
+ * with the tensor's lr_scale f and weight_decay wd, in binary64 from the stored
+ * values, each result rounded once to binary32: with n_d = 1 and a bf16
+ * gradient whose values are the averages, zero_shard_step's bits.
+ *
+ * ZS_STATE_8: m and r = sqrt(v) are each an e4m3 number (sign, 4 bits of exponent with
+ * bias 7, 3 of mantissa; no infinities) times the scale of its block, the
+ * tensor's elements [256 b, 256 b + 256); m = binary32(number scale), v = r r.  Storing
+ * binary32 values x of a block (of m', or of sqrt(v')):
+ *   top = max |x|;  scale = top / 256
+ *   q = min(binary32(|x| binary32(1 / top)), 1) is rounded to an e4m3 number of
+ *   256 q by chance, down or up in proportion to how near each is: bits(q 2^-112) +
+ *   16 d + 8, cut after 3 bits of mantissa.  d is 16 bits of h (the lower ones for m,
+ *   the upper ones for r):
+ *   h = mix(mix(key + c (k + 1)) + c mix(i >> 32) + i), modulo 2^32, k the tensor's number,
+ *   c = 0x9e3779b9, mix(x): x ^= x >> 16; x *= 0x6a09e667; x ^= x >> 15;
+ *   x *= 0xbb67ae85; x ^= x >> 16
+ * so that the average of what is stored is what was computed: to nearest, a moment
+ * whose step is below half a step of the type (v's, with beta2 = 0.999) would never
+ * move.  r' > 0 does not become 0.  top < 2^-126: the block is zeros.  A block that
+ * holds an infinity or NaN has no finite values from then on.  All zeros are the state
+ * at the start. */
+#define ZS_ADAMW_BLOCK 256
+#define ZS_ADAMW_MAX_TENSORS (INT64_C(1) << 20)
+#define ZS_ADAMW_MAX_ELEMENTS (INT64_C(1) << 34) /* of a tensor; all together
+                                     take at most 2^23 - 1 chunks of 4096 */
+typedef enum zs_state { ZS_STATE_32 = 0, ZS_STATE_8 = 1 } zs_state;
+
+/* A tensor.  All arrays are flat and contiguous, aligned to their elements; *_out
+ * may be the *_in of the same tensor, otherwise outputs overlap nothing (a plan whose
+ * outputs overlap each other is refused). */
+typedef struct zs_adamw_tensor {
+  int64_t n;                 /* elements, >= 0                                */
+  const float *master_in;    /* fp32[n]                                       */
+  float *master_out;
+  const void *m_in, *v_in;   /* fp32[n], or e4m3 bytes [n] of m and sqrt(v)   */
+  void *m_out, *v_out;
+  const float *m_scale_in, *v_scale_in; /* fp32[ceil(n / 256)], 8 bits only:  */
+  float *m_scale_out, *v_scale_out;     /* NULL with 32                       */
+  void *param_out;           /* NULL, or the 16-bit copy of the new weights   */
+  float weight_decay, lr_scale; /* >= 0                                       */
+  int32_t state;             /* zs_state                                      */
+  int32_t grad_dtype;        /* zs_dtype of its gradient                      */
+  int32_t param_dtype;       /* of param_out: ZS_BF16 or ZS_F16               */
+} zs_adamw_tensor;
+
+typedef struct zs_adamw_desc {
+  int64_t count;             /* tensors, 0 .. ZS_ADAMW_MAX_TENSORS            */
+  float beta1, beta2, eps;   /* as in zs_desc                                 */
+  int32_t bias_correction;   /* 0 or 1                                        */
+  float max_norm;            /* > 0: clip by the global norm; <= 0: no        */
+  void *stream;              /* hipStream_t, NULL = null stream               */
+} zs_adamw_desc;
+
+/* Bytes of a plan of d->count tensors (a HOST array), or -1 where a count or a
+ * length is out of range (or all of them together). */
+int64_t zero_shard_adamw_plan_bytes(const zs_adamw_desc *d, const zs_adamw_tensor *tensors);
+
+/* Fill a plan (HOST memory, 16-byte aligned).  The caller then copies it to
+ * device memory, 256-byte aligned, plan_bytes long, and keeps both for the calls
+ * below; the device copy also holds the norm's partial sums.  Tensors keep the
+ * addresses given here.  Errors: ZS_EINVAL, ZS_EALIGN, ZS_ENOMEM. */
+int zero_shard_adamw_plan(const zs_adamw_desc *d, const zs_adamw_tensor *tensors, void *plan,
+                          int64_t plan_bytes);
+
+/* The sum of squares of all gradients (binary64, a fixed order), to *sumsq_dev
+ * (device).  grads: HOST array of count device pointers, aligned to their elements
+ * (NULL for an empty tensor).  Summed over ranks whose tensors differ it is the step's
+ * global_sumsq_dev.  Errors: ZS_EINVAL, ZS_EALIGN, ZS_EDEVICE, ZS_EHIP. */
+int zero_shard_adamw_gnorm(const zs_adamw_desc *d, const void *plan, void *plan_dev,
+                           const void *const *grads, double *sumsq_dev);
+
+/* The step t >= 1 at learning rate lr >= 0.  key: any number, another one each step
+ * (the step's own will do); it is used by 8-bit states only.  global_sumsq_dev: iff
+ * max_norm > 0.  Errors: ZS_EINVAL, ZS_EALIGN, ZS_EDEVICE, ZS_EHIP. */
+int zero_shard_adamw(const zs_adamw_desc *d, const void *plan, void *plan_dev,
+                     const void *const *grads, float lr, int64_t t, uint32_t key,
+                     const double *global_sumsq_dev);
+
+/* The step with its constants read on the device when the kernel runs, so that a
+ * captured step serves every step: consts_dev (device, 4 doubles, 8-byte aligned) as
+ * zero_shard_adamw_consts writes them (HOST): lr, bc1, bc2, key.  They are trusted as
+ * given.  Errors: as above. */
+int zero_shard_adamw_consts(const zs_adamw_desc *d, float lr, int64_t t, uint32_t key,
+                            double *out);
+int zero_shard_adamw_dev(const zs_adamw_desc *d, const void *plan, void *plan_dev,
+                         const void *const *grads, const double *consts_dev,
+                         const double *global_sumsq_dev);
+
 /* Wait for the handle's stream, release its scratch and the handle.
  * Passing NULL is a no-op returning ZS_OK. */
 int zero_shard_free(zs_handle *h);

@@ -25,6 +25,8 @@ ZS_ORTHO_MAX_STEPS = 32
 ZS_NORM_LAYER, ZS_NORM_RMS = 0, 1
 ZS_GATE_NONE, ZS_GATE_COLUMN, ZS_GATE_SIGMOID = 0, 1, 2
 ZS_BLOCKNORM_MAX_COLS = 16384
+ZS_ADAMW_BLOCK, ZS_ADAMW_MAX_TENSORS, ZS_ADAMW_MAX_ELEMENTS = 256, 1 << 20, 1 << 34
+ZS_STATE_32, ZS_STATE_8 = 0, 1
 ZS_EMBEDDING_MAX_TOKENS, ZS_EMBEDDING_MAX_VOCAB = 1 << 27, (1 << 31) - 1
 # how a call's work is split into kernel launches (zero_shard.h)
 ZS_NORM_LAUNCH_LEN = 1 << 26
@@ -164,6 +166,40 @@ class zs_embedding_desc(ctypes.Structure):  # noqa: N801
     ]
 
 
+class zs_adamw_tensor(ctypes.Structure):  # noqa: N801
+    _fields_ = [
+        ("n", ctypes.c_int64),
+        ("master_in", ctypes.c_void_p),
+        ("master_out", ctypes.c_void_p),
+        ("m_in", ctypes.c_void_p),
+        ("v_in", ctypes.c_void_p),
+        ("m_out", ctypes.c_void_p),
+        ("v_out", ctypes.c_void_p),
+        ("m_scale_in", ctypes.c_void_p),
+        ("v_scale_in", ctypes.c_void_p),
+        ("m_scale_out", ctypes.c_void_p),
+        ("v_scale_out", ctypes.c_void_p),
+        ("param_out", ctypes.c_void_p),
+        ("weight_decay", ctypes.c_float),
+        ("lr_scale", ctypes.c_float),
+        ("state", ctypes.c_int32),
+        ("grad_dtype", ctypes.c_int32),
+        ("param_dtype", ctypes.c_int32),
+    ]
+
+
+class zs_adamw_desc(ctypes.Structure):  # noqa: N801
+    _fields_ = [
+        ("count", ctypes.c_int64),
+        ("beta1", ctypes.c_float),
+        ("beta2", ctypes.c_float),
+        ("eps", ctypes.c_float),
+        ("bias_correction", ctypes.c_int32),
+        ("max_norm", ctypes.c_float),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _handle_p = ctypes.c_void_p
 _lib.zero_shard_init.restype = ctypes.c_int
 _lib.zero_shard_init.argtypes = [ctypes.POINTER(zs_desc), ctypes.POINTER(_handle_p)]
@@ -256,6 +292,22 @@ _lib.zero_shard_embedding_workspace.argtypes = [ctypes.POINTER(zs_embedding_desc
 _lib.zero_shard_embedding_bwd.restype = ctypes.c_int
 _lib.zero_shard_embedding_bwd.argtypes = ([ctypes.POINTER(zs_embedding_desc)]
                                           + [ctypes.c_void_p] * 4 + [ctypes.c_int64])
+_adamw_call = [ctypes.POINTER(zs_adamw_desc), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
+_lib.zero_shard_adamw_plan_bytes.restype = ctypes.c_int64
+_lib.zero_shard_adamw_plan_bytes.argtypes = [ctypes.POINTER(zs_adamw_desc), ctypes.c_void_p]
+_lib.zero_shard_adamw_plan.restype = ctypes.c_int
+_lib.zero_shard_adamw_plan.argtypes = [ctypes.POINTER(zs_adamw_desc), ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_int64]
+_lib.zero_shard_adamw_gnorm.restype = ctypes.c_int
+_lib.zero_shard_adamw_gnorm.argtypes = _adamw_call + [ctypes.c_void_p]
+_lib.zero_shard_adamw.restype = ctypes.c_int
+_lib.zero_shard_adamw.argtypes = _adamw_call + [ctypes.c_float, ctypes.c_int64, ctypes.c_uint32,
+                                                ctypes.c_void_p]
+_lib.zero_shard_adamw_consts.restype = ctypes.c_int
+_lib.zero_shard_adamw_consts.argtypes = [ctypes.POINTER(zs_adamw_desc), ctypes.c_float,
+                                         ctypes.c_int64, ctypes.c_uint32, ctypes.c_void_p]
+_lib.zero_shard_adamw_dev.restype = ctypes.c_int
+_lib.zero_shard_adamw_dev.argtypes = _adamw_call + [ctypes.c_void_p, ctypes.c_void_p]
 _lib.zero_shard_free.restype = ctypes.c_int
 _lib.zero_shard_free.argtypes = [_handle_p]
 _lib.zero_shard_strerror.restype = ctypes.c_char_p
@@ -275,7 +327,9 @@ EXPORTS = ("zero_shard_init", "zero_shard_gnorm", "zero_shard_gnorm_noalloc", "z
            "zero_shard_muon_momentum", "zero_shard_muon_apply", "zero_shard_ortho_workspace",
            "zero_shard_ortho", "zero_shard_blocknorm", "zero_shard_blocknorm_workspace",
            "zero_shard_blocknorm_bwd", "zero_shard_embedding", "zero_shard_embedding_workspace",
-           "zero_shard_embedding_bwd", "zero_shard_free", "zero_shard_strerror", "zero_shard_len")
+           "zero_shard_embedding_bwd", "zero_shard_adamw_plan_bytes", "zero_shard_adamw_plan",
+           "zero_shard_adamw_gnorm", "zero_shard_adamw", "zero_shard_adamw_consts",
+           "zero_shard_adamw_dev", "zero_shard_free", "zero_shard_strerror", "zero_shard_len")
 
 
 class ZeroShardError(RuntimeError):
@@ -666,6 +720,106 @@ def zero_shard_embedding_bwd(desc: zs_embedding_desc, ids, dy, dtable, workspace
                                          _nbytes(workspace))
 
 
+def adamw_tensor(master, m, v, *, param_out=None, m_scale=None, v_scale=None, master_out=None,
+                 m_out=None, v_out=None, m_scale_out=None, v_scale_out=None,
+                 grad_dtype=torch.bfloat16, weight_decay: float = 0.0,
+                 lr_scale: float = 1.0) -> zs_adamw_tensor:
+    """A tensor of an AdamW plan, from contiguous device tensors of any shape.
+    master: float32; m, v: float32, or, for a state in 8 bits, float8_e4m3fn (or uint8
+    patterns) of m and sqrt(v) with their scales, float32[ceil(n / 256)];
+    param_out: bfloat16 or float16, or None; *_out: where the results go (default: in
+    place).  The struct keeps the tensors alive."""
+    n = master.numel()
+    eight = m.dtype in _E4M3_LIKE
+    scales = (n + ZS_ADAMW_BLOCK - 1) // ZS_ADAMW_BLOCK
+    state = _E4M3_LIKE if eight else (torch.float32,)
+    ins = {"master": master, "m": m, "v": v, "m_scale": m_scale, "v_scale": v_scale}
+    outs = {"master": master_out, "m": m_out, "v": v_out, "m_scale": m_scale_out,
+            "v_scale": v_scale_out}
+    outs = {k: ins[k] if t is None else t for k, t in outs.items()}
+    for what, types, size in (("master", (torch.float32,), n), ("m", state, n), ("v", state, n),
+                              ("m_scale", (torch.float32,), scales),
+                              ("v_scale", (torch.float32,), scales)):
+        for t in (ins[what], outs[what]):
+            if what.endswith("scale") and not eight:
+                _require(t is None, what)
+            else:
+                _require(t is not None and t.dtype in types and t.numel() == size and t.is_cuda
+                         and t.is_contiguous(), what)
+    if param_out is not None:
+        _require(param_out.dtype in (torch.bfloat16, torch.float16) and param_out.numel() == n
+                 and param_out.is_cuda and param_out.is_contiguous(), "param_out")
+    t = zs_adamw_tensor(
+        n=n, weight_decay=weight_decay, lr_scale=lr_scale,
+        state=ZS_STATE_8 if eight else ZS_STATE_32, grad_dtype=dtype_code(grad_dtype),
+        param_dtype=ZS_BF16 if param_out is None else dtype_code(param_out.dtype),
+        param_out=_ptr(param_out), **{k + "_in": _ptr(x) for k, x in ins.items()},
+        **{k + "_out": _ptr(x) for k, x in outs.items()})
+    t._keep = (ins, outs, param_out)
+    return t
+
+
+_E4M3_LIKE = (torch.float8_e4m3fn, torch.uint8)  # e4m3 numbers or their patterns
+
+
+def adamw_state(n: int, bits: int = 32, device="cuda") -> dict:
+    """The state that a tensor of n elements starts with, as arguments of
+    adamw_tensor: m and v, and with 8 bits m_scale and v_scale."""
+    _require(bits in (8, 32), f"bits {bits}")
+    if bits == 32:
+        return {k: torch.zeros(n, device=device) for k in ("m", "v")}
+    blocks = (n + ZS_ADAMW_BLOCK - 1) // ZS_ADAMW_BLOCK
+    state = {k: torch.zeros(n, device=device, dtype=torch.uint8).view(torch.float8_e4m3fn)
+             for k in ("m", "v")}
+    state.update({k: torch.zeros(blocks, device=device) for k in ("m_scale", "v_scale")})
+    return state
+
+
+def adamw_desc(*, count: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+               bias_correction: bool = True, max_norm: float = 0.0, stream=None) -> zs_adamw_desc:
+    return zs_adamw_desc(count=int(count), beta1=beta1, beta2=beta2, eps=eps,
+                         bias_correction=int(bool(bias_correction)), max_norm=max_norm,
+                         stream=_stream(stream))
+
+
+def zero_shard_adamw_plan_bytes(desc: zs_adamw_desc, tensors) -> int:
+    """tensors: an array of zs_adamw_tensor ((zs_adamw_tensor * n)(...))."""
+    return int(_lib.zero_shard_adamw_plan_bytes(ctypes.byref(desc), tensors))
+
+
+def zero_shard_adamw_plan(desc: zs_adamw_desc, tensors, plan) -> int:
+    """plan: a contiguous CPU tensor (its size in bytes is passed on)."""
+    return _lib.zero_shard_adamw_plan(ctypes.byref(desc), tensors, _ptr(plan), _nbytes(plan))
+
+
+def zero_shard_adamw_gnorm(desc: zs_adamw_desc, plan, plan_dev, grads, sumsq_dev) -> int:
+    """plan, plan_dev: the plan on the CPU and its copy on the device."""
+    return _lib.zero_shard_adamw_gnorm(ctypes.byref(desc), _ptr(plan), _ptr(plan_dev),
+                                       contrib_table(grads), _ptr(sumsq_dev))
+
+
+def zero_shard_adamw(desc: zs_adamw_desc, plan, plan_dev, grads, lr: float, t: int, key: int,
+                     global_sumsq_dev=None) -> int:
+    return _lib.zero_shard_adamw(ctypes.byref(desc), _ptr(plan), _ptr(plan_dev),
+                                 contrib_table(grads), float(lr), int(t), int(key) & 0xFFFFFFFF,
+                                 _ptr(global_sumsq_dev))
+
+
+def zero_shard_adamw_consts(desc: zs_adamw_desc, lr: float, t: int, key: int):
+    """-> (status, [lr, bc1, bc2, key])."""
+    out = (ctypes.c_double * 4)()
+    rc = _lib.zero_shard_adamw_consts(ctypes.byref(desc), float(lr), int(t),
+                                      int(key) & 0xFFFFFFFF, out)
+    return rc, list(out)
+
+
+def zero_shard_adamw_dev(desc: zs_adamw_desc, plan, plan_dev, grads, consts_dev,
+                         global_sumsq_dev=None) -> int:
+    return _lib.zero_shard_adamw_dev(ctypes.byref(desc), _ptr(plan), _ptr(plan_dev),
+                                     contrib_table(grads), _ptr(consts_dev),
+                                     _ptr(global_sumsq_dev))
+
+
 # ------------------------------------------------------------ owner objects
 
 class ZeroShard:
@@ -1005,6 +1159,78 @@ class ZeroEmbedding:
                                            self._workspace_bytes)
         if rc:
             _check(rc, "zero_shard_embedding_bwd")
+
+
+class ZeroAdamW:
+    """The AdamW step of a list of tensors (adamw_tensor), with the plan of them.
+
+    The gradients of a call are a list of contiguous device tensors, one a tensor of its
+    ``grad_dtype`` and length (None for an empty one), or a table of theirs that the
+    caller keeps (contrib_table).  ``max_norm`` > 0: gnorm, the all-reduce of its
+    sum across ranks, then step with it.  ``stream`` as for ZeroLayerNorm."""
+
+    def __init__(self, tensors, *, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                 bias_correction: bool = True, max_norm: float = 0.0, stream=None):
+        self.tensors = list(tensors)
+        self._stream = torch.cuda.current_stream() if stream is None else stream
+        self.desc = adamw_desc(count=len(self.tensors), beta1=beta1, beta2=beta2, eps=eps,
+                               bias_correction=bias_correction, max_norm=max_norm,
+                               stream=self._stream)
+        self._ref = ctypes.byref(self.desc)
+        array = (zs_adamw_tensor * max(1, len(self.tensors)))(*self.tensors)
+        size = zero_shard_adamw_plan_bytes(self.desc, array)
+        _require(size >= 0, "adamw's sizes")
+        self.plan = torch.empty(size, dtype=torch.uint8)
+        _check(zero_shard_adamw_plan(self.desc, array, self.plan), "zero_shard_adamw_plan")
+        with torch.cuda.stream(self._stream):
+            self.plan_dev = self.plan.to("cuda")
+        self._args = (self._ref, self.plan.data_ptr(), self.plan_dev.data_ptr())
+
+    def _grads(self, grads):
+        if isinstance(grads, ctypes.Array):  # kept by the caller
+            _require(len(grads) >= len(self.tensors), "grads")
+            return grads
+        grads = list(grads)
+        _require(len(grads) == len(self.tensors), "grads")
+        for g, t in zip(grads, self.tensors):
+            if t.n or g is not None:
+                _require(g is not None and g.numel() == t.n and g.is_cuda and g.is_contiguous()
+                         and _DTYPES.get(g.dtype) == t.grad_dtype, "grads")
+        return contrib_table(grads)
+
+    @staticmethod
+    def _double(t, n: int, what: str):
+        if t is not None:
+            _require(t.dtype is torch.float64 and t.numel() >= n and t.is_cuda
+                     and t.is_contiguous(), what)
+        return _ptr(t)
+
+    def gnorm(self, grads, sumsq_dev) -> None:
+        """The sum of squares of all gradients, to sumsq_dev (float64)."""
+        _check(_lib.zero_shard_adamw_gnorm(*self._args, self._grads(grads),
+                                           self._double(sumsq_dev, 1, "sumsq_dev")),
+               "zero_shard_adamw_gnorm")
+
+    def step(self, grads, lr: float, t: int, global_sumsq_dev=None, key: int | None = None) -> None:
+        """Step t.  key: of the rounding of 8-bit states, another one each step
+        (default: t)."""
+        _check(_lib.zero_shard_adamw(*self._args, self._grads(grads), float(lr), int(t),
+                                     (int(t) if key is None else int(key)) & 0xFFFFFFFF,
+                                     self._double(global_sumsq_dev, 1, "global_sumsq_dev")),
+               "zero_shard_adamw")
+
+    def consts(self, lr: float, t: int, key: int | None = None) -> list[float]:
+        rc, out = zero_shard_adamw_consts(self.desc, lr, t, t if key is None else key)
+        _check(rc, "zero_shard_adamw_consts")
+        return out
+
+    def step_dev(self, grads, consts_dev, global_sumsq_dev=None) -> None:
+        """The step of the constants that consts_dev (float64[4], see consts) holds
+        when the kernel runs."""
+        _check(_lib.zero_shard_adamw_dev(*self._args, self._grads(grads),
+                                         self._double(consts_dev, 4, "consts_dev"),
+                                         self._double(global_sumsq_dev, 1, "global_sumsq_dev")),
+               "zero_shard_adamw_dev")
 
 
 class ZeroOrtho:
