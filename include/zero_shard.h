@@ -633,21 +633,26 @@ int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const 
  *
  * ZS_STATE_8: m and r = sqrt(v) are each an e4m3 number (sign, 4 bits of exponent with
  * bias 7, 3 of mantissa; no infinities) times the scale of its block, the
- * tensor's elements [256 b, 256 b + 256); m = binary32(number scale), v = r r.  Storing
- * binary32 values x of a block (of m', or of sqrt(v')):
+ * tensor's elements [256 b, 256 b + 256).  Their moments are binary32 throughout (with
+ * coef, b, 1-b and 1/sqrt(bc2) rounded to it), every operation rounded:
+ *   m' = b1 m + (1-b1) g'      r' = sqrt((b2 r) r + ((1-b2) g') g')
+ *   u = m' / (r' / sqrt(bc2) + eps)
+ *   theta' = theta - (lr f wd) theta - (lr f / bc1) u   (binary64, rounded once)
+ * (gradients whose squares are beyond binary32 count as infinities or zeros).
+ * Storing values x of a block (of m', or of r'):
  *   top = max |x|;  scale = top / 256
- *   q = min(binary32(|x| binary32(1 / top)), 1) is rounded to an e4m3 number of
- *   256 q by chance, down or up in proportion to how near each is: bits(q 2^-112) +
- *   16 d + 8, cut after 3 bits of mantissa.  d is 16 bits of h (the lower ones for m,
- *   the upper ones for r):
+ *   y = |x| binary32(1 / scale), at most 256, and at least 2^-9 for an r' > 0, becomes
+ *   an e4m3 number (with x's sign, a zero's too) by chance, the one below or above it in proportion to how near
+ *   each is: above where the 2^20ths of its way from the one below to the one above,
+ *   cut to a whole number, plus 16 d + 8 reach 2^20.  d is 16 bits of h (the lower ones
+ *   for m, the upper ones for r):
  *   h = mix(mix(key + c (k + 1)) + c mix(i >> 32) + i), modulo 2^32, k the tensor's number,
  *   c = 0x9e3779b9, mix(x): x ^= x >> 16; x *= 0x6a09e667; x ^= x >> 15;
  *   x *= 0xbb67ae85; x ^= x >> 16
  * so that the average of what is stored is what was computed: to nearest, a moment
  * whose step is below half a step of the type (v's, with beta2 = 0.999) would never
- * move.  r' > 0 does not become 0.  top < 2^-126: the block is zeros.  A block that
- * holds an infinity or NaN has no finite values from then on.  All zeros are the state
- * at the start. */
+ * move.  top < 2^-100: the block is zeros.  A block that holds an infinity or NaN
+ * has no finite scale from then on.  All zeros are the state at the start. */
 #define ZS_ADAMW_BLOCK 256
 #define ZS_ADAMW_MAX_TENSORS (INT64_C(1) << 20)
 #define ZS_ADAMW_MAX_ELEMENTS (INT64_C(1) << 34) /* of a tensor; all together

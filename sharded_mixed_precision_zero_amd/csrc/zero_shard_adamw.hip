@@ -69,7 +69,7 @@ struct Grads {
 };
 
 struct Consts {
-  double b1, omb1, b2, omb2, bc1, bc2, lr, eps;
+  double b1, omb1, b2, omb2, bc1, bc2, lr, eps, root;  // root = 1 / sqrt(bc2)
 };
 
 struct StepArgs {
@@ -92,42 +92,43 @@ struct NormArgs {
   double *partials;  // of all chunks
 };
 
-// Four consecutive elements of any alignment.
+// The plan's addresses are all of global memory, which the compiler cannot see
+// once they come out of a table.
+#define ZS_GLOBAL __attribute__((address_space(1)))
+template <class T>
+__device__ __forceinline__ const ZS_GLOBAL T *global(const void *p, int64_t i) {
+  return (const ZS_GLOBAL T *)(uintptr_t(p) + i * int64_t(sizeof(T)));
+}
+template <class T>
+__device__ __forceinline__ ZS_GLOBAL T *global(void *p, int64_t i) {
+  return (ZS_GLOBAL T *)(uintptr_t(p) + i * int64_t(sizeof(T)));
+}
+
+// Four consecutive elements of any alignment.  They are touched once a step and
+// go past the caches.
 template <class T>
 struct Four {
   using V = T __attribute__((ext_vector_type(4), aligned(sizeof(T))));
-  T v[4];
-  __device__ __forceinline__ void load(const void *p, int64_t i) {
-    const V x = __builtin_nontemporal_load(
-        reinterpret_cast<const V *>(static_cast<const T *>(p) + i));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = x[e];
-  }
-  __device__ __forceinline__ void store(void *p, int64_t i) const {
-    V x;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = v[e];
-    __builtin_nontemporal_store(x, reinterpret_cast<V *>(static_cast<T *>(p) + i));
-  }
-  // the first `left` of them, zeros behind
-  __device__ __forceinline__ void load_some(const void *p, int64_t i, int64_t left) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = e < left ? static_cast<const T *>(p)[i + e] : T(0);
-  }
-  __device__ __forceinline__ void store_some(void *p, int64_t i, int64_t left) const {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < left) static_cast<T *>(p)[i + e] = v[e];
-  }
+  V v;
+  // the first `left` of them where that may be fewer, zeros behind
   template <bool TAIL>
   __device__ __forceinline__ void get(const void *p, int64_t i, int64_t left) {
-    if (!TAIL || left >= 4) load(p, i);
-    else load_some(p, i, left);
+    if (!TAIL || left >= 4) {
+      v = __builtin_nontemporal_load((const ZS_GLOBAL V *)global<T>(p, i));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = e < left ? *global<T>(p, i + e) : T(0);
+    }
   }
   template <bool TAIL>
   __device__ __forceinline__ void put(void *p, int64_t i, int64_t left) const {
-    if (!TAIL || left >= 4) store(p, i);
-    else store_some(p, i, left);
+    if (!TAIL || left >= 4) {
+      __builtin_nontemporal_store(v, (ZS_GLOBAL V *)global<T>(p, i));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < left) *global<T>(p, i + e) = v[e];
+    }
   }
 };
 
@@ -146,41 +147,33 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// The largest of the wave's magnitudes, as bits: a NaN is larger than all else.
+// The largest of the wave's magnitudes as bits (a NaN is larger than all else),
+// uniform.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ unsigned dpp_max(unsigned v) {
+  const unsigned w = __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+  return w > v ? w : v;
+}
 __device__ __forceinline__ unsigned wave_max(unsigned v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const unsigned w = __shfl_xor(v, o, 64);
-    v = w > v ? w : v;
-  }
-  return v;
+  v = dpp_max<0xb1>(v);   // lanes 1 apart
+  v = dpp_max<0x4e>(v);   // 2 apart
+  v = dpp_max<0x141>(v);  // half row mirrored
+  v = dpp_max<0x140>(v);  // row mirrored
+  v = dpp_max<0x142, 0xa>(v);  // rows 1 and 3: with the row before
+  v = dpp_max<0x143, 0xc>(v);  // rows 2 and 3: with the first half
+  return __builtin_amdgcn_readlane(v, 63);
 }
 
-// ---- states in 8 bits: e4m3 numbers (bias 7) of at most 256, times a scale
-//
-// The number of magnitude x is x 2^-120 read as binary32 and cut after three
-// bits of mantissa: there the smallest exponents of the two types coincide,
-// subnormals included.
-
-__device__ __forceinline__ float e4m3_value(unsigned byte) {
-  return __uint_as_float((byte & 0x7fu) << 20) * 0x1p120f;
-}
+// ---- states in 8 bits: e4m3 numbers of at most 256, times a scale
 
 // A block's scale from its largest magnitude, and the factor that takes
-// magnitudes to e4m3 read as above.  Blocks of nothing but numbers below 2^-126 are
-// zeros (NaN is not below).
+// magnitudes to [0, 256].  Blocks of nothing but numbers below 2^-100 are zeros (NaN is
+// not below), so that neither leaves binary32.
 __device__ __forceinline__ void scale_of(unsigned top_bits, float &scale, float &inv) {
   const float top = __uint_as_float(top_bits);
-  const bool none = top < 0x1p-126f;
+  const bool none = top < 0x1p-100f;
   scale = none ? 0.0f : top * 0x1p-8f;
-  inv = none ? 0.0f : 1.0f / top;
-}
-
-// x / top as an e4m3 number times 2^-8: down, or up where the dither (20 bits)
-// carries, in proportion to how near each of the two is.
-__device__ __forceinline__ unsigned encode(float x, float inv, unsigned dither) {
-  const float q = fminf(x * inv, 1.0f) * 0x1p-112f;
-  return (__float_as_uint(q) + dither) >> 20;
+  inv = none ? 0.0f : 1.0f / scale;
 }
 
 struct Lane {
@@ -198,130 +191,147 @@ __device__ __forceinline__ void load_state(const Tensor &T, Lane &s, int64_t i, 
   if constexpr (EIGHT) {
     using Word = unsigned __attribute__((aligned(1)));
     if (!TAIL || left >= 4) {
-      s.m8 = __builtin_nontemporal_load(
-          reinterpret_cast<const Word *>(static_cast<const uint8_t *>(T.m_in) + i));
-      s.v8 = __builtin_nontemporal_load(
-          reinterpret_cast<const Word *>(static_cast<const uint8_t *>(T.v_in) + i));
+      s.m8 = __builtin_nontemporal_load((const ZS_GLOBAL Word *)global<uint8_t>(T.m_in, i));
+      s.v8 = __builtin_nontemporal_load((const ZS_GLOBAL Word *)global<uint8_t>(T.v_in, i));
     } else {
       s.m8 = s.v8 = 0;
 #pragma unroll
       for (int e = 0; e < 3; ++e)
         if (e < left) {
-          s.m8 |= unsigned(static_cast<const uint8_t *>(T.m_in)[i + e]) << (8 * e);
-          s.v8 |= unsigned(static_cast<const uint8_t *>(T.v_in)[i + e]) << (8 * e);
+          s.m8 |= unsigned(*global<uint8_t>(T.m_in, i + e)) << (8 * e);
+          s.v8 |= unsigned(*global<uint8_t>(T.v_in, i + e)) << (8 * e);
         }
     }
-    const bool in = !TAIL || i / kBlock * kBlock < T.n;
-    s.ms = in ? T.m_scale_in[i / kBlock] : 0.0f;
-    s.vs = in ? T.v_scale_in[i / kBlock] : 0.0f;
+    // one for the wave
+    const int64_t block = (i - int64_t(threadIdx.x & 63) * 4) / kBlock;
+    const bool in = !TAIL || block * kBlock < T.n;
+    s.ms = in ? *global<float>(T.m_scale_in, block) : 0.0f;
+    s.vs = in ? *global<float>(T.v_scale_in, block) : 0.0f;
   } else {
     s.m32.template get<TAIL>(T.m_in, i, left);
     s.v32.template get<TAIL>(T.v_in, i, left);
   }
 }
 
-template <bool WIDE, bool TAIL>
+template <class TG, bool TAIL>
 __device__ __forceinline__ void load_grad(const void *g, Lane &s, int64_t i, int64_t left) {
-  if constexpr (WIDE) s.g32.template get<TAIL>(g, i, left);
+  if constexpr (std::is_same_v<TG, F32>) s.g32.template get<TAIL>(g, i, left);
   else s.g16.template get<TAIL>(g, i, left);
 }
 
-template <bool WIDE>
-__device__ __forceinline__ float grad_of(const Tensor &T, const Lane &s, int e) {
-  if constexpr (WIDE) return s.g32.v[e];
-  else return T.grad_dtype == ZS_BF16 ? Bf16::load(s.g16.v[e]) : F16::load(s.g16.v[e]);
+template <class TG>
+__device__ __forceinline__ float grad_of(const Lane &s, int e) {
+  if constexpr (std::is_same_v<TG, F32>) return s.g32.v[e];
+  else return TG::load(s.g16.v[e]);
+}
+
+// A tensor's constants of the step.
+struct Rates {
+  double coef, decay, lr;  // lr times the tensor's factor, and that times its weight decay
+  float coef32, b1, omb1, b2, omb2, root, eps;  // 8 bits: root = 1 / sqrt(bc2)
+  double step;                                  // lr / bc1
+};
+
+template <class T, bool TAIL>
+__device__ __forceinline__ void put_copy(const Tensor &t, const Four<float> &w, int64_t i,
+                                         int64_t left) {
+  Four<uint16_t> p;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) p.v[e] = T::store(w.v[e]);
+  p.template put<TAIL>(t.param, i, left);
+}
+
+template <bool TAIL>
+__device__ __forceinline__ void put_weights(const Tensor &T, const Four<float> &w, int64_t i,
+                                            int64_t left) {
+  w.template put<TAIL>(T.master_out, i, left);
+  if (!T.param) return;
+  if (T.param_dtype == ZS_BF16) put_copy<Bf16, TAIL>(T, w, i, left);
+  else put_copy<F16, TAIL>(T, w, i, left);
 }
 
 // AdamW on a lane's four elements: binary64 from the binary32 state, one
-// rounding per stored value, in the shard step's order.  With an 8-bit state m
-// and sqrt(v) are binary32 numbers first, and what their block keeps of
-// them is chosen at random between the two neighbours.
-template <bool EIGHT, bool WIDE, bool TAIL>
-__device__ __forceinline__ void update(const Tensor &T, const Consts &k, double coef,
-                                       uint32_t base, Lane &s, int64_t i, int64_t left) {
-  const double lr = k.lr * double(T.lr_scale), decay = lr * double(T.weight_decay);
-  Four<float> m, v;
+// rounding per stored value, in the shard step's order.
+template <class TG, bool TAIL>
+__device__ __forceinline__ void update32(const Tensor &T, const Consts &k, const Rates &rates,
+                                         Lane &s, int64_t i, int64_t left) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const double g = coef * double(grad_of<WIDE>(T, s, e));
-    double m0, v0;
-    if constexpr (EIGHT) {
-      const unsigned mb = s.m8 >> (8 * e), vb = s.v8 >> (8 * e);
-      const float mag = e4m3_value(mb) * s.ms, r = e4m3_value(vb) * s.vs;
-      m0 = double(mb & 0x80u ? -mag : mag);
-      v0 = double(r) * double(r);
-    } else {
-      m0 = double(s.m32.v[e]);
-      v0 = double(s.v32.v[e]);
-    }
-    const double m1 = k.b1 * m0 + k.omb1 * g;
-    const double v1 = k.b2 * v0 + k.omb2 * (g * g);
+    const double g = rates.coef * double(grad_of<TG>(s, e));
+    const double m1 = k.b1 * double(s.m32.v[e]) + k.omb1 * g;
+    const double v1 = k.b2 * double(s.v32.v[e]) + k.omb2 * (g * g);
     const double mhat = m1 / k.bc1;
     const double vhat = v1 / k.bc2;
     const double t0 = double(s.w.v[e]);
-    const double t1 = t0 - decay * t0 - lr * mhat / (sqrt(vhat) + k.eps);
+    const double t1 = t0 - rates.decay * t0 - rates.lr * mhat / (sqrt(vhat) + k.eps);
     s.w.v[e] = float(t1);
-    m.v[e] = float(m1);
-    v.v[e] = EIGHT ? float(sqrt(v1)) : float(v1);
+    s.m32.v[e] = float(m1);
+    s.v32.v[e] = float(v1);
   }
-  s.w.template put<TAIL>(T.master_out, i, left);
-  if (T.param) {
-    Four<uint16_t> p;
+  put_weights<TAIL>(T, s.w, i, left);
+  s.m32.template put<TAIL>(T.m_out, i, left);
+  s.v32.template put<TAIL>(T.v_out, i, left);
+}
+
+// The same with a state in 8 bits.  The moments are binary32 numbers, which
+// rounding to 4 significant bits makes little of (binary64 as above: 1.5 times the
+// instructions that there is time for); the weights are binary64 as above.
+template <class TG, bool TAIL>
+__device__ __forceinline__ void update8(const Tensor &T, const Rates &rates, uint32_t base,
+                                        Lane &s, int64_t i, int64_t left) {
+  float m[4], r[4];
+  unsigned mtop = 0, vtop = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      p.v[e] = T.param_dtype == ZS_BF16 ? Bf16::store(s.w.v[e]) : F16::store(s.w.v[e]);
-    p.template put<TAIL>(T.param, i, left);
+  for (int e = 0; e < 4; ++e) {
+    const float g = rates.coef32 * grad_of<TG>(s, e);
+    const float m0 = __builtin_amdgcn_cvt_f32_fp8(s.m8 >> (8 * e), 0) * s.ms;
+    const float r0 = __builtin_amdgcn_cvt_f32_fp8(s.v8 >> (8 * e), 0) * s.vs;
+    m[e] = rates.b1 * m0 + rates.omb1 * g;
+    r[e] = sqrtf((rates.b2 * r0) * r0 + (rates.omb2 * g) * g);
+    const double t0 = double(s.w.v[e]);
+    const float u = m[e] / (r[e] * rates.root + rates.eps);
+    s.w.v[e] = float(t0 - rates.decay * t0 - rates.step * double(u));
+    // what is not there counts for nothing: its gradient and state are 0
+    const unsigned a = __float_as_uint(m[e]) & 0x7fffffffu, b = __float_as_uint(r[e]) & 0x7fffffffu;
+    mtop = a > mtop ? a : mtop;
+    vtop = b > vtop ? b : vtop;
   }
-  if constexpr (!EIGHT) {
-    m.template put<TAIL>(T.m_out, i, left);
-    v.template put<TAIL>(T.v_out, i, left);
+  put_weights<TAIL>(T, s.w, i, left);
+  float ms, vs, minv, vinv;
+  scale_of(wave_max(mtop), ms, minv);
+  scale_of(wave_max(vtop), vs, vinv);
+  // to e4m3, down or up where 20 bits of dither carry into the number
+  unsigned mw = 0, vw = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t h = mix(base + uint32_t(i + e));
+    const float a = __builtin_amdgcn_fmed3f(m[e] * minv, -256.0f, 256.0f);
+    // a root that is there stays above the least number
+    const float b = __builtin_amdgcn_fmed3f(r[e] * vinv, r[e] > 0.0f ? 0x1p-9f : 0.0f, 256.0f);
+    mw |= (__builtin_amdgcn_cvt_sr_fp8_f32(a, h << 16 | 0x8000u, 0, 0) & 0xffu) << (8 * e);
+    vw |= (__builtin_amdgcn_cvt_sr_fp8_f32(b, (h & 0xffff0000u) | 0x8000u, 0, 0) & 0xffu) << (8 * e);
+  }
+  if (!TAIL || left >= 4) {
+    using Word = unsigned __attribute__((aligned(1)));
+    __builtin_nontemporal_store(mw, (ZS_GLOBAL Word *)global<uint8_t>(T.m_out, i));
+    __builtin_nontemporal_store(vw, (ZS_GLOBAL Word *)global<uint8_t>(T.v_out, i));
   } else {
-    unsigned mtop = 0, vtop = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // what is not there counts for nothing: its gradient and state are 0
-      const unsigned a = __float_as_uint(m.v[e]) & 0x7fffffffu, b = __float_as_uint(v.v[e]);
-      mtop = a > mtop ? a : mtop;
-      vtop = b > vtop ? b : vtop;
-    }
-    float ms, vs, minv, vinv;
-    scale_of(wave_max(mtop), ms, minv);
-    scale_of(wave_max(vtop), vs, vinv);
-    unsigned mw = 0, vw = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t h = mix(base + uint32_t(i + e));
-      mw |= (encode(fabsf(m.v[e]), minv, (h & 0xffffu) << 4 | 8u) | (m.v[e] < 0.0f ? 0x80u : 0u))
-            << (8 * e);
-      unsigned c = encode(v.v[e], vinv, h >> 16 << 4 | 8u);
-      // a second moment that is there never becomes 0
-      if (c == 0 && v.v[e] > 0.0f && vinv != 0.0f) c = 1;
-      vw |= c << (8 * e);
-    }
-    if (!TAIL || left >= 4) {
-      using Word = unsigned __attribute__((aligned(1)));
-      __builtin_nontemporal_store(
-          mw, reinterpret_cast<Word *>(static_cast<uint8_t *>(T.m_out) + i));
-      __builtin_nontemporal_store(
-          vw, reinterpret_cast<Word *>(static_cast<uint8_t *>(T.v_out) + i));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 3; ++e)
-        if (e < left) {
-          static_cast<uint8_t *>(T.m_out)[i + e] = uint8_t(mw >> (8 * e));
-          static_cast<uint8_t *>(T.v_out)[i + e] = uint8_t(vw >> (8 * e));
-        }
-    }
-    if ((threadIdx.x & 63) == 0 && i < T.n) {
-      T.m_scale_out[i / kBlock] = ms;
-      T.v_scale_out[i / kBlock] = vs;
-    }
+    for (int e = 0; e < 3; ++e)
+      if (e < left) {
+        *global<uint8_t>(T.m_out, i + e) = uint8_t(mw >> (8 * e));
+        *global<uint8_t>(T.v_out, i + e) = uint8_t(vw >> (8 * e));
+      }
+  }
+  if ((threadIdx.x & 63) == 0 && left > 0) {
+    *global<float>(T.m_scale_out, i / kBlock) = ms;
+    *global<float>(T.v_scale_out, i / kBlock) = vs;
   }
 }
 
-template <bool EIGHT, bool WIDE, bool TAIL>
+template <bool EIGHT, class TG, bool TAIL>
 __device__ __forceinline__ void step_chunk(const Tensor &T, const void *g, const Consts &k,
-                                           double coef, uint32_t key, int64_t from) {
+                                           const Rates &rates, uint32_t key, int64_t from) {
   const int64_t i0 = from + int64_t(threadIdx.x >> 6) * (kBlock * kRounds) + (threadIdx.x & 63) * 4;
   const uint32_t base = mix(key + 0x9e3779b9u * uint32_t(T.number + 1)) +
                         mix(uint32_t(uint64_t(from) >> 32)) * 0x9e3779b9u;
@@ -330,13 +340,21 @@ __device__ __forceinline__ void step_chunk(const Tensor &T, const void *g, const
   for (int r = 0; r < kRounds; ++r) {
     const int64_t i = i0 + r * kBlock;
     load_state<EIGHT, TAIL>(T, s[r], i, T.n - i);
-    load_grad<WIDE, TAIL>(g, s[r], i, T.n - i);
+    load_grad<TG, TAIL>(g, s[r], i, T.n - i);
   }
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
     const int64_t i = i0 + r * kBlock;
-    update<EIGHT, WIDE, TAIL>(T, k, coef, base, s[r], i, T.n - i);
+    if constexpr (EIGHT) update8<TG, TAIL>(T, rates, base, s[r], i, T.n - i);
+    else update32<TG, TAIL>(T, k, rates, s[r], i, T.n - i);
   }
+}
+
+template <bool EIGHT, class TG>
+__device__ __forceinline__ void step_any(const Tensor &T, const void *g, const Consts &k,
+                                         const Rates &rates, uint32_t key, int64_t from) {
+  if (T.n - from < kChunk) step_chunk<EIGHT, TG, true>(T, g, k, rates, key, from);
+  else step_chunk<EIGHT, TG, false>(T, g, k, rates, key, from);
 }
 
 __global__ void __launch_bounds__(kThreads) adamw_step_kernel(const StepArgs A, const Grads G) {
@@ -350,45 +368,48 @@ __global__ void __launch_bounds__(kThreads) adamw_step_kernel(const StepArgs A, 
     k.lr = A.dyn[0];
     k.bc1 = A.dyn[1];
     k.bc2 = A.dyn[2];
+    k.root = 1.0 / sqrt(k.bc2);
     key = uint32_t(A.dyn[3]);
   }
-  const double coef = A.sumsq ? clip_coef(*A.sumsq, A.max_norm) : 1.0;
+  Rates rates;
+  rates.coef = A.sumsq ? clip_coef(*A.sumsq, A.max_norm) : 1.0;
+  rates.lr = k.lr * double(T.lr_scale);
+  rates.decay = rates.lr * double(T.weight_decay);
   const int64_t from = (chunk - T.chunk0) * kChunk;
-  const bool tail = T.n - from < kChunk, wide = T.grad_dtype == ZS_F32;
   if (T.state == ZS_STATE_8) {
-    if (wide) {
-      if (tail) step_chunk<true, true, true>(T, g, k, coef, key, from);
-      else step_chunk<true, true, false>(T, g, k, coef, key, from);
-    } else {
-      if (tail) step_chunk<true, false, true>(T, g, k, coef, key, from);
-      else step_chunk<true, false, false>(T, g, k, coef, key, from);
-    }
+    rates.coef32 = float(rates.coef);
+    rates.b1 = float(k.b1);
+    rates.omb1 = float(k.omb1);
+    rates.b2 = float(k.b2);
+    rates.omb2 = float(k.omb2);
+    rates.root = float(k.root);
+    rates.eps = float(k.eps);
+    rates.step = rates.lr / k.bc1;
+    if (T.grad_dtype == ZS_F32) step_any<true, F32>(T, g, k, rates, key, from);
+    else if (T.grad_dtype == ZS_BF16) step_any<true, Bf16>(T, g, k, rates, key, from);
+    else step_any<true, F16>(T, g, k, rates, key, from);
   } else {
-    if (wide) {
-      if (tail) step_chunk<false, true, true>(T, g, k, coef, key, from);
-      else step_chunk<false, true, false>(T, g, k, coef, key, from);
-    } else {
-      if (tail) step_chunk<false, false, true>(T, g, k, coef, key, from);
-      else step_chunk<false, false, false>(T, g, k, coef, key, from);
-    }
+    if (T.grad_dtype == ZS_F32) step_any<false, F32>(T, g, k, rates, key, from);
+    else if (T.grad_dtype == ZS_BF16) step_any<false, Bf16>(T, g, k, rates, key, from);
+    else step_any<false, F16>(T, g, k, rates, key, from);
   }
 }
 
 // A chunk's sum of squares (binary64): a lane's elements in order, a
 // butterfly over the wave, the waves in order.
-template <bool WIDE>
+template <class TG>
 __device__ __forceinline__ double chunk_squares(const Tensor &T, const void *g, int64_t from) {
   const int64_t i0 = from + int64_t(threadIdx.x >> 6) * (kBlock * kRounds) + (threadIdx.x & 63) * 4;
   Lane s[kRounds];
 #pragma unroll
   for (int r = 0; r < kRounds; ++r)
-    load_grad<WIDE, true>(g, s[r], i0 + r * kBlock, T.n - i0 - r * kBlock);
+    load_grad<TG, true>(g, s[r], i0 + r * kBlock, T.n - i0 - r * kBlock);
   double sum = 0.0;
 #pragma unroll
   for (int r = 0; r < kRounds; ++r)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const double x = double(grad_of<WIDE>(T, s[r], e));
+      const double x = double(grad_of<TG>(s[r], e));
       sum += x * x;
     }
   return sum;
@@ -400,8 +421,9 @@ __global__ void __launch_bounds__(kThreads) adamw_norm_kernel(const NormArgs A, 
   const int at = __builtin_amdgcn_readfirstlane(A.map[chunk]) - A.tensor0;
   const Tensor &T = A.tensors[at];
   const int64_t from = (chunk - T.chunk0) * kChunk;
-  double sum = T.grad_dtype == ZS_F32 ? chunk_squares<true>(T, G.p[at], from)
-                                      : chunk_squares<false>(T, G.p[at], from);
+  double sum = T.grad_dtype == ZS_F32    ? chunk_squares<F32>(T, G.p[at], from)
+               : T.grad_dtype == ZS_BF16 ? chunk_squares<Bf16>(T, G.p[at], from)
+                                         : chunk_squares<F16>(T, G.p[at], from);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
   if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = sum;
@@ -562,9 +584,12 @@ int step(const zs_adamw_desc *d, const void *plan, void *plan_dev, const void *c
   if (h->chunks == 0) return ZS_OK;
   if (const int rc = device_is_gfx950()) return rc;
   const double b1 = double(d->beta1), b2 = double(d->beta2);
-  const Consts k{b1, 1.0 - b1, b2, 1.0 - b2,
-                 d->bias_correction ? 1.0 - std::pow(b1, double(t)) : 1.0,
-                 d->bias_correction ? 1.0 - std::pow(b2, double(t)) : 1.0, lr, double(d->eps)};
+  Consts k{b1, 1.0 - b1, b2, 1.0 - b2, 1.0, 1.0, lr, double(d->eps), 1.0};
+  if (d->bias_correction) {
+    k.bc1 = 1.0 - std::pow(b1, double(t));
+    k.bc2 = 1.0 - std::pow(b2, double(t));
+    k.root = 1.0 / std::sqrt(k.bc2);
+  }
   const char *dev = static_cast<const char *>(plan_dev);
   return by_launch(plan, grads, [&](int64_t tensor0, int64_t chunk0, unsigned chunks,
                                     const Grads &G) {

@@ -116,57 +116,56 @@ def _stored(x, bits, least):
     pad[:n] = np.abs(x)
     blocks = pad.reshape(-1, 256)
     top = blocks.max(1)
-    ok = ~(top < np.float32(2.0 ** -126))
-    with np.errstate(divide="ignore"):
-        inv = np.where(ok, np.float32(1) / top, np.float32(0)).astype(np.float32)
+    ok = ~(top < np.float32(2.0 ** -100))
     scale = np.where(ok, top / np.float32(256), np.float32(0)).astype(np.float32)
-    q = np.minimum(blocks * inv[:, None], np.float32(1)).astype(np.float32).reshape(-1)[:n]
-    # in steps of the e4m3 numbers' spacing at q 256, then down or up
-    v = q.astype(np.float64) * 256
-    e = np.maximum(np.floor(np.log2(np.maximum(v, 2.0 ** -40))), -6)
+    inv = np.where(ok, np.float32(1) / np.where(ok, scale, np.float32(1)), np.float32(0))
+    y = np.minimum(blocks * inv.astype(np.float32)[:, None], np.float32(256)).reshape(-1)[:n]
+    assert y.dtype == np.float32
+    if least:
+        y = np.where((x > 0), np.maximum(y, np.float32(2.0 ** -9)), y)
+    # in steps of the e4m3 numbers' spacing there, then down or up
+    y = y.astype(np.float64)
+    e = np.maximum(np.floor(np.log2(np.maximum(y, 2.0 ** -40))), -6)
     step = 2.0 ** (e - 3)
-    steps = v / step  # exact
-    lower = np.floor(steps)
-    # 20 bits of what lies above the lower neighbour, as binary32 holds them
-    rest = np.rint((steps - lower) * 2.0 ** 20)
-    up = rest + (bits.astype(np.int64) * 16 + 8) >= 2.0 ** 20
-    value = (lower + up) * step
+    lower = np.floor(y / step)  # both exact
+    rest = np.floor((y / step - lower) * 2.0 ** 20)
+    value = (lower + (rest + (bits.astype(np.int64) * 16 + 8) >= 2.0 ** 20)) * step
     # the byte of that value
     e = np.where(value >= 2.0 ** -6, np.floor(np.log2(np.maximum(value, 2.0 ** -40))), -7)
     code = np.where(value < 2.0 ** -6, value * 512, (e + 7) * 8 + (value / 2.0 ** e - 1) * 8)
-    code = code.astype(np.uint8)
-    live = ok[np.arange(n) // 256]
-    if least:
-        code = np.where((x > 0) & live & (code == 0), 1, code).astype(np.uint8)
-    return code, scale
+    return code.astype(np.uint8), scale
 
 
-def reference(case, number, it, t, coef=1.0, key=None, wd=None):
-    """The step by its definition in numpy binary64."""
+def reference(case, number, it, t, coef=1.0, key=None):
+    """The step by its definition in numpy: binary64, the moments of a state in 8
+    bits binary32."""
     n = it["master"].numel()
-    g = coef * it["grad"].cpu().to(F64).numpy()
     w = it["master"].cpu().numpy().astype(np.float64)
-    b1, b2, eps = _f32(B1), _f32(B2), _f32(EPS)
+    g = it["grad"].cpu().to(F64).numpy()
+    lr, decay = _f32(LR) * _f32(case.lr_scale), _f32(case.decay)
+    bc1, bc2 = 1 - _f32(B1) ** t, 1 - _f32(B2) ** t
     if case.bits == 32:
-        m0, v0 = (it[k].cpu().numpy().astype(np.float64) for k in ("m", "v"))
-    else:
-        at = np.arange(n) // 256
-        m0, r = ((_numbers(it[k].cpu().numpy()).astype(np.float32)
-                  * it[k + "_scale"].cpu().numpy()[at]).astype(np.float64) for k in ("m", "v"))
-        v0 = r * r
-    m1, v1 = b1 * m0 + (1 - b1) * g, b2 * v0 + (1 - b2) * (g * g)
-    lr = _f32(LR) * _f32(case.lr_scale)
-    w1 = w - (lr * _f32(case.decay)) * w - lr * (m1 / (1 - b1 ** t)) / (
-        np.sqrt(v1 / (1 - b2 ** t)) + eps)
-    out = {"master": w1.astype(np.float32)}
-    if case.bits == 32:
-        out.update(m=m1.astype(np.float32), v=v1.astype(np.float32))
-    else:
-        h = _bits_of(key, number, n)
-        m32, r32 = m1.astype(np.float32), np.sqrt(v1).astype(np.float32)
-        code, out["m_scale"] = _stored(m32, h & np.uint32(0xFFFF), False)
-        out["m"] = np.where(m32 < 0, code | 0x80, code).astype(np.uint8)
-        out["v"], out["v_scale"] = _stored(r32, h >> np.uint32(16), True)
+        g = coef * g
+        b1, b2 = _f32(B1), _f32(B2)
+        m, v = (it[k].cpu().numpy().astype(np.float64) for k in ("m", "v"))
+        m, v = b1 * m + (1 - b1) * g, b2 * v + (1 - b2) * (g * g)
+        w = w - (lr * decay) * w - lr * (m / bc1) / (np.sqrt(v / bc2) + _f32(EPS))
+        return {"master": w.astype(np.float32), "m": m.astype(np.float32),
+                "v": v.astype(np.float32)}
+    f = np.float32
+    g = f(coef) * g.astype(f)
+    b1, b2, c1, c2 = f(B1), f(B2), f(1 - _f32(B1)), f(1 - _f32(B2))
+    at = np.arange(n) // 256
+    m, r = (_numbers(it[k].cpu().numpy()).astype(f) * it[k + "_scale"].cpu().numpy()[at]
+            for k in ("m", "v"))
+    m, r = b1 * m + c1 * g, np.sqrt((b2 * r) * r + (c2 * g) * g)
+    u = m / (r * f(1 / np.sqrt(bc2)) + f(EPS))
+    assert m.dtype == r.dtype == u.dtype == f
+    w = w - (lr * decay) * w - (lr / bc1) * u.astype(np.float64)
+    out, h = {"master": w.astype(f)}, _bits_of(key, number, n)
+    code, out["m_scale"] = _stored(m, h & np.uint32(0xFFFF), False)
+    out["m"] = np.where(np.signbit(m), code | 0x80, code).astype(np.uint8)
+    out["v"], out["v_scale"] = _stored(r, h >> np.uint32(16), True)
     return out
 
 
@@ -337,7 +336,7 @@ def test_the_average_of_what_is_stored_is_what_was_computed(which):
         total += outs[0][which].view(F8).double() * outs[0][which + "_scale"].double()
     b1, b2 = _f32(B1), _f32(B2)
     g = g.double()
-    x = (1 - b1) * g if which == "m" else torch.sqrt((1 - b2) * g * g)
+    x = (1 - b1) * g if which == "m" else (1 - b2) ** 0.5 * g
     top = x.max() / 256
     step = torch.clamp(2.0 ** (torch.floor(torch.log2(x / top)) - 3), min=2.0 ** -9) * top
     off = (total / keys - x).abs()
@@ -381,9 +380,9 @@ def test_blocks_of_zeros_and_tiny_numbers():
         it[k].zero_()
         it[k + "_scale"].zero_()
     it["grad"].zero_()
-    it["grad"][256:512] = 1e-39   # of which neither m' nor sqrt(v') reaches 2^-126
-    it["grad"][512] = 1e-30
-    it["grad"][513:768] = 1e-36   # below the least number beside 1e-30: never 0 in v
+    it["grad"][256:512] = 1e-31   # m' is below 2^-100, the square is 0
+    it["grad"][512] = 1e-12
+    it["grad"][513:768] = 1e-20   # below the least number beside 1e-12: never 0 in v
     before = case.state()
     Z.ZeroAdamW(case.tensors()).step(case.grads(), LR, 1, key=5)
     _compare(case, before, 1, key=5)
@@ -492,9 +491,8 @@ def test_elements_past_32_bits():
     c, key = 0x9E3779B9, 5
     base = int(mix(np.array([(key + c) & 0xFFFFFFFF]))[0]) + c * int(mix(np.array([1]))[0])
     bits = mix((base + np.arange(300, dtype=np.int64)).astype(np.uint32))
-    b1 = _f32(B1)
-    m32 = ((1 - b1) * grad[at:].double().cpu().numpy()).astype(np.float32)
+    m32 = np.float32(1 - _f32(B1)) * grad[at:].float().cpu().numpy()
     code, scale = _stored(m32, bits & np.uint32(0xFFFF), False)
-    code = np.where(m32 < 0, code | 0x80, code).astype(np.uint8)
+    code = np.where(np.signbit(m32), code | 0x80, code).astype(np.uint8)
     assert (state["m"][at:].view(torch.uint8).cpu().numpy() == code).all()
     assert (state["m_scale"][at // 256:].cpu().numpy() == scale).all()
