@@ -46,6 +46,113 @@ __device__ __forceinline__ float sigmoid(float z, float &slope) {
   return z < 0.0f ? t * inv : inv;  // of a NaN: a NaN
 }
 
+// A row's mean and variance with one barrier: each wave centres its own columns,
+// and the waves' sums are joined as those of samples with means of their own:
+//   mean = sum n_w mean_w / cols;  cols var = sum (sq_w + n_w (mean_w - mean)^2)
+// What a wave's mean is off by (off, the sum of its deviations, zero but for
+// rounding) is made good, so that rows far from zero keep their digits.
+struct Moments {
+  float (*lds)[16][8];     // [2][wave of the workgroup][value], as for Sums
+  int first, waves;        // of this row group
+  float inv;               // 1 / cols
+  float inv_own;           // 1 / columns of this wave (0: none)
+  float n_lane, inv_lane;  // columns of the row group's wave lane % 16, and their inverse
+
+  // A wave's columns: `per` threads share the row's pieces of eight, N of them each.
+  template <int N>
+  static __device__ __forceinline__ float columns(int wave, int per, int cols) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int left = cols - (k * per + wave * 64) * 8;
+      n += left < 0 ? 0 : left < 512 ? left : 512;
+    }
+    return float(n);
+  }
+
+  // Deviations of R rows from their waves' means, in v's place (live(n, e): a column of
+  // the row); afterwards (v + shift) rstd is normalised.
+  template <int N, int R, class Live>
+  __device__ __forceinline__ void of(float (&v)[R][N][8], int &turn, Live live, float eps,
+                                     float (&mean)[R], float (&rstd)[R], float (&shift)[R]) {
+    float own[R], sq[R], off[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += v[k][n][e];
+      own[k] = wave_sum(sum) * inv_own;
+      sq[k] = off[k] = 0.0f;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = live(n, e) ? v[k][n][e] - own[k] : 0.0f;
+          sq[k] = __builtin_fmaf(d, d, sq[k]);
+          off[k] += d;
+          v[k][n][e] = d;
+        }
+      sq[k] = wave_sum(sq[k]);
+      off[k] = wave_sum(off[k]);
+    }
+    float square[R];
+    if (waves == 1) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        const float o = finite(off[k] * inv);
+        mean[k] = own[k] + o;
+        square[k] = sq[k] - o * off[k];
+      }
+    } else {
+      const int lane = threadIdx.x & 63;
+      float (*buf)[8] = lds[turn];
+      turn ^= 1;
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          float *to = buf[threadIdx.x >> 6] + 3 * k;
+          to[0] = own[k];
+          to[1] = off[k];
+          to[2] = sq[k];
+        }
+      }
+      // all of LDS is there; loads from memory stay in flight
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      // sixteen lanes a row, one a wave
+      const int w = lane & 15, k = lane >> 4;
+      const bool in = k < R && w < waves;
+      const float *from = buf[first + (in ? w : 0)] + 3 * (in ? k : 0);
+      const float pivot = buf[first][3 * (k < R ? k : 0)];
+      const float o = in ? finite(from[1]) * inv_lane : 0.0f;
+      const float at = in && n_lane > 0.0f ? from[0] + o : pivot;
+      const float m = pivot + sum16(in ? n_lane * (at - pivot) : 0.0f) * inv;
+      const float d = in && n_lane > 0.0f ? at - m : 0.0f;
+      const float all = sum16(in ? (from[2] - o * o * n_lane) + n_lane * d * d : 0.0f);
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        mean[j] = lane_value(m, j * 16);
+        square[j] = lane_value(all, j * 16);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      // of a constant row a difference of two equal values up to rounding; a NaN stays one
+      const float var = square[k] * inv;
+      rstd[k] = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps);
+      shift[k] = own[k] - mean[k];
+    }
+  }
+
+  // An infinite row keeps its mean.
+  static __device__ __forceinline__ float finite(float v) {
+    return fabsf(v) < INFINITY ? v : 0.0f;
+  }
+};
+
 struct FwdArgs {
   int64_t rows, cols;
   int64_t ld_x, ld_b, ld_z, ld_s, ld_y;  // elements
@@ -55,7 +162,8 @@ struct FwdArgs {
   float *stats;
   float eps, scale;
   int32_t center, post;
-  int32_t per;  // threads of a row
+  int32_t per;   // threads of a row
+  int32_t take;  // rows at a time, at most R
 };
 
 // R rows at a time, each over `per` threads (a multiple of 64) of the
@@ -66,27 +174,46 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
   __shared__ float lds[2][16][8];
   const int per = A.per, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / per);
   const int t = threadIdx.x - sub * per, subs = blockDim.x / per;
+  const int wave = __builtin_amdgcn_readfirstlane(t / 64), cols = int(A.cols);
   Sums sums{lds, sub * per / 64, per / 64};
-  const Columns<N> c(t, per, int(A.cols));
-  Eight<TP> gate[N], gamma0[N], beta0[N], gamma[N], beta[N];
-  load_params<TAIL>(gate, A.gate, 1.0f, c);
-  load_params<TAIL>(gamma0, A.gamma0, 1.0f, c);
-  load_params<TAIL>(beta0, A.beta0, 0.0f, c);
+  const float own = Moments::columns<N>(wave, per, cols);
+  const float other = Moments::columns<N>(threadIdx.x & 15, per, cols);
+  Moments moments{lds, sub * per / 64, per / 64, 1.0f / float(cols),
+                  own > 0.0f ? 1.0f / own : 0.0f, other, other > 0.0f ? 1.0f / other : 0.0f};
+  const Columns<N> c(t, per, cols);
+  const auto live = [&](int n, int e) { return (TAIL ? e : 0) < c.left[n]; };
+  // the gate of a column joins the first norm's gain and bias
+  float gain[N][8], bias[N][8];
+  {
+    Eight<TP> g[N], p[N];
+    load_params<TAIL>(g, A.gate, 1.0f, c);
+    load_params<TAIL>(p, A.gamma0, 1.0f, c);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) gain[n][e] = g[n].get(e) * p[n].get(e);
+    load_params<TAIL>(p, A.beta0, 0.0f, c);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) bias[n][e] = g[n].get(e) * p[n].get(e);
+  }
+  Eight<TP> gamma[N], beta[N];
   load_params<TAIL>(gamma, A.gamma, 1.0f, c);
   load_params<TAIL>(beta, A.beta, 0.0f, c);
-  const float inv = 1.0f / float(A.cols);
-  const auto live = [&](int n, int e) { return (TAIL ? e : 0) < c.left[n]; };
   constexpr bool kOnce = N == 1 && !TAIL && sizeof(typename TX::raw) == 2;
-  const int64_t step = int64_t(gridDim.x) * subs * R;
+  const int take = A.take;
+  const int64_t step = int64_t(gridDim.x) * subs * take;
   struct Rows {
     Eight<TX> x[R][N], b[R][N], z[WIDE ? R : 1][WIDE ? N : 1];
   };
+  const auto is = [&](int64_t r0, int k) { return k < take && r0 + k < A.rows; };
   const auto load = [&](Rows &v, int64_t r0) {
 #pragma unroll
     for (int k = 0; k < R; ++k)
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const int left = r0 + k < A.rows ? c.left[n] : 0;
+        const int left = is(r0, k) ? c.left[n] : 0;
         v.x[k][n].template load<TAIL, kOnce>(row_of<TX>(A.x, r0 + k, A.ld_x), c.i[n], left);
         v.b[k][n].template load<TAIL, kOnce>(row_of<TX>(A.block, r0 + k, A.ld_b), c.i[n],
                                              A.block ? left : 0);
@@ -94,50 +221,17 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
           v.z[k][n].template load<TAIL, kOnce>(row_of<TX>(A.z, r0 + k, A.ld_z), c.i[n], left);
       }
   };
-  // Rows of values (zeros past their ends) to their normalised ones.
-  float v[R][N][8], mean[R], rstd[R];
-  const auto normalise = [&]() {
+  // Rows of values (zeros past their ends) to their normalised ones: v scale + shift.
+  float v[R][N][8], mean[R], rstd[R], shift[R];
+  const auto statistics = [&]() {
     if (A.center) {
+      moments.of<N, R>(v, sums.turn, live, A.eps, mean, rstd, shift);
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
-        mean[k] = 0.0f;
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) mean[k] += v[k][n][e];
-      }
-      sums.add(mean);
-      float both[2 * R];
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        mean[k] *= inv;
-        float sq = 0.0f, off = 0.0f;
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float d = live(n, e) ? v[k][n][e] - mean[k] : 0.0f;
-            sq = __builtin_fmaf(d, d, sq);
-            off += d;
-            v[k][n][e] = d;
-          }
-        both[2 * k] = sq;
-        both[2 * k + 1] = off;
-      }
-      sums.add(both);
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        float off = both[2 * k + 1];
-        rstd[k] = finish(both[2 * k], off, inv, A.eps, mean[k]);
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[k][n][e] = (v[k][n][e] - off) * rstd[k];
-      }
+      for (int k = 0; k < R; ++k) shift[k] *= rstd[k];
     } else {
 #pragma unroll
       for (int k = 0; k < R; ++k) {
-        rstd[k] = 0.0f;
+        rstd[k] = shift[k] = 0.0f;
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
@@ -145,20 +239,14 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
       }
       sums.add(rstd);
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
-        rstd[k] = 1.0f / sqrtf(rstd[k] * inv + A.eps);
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[k][n][e] *= rstd[k];
-      }
+      for (int k = 0; k < R; ++k) rstd[k] = 1.0f / sqrtf(rstd[k] * moments.inv + A.eps);
     }
   };
   const auto keep = [&](int64_t r0, int which) {
     if (t != 0 || !A.stats) return;
 #pragma unroll
     for (int k = 0; k < R; ++k)
-      if (r0 + k < A.rows) {
+      if (is(r0, k)) {
         A.stats[which * A.rows + r0 + k] = rstd[k];
         if (A.center) A.stats[(which + 2) * A.rows + r0 + k] = mean[k];
       }
@@ -167,9 +255,9 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
   // registers hold both.
   constexpr bool kAhead = N == 1;
   Rows ahead;
-  if constexpr (kAhead) load(ahead, (int64_t(blockIdx.x) * subs + sub) * R);
-  for (int64_t first = int64_t(blockIdx.x) * subs * R; first < A.rows; first += step) {
-    const int64_t r0 = first + sub * R;
+  if constexpr (kAhead) load(ahead, (int64_t(blockIdx.x) * subs + sub) * take);
+  for (int64_t first = int64_t(blockIdx.x) * subs * take; first < A.rows; first += step) {
+    const int64_t r0 = first + sub * take;
     Rows now;
     if constexpr (kAhead) {
       now = ahead;
@@ -182,8 +270,14 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
 #pragma unroll
       for (int n = 0; n < N; ++n) now.b[k][n].get(v[k][n]);
     if (A.post) {
-      normalise();
+      statistics();
       keep(r0, 0);
+    } else {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        rstd[k] = 1.0f;
+        shift[k] = 0.0f;
+      }
     }
 #pragma unroll
     for (int k = 0; k < R; ++k)
@@ -191,34 +285,34 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
       for (int n = 0; n < N; ++n) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float g = v[k][n][e];
-          if (A.post) g = __builtin_fmaf(g, gamma0[n].get(e), beta0[n].get(e));
+          float g = __builtin_fmaf(v[k][n][e], rstd[k], shift[k]);
+          g = __builtin_fmaf(g, gain[n][e], bias[n][e]);
           if constexpr (WIDE) {
             float slope;
             g *= sigmoid(now.z[k][n].get(e), slope);
-          } else {
-            g *= gate[n].get(e);
           }
           g = __builtin_fmaf(A.scale, now.x[k][n].get(e), g);
           v[k][n][e] = live(n, e) ? g : 0.0f;
         }
         if (A.block) {
           now.x[k][n].set(v[k][n]);
-          if (r0 + k < A.rows)
+          if (is(r0, k))
             now.x[k][n].template store<TAIL>(row_of<TX>(A.sum, r0 + k, A.ld_s), c.i[n], c.left[n]);
         }
         now.x[k][n].get(v[k][n]);  // as it was rounded
       }
-    normalise();
+    statistics();
     keep(r0, 1);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      if (r0 + k >= A.rows) break;
+      if (!is(r0, k)) break;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          v[k][n][e] = __builtin_fmaf(v[k][n][e], gamma[n].get(e), beta[n].get(e));
+        for (int e = 0; e < 8; ++e) {
+          const float h = __builtin_fmaf(v[k][n][e], rstd[k], shift[k]);
+          v[k][n][e] = __builtin_fmaf(h, gamma[n].get(e), beta[n].get(e));
+        }
         now.x[k][n].set(v[k][n]);
         now.x[k][n].template store<TAIL>(row_of<TX>(A.y, r0 + k, A.ld_y), c.i[n], c.left[n]);
       }
@@ -242,22 +336,65 @@ struct BwdArgs {
   int32_t per;    // threads of a row
 };
 
+// The columns' sums are in registers, or, where those do not hold them beside the
+// rows, in LDS, a thread's own places of it: all four, or the first two of sixteen
+// columns a thread.
 template <class TX, class TP, int N, bool TAIL, bool WIDE>
 __global__ void __launch_bounds__(1024) seam_bwd_kernel(const BwdArgs A) {
+  constexpr bool kLds = WIDE || N == 2 || sizeof(typename TX::raw) == 4;
+  constexpr int kInLds = !kLds ? 0 : N == 2 ? 2 : 4;
   __shared__ float lds[2][16][8];
-  __shared__ float join[1024 * 8];
+  __shared__ __align__(16) float store[kLds ? kInLds * N * 8 * 1024 : 8 * 1024];
   const int per = A.per, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / per);
   const int t = threadIdx.x - sub * per, subs = blockDim.x / per;
   Sums sums{lds, sub * per / 64, per / 64};
   const Columns<N> c(t, per, int(A.cols));
-  Eight<TP> gate[N], gamma0[N], beta0[N], gamma[N];
-  load_params<TAIL>(gate, A.gate, 1.0f, c);
-  load_params<TAIL>(gamma0, A.gamma0, 1.0f, c);
-  if constexpr (WIDE) load_params<TAIL>(beta0, A.beta0, 0.0f, c);
-  load_params<TAIL>(gamma, A.gamma, 1.0f, c);
-  const float inv = 1.0f / float(A.cols);
   const auto live = [&](int n, int e) { return (TAIL ? e : 0) < c.left[n]; };
+  Eight<TP> gamma[N], gamma0[WIDE ? N : 1], beta0[WIDE ? N : 1];
+  load_params<TAIL>(gamma, A.gamma, 1.0f, c);
+  float gain[WIDE ? 1 : N][8];  // gate gamma0, of a column
+  if constexpr (WIDE) {
+    load_params<TAIL>(gamma0, A.gamma0, 1.0f, c);
+    load_params<TAIL>(beta0, A.beta0, 0.0f, c);
+  } else {
+    Eight<TP> g[N], p[N];
+    load_params<TAIL>(g, A.gate, 1.0f, c);
+    load_params<TAIL>(p, A.gamma0, 1.0f, c);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) gain[n][e] = g[n].get(e) * p[n].get(e);
+  }
+  const float inv = 1.0f / float(A.cols);
   float acc[4][N][8] = {};
+  // fours of a thread's sums, side by side over the threads
+  const auto place = [&](int which, int n, int half) {
+    return reinterpret_cast<f32x4 *>(store) + ((which * N + n) * 2 + half) * 1024 + threadIdx.x;
+  };
+  // sum `which` += a b
+  const auto add = [&](int which, int n, const float (&a)[8], const float (&b)[8]) {
+    if (which < kInLds) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        f32x4 *p = place(which, n, half);
+        f32x4 v = *p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(a[half * 4 + e], b[half * 4 + e], v[e]);
+        *p = v;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[which][n][e] = __builtin_fmaf(a[e], b[e], acc[which][n][e]);
+    }
+  };
+#pragma unroll
+  for (int which = 0; which < kInLds; ++which)
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      *place(which, n, 0) = f32x4{};
+      *place(which, n, 1) = f32x4{};
+    }
+  constexpr float kOnes[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
   constexpr bool kOnce = N == 1 && !TAIL && sizeof(typename TX::raw) == 2;
   const int64_t step = int64_t(gridDim.x) * subs;
   struct Rows {
@@ -284,7 +421,7 @@ __global__ void __launch_bounds__(1024) seam_bwd_kernel(const BwdArgs A) {
         v.z[n].template load<TAIL, kOnce>(row_of<TX>(A.z, r, A.ld_z), c.i[n], left);
     }
   };
-  constexpr bool kAhead = N == 1;  // as in the forward pass
+  constexpr bool kAhead = N == 1 && sizeof(typename TX::raw) == 2;  // registers hold both
   Rows ahead;
   if constexpr (kAhead) load(ahead, int64_t(blockIdx.x) * subs + sub);
   for (int64_t first = int64_t(blockIdx.x) * subs; first < A.rows; first += step) {
@@ -306,18 +443,22 @@ __global__ void __launch_bounds__(1024) seam_bwd_kernel(const BwdArgs A) {
     };
     float both[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+    for (int n = 0; n < N; ++n) {
+      float h[8], d[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float h = h1(n, e), d = now.dy[n].get(e), g = d * gamma[n].get(e);
-        acc[0][n][e] = __builtin_fmaf(d, h, acc[0][n][e]);
-        acc[1][n][e] += d;
+        h[e] = h1(n, e);
+        d[e] = now.dy[n].get(e);
+        const float g = d[e] * gamma[n].get(e);
         both[0] += g;
-        both[1] = __builtin_fmaf(g, h, both[1]);
+        both[1] = __builtin_fmaf(g, h[e], both[1]);
       }
+      add(0, n, d, h);
+      add(1, n, d, kOnes);
+    }
     sums.add(both);
     float c1 = A.center ? both[0] * inv : 0.0f, c2 = both[1] * inv;
-    float D[N][8];  // then, normalised through the gate, the gradient of h0
+    float D[N][8];  // then, through the gate and the gain, the gradient of h0
     both[0] = both[1] = 0.0f;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
@@ -334,28 +475,31 @@ __global__ void __launch_bounds__(1024) seam_bwd_kernel(const BwdArgs A) {
       now.dy[n].set(out);
       if (r < A.rows)
         now.dy[n].template store<TAIL>(row_of<TX>(A.dx, r, A.ld_dx), c.i[n], c.left[n]);
+      float h[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = h0(n, e);
       if constexpr (WIDE) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float slope;
-          const float gain = sigmoid(now.z[n].get(e), slope);
-          float v = h0(n, e);
+          const float open = sigmoid(now.z[n].get(e), slope);
+          float v = h[e];
           if (A.post) v = __builtin_fmaf(v, gamma0[n].get(e), beta0[n].get(e));
           out[e] = D[n][e] * v * slope;
-          D[n][e] = live(n, e) ? D[n][e] * gain : 0.0f;
+          D[n][e] = live(n, e) ? D[n][e] * open : 0.0f;
         }
         now.z[n].set(out);
         if (r < A.rows && A.dz)
           now.z[n].template store<TAIL>(row_of<TX>(A.dz, r, A.ld_dz), c.i[n], c.left[n]);
       }
+      add(2, n, D[n], h);
+      add(3, n, D[n], kOnes);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float h = h0(n, e);
-        acc[2][n][e] = __builtin_fmaf(D[n][e], h, acc[2][n][e]);
-        acc[3][n][e] += D[n][e];
-        D[n][e] *= WIDE ? gamma0[n].get(e) : gamma0[n].get(e) * gate[n].get(e);
+        if constexpr (WIDE) D[n][e] *= gamma0[n].get(e);
+        else D[n][e] *= gain[n][e];
         both[0] += D[n][e];
-        both[1] = __builtin_fmaf(D[n][e], h, both[1]);
+        both[1] = __builtin_fmaf(D[n][e], h[e], both[1]);
       }
     }
     if (!A.block) continue;
@@ -378,23 +522,32 @@ __global__ void __launch_bounds__(1024) seam_bwd_kernel(const BwdArgs A) {
   }
   if (!A.part) return;
   // the row groups' sums, then the workgroup's partial rows
+  if (kLds && subs > 1) __syncthreads();
 #pragma unroll
   for (int which = 0; which < 4; ++which) {
     if (!(A.want & (which < 2 ? 1 : 2))) continue;
     float *out = A.part + (int64_t(which) * A.parts + blockIdx.x) * A.cols;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      if (subs > 1) {
+      if (which < kInLds) {
+        if (sub > 0) continue;
+        for (int w = 0; w < subs; ++w)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float v = (*(place(which, n, e / 4) + w * per))[e % 4];
+            acc[which][n][e] = w ? acc[which][n][e] + v : v;
+          }
+      } else if (subs > 1) {  // not with sixteen columns a thread
         __syncthreads();
         if (sub > 0) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) join[((sub - 1) * 8 + e) * per + t] = acc[which][n][e];
+          for (int e = 0; e < 8; ++e) store[((sub - 1) * 8 + e) * per + t] = acc[which][n][e];
         }
         __syncthreads();
         if (sub > 0) continue;
         for (int w = 0; w < subs - 1; ++w)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[which][n][e] += join[(w * 8 + e) * per + t];
+          for (int e = 0; e < 8; ++e) acc[which][n][e] += store[(w * 8 + e) * per + t];
       }
       Eight<F32> v;
       v.set(acc[which][n]);
@@ -553,21 +706,28 @@ int zero_shard_blocknorm(const zs_blocknorm_desc *d, const void *x, const void *
   if (const int rc = device_is_gfx950()) return rc;
   const auto ld = [&](int64_t v) { return v ? v : d->cols; };
   const Way w = way_of(*d, kThreads);
-  const FwdArgs A{d->rows, d->cols, ld(d->ld_x), ld(d->ld_block), ld(d->ld_gate), ld(d->ld_sum),
+  FwdArgs A{d->rows, d->cols, ld(d->ld_x), ld(d->ld_block), ld(d->ld_gate), ld(d->ld_sum),
                   ld(d->ld_y), x, block, wide ? gate : nullptr, wide ? nullptr : gate, gamma_post,
                   beta_post, gamma, beta, sum, y, stats, d->eps, d->residual_scale,
-                  d->kind == ZS_NORM_LAYER, d->post, w.per};
+                  d->kind == ZS_NORM_LAYER, d->post, w.per, 1};
   const bool even = rows_even(x, A.ld_x, size) && rows_even(block, A.ld_b, size) &&
                     rows_even(A.z, A.ld_z, size) && rows_even(sum, A.ld_s, size) &&
                     rows_even(y, A.ld_y, size);
   const int threads = w.per * w.subs;
-  const int64_t groups = (A.rows + w.subs - 1) / w.subs;
-  const int64_t most = int64_t(kCus) * (2048 / threads);
   return by_type(*d, [&](auto tx, auto tp) {
     using TX = decltype(tx);
     using TP = decltype(tp);
     return by_way(w.n, d->cols % 8 != 0 || !even, wide, [&](auto n, auto tail, auto wd) {
-      hipLaunchKernelGGL((seam_fwd_kernel<TX, TP, n.value, 1, tail.value, wd.value>),
+#ifndef FR
+#define FR 2
+#define FW 1280
+#endif
+      // two rows at a time once every CU has some, where the registers hold them
+      constexpr int R = n.value == 1 && sizeof(typename TX::raw) == 2 && !wd.value ? FR : 1;
+      A.take = A.rows >= 4 * kCus ? R : 1;
+      const int64_t groups = (A.rows + w.subs * A.take - 1) / (w.subs * A.take);
+      const int64_t most = int64_t(kCus) * (FW > threads ? FW / threads : 1);
+      hipLaunchKernelGGL((seam_fwd_kernel<TX, TP, n.value, R, tail.value, wd.value>),
                          dim3(unsigned(groups < most ? groups : most)), dim3(threads), 0,
                          static_cast<hipStream_t>(d->stream), A);
       return launched();
