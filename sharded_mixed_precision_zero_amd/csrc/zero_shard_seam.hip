@@ -46,14 +46,72 @@ __device__ __forceinline__ float sigmoid(float z, float &slope) {
   return z < 0.0f ? t * inv : inv;  // of a NaN: a NaN
 }
 
-// A row's mean and variance with one barrier: each wave centres its own columns,
+// Sums of M values (1, 2 or 4) over the wave in one register: afterwards its M
+// equal parts hold one each, in order, in every lane.  Exchanging halves lets each
+// lane carry on with one value instead of M: 10 instructions for 4 values where one
+// after another took 44.
+template <int M>
+__device__ __forceinline__ float wave_sums(const float (&v)[M]) {
+  static_assert(M == 1 || M == 2 || M == 4, "parts of a wave");
+  const auto halves = [](float a, float b) {  // lanes 0-31: a, 32-63: b
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false,
+                                                    false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  };
+  const auto rows = [](float a, float b) {  // of sixteen lanes: a, b, a, b
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false,
+                                                    false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  };
+  float x;
+  if constexpr (M == 4) {
+    x = rows(halves(v[0], v[2]), halves(v[1], v[3]));
+  } else {
+    const float h = halves(v[0], v[M - 1]);
+    x = rows(h, h);
+  }
+  return sum16(x);
+}
+
+// The waves of a row group, and the LDS they exchange sums through.  One barrier an
+// exchange: two buffers take turns, so a buffer is written again only after all have
+// passed the next exchange's barrier.
+struct Waves {
+  float (*lds)[16][8];  // [2][wave of the workgroup][value]
+  int first, count;     // of this row group
+  int turn = 0;
+
+  __device__ __forceinline__ float (*exchange(float x, int parts, float extra))[8] {
+    const int lane = threadIdx.x & 63;
+    float (*buf)[8] = lds[turn];
+    turn ^= 1;
+    float *own = buf[threadIdx.x >> 6];
+    if ((lane & (64 / parts - 1)) == 0) own[lane * parts / 64] = x;
+    if ((lane & 15) == 1) own[4 + (lane >> 4)] = extra;
+    // all of LDS is there; loads from memory stay in flight
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    return buf + first;
+  }
+
+  // As wave_sums, over the row group.
+  template <int M>
+  __device__ __forceinline__ float sums(const float (&v)[M]) {
+    const float x = wave_sums(v);
+    if (count == 1) return x;
+    const int lane = threadIdx.x & 63, w = lane & 15;
+    float (*buf)[8] = exchange(x, M, 0.0f);
+    return sum16(w < count ? buf[w][lane * M / 64] : 0.0f);
+  }
+};
+
+// A row's mean and variance with one exchange: each wave centres its own columns,
 // and the waves' sums are joined as those of samples with means of their own:
 //   mean = sum n_w mean_w / cols;  cols var = sum (sq_w + n_w (mean_w - mean)^2)
 // What a wave's mean is off by (off, the sum of its deviations, zero but for
 // rounding) is made good, so that rows far from zero keep their digits.
 struct Moments {
-  float (*lds)[16][8];     // [2][wave of the workgroup][value], as for Sums
-  int first, waves;        // of this row group
   float inv;               // 1 / cols
   float inv_own;           // 1 / columns of this wave (0: none)
   float n_lane, inv_lane;  // columns of the row group's wave lane % 16, and their inverse
@@ -70,86 +128,81 @@ struct Moments {
     return float(n);
   }
 
-  // Deviations of R rows from their waves' means, in v's place (live(n, e): a column of
-  // the row); afterwards (v + shift) rstd is normalised.
-  template <int N, int R, class Live>
-  __device__ __forceinline__ void of(float (&v)[R][N][8], int &turn, Live live, float eps,
-                                     float (&mean)[R], float (&rstd)[R], float (&shift)[R]) {
-    float own[R], sq[R], off[R];
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += v[k][n][e];
-      own[k] = wave_sum(sum) * inv_own;
-      sq[k] = off[k] = 0.0f;
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float d = live(n, e) ? v[k][n][e] - own[k] : 0.0f;
-          sq[k] = __builtin_fmaf(d, d, sq[k]);
-          off[k] += d;
-          v[k][n][e] = d;
-        }
-      sq[k] = wave_sum(sq[k]);
-      off[k] = wave_sum(off[k]);
-    }
-    float square[R];
-    if (waves == 1) {
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        const float o = finite(off[k] * inv);
-        mean[k] = own[k] + o;
-        square[k] = sq[k] - o * off[k];
-      }
-    } else {
-      const int lane = threadIdx.x & 63;
-      float (*buf)[8] = lds[turn];
-      turn ^= 1;
-      if (lane == 0) {
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-          float *to = buf[threadIdx.x >> 6] + 3 * k;
-          to[0] = own[k];
-          to[1] = off[k];
-          to[2] = sq[k];
-        }
-      }
-      // all of LDS is there; loads from memory stay in flight
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      // sixteen lanes a row, one a wave
-      const int w = lane & 15, k = lane >> 4;
-      const bool in = k < R && w < waves;
-      const float *from = buf[first + (in ? w : 0)] + 3 * (in ? k : 0);
-      const float pivot = buf[first][3 * (k < R ? k : 0)];
-      const float o = in ? finite(from[1]) * inv_lane : 0.0f;
-      const float at = in && n_lane > 0.0f ? from[0] + o : pivot;
-      const float m = pivot + sum16(in ? n_lane * (at - pivot) : 0.0f) * inv;
-      const float d = in && n_lane > 0.0f ? at - m : 0.0f;
-      const float all = sum16(in ? (from[2] - o * o * n_lane) + n_lane * d * d : 0.0f);
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        mean[j] = lane_value(m, j * 16);
-        square[j] = lane_value(all, j * 16);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      // of a constant row a difference of two equal values up to rounding; a NaN stays one
-      const float var = square[k] * inv;
-      rstd[k] = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps);
-      shift[k] = own[k] - mean[k];
-    }
-  }
-
   // An infinite row keeps its mean.
   static __device__ __forceinline__ float finite(float v) {
     return fabsf(v) < INFINITY ? v : 0.0f;
+  }
+
+  // Deviations of R rows from their waves' means, in v's place; afterwards
+  // (v + shift) rstd is normalised.
+  template <bool TAIL, int N, int R>
+  __device__ __forceinline__ void of(float (&v)[R][N][8], Waves &waves, const Columns<N> &c,
+                                     float eps, float (&mean)[R], float (&rstd)[R],
+                                     float (&shift)[R]) {
+    const int lane = threadIdx.x & 63;
+    float own[R], two[2 * R];
+    {
+      float sum[R];
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        sum[k] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum[k] += v[k][n][e];
+      }
+      const float x = wave_sums(sum) * inv_own;
+#pragma unroll
+      for (int k = 0; k < R; ++k) own[k] = lane_value(x, k * 64 / R);
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      float sq = 0.0f, off = 0.0f;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        // columns that are not the row's have no deviation from 0
+        const float m = c.left[n] > 0 ? own[k] : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = !TAIL || e < c.left[n] ? v[k][n][e] - m : 0.0f;
+          sq = __builtin_fmaf(d, d, sq);
+          off += d;
+          v[k][n][e] = d;
+        }
+      }
+      two[2 * k] = sq;
+      two[2 * k + 1] = off;
+    }
+    const float x = wave_sums(two);
+    // sixteen lanes a row, one a wave
+    const int w = lane & 15, k = R == 2 ? lane >> 4 & 1 : 0;
+    float m, square;
+    if (waves.count == 1) {
+      const float sq = R == 2 && k ? lane_value(x, 32) : lane_value(x, 0);
+      const float off = R == 2 && k ? lane_value(x, 48) : lane_value(x, 64 / R / 2);
+      const float o = finite(off) * inv;
+      m = (R == 2 && k ? own[R - 1] : own[0]) + o;
+      square = sq - o * o / inv;
+    } else {
+      float (*buf)[8] = waves.exchange(x, 2 * R, R == 2 && k ? own[R - 1] : own[0]);
+      const bool in = w < waves.count;
+      const float *from = buf[in ? w : 0];
+      const float pivot = buf[0][4 + k];
+      const float o = in ? finite(from[2 * k + 1]) * inv_lane : 0.0f;
+      const float at = in && n_lane > 0.0f ? from[4 + k] + o : pivot;
+      m = pivot + sum16(in ? n_lane * (at - pivot) : 0.0f) * inv;
+      const float d = in && n_lane > 0.0f ? at - m : 0.0f;
+      square = sum16(in ? (from[2 * k] - o * o * n_lane) + n_lane * d * d : 0.0f);
+    }
+    // of a constant row a difference of two equal values up to rounding; a NaN stays one
+    const float var = square * inv;
+    const float r = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      mean[j] = lane_value(m, j * 16);
+      rstd[j] = lane_value(r, j * 16);
+      shift[j] = own[j] - mean[j];
+    }
   }
 };
 
@@ -175,14 +228,15 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
   const int per = A.per, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / per);
   const int t = threadIdx.x - sub * per, subs = blockDim.x / per;
   const int wave = __builtin_amdgcn_readfirstlane(t / 64), cols = int(A.cols);
-  Sums sums{lds, sub * per / 64, per / 64};
+  Waves waves{lds, sub * per / 64, per / 64};
   const float own = Moments::columns<N>(wave, per, cols);
   const float other = Moments::columns<N>(threadIdx.x & 15, per, cols);
-  Moments moments{lds, sub * per / 64, per / 64, 1.0f / float(cols),
-                  own > 0.0f ? 1.0f / own : 0.0f, other, other > 0.0f ? 1.0f / other : 0.0f};
+  Moments moments{1.0f / float(cols), own > 0.0f ? 1.0f / own : 0.0f, other,
+                  other > 0.0f ? 1.0f / other : 0.0f};
   const Columns<N> c(t, per, cols);
   const auto live = [&](int n, int e) { return (TAIL ? e : 0) < c.left[n]; };
-  // the gate of a column joins the first norm's gain and bias
+  // the gate of a column joins the first norm's gain and bias; both are 0 past the
+  // row's end, and so is the sum there
   float gain[N][8], bias[N][8];
   {
     Eight<TP> g[N], p[N];
@@ -191,12 +245,12 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) gain[n][e] = g[n].get(e) * p[n].get(e);
+      for (int e = 0; e < 8; ++e) gain[n][e] = live(n, e) ? g[n].get(e) * p[n].get(e) : 0.0f;
     load_params<TAIL>(p, A.beta0, 0.0f, c);
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) bias[n][e] = g[n].get(e) * p[n].get(e);
+      for (int e = 0; e < 8; ++e) bias[n][e] = live(n, e) ? g[n].get(e) * p[n].get(e) : 0.0f;
   }
   Eight<TP> gamma[N], beta[N];
   load_params<TAIL>(gamma, A.gamma, 1.0f, c);
@@ -225,21 +279,22 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
   float v[R][N][8], mean[R], rstd[R], shift[R];
   const auto statistics = [&]() {
     if (A.center) {
-      moments.of<N, R>(v, sums.turn, live, A.eps, mean, rstd, shift);
+      moments.of<TAIL>(v, waves, c, A.eps, mean, rstd, shift);
 #pragma unroll
       for (int k = 0; k < R; ++k) shift[k] *= rstd[k];
     } else {
+      float sq[R];
 #pragma unroll
       for (int k = 0; k < R; ++k) {
-        rstd[k] = shift[k] = 0.0f;
+        sq[k] = shift[k] = 0.0f;
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) rstd[k] = __builtin_fmaf(v[k][n][e], v[k][n][e], rstd[k]);
+          for (int e = 0; e < 8; ++e) sq[k] = __builtin_fmaf(v[k][n][e], v[k][n][e], sq[k]);
       }
-      sums.add(rstd);
+      const float r = 1.0f / sqrtf(waves.sums(sq) * moments.inv + A.eps);
 #pragma unroll
-      for (int k = 0; k < R; ++k) rstd[k] = 1.0f / sqrtf(rstd[k] * moments.inv + A.eps);
+      for (int k = 0; k < R; ++k) rstd[k] = lane_value(r, k * 64 / R);
     }
   };
   const auto keep = [&](int64_t r0, int which) {
@@ -291,8 +346,7 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
             float slope;
             g *= sigmoid(now.z[k][n].get(e), slope);
           }
-          g = __builtin_fmaf(A.scale, now.x[k][n].get(e), g);
-          v[k][n][e] = live(n, e) ? g : 0.0f;
+          v[k][n][e] = __builtin_fmaf(A.scale, now.x[k][n].get(e), g);
         }
         if (A.block) {
           now.x[k][n].set(v[k][n]);
@@ -347,7 +401,7 @@ __global__ void __launch_bounds__(1024) seam_bwd_kernel(const BwdArgs A) {
   __shared__ __align__(16) float store[kLds ? kInLds * N * 8 * 1024 : 8 * 1024];
   const int per = A.per, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / per);
   const int t = threadIdx.x - sub * per, subs = blockDim.x / per;
-  Sums sums{lds, sub * per / 64, per / 64};
+  Waves waves{lds, sub * per / 64, per / 64};
   const Columns<N> c(t, per, int(A.cols));
   const auto live = [&](int n, int e) { return (TAIL ? e : 0) < c.left[n]; };
   Eight<TP> gamma[N], gamma0[WIDE ? N : 1], beta0[WIDE ? N : 1];
@@ -456,8 +510,8 @@ __global__ void __launch_bounds__(1024) seam_bwd_kernel(const BwdArgs A) {
       add(0, n, d, h);
       add(1, n, d, kOnes);
     }
-    sums.add(both);
-    float c1 = A.center ? both[0] * inv : 0.0f, c2 = both[1] * inv;
+    float total = waves.sums(both) * inv;
+    float c1 = A.center ? lane_value(total, 0) : 0.0f, c2 = lane_value(total, 32);
     float D[N][8];  // then, through the gate and the gain, the gradient of h0
     both[0] = both[1] = 0.0f;
 #pragma unroll
@@ -505,9 +559,9 @@ __global__ void __launch_bounds__(1024) seam_bwd_kernel(const BwdArgs A) {
     if (!A.block) continue;
     c1 = c2 = 0.0f;
     if (A.post) {
-      sums.add(both);
-      c1 = A.center ? both[0] * inv : 0.0f;
-      c2 = both[1] * inv;
+      total = waves.sums(both) * inv;
+      c1 = A.center ? lane_value(total, 0) : 0.0f;
+      c2 = lane_value(total, 32);
     }
     if (r >= A.rows) continue;
 #pragma unroll

@@ -53,6 +53,11 @@ struct Bf16 {
   static __device__ __forceinline__ raw store(float v) {
     return __builtin_bit_cast(raw, static_cast<__bf16>(v));
   }
+  static __device__ __forceinline__ unsigned store2(float lo, float hi) {  // one instruction
+    using Two = float __attribute__((ext_vector_type(2)));
+    using Out = __bf16 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(unsigned, __builtin_convertvector((Two{lo, hi}), Out));
+  }
 };
 struct F16 {
   using raw = uint16_t;
@@ -61,6 +66,9 @@ struct F16 {
   }
   static __device__ __forceinline__ raw store(float v) {
     return __builtin_bit_cast(raw, static_cast<_Float16>(v));
+  }
+  static __device__ __forceinline__ unsigned store2(float lo, float hi) {
+    return unsigned(store(lo)) | unsigned(store(hi)) << 16;
   }
 };
 
@@ -89,7 +97,7 @@ struct Eight {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       if constexpr (sizeof(raw) == 4) w[i] = __float_as_uint(in[i]);
-      else w[i] = unsigned(T::store(in[2 * i])) | unsigned(T::store(in[2 * i + 1])) << 16;
+      else w[i] = T::store2(in[2 * i], in[2 * i + 1]);
     }
   }
   // Values taken from here on are converted anew, not kept in registers.
