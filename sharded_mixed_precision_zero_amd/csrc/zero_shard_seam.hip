@@ -37,13 +37,25 @@ constexpr int kThreads = 256;
 constexpr int kMaxCols = ZS_BLOCKNORM_MAX_COLS;  // sixteen columns of 1024 threads
 constexpr int kCus = 256;
 constexpr int kMaxParts = 256;  // partial rows of the columns' sums
+constexpr int kResident = 1280;    // threads of the forward pass on a CU
+constexpr int kPairThreads = 768;  // most that hold two rows of the backward pass
 
-// sigmoid and its derivative; exp of a negative number only, so neither
-// overflows and 1 - sigmoid loses nothing
+// sigmoid and its derivative, from t = exp(-|z|): nothing overflows and 1 - sigmoid
+// loses nothing.  exp2 of the product's leading part, the rest to first order (below
+// 2^-17 of it); the quotient by one Newton step.  Within 4 half steps of binary32.
 __device__ __forceinline__ float sigmoid(float z, float &slope) {
-  const float t = expf(-fabsf(z)), inv = 1.0f / (1.0f + t);
+  constexpr float kLog2e = 1.44269504f, kRest = 1.92596304e-8f;  // of log2 e
+  float a = -fabsf(z);
+  a = a < -150.0f ? -150.0f : a;  // there t is 0; a NaN stays one
+  const float hi = a * kLog2e;
+  const float lo = __builtin_fmaf(a, kLog2e, -hi) + a * kRest;
+  float t = __builtin_amdgcn_exp2f(hi);
+  t = __builtin_fmaf(t, lo * 0.693147181f, t);
+  const float y = 1.0f + t;
+  float inv = __builtin_amdgcn_rcpf(y);
+  inv = __builtin_fmaf(__builtin_fmaf(-y, inv, 1.0f), inv, inv);
   slope = t * inv * inv;
-  return z < 0.0f ? t * inv : inv;  // of a NaN: a NaN
+  return z < 0.0f ? t * inv : inv;
 }
 
 // Sums of M values (1, 2 or 4) over the wave in one register: afterwards its M
@@ -388,57 +400,73 @@ struct BwdArgs {
   int32_t want;   // 1: the sums of dy h1 and dy, 2: of E h0 and E
   int32_t parts;  // 0: no rows (the gradients are zero)
   int32_t per;    // threads of a row
+  int32_t take;   // rows at a time, at most R
 };
 
-// The columns' sums are in registers, or, where those do not hold them beside the
-// rows, in LDS, a thread's own places of it: all four, or the first two of sixteen
-// columns a thread.
-template <class TX, class TP, int N, bool TAIL, bool WIDE>
-__global__ void __launch_bounds__(1024) seam_bwd_kernel(const BwdArgs A) {
-  constexpr bool kLds = WIDE || N == 2 || sizeof(typename TX::raw) == 4;
-  constexpr int kInLds = !kLds ? 0 : N == 2 ? 2 : 4;
+// R rows at a time.  The columns' sums are in LDS, a thread's own places of it, all
+// four, or of sixteen columns a thread the first two: with them in registers beside the
+// rows 8192 x 5120 bf16 with element gates took 449 us for 183, fp32 349 for 199,
+// and two rows at a time did not fit.
+template <class TX, class TP, int N, int R, bool TAIL, bool WIDE>
+__global__ void __launch_bounds__(R == 2 ? kPairThreads : 1024) seam_bwd_kernel(const BwdArgs A) {
+  constexpr int kInLds = N == 2 ? 2 : 4, kMost = R == 2 ? kPairThreads : 1024;
   __shared__ float lds[2][16][8];
-  __shared__ __align__(16) float store[kLds ? kInLds * N * 8 * 1024 : 8 * 1024];
+  __shared__ f32x4 store[kInLds * N * 2 * kMost];
   const int per = A.per, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / per);
   const int t = threadIdx.x - sub * per, subs = blockDim.x / per;
   Waves waves{lds, sub * per / 64, per / 64};
   const Columns<N> c(t, per, int(A.cols));
-  const auto live = [&](int n, int e) { return (TAIL ? e : 0) < c.left[n]; };
-  Eight<TP> gamma[N], gamma0[WIDE ? N : 1], beta0[WIDE ? N : 1];
-  load_params<TAIL>(gamma, A.gamma, 1.0f, c);
-  float gain[WIDE ? 1 : N][8];  // gate gamma0, of a column
-  if constexpr (WIDE) {
-    load_params<TAIL>(gamma0, A.gamma0, 1.0f, c);
-    load_params<TAIL>(beta0, A.beta0, 0.0f, c);
-  } else {
-    Eight<TP> g[N], p[N];
-    load_params<TAIL>(g, A.gate, 1.0f, c);
-    load_params<TAIL>(p, A.gamma0, 1.0f, c);
+  // past a row's end: whole threads, or (TAIL) single elements
+  const auto live = [&](int n, int e) { return !TAIL || e < c.left[n]; };
+  // Gains and the like stay in registers, or, with sixteen columns a thread, come
+  // out of the caches for each row.
+  constexpr bool kHeld = N == 1;
+  Eight<TP> gamma_held, gamma0_held, beta0_held;
+  float gain_held[8];  // gate gamma0, of a column
+  const auto fetch = [&](Eight<TP> &v, const void *p, float none, int n) {
+    if (p) {
+      v.template load<TAIL>(p, c.i[n], c.left[n]);
+    } else {
+      const float all[8] = {none, none, none, none, none, none, none, none};
+      v.set(all);
+    }
+  };
+  const auto fetch_gain = [&](float (&v)[8], int n) {
+    Eight<TP> g, p;
+    fetch(g, A.gate, 1.0f, n);
+    fetch(p, A.gamma0, 1.0f, n);
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) gain[n][e] = g[n].get(e) * p[n].get(e);
+    for (int e = 0; e < 8; ++e) v[e] = g.get(e) * p.get(e);
+  };
+  if constexpr (kHeld) {
+    fetch(gamma_held, A.gamma, 1.0f, 0);
+    if constexpr (WIDE) {
+      fetch(gamma0_held, A.gamma0, 1.0f, 0);
+      fetch(beta0_held, A.beta0, 0.0f, 0);
+    } else {
+      fetch_gain(gain_held, 0);
+    }
   }
   const float inv = 1.0f / float(A.cols);
-  float acc[4][N][8] = {};
+  float acc[N == 2 ? 2 : 1][N][8] = {};  // what is not in LDS
   // fours of a thread's sums, side by side over the threads
   const auto place = [&](int which, int n, int half) {
-    return reinterpret_cast<f32x4 *>(store) + ((which * N + n) * 2 + half) * 1024 + threadIdx.x;
+    return store + ((which * N + n) * 2 + half) * kMost + threadIdx.x;
   };
-  // sum `which` += a b
-  const auto add = [&](int which, int n, const float (&a)[8], const float (&b)[8]) {
+  // sum `which` += that
+  const auto add = [&](int which, int n, const float (&that)[8]) {
     if (which < kInLds) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         f32x4 *p = place(which, n, half);
         f32x4 v = *p;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(a[half * 4 + e], b[half * 4 + e], v[e]);
+        for (int e = 0; e < 4; ++e) v[e] += that[half * 4 + e];
         *p = v;
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[which][n][e] = __builtin_fmaf(a[e], b[e], acc[which][n][e]);
+      for (int e = 0; e < 8; ++e) acc[which - kInLds][n][e] += that[e];
     }
   };
 #pragma unroll
@@ -448,163 +476,195 @@ __global__ void __launch_bounds__(1024) seam_bwd_kernel(const BwdArgs A) {
       *place(which, n, 0) = f32x4{};
       *place(which, n, 1) = f32x4{};
     }
-  constexpr float kOnes[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
   constexpr bool kOnce = N == 1 && !TAIL && sizeof(typename TX::raw) == 2;
-  const int64_t step = int64_t(gridDim.x) * subs;
+  const int take = A.take;
+  const int64_t step = int64_t(gridDim.x) * subs * take;
   struct Rows {
-    Eight<TX> dy[N], ds[N], s[N], b[N], z[WIDE ? N : 1];
-    float r0, r1, m0, m1;
+    Eight<TX> dy[R][N], ds[R][N], s[R][N], b[R][N], z[WIDE ? R : 1][WIDE ? N : 1];
+    float r0[R], r1[R], m0[R], m1[R];
   };
-  const auto load = [&](Rows &v, int64_t r) {
-    const bool in = r < A.rows;
-    // a block that is not normalised is its own h0
-    v.r0 = !in ? 0.0f : A.post ? A.stats[r] : 1.0f;
-    v.r1 = in ? A.stats[A.rows + r] : 0.0f;
-    v.m0 = in && A.post && A.center ? A.stats[2 * A.rows + r] : 0.0f;
-    v.m1 = in && A.center ? A.stats[3 * A.rows + r] : 0.0f;
+  const auto is = [&](int64_t first, int k) { return k < take && first + k < A.rows; };
+  const auto load = [&](Rows &v, int64_t first) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int left = in ? c.left[n] : 0;
-      v.dy[n].template load<TAIL, kOnce>(row_of<TX>(A.dy, r, A.ld_dy), c.i[n], left);
-      v.s[n].template load<TAIL, kOnce>(row_of<TX>(A.sum, r, A.ld_s), c.i[n], left);
-      v.ds[n].template load<TAIL, kOnce>(row_of<TX>(A.dsum, r, A.ld_ds), c.i[n],
-                                         A.dsum ? left : 0);
-      v.b[n].template load<TAIL, kOnce>(row_of<TX>(A.block, r, A.ld_b), c.i[n],
-                                        A.block ? left : 0);
-      if constexpr (WIDE)
-        v.z[n].template load<TAIL, kOnce>(row_of<TX>(A.z, r, A.ld_z), c.i[n], left);
+    for (int k = 0; k < R; ++k) {
+      const bool in = is(first, k);
+      const int64_t r = first + k;
+      // a block that is not normalised is its own h0
+      v.r0[k] = !in ? 0.0f : A.post ? A.stats[r] : 1.0f;
+      v.r1[k] = in ? A.stats[A.rows + r] : 0.0f;
+      v.m0[k] = in && A.post && A.center ? A.stats[2 * A.rows + r] : 0.0f;
+      v.m1[k] = in && A.center ? A.stats[3 * A.rows + r] : 0.0f;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int left = in ? c.left[n] : 0;
+        v.dy[k][n].template load<TAIL, kOnce>(row_of<TX>(A.dy, r, A.ld_dy), c.i[n], left);
+        v.s[k][n].template load<TAIL, kOnce>(row_of<TX>(A.sum, r, A.ld_s), c.i[n], left);
+        v.ds[k][n].template load<TAIL, kOnce>(row_of<TX>(A.dsum, r, A.ld_ds), c.i[n],
+                                              A.dsum ? left : 0);
+        v.b[k][n].template load<TAIL, kOnce>(row_of<TX>(A.block, r, A.ld_b), c.i[n],
+                                             A.block ? left : 0);
+        if constexpr (WIDE)
+          v.z[k][n].template load<TAIL, kOnce>(row_of<TX>(A.z, r, A.ld_z), c.i[n], left);
+      }
     }
   };
   constexpr bool kAhead = N == 1 && sizeof(typename TX::raw) == 2;  // registers hold both
   Rows ahead;
-  if constexpr (kAhead) load(ahead, int64_t(blockIdx.x) * subs + sub);
-  for (int64_t first = int64_t(blockIdx.x) * subs; first < A.rows; first += step) {
-    const int64_t r = first + sub;
+  if constexpr (kAhead) load(ahead, (int64_t(blockIdx.x) * subs + sub) * take);
+  for (int64_t at = int64_t(blockIdx.x) * subs * take; at < A.rows; at += step) {
+    const int64_t first = at + sub * take;
     Rows now;
     if constexpr (kAhead) {
       now = ahead;
-      if (first + step < A.rows) load(ahead, r + step);
+      if (at + step < A.rows) load(ahead, first + step);
     } else {
-      load(now, r);
+      load(now, first);
     }
     // Past a row's end the gradients are 0 and so are the factors they meet: rstd is
     // taken as 0 there, since mean rstd may be beyond binary32.
-    const auto h1 = [&](int n, int e) {
-      return (now.s[n].get(e) - now.m1) * (live(n, e) ? now.r1 : 0.0f);
+    const auto own = [&](int n, float v) { return c.left[n] > 0 ? v : 0.0f; };
+    const auto h1 = [&](int k, int n, int e) {
+      return (now.s[k][n].get(e) - now.m1[k]) * (live(n, e) ? own(n, now.r1[k]) : 0.0f);
     };
-    const auto h0 = [&](int n, int e) {
-      return (now.b[n].get(e) - now.m0) * (live(n, e) ? now.r0 : 0.0f);
+    const auto h0 = [&](int k, int n, int e) {
+      return (now.b[k][n].get(e) - now.m0[k]) * (live(n, e) ? own(n, now.r0[k]) : 0.0f);
     };
-    float both[2] = {0.0f, 0.0f};
+    float both[2 * R] = {};
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      float h[8], d[8];
+      float dh[8] = {}, dd[8] = {};
+      if constexpr (!kHeld) fetch(gamma_held, A.gamma, 1.0f, n);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[e] = h1(n, e);
-        d[e] = now.dy[n].get(e);
-        const float g = d[e] * gamma[n].get(e);
-        both[0] += g;
-        both[1] = __builtin_fmaf(g, h[e], both[1]);
-      }
-      add(0, n, d, h);
-      add(1, n, d, kOnes);
-    }
-    float total = waves.sums(both) * inv;
-    float c1 = A.center ? lane_value(total, 0) : 0.0f, c2 = lane_value(total, 32);
-    float D[N][8];  // then, through the gate and the gain, the gradient of h0
-    both[0] = both[1] = 0.0f;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      now.dy[n].forget();
-      now.s[n].forget();
-      float out[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float g = now.dy[n].get(e) * gamma[n].get(e) - c1;
-        const float d = now.r1 * __builtin_fmaf(-h1(n, e), c2, g) + now.ds[n].get(e);
-        D[n][e] = live(n, e) ? d : 0.0f;
-        out[e] = A.scale * d;
-      }
-      now.dy[n].set(out);
-      if (r < A.rows)
-        now.dy[n].template store<TAIL>(row_of<TX>(A.dx, r, A.ld_dx), c.i[n], c.left[n]);
-      float h[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = h0(n, e);
-      if constexpr (WIDE) {
+      for (int k = 0; k < R; ++k)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float slope;
-          const float open = sigmoid(now.z[n].get(e), slope);
-          float v = h[e];
-          if (A.post) v = __builtin_fmaf(v, gamma0[n].get(e), beta0[n].get(e));
-          out[e] = D[n][e] * v * slope;
-          D[n][e] = live(n, e) ? D[n][e] * open : 0.0f;
+          const float h = h1(k, n, e), d = now.dy[k][n].get(e), g = d * gamma_held.get(e);
+          both[2 * k] += g;
+          both[2 * k + 1] = __builtin_fmaf(g, h, both[2 * k + 1]);
+          dh[e] = __builtin_fmaf(d, h, dh[e]);
+          dd[e] += d;
         }
-        now.z[n].set(out);
-        if (r < A.rows && A.dz)
-          now.z[n].template store<TAIL>(row_of<TX>(A.dz, r, A.ld_dz), c.i[n], c.left[n]);
-      }
-      add(2, n, D[n], h);
-      add(3, n, D[n], kOnes);
+      add(0, n, dh);
+      add(1, n, dd);
+    }
+    float total = waves.sums(both) * inv;
+    // rstd (g - c1 - h1 c2) = rstd g - rstd c1 - (s - mean) rstd^2 c2
+    float c1[R], c2[R], D[R][N][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if constexpr (WIDE) D[n][e] *= gamma0[n].get(e);
-        else D[n][e] *= gain[n][e];
-        both[0] += D[n][e];
-        both[1] = __builtin_fmaf(D[n][e], h[e], both[1]);
-      }
+    for (int k = 0; k < R; ++k) {
+      c1[k] = A.center ? now.r1[k] * lane_value(total, 64 / R * k) : 0.0f;
+      c2[k] = now.r1[k] * (now.r1[k] * lane_value(total, 64 / R * k + 32 / R));
+      both[2 * k] = both[2 * k + 1] = 0.0f;
     }
-    if (!A.block) continue;
-    c1 = c2 = 0.0f;
-    if (A.post) {
-      total = waves.sums(both) * inv;
-      c1 = A.center ? lane_value(total, 0) : 0.0f;
-      c2 = lane_value(total, 32);
-    }
-    if (r >= A.rows) continue;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      now.b[n].forget();
+      float dh[8] = {}, dd[8] = {};
+      if constexpr (!kHeld) {
+        fetch(gamma_held, A.gamma, 1.0f, n);
+        if constexpr (WIDE) {
+          fetch(gamma0_held, A.gamma0, 1.0f, n);
+          fetch(beta0_held, A.beta0, 0.0f, n);
+        } else {
+          fetch_gain(gain_held, n);
+        }
+      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        D[n][e] = now.r0 * __builtin_fmaf(-h0(n, e), c2, D[n][e] - c1);
-      now.b[n].set(D[n]);
-      now.b[n].template store<TAIL>(row_of<TX>(A.dblock, r, A.ld_db), c.i[n], c.left[n]);
+      for (int k = 0; k < R; ++k) {
+        now.dy[k][n].forget();
+        now.s[k][n].forget();
+        float out[8], h[8];
+        const float o1 = own(n, c1[k]), o2 = own(n, c2[k]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float g = now.dy[k][n].get(e) * gamma_held.get(e);
+          float d = __builtin_fmaf(-(now.s[k][n].get(e) - now.m1[k]), o2,
+                                   now.ds[k][n].get(e) - o1);
+          d = __builtin_fmaf(g, now.r1[k], d);
+          D[k][n][e] = live(n, e) ? d : 0.0f;
+          out[e] = A.scale * d;
+          h[e] = h0(k, n, e);
+        }
+        now.dy[k][n].set(out);
+        if (is(first, k))
+          now.dy[k][n].template store<TAIL>(row_of<TX>(A.dx, first + k, A.ld_dx), c.i[n],
+                                            c.left[n]);
+        if constexpr (WIDE) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float slope;
+            const float open = sigmoid(now.z[k][n].get(e), slope);
+            float v = h[e];
+            if (A.post) v = __builtin_fmaf(v, gamma0_held.get(e), beta0_held.get(e));
+            out[e] = D[k][n][e] * v * slope;
+            D[k][n][e] *= open;
+          }
+          now.z[k][n].set(out);
+          if (is(first, k) && A.dz)
+            now.z[k][n].template store<TAIL>(row_of<TX>(A.dz, first + k, A.ld_dz), c.i[n],
+                                             c.left[n]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dh[e] = __builtin_fmaf(D[k][n][e], h[e], dh[e]);
+          dd[e] += D[k][n][e];
+          if constexpr (WIDE) D[k][n][e] *= gamma0_held.get(e);
+          else D[k][n][e] *= gain_held[e];
+          both[2 * k] += D[k][n][e];
+          both[2 * k + 1] = __builtin_fmaf(D[k][n][e], h[e], both[2 * k + 1]);
+        }
+      }
+      add(2, n, dh);
+      add(3, n, dd);
+    }
+    if (!A.block) continue;
+#pragma unroll
+    for (int k = 0; k < R; ++k) c1[k] = c2[k] = 0.0f;
+    if (A.post) {
+      total = waves.sums(both) * inv;
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        c1[k] = A.center ? now.r0[k] * lane_value(total, 64 / R * k) : 0.0f;
+        c2[k] = now.r0[k] * (now.r0[k] * lane_value(total, 64 / R * k + 32 / R));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (!is(first, k)) break;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        now.b[k][n].forget();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = __builtin_fmaf(-(now.b[k][n].get(e) - now.m0[k]), c2[k], -c1[k]);
+          D[k][n][e] = __builtin_fmaf(D[k][n][e], now.r0[k], d);
+        }
+        now.b[k][n].set(D[k][n]);
+        now.b[k][n].template store<TAIL>(row_of<TX>(A.dblock, first + k, A.ld_db), c.i[n],
+                                         c.left[n]);
+      }
     }
   }
   if (!A.part) return;
-  // the row groups' sums, then the workgroup's partial rows
-  if (kLds && subs > 1) __syncthreads();
+  // the row groups' sums (with sixteen columns a thread there is one), then the
+  // workgroup's partial rows
+  if (subs > 1) __syncthreads();
+  if (sub > 0) return;
 #pragma unroll
   for (int which = 0; which < 4; ++which) {
     if (!(A.want & (which < 2 ? 1 : 2))) continue;
     float *out = A.part + (int64_t(which) * A.parts + blockIdx.x) * A.cols;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      if (which < kInLds) {
-        if (sub > 0) continue;
-        for (int w = 0; w < subs; ++w)
+      float sum[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float v = (*(place(which, n, e / 4) + w * per))[e % 4];
-            acc[which][n][e] = w ? acc[which][n][e] + v : v;
-          }
-      } else if (subs > 1) {  // not with sixteen columns a thread
-        __syncthreads();
-        if (sub > 0) {
+      for (int e = 0; e < 8; ++e)
+        sum[e] = which < kInLds ? (*place(which, n, e / 4))[e % 4]
+                                : acc[N == 2 && which >= 2 ? which - 2 : 0][n][e];
+      for (int w = 1; w < subs; ++w)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) store[((sub - 1) * 8 + e) * per + t] = acc[which][n][e];
-        }
-        __syncthreads();
-        if (sub > 0) continue;
-        for (int w = 0; w < subs - 1; ++w)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[which][n][e] += store[(w * 8 + e) * per + t];
-      }
+        for (int e = 0; e < 8; ++e) sum[e] += (*(place(which, n, e / 4) + w * per))[e % 4];
       Eight<F32> v;
-      v.set(acc[which][n]);
+      v.set(sum);
       v.template store<TAIL>(out, c.i[n], c.left[n]);
     }
   }
@@ -707,9 +767,17 @@ Way way_of(const zs_blocknorm_desc &d, int threads) {
   return w;
 }
 
+// The backward pass takes two rows at a time once every CU has some, where the
+// registers hold them.
+bool pairs(const zs_blocknorm_desc &d) {
+  return d.rows >= 4 * kCus && d.cols <= 8 * kPairThreads && d.dtype != ZS_F32 &&
+         d.gate != ZS_GATE_SIGMOID;
+}
+Way bwd_way_of(const zs_blocknorm_desc &d) { return way_of(d, pairs(d) ? kPairThreads : 1024); }
+
 int64_t parts_of(const zs_blocknorm_desc &d) {
-  const Way w = way_of(d, 1024);
-  const int64_t b = (d.rows + w.subs - 1) / w.subs;
+  const int rows = bwd_way_of(d).subs * (pairs(d) ? 2 : 1);
+  const int64_t b = (d.rows + rows - 1) / rows;
   return b < kMaxParts ? b : kMaxParts;
 }
 
@@ -772,15 +840,12 @@ int zero_shard_blocknorm(const zs_blocknorm_desc *d, const void *x, const void *
     using TX = decltype(tx);
     using TP = decltype(tp);
     return by_way(w.n, d->cols % 8 != 0 || !even, wide, [&](auto n, auto tail, auto wd) {
-#ifndef FR
-#define FR 2
-#define FW 1280
-#endif
       // two rows at a time once every CU has some, where the registers hold them
-      constexpr int R = n.value == 1 && sizeof(typename TX::raw) == 2 && !wd.value ? FR : 1;
+      constexpr int R = n.value == 1 && sizeof(typename TX::raw) == 2 && !wd.value ? 2 : 1;
       A.take = A.rows >= 4 * kCus ? R : 1;
       const int64_t groups = (A.rows + w.subs * A.take - 1) / (w.subs * A.take);
-      const int64_t most = int64_t(kCus) * (FW > threads ? FW / threads : 1);
+      // about as many as there is room for at once: later ones would run alone
+      const int64_t most = int64_t(kCus) * (kResident > threads ? kResident / threads : 1);
       hipLaunchKernelGGL((seam_fwd_kernel<TX, TP, n.value, R, tail.value, wd.value>),
                          dim3(unsigned(groups < most ? groups : most)), dim3(threads), 0,
                          static_cast<hipStream_t>(d->stream), A);
@@ -824,15 +889,15 @@ int zero_shard_blocknorm_bwd(const zs_blocknorm_desc *d, const void *dy, const v
   if (d->rows == 0 && !want) return ZS_OK;
   if (const int rc = device_is_gfx950()) return rc;
   const auto ld = [&](int64_t v) { return v ? v : d->cols; };
-  const Way w = way_of(*d, 1024);
-  const BwdArgs A{d->rows, d->cols, ld(d->ld_dy), ld(d->ld_dsum), ld(d->ld_sum), ld(d->ld_block),
+  const Way w = bwd_way_of(*d);
+  BwdArgs A{d->rows, d->cols, ld(d->ld_dy), ld(d->ld_dsum), ld(d->ld_sum), ld(d->ld_block),
                   ld(d->ld_gate), ld(d->ld_dx), ld(d->ld_dblock), ld(d->ld_dgate),
                   dy, dsum, sum, block, wide ? gate : nullptr,
                   wide ? nullptr : gate, gamma_post, beta_post, gamma, stats,
                   dx, dblock, wide ? dgate : nullptr, column ? dgate : nullptr, dgamma_post,
                   dbeta_post, dgamma, dbeta, want ? static_cast<float *>(workspace) : nullptr,
                   d->residual_scale, d->kind == ZS_NORM_LAYER, d->post, want,
-                  int32_t(parts_of(*d)), w.per};
+                  int32_t(parts_of(*d)), w.per, pairs(*d) ? 2 : 1};
   const bool even = rows_even(dy, A.ld_dy, size) && rows_even(dsum, A.ld_ds, size) &&
                     rows_even(sum, A.ld_s, size) && rows_even(block, A.ld_b, size) &&
                     rows_even(A.z, A.ld_z, size) && rows_even(dx, A.ld_dx, size) &&
@@ -844,9 +909,14 @@ int zero_shard_blocknorm_bwd(const zs_blocknorm_desc *d, const void *dy, const v
     int rc = ZS_OK;
     if (A.rows > 0)
       rc = by_way(w.n, d->cols % 8 != 0 || !even, wide, [&](auto n, auto tail, auto wd) {
-        hipLaunchKernelGGL((seam_bwd_kernel<TX, TP, n.value, tail.value, wd.value>),
-                           dim3(unsigned(A.parts)), dim3(w.per * w.subs), 0, st, A);
-        return launched();
+        const auto launch = [&](auto r) {
+          hipLaunchKernelGGL((seam_bwd_kernel<TX, TP, n.value, r.value, tail.value, wd.value>),
+                             dim3(unsigned(A.parts)), dim3(w.per * w.subs), 0, st, A);
+          return launched();
+        };
+        if constexpr (n.value == 1 && sizeof(typename TX::raw) == 2 && !wd.value)
+          if (A.take == 2) return launch(std::integral_constant<int, 2>{});
+        return launch(std::integral_constant<int, 1>{});
       });
     if (rc || !want) return rc;
     hipLaunchKernelGGL((seam_join_kernel<TP>), dim3(unsigned((A.cols + 63) / 64), 2),
