@@ -38,7 +38,8 @@ constexpr int kMaxCols = ZS_BLOCKNORM_MAX_COLS;  // sixteen columns of 1024 thre
 constexpr int kCus = 256;
 constexpr int kMaxParts = 256;  // partial rows of the columns' sums
 constexpr int kResident = 1280;    // threads of the forward pass on a CU
-constexpr int kPairThreads = 768;  // most that hold two rows of the backward pass
+constexpr int kPairThreads = 768;  // most that hold two rows, or sixteen columns, of the
+                                  // backward pass without spilling
 
 // sigmoid and its derivative, from t = exp(-|z|): nothing overflows and 1 - sigmoid
 // loses nothing.  exp2 of the product's leading part, the rest to first order (below
@@ -227,8 +228,7 @@ struct FwdArgs {
   float *stats;
   float eps, scale;
   int32_t center, post;
-  int32_t per;   // threads of a row
-  int32_t take;  // rows at a time, at most R
+  int32_t per;  // threads of a row
 };
 
 // R rows at a time, each over `per` threads (a multiple of 64) of the
@@ -268,12 +268,11 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
   load_params<TAIL>(gamma, A.gamma, 1.0f, c);
   load_params<TAIL>(beta, A.beta, 0.0f, c);
   constexpr bool kOnce = N == 1 && !TAIL && sizeof(typename TX::raw) == 2;
-  const int take = A.take;
-  const int64_t step = int64_t(gridDim.x) * subs * take;
+  const int64_t step = int64_t(gridDim.x) * subs * R;
   struct Rows {
     Eight<TX> x[R][N], b[R][N], z[WIDE ? R : 1][WIDE ? N : 1];
   };
-  const auto is = [&](int64_t r0, int k) { return k < take && r0 + k < A.rows; };
+  const auto is = [&](int64_t r0, int k) { return r0 + k < A.rows; };
   const auto load = [&](Rows &v, int64_t r0) {
 #pragma unroll
     for (int k = 0; k < R; ++k)
@@ -322,9 +321,9 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
   // registers hold both.
   constexpr bool kAhead = N == 1;
   Rows ahead;
-  if constexpr (kAhead) load(ahead, (int64_t(blockIdx.x) * subs + sub) * take);
-  for (int64_t first = int64_t(blockIdx.x) * subs * take; first < A.rows; first += step) {
-    const int64_t r0 = first + sub * take;
+  if constexpr (kAhead) load(ahead, (int64_t(blockIdx.x) * subs + sub) * R);
+  for (int64_t first = int64_t(blockIdx.x) * subs * R; first < A.rows; first += step) {
+    const int64_t r0 = first + sub * R;
     Rows now;
     if constexpr (kAhead) {
       now = ahead;
@@ -400,16 +399,15 @@ struct BwdArgs {
   int32_t want;   // 1: the sums of dy h1 and dy, 2: of E h0 and E
   int32_t parts;  // 0: no rows (the gradients are zero)
   int32_t per;    // threads of a row
-  int32_t take;   // rows at a time, at most R
 };
 
 // R rows at a time.  The columns' sums are in LDS, a thread's own places of it, all
 // four, or of sixteen columns a thread the first two: with them in registers beside the
 // rows 8192 x 5120 bf16 with element gates took 449 us for 183, fp32 349 for 199,
 // and two rows at a time did not fit.
-template <class TX, class TP, int N, int R, bool TAIL, bool WIDE>
-__global__ void __launch_bounds__(R == 2 ? kPairThreads : 1024) seam_bwd_kernel(const BwdArgs A) {
-  constexpr int kInLds = N == 2 ? 2 : 4, kMost = R == 2 ? kPairThreads : 1024;
+template <class TX, class TP, int N, int R, bool TAIL, bool WIDE, int kMost>
+__global__ void __launch_bounds__(kMost) seam_bwd_kernel(const BwdArgs A) {
+  constexpr int kInLds = N == 2 ? 2 : 4;
   __shared__ float lds[2][16][8];
   __shared__ f32x4 store[kInLds * N * 2 * kMost];
   const int per = A.per, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / per);
@@ -477,13 +475,12 @@ __global__ void __launch_bounds__(R == 2 ? kPairThreads : 1024) seam_bwd_kernel(
       *place(which, n, 1) = f32x4{};
     }
   constexpr bool kOnce = N == 1 && !TAIL && sizeof(typename TX::raw) == 2;
-  const int take = A.take;
-  const int64_t step = int64_t(gridDim.x) * subs * take;
+  const int64_t step = int64_t(gridDim.x) * subs * R;
   struct Rows {
     Eight<TX> dy[R][N], ds[R][N], s[R][N], b[R][N], z[WIDE ? R : 1][WIDE ? N : 1];
     float r0[R], r1[R], m0[R], m1[R];
   };
-  const auto is = [&](int64_t first, int k) { return k < take && first + k < A.rows; };
+  const auto is = [&](int64_t first, int k) { return first + k < A.rows; };
   const auto load = [&](Rows &v, int64_t first) {
 #pragma unroll
     for (int k = 0; k < R; ++k) {
@@ -510,9 +507,9 @@ __global__ void __launch_bounds__(R == 2 ? kPairThreads : 1024) seam_bwd_kernel(
   };
   constexpr bool kAhead = N == 1 && sizeof(typename TX::raw) == 2;  // registers hold both
   Rows ahead;
-  if constexpr (kAhead) load(ahead, (int64_t(blockIdx.x) * subs + sub) * take);
-  for (int64_t at = int64_t(blockIdx.x) * subs * take; at < A.rows; at += step) {
-    const int64_t first = at + sub * take;
+  if constexpr (kAhead) load(ahead, (int64_t(blockIdx.x) * subs + sub) * R);
+  for (int64_t at = int64_t(blockIdx.x) * subs * R; at < A.rows; at += step) {
+    const int64_t first = at + sub * R;
     Rows now;
     if constexpr (kAhead) {
       now = ahead;
@@ -828,10 +825,10 @@ int zero_shard_blocknorm(const zs_blocknorm_desc *d, const void *x, const void *
   if (const int rc = device_is_gfx950()) return rc;
   const auto ld = [&](int64_t v) { return v ? v : d->cols; };
   const Way w = way_of(*d, kThreads);
-  FwdArgs A{d->rows, d->cols, ld(d->ld_x), ld(d->ld_block), ld(d->ld_gate), ld(d->ld_sum),
+  const FwdArgs A{d->rows, d->cols, ld(d->ld_x), ld(d->ld_block), ld(d->ld_gate), ld(d->ld_sum),
                   ld(d->ld_y), x, block, wide ? gate : nullptr, wide ? nullptr : gate, gamma_post,
                   beta_post, gamma, beta, sum, y, stats, d->eps, d->residual_scale,
-                  d->kind == ZS_NORM_LAYER, d->post, w.per, 1};
+                  d->kind == ZS_NORM_LAYER, d->post, w.per};
   const bool even = rows_even(x, A.ld_x, size) && rows_even(block, A.ld_b, size) &&
                     rows_even(A.z, A.ld_z, size) && rows_even(sum, A.ld_s, size) &&
                     rows_even(y, A.ld_y, size);
@@ -840,16 +837,19 @@ int zero_shard_blocknorm(const zs_blocknorm_desc *d, const void *x, const void *
     using TX = decltype(tx);
     using TP = decltype(tp);
     return by_way(w.n, d->cols % 8 != 0 || !even, wide, [&](auto n, auto tail, auto wd) {
+      const auto launch = [&](auto r) {
+        const int64_t groups = (A.rows + w.subs * r.value - 1) / (w.subs * r.value);
+        // about as many as there is room for at once: later ones would run alone
+        const int64_t most = int64_t(kCus) * (kResident > threads ? kResident / threads : 1);
+        hipLaunchKernelGGL((seam_fwd_kernel<TX, TP, n.value, r.value, tail.value, wd.value>),
+                           dim3(unsigned(groups < most ? groups : most)), dim3(threads), 0,
+                           static_cast<hipStream_t>(d->stream), A);
+        return launched();
+      };
       // two rows at a time once every CU has some, where the registers hold them
-      constexpr int R = n.value == 1 && sizeof(typename TX::raw) == 2 && !wd.value ? 2 : 1;
-      A.take = A.rows >= 4 * kCus ? R : 1;
-      const int64_t groups = (A.rows + w.subs * A.take - 1) / (w.subs * A.take);
-      // about as many as there is room for at once: later ones would run alone
-      const int64_t most = int64_t(kCus) * (kResident > threads ? kResident / threads : 1);
-      hipLaunchKernelGGL((seam_fwd_kernel<TX, TP, n.value, R, tail.value, wd.value>),
-                         dim3(unsigned(groups < most ? groups : most)), dim3(threads), 0,
-                         static_cast<hipStream_t>(d->stream), A);
-      return launched();
+      if constexpr (n.value == 1 && sizeof(typename TX::raw) == 2 && !wd.value)
+        if (A.rows >= 4 * kCus) return launch(std::integral_constant<int, 2>{});
+      return launch(std::integral_constant<int, 1>{});
     });
   });
 }
@@ -890,14 +890,14 @@ int zero_shard_blocknorm_bwd(const zs_blocknorm_desc *d, const void *dy, const v
   if (const int rc = device_is_gfx950()) return rc;
   const auto ld = [&](int64_t v) { return v ? v : d->cols; };
   const Way w = bwd_way_of(*d);
-  BwdArgs A{d->rows, d->cols, ld(d->ld_dy), ld(d->ld_dsum), ld(d->ld_sum), ld(d->ld_block),
+  const BwdArgs A{d->rows, d->cols, ld(d->ld_dy), ld(d->ld_dsum), ld(d->ld_sum), ld(d->ld_block),
                   ld(d->ld_gate), ld(d->ld_dx), ld(d->ld_dblock), ld(d->ld_dgate),
                   dy, dsum, sum, block, wide ? gate : nullptr,
                   wide ? nullptr : gate, gamma_post, beta_post, gamma, stats,
                   dx, dblock, wide ? dgate : nullptr, column ? dgate : nullptr, dgamma_post,
                   dbeta_post, dgamma, dbeta, want ? static_cast<float *>(workspace) : nullptr,
                   d->residual_scale, d->kind == ZS_NORM_LAYER, d->post, want,
-                  int32_t(parts_of(*d)), w.per, pairs(*d) ? 2 : 1};
+                  int32_t(parts_of(*d)), w.per};
   const bool even = rows_even(dy, A.ld_dy, size) && rows_even(dsum, A.ld_ds, size) &&
                     rows_even(sum, A.ld_s, size) && rows_even(block, A.ld_b, size) &&
                     rows_even(A.z, A.ld_z, size) && rows_even(dx, A.ld_dx, size) &&
@@ -909,14 +909,21 @@ int zero_shard_blocknorm_bwd(const zs_blocknorm_desc *d, const void *dy, const v
     int rc = ZS_OK;
     if (A.rows > 0)
       rc = by_way(w.n, d->cols % 8 != 0 || !even, wide, [&](auto n, auto tail, auto wd) {
-        const auto launch = [&](auto r) {
-          hipLaunchKernelGGL((seam_bwd_kernel<TX, TP, n.value, r.value, tail.value, wd.value>),
-                             dim3(unsigned(A.parts)), dim3(w.per * w.subs), 0, st, A);
+        using std::integral_constant;
+        const auto launch = [&](auto r, auto most) {
+          hipLaunchKernelGGL(
+              (seam_bwd_kernel<TX, TP, n.value, r.value, tail.value, wd.value, most.value>),
+              dim3(unsigned(A.parts)), dim3(w.per * w.subs), 0, st, A);
           return launched();
         };
-        if constexpr (n.value == 1 && sizeof(typename TX::raw) == 2 && !wd.value)
-          if (A.take == 2) return launch(std::integral_constant<int, 2>{});
-        return launch(std::integral_constant<int, 1>{});
+        if constexpr (n.value == 2) {
+          if (w.per <= kPairThreads)  // a third more registers for 12288 columns and fewer
+            return launch(integral_constant<int, 1>{}, integral_constant<int, kPairThreads>{});
+        } else if constexpr (sizeof(typename TX::raw) == 2 && !wd.value) {
+          if (pairs(*d))
+            return launch(integral_constant<int, 2>{}, integral_constant<int, kPairThreads>{});
+        }
+        return launch(integral_constant<int, 1>{}, integral_constant<int, 1024>{});
       });
     if (rc || !want) return rc;
     hipLaunchKernelGGL((seam_join_kernel<TP>), dim3(unsigned((A.cols + 63) / 64), 2),
