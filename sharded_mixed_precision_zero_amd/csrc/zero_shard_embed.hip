@@ -11,16 +11,14 @@
 // order: a thread holds eight columns of a row's sum in registers.  No atomics:
 // the same inputs give the same bits.
 //
-//   sort   tiles of 8192 tokens by counting: a token's place is the number of
-//          tokens of its tile that come before it.  That is 2^26 comparisons at
-//          two instructions each for a full tile, one launch, no passes over
-//          digits that wait for each other (a tile takes about as long as a
-//          launch).  Longer lists merge up to eight runs at a time, each token
-//          finding its place by binary search in the other runs.
-//   sum    pieces of kRun sorted tokens.  A row's tokens belong to the piece they
-//          begin in; a row of more than kRun tokens is cut every kRun of them,
-//          and each part belongs to the piece it begins in, so no piece does more
-//          than twice its share however the tokens are distributed.
+//   sort   tiles of kTile tokens by counting: a token's place is the number of
+//          tokens of its tile that come before it.  One launch, no passes over
+//          digits that wait for each other.  Longer lists merge up to eight runs
+//          at a time, each token finding its place by binary search in the other runs.
+//   sum    pieces of kPiece sorted tokens.  A row is cut every kRun tokens, and
+//          each part, or the whole of a shorter row, belongs to the piece that it
+//          begins in, so that no piece does much more than its share however
+//          the tokens are distributed.
 //   join   the parts of those long rows, in order.
 
 #include <hip/hip_runtime.h>
@@ -37,12 +35,14 @@ namespace {
 using namespace zs_dev;
 
 constexpr int kThreads = 256;
-constexpr int kTile = 8192;       // tokens sorted by counting
+// Tokens sorted by counting: 8192 of them as one tile took 17 us, the tile's keys
+// coming out of LDS at eight cycles for four; as four tiles and a merge TILEUS.
+constexpr int kTile = 2048;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kRuns = 8;          // runs merged at a time
-constexpr int kRun = 32;          // tokens of a piece, and of a long row's part
-constexpr int kBatch = 8;         // rows of dy in flight
+constexpr int kRun = 32;          // tokens of a long row's part
+constexpr int kPiece = 8;         // tokens of a piece, and rows of dy in flight
 constexpr int kJoinWaves = 8;
 constexpr int kEach = 4;          // pieces of eight columns of a forward thread
 constexpr unsigned kNone = 0xffffffffu;  // sorts behind every row
@@ -227,8 +227,7 @@ struct SumArgs {
   const int *order;
   const void *dy;
   void *out;
-  float *part;  // [2 pieces][per * 8]: a piece's part of a row begun before it, and of
-                // a row that goes on behind it
+  float *part;  // [2 tokens / kRun][per * 8], see part_of
   float scale;
   int32_t add;        // to what is there
   unsigned per;       // pieces of eight columns
@@ -245,6 +244,13 @@ __device__ __forceinline__ int64_t first_not_below(const unsigned *keys, int64_t
     else hi = mid;
   }
   return lo;
+}
+
+// Where the part of a long row that begins at sorted token `at` is kept.  Of the parts
+// that begin within kRun tokens one at most is its row's first (its row goes on
+// for all of them) and one at most is not.
+__device__ __forceinline__ int64_t part_of(int64_t at, bool first) {
+  return at / kRun * 2 + (first ? 1 : 0);
 }
 
 // A row's sum, scaled and joined with what is there, into the table's gradient.
@@ -288,9 +294,35 @@ __device__ __forceinline__ void clear_rows(const SumArgs &A, int64_t block) {
     if (used[r]) continue;
     void *to = row_of<TG>(A.out, r0 + r, A.ld_out);
     for (unsigned c = threadIdx.x - sub * across; c < A.per; c += across)
-      zero.template store<TAIL>(to, c * 8, A.cols - int64_t(c) * 8);
+      zero.template store<TAIL, true>(to, c * 8, A.cols - int64_t(c) * 8);
   }
 }
+
+// Keys and tokens of kPiece sorted places from `at` on, a multiple of kPiece.
+struct Places {
+  unsigned key[kPiece];
+  int token[kPiece];
+  __device__ __forceinline__ void load(const SumArgs &A, int64_t at) {
+    if (at + kPiece <= A.tokens) {
+#pragma unroll
+      for (int q = 0; q < kPiece / 4; ++q) {
+        const u32x4 k = *reinterpret_cast<const u32x4 *>(A.keys + at + q * 4);
+        const u32x4 t = *reinterpret_cast<const u32x4 *>(A.order + at + q * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          key[q * 4 + e] = k[e];
+          token[q * 4 + e] = int(t[e]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kPiece; ++e) {
+        key[e] = at + e < A.tokens ? A.keys[at + e] : kNone;
+        token[e] = at + e < A.tokens ? A.order[at + e] : 0;
+      }
+    }
+  }
+};
 
 template <class TY, class TG, bool TAIL>
 __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const SumArgs A) {
@@ -301,112 +333,129 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const SumArgs A) {
   const int64_t base = int64_t(blockIdx.x) * kThreads;
   const int64_t p0 = base / A.per;
   const unsigned q = unsigned(base - p0 * A.per) + threadIdx.x, up = q / A.per;
-  const int64_t piece = p0 + up;
   const unsigned col = (q - up * A.per) * 8;
-  const int64_t from = piece * kRun;
+  const int64_t from = (p0 + up) * kPiece;
   if (from >= A.tokens) return;
-  const int64_t to = from + kRun < A.tokens ? from + kRun : A.tokens;
-  const unsigned last = A.keys[to - 1];
-  unsigned key = A.keys[from];
-  int64_t i = from;
-  bool begun = false;  // the row at `start` began in an earlier piece
-  if (from > 0 && A.keys[from - 1] == key) {
-    // where that row's parts begin: in most cases less than kRun back
-    const int64_t near = from - kRun;
-    const int64_t row0 = near >= 0 && A.keys[near] == key
-                             ? first_not_below(A.keys, 0, near, key)
-                             : first_not_below(A.keys, near < 0 ? 0 : near + 1, from, key);
-    i = row0 + (from - row0 + kRun - 1) / kRun * kRun;
-    begun = true;
-    if (i >= to || A.keys[i] != key) {  // no part begins here: on to the next row
-      i = first_not_below(A.keys, from, to, key + 1);
-      if (i >= to) return;
-      key = A.keys[i];
-      begun = false;
-    }
-  }
-  int64_t start = i;
-  float acc[8] = {};
-  const auto flush = [&](bool whole) {
-    if (key < unsigned(A.vocab)) {
-      if (whole && !begun) {
-        put_row<TG, TAIL>(A, key, col, acc);
-      } else {
-        Eight<F32> v;
-        v.set(acc);
-        v.template store<false>(A.part + (piece * 2 + (begun ? 0 : 1)) * (int64_t(A.per) * 8), col,
-                                8);
+  // this piece's places, the next one's, and how many of the kRun before it are of its
+  // first row: three loads side by side
+  Places now, next;
+  now.load(A, from);
+  next.load(A, from + kPiece);
+  int before = 0;
+#pragma unroll
+  for (int k = kPiece; k <= kRun; k += kPiece)
+    if (from >= k) {
+#pragma unroll
+      for (int h = 0; h < kPiece / 4; ++h) {
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(A.keys + from - k + h * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) before += v[e] == now.key[0] ? 1 : 0;
       }
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-  };
-  bool more = true;
-  while (more) {
-    unsigned k[kBatch];
-    Eight<TY> v[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) k[j] = i + j < A.tokens ? A.keys[i + j] : kNone;
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      // a row of this piece, or of the row that goes on behind it
-      const bool take = k[j] < unsigned(A.vocab) && (i + j < to || k[j] == last);
-      const int64_t t = take ? A.order[i + j] : 0;
-      v[j].template load<TAIL, !TAIL>(row_of<TY>(A.dy, t, A.ld_dy), col, take ? A.cols - col : 0);
+  // a row that began before this piece: its next part may begin in here
+  const unsigned first = now.key[0], last = now.key[kPiece - 1];
+  int64_t part = from;
+  if (before) {
+    const int64_t row0 =
+        before < kRun ? from - before : first_not_below(A.keys, 0, from - kRun, first);
+    part = row0 + (from - row0 + kRun - 1) / kRun * kRun;
+  }
+  const int64_t to = from + kPiece;
+  unsigned key = kNone;  // of the row being summed
+  int64_t start = 0;     // its part's first place
+  bool active = false, whole = false;  // whole: that is the row's first place too
+  float acc[8];
+  const auto flush = [&](bool ended) {
+    if (whole && ended) {
+      put_row<TG, TAIL>(A, key, col, acc);
+    } else {
+      Eight<F32> v;
+      v.set(acc);
+      v.template store<false>(A.part + part_of(start, whole) * (int64_t(A.per) * 8), col, 8);
     }
+  };
+  for (int64_t at = from;; at += kPiece) {
+    Eight<TY> v[kPiece];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      if (!more) break;
-      const int64_t at = i + j;
-      if (k[j] != key) {
-        flush(true);
-        if (at >= to) {
-          more = false;
-          break;
-        }
-        key = k[j];
-        start = at;
-        begun = false;
-      } else if (at - start == kRun) {
-        flush(false);
-        more = false;
+    for (int j = 0; j < kPiece; ++j) {
+      const unsigned k = now.key[j];
+      const bool mine = at == from ? !(before && k == first && at + j < part)
+                                   : k == last && at + j - start < kRun;
+      const bool take = mine && k < unsigned(A.vocab);
+      v[j].template load<TAIL, !TAIL>(row_of<TY>(A.dy, take ? now.token[j] : 0, A.ld_dy), col,
+                                      take ? A.cols - col : 0);
+    }
+    Places after;
+    after.load(A, at + 2 * kPiece);
+    bool done = false;
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+      const unsigned k = now.key[j];
+      const int64_t i = at + j;
+      const bool row = j ? k != now.key[j - 1] : at == from ? !before : k != key;
+      const bool none = k >= unsigned(A.vocab);  // and so are all places behind
+      if (active && (row || none || i - start == kRun)) {
+        flush(row || none);
+        active = false;
+      }
+      if (none || (i >= to && !active)) {
+        done = true;
         break;
       }
+      if (row || (before && i == part && k == first)) {
+        key = k;
+        start = i;
+        whole = row;
+        active = true;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += v[j].get(e);
+        for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+      }
+      if (active) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += v[j].get(e);
+      }
     }
-    i += kBatch;
+    if (done || !active) break;
+    now = next;
+    next = after;
   }
 }
 
-// The parts of the row that begins in piece blockIdx.x and goes on for more
-// than kRun tokens, if there is one: each wave adds a stretch of them, then the
-// waves' sums are added in order.
+// The parts of the row that begins among the kRun places from blockIdx.x kRun on and
+// goes on for more than kRun, if there is one: each wave adds a stretch of them, then
+// the waves' sums are added in order.
 template <class TG, bool TAIL>
 __global__ void __launch_bounds__(64 * kJoinWaves) embed_join_kernel(const SumArgs A) {
   __shared__ float sums[kJoinWaves][8][64];
-  const int64_t piece = blockIdx.x, from = piece * kRun, to = from + kRun;
-  if (to >= A.tokens) return;
-  const unsigned key = A.keys[to - 1];
-  if (key >= unsigned(A.vocab) || A.keys[to] != key) return;
-  const int64_t start = first_not_below(A.keys, from, to, key);
-  if (start == from && from > 0 && A.keys[from - 1] == key) return;  // begun before
-  if (start + kRun >= A.tokens || A.keys[start + kRun] != key) return;
-  const int64_t end = first_not_below(A.keys, start + kRun, A.tokens, key + 1);
-  const int64_t parts = (end - start + kRun - 1) / kRun;
+  const int64_t from = int64_t(blockIdx.x) * kRun, to = from + kRun;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (to >= A.tokens) return;
+  // lanes: the place before, the kRun places, the one behind
+  const int64_t look = from - 1 + lane;
+  const unsigned near = lane < kRun + 2 && look >= 0 ? A.keys[look] : kNone;
+  const unsigned key = __builtin_amdgcn_readlane(near, kRun);
+  if (key >= unsigned(A.vocab)) return;
+  const uint64_t same = __ballot(near == key);
+  if (!(same >> (kRun + 1) & 1) || (same & 1)) return;  // ends in here, or began before
+  const int64_t start = from - 1 + __builtin_ctzll(same);
+  if (start + kRun >= A.tokens || A.keys[start + kRun] != key) return;
+  // a part a lane: how many begin within the row
+  int64_t parts = 1;
+  for (;;) {
+    const int64_t at = start + (parts + lane) * kRun;
+    const uint64_t more = __ballot(at < A.tokens && A.keys[at < A.tokens ? at : start] == key);
+    parts += __builtin_popcountll(more);
+    if (more != ~uint64_t(0)) break;
+  }
   const unsigned c = blockIdx.y * 64 + lane, col = c * 8;
   const int64_t width = int64_t(A.per) * 8, each = (parts + kJoinWaves - 1) / kJoinWaves;
   float acc[8] = {};
   if (c < A.per) {
     const int64_t lo = wave * each, hi = lo + each < parts ? lo + each : parts;
-    // part 0 lies in its piece's second row, part j in the first row of the j-th
-    // piece after it
-    const float *p = A.part + (piece * 2) * width;
 #pragma unroll 4
     for (int64_t j = lo; j < hi; ++j) {
       Eight<F32> v;
-      v.template load<false>(p + (j == 0 ? 1 : 2 * j) * width, col, 8);
+      v.template load<false>(A.part + part_of(start + j * kRun, j == 0) * width, col, 8);
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] += v.get(e);
     }
@@ -447,14 +496,14 @@ struct Plan {
   int64_t keys[2], order[2], part, bytes;
   bool merged;
   explicit Plan(const zs_embedding_desc &d) {
-    const int64_t list = up(d.tokens * 4, 256), pieces = (d.tokens + kRun - 1) / kRun;
+    const int64_t list = up(d.tokens * 4, 256), runs = (d.tokens + kRun - 1) / kRun;
     merged = d.tokens > kTile;
     keys[0] = 0;
     order[0] = list;
     keys[1] = merged ? 2 * list : 0;
     order[1] = merged ? 3 * list : list;
     part = merged ? 4 * list : 2 * list;
-    bytes = part + (pieces > 1 ? pieces * 2 * per_of(d) * 8 * 4 : 0);
+    bytes = part + (runs > 1 ? runs * 2 * per_of(d) * 8 * 4 : 0);
   }
 };
 
@@ -535,7 +584,7 @@ int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const 
       !aligned(workspace, 256))
     return ZS_EALIGN;
   const auto ld = [&](int64_t v) { return v ? v : d->cols; };
-  const int64_t pieces = (d->tokens + kRun - 1) / kRun;
+  const int64_t pieces = (d->tokens + kPiece - 1) / kPiece, runs = (d->tokens + kRun - 1) / kRun;
   SumArgs A{d->tokens, d->vocab, d->cols, ld(d->ld_dy), ld(d->ld_dtable), nullptr, nullptr, dy,
             dtable, nullptr, d->scale, d->accumulate, per_of(*d), 0, 0};
   A.sum_blocks = (pieces * A.per + kThreads - 1) / kThreads;
@@ -560,9 +609,9 @@ int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const 
     return by_tail(d->cols % 8 != 0 || !even, [&](auto tail) {
       hipLaunchKernelGGL((embed_sum_kernel<decltype(ty), TG, tail.value>),
                          dim3(unsigned(A.sum_blocks + clear)), dim3(kThreads), 0, st, A);
-      if (pieces > 1)
+      if (runs > 1)
         hipLaunchKernelGGL((embed_join_kernel<TG, tail.value>),
-                           dim3(unsigned(pieces), (A.per + 63) / 64), dim3(64 * kJoinWaves), 0, st,
+                           dim3(unsigned(runs), (A.per + 63) / 64), dim3(64 * kJoinWaves), 0, st,
                            A);
       return launched();
     });

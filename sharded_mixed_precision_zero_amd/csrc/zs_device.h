@@ -132,10 +132,17 @@ struct Eight {
         }
     }
   }
-  template <bool TAIL = true, class I, class L>
+  template <bool TAIL = true, bool ONCE = false, class I, class L>
   __device__ __forceinline__ void store(void *row, I i, L left) const {
     raw *p = reinterpret_cast<raw *>(static_cast<char *>(row) + I(i * I(sizeof(raw))));
     if (left >= 8) {
+      if constexpr (ONCE) {
+#pragma unroll
+        for (int k = 0; k < kWords; k += 4)
+          __builtin_nontemporal_store(Four{w[k], w[k + 1], w[k + 2], w[k + 3]},
+                                      reinterpret_cast<Four *>(p) + k / 4);
+        return;
+      }
       Words v;
 #pragma unroll
       for (int k = 0; k < kWords; ++k) v.w[k] = w[k];
