@@ -35,9 +35,11 @@ namespace {
 using namespace zs_dev;
 
 constexpr int kThreads = 256;
-// Tokens sorted by counting: 8192 of them as one tile took 17 us, the tile's keys
-// coming out of LDS at eight cycles for four; as four tiles and a merge TILEUS.
-constexpr int kTile = 2048;
+// Tokens sorted by counting: up to kTile as one tile (8192: 10 us, 6 and 11 as four
+// tiles and a merge), more in tiles of kSmallTile, whose cost does not grow with the
+// square of their length (65536: 371 us the whole pass, 418 with long tiles).
+constexpr int kTile = 8192, kSmallTile = 2048;
+constexpr int kPlaced = 32;       // of them, that a workgroup places
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kRuns = 8;          // runs merged at a time
@@ -115,65 +117,72 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const FwdArgs A) {
       asm volatile("" : "+v"(v[e]));
     }
     y.set(v);
-    y.template store<TAIL>(row_of<TY>(A.y, token[k], A.ld_y), col[k], A.cols - col[k]);
+    // past the caches, which the table should stay in (65536 x 5120: 189 us for 195)
+    y.template store<TAIL, !TAIL>(row_of<TY>(A.y, token[k], A.ld_y), col[k], A.cols - col[k]);
   }
 }
 
 struct SortArgs {
   Ids ids;
   int64_t tokens;
+  int32_t tile;
   unsigned *keys;  // rows, sorted; vocab: no row of this table
   int *order;      // their tokens
 };
 
-// A workgroup places 64 tokens, a lane of every wave for each; the waves share the
-// tile's tokens in chunks of 64.  Of equal rows the earlier token comes first:
-// tokens of earlier chunks count up to the same row, those of later ones
-// below it.
+// A workgroup places kPlaced tokens.  Its waves share the tile's tokens in chunks of 64;
+// in each wave two lanes take a token, one for either half of a chunk (with 64
+// tokens a wave, half of the CUs had nothing to do and each of the others
+// read all keys out of LDS twice as often: 17 us for SORTUS).  Of equal rows the
+// earlier token comes first: tokens of earlier chunks count up to the same row,
+// those of later ones below it.
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs A) {
   __shared__ __align__(16) unsigned keys[kTile];
-  __shared__ unsigned counts[kSortWaves][64];
+  __shared__ unsigned counts[kSortWaves][kPlaced];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t tile = int64_t(blockIdx.x) / (kTile / 64) * kTile;
-  const int own = int(blockIdx.x % (kTile / 64));
+  const unsigned blocks = unsigned(A.tile) / kPlaced;  // of a tile
+  const int64_t tile = int64_t(blockIdx.x / blocks) * A.tile;
+  const int own = int(blockIdx.x % blocks) * kPlaced;  // in the tile
   const int64_t left = A.tokens - tile;
-  const int n = left < kTile ? int(left) : kTile, chunks = (n + 63) / 64;
+  const int n = left < A.tile ? int(left) : A.tile, chunks = (n + 63) / 64;
 #pragma unroll
   for (int i = 0; i < kTile / kSortThreads; ++i) {
     const int s = i * kSortThreads + int(threadIdx.x);
     if (s < chunks * 64) keys[s] = s < n ? A.ids.key(tile + s) : kNone;
   }
   __syncthreads();
-  const unsigned mine = keys[own * 64 + lane];
+  const int at = own + lane % kPlaced, half = lane / kPlaced * 32;
+  const unsigned mine = keys[at];
   unsigned count = 0;
   for (int c = wave; c < chunks; c += kSortWaves) {
-    const u32x4 *from = reinterpret_cast<const u32x4 *>(keys + c * 64);
-    if (c != own) {
-      const unsigned below = c < own ? mine + 1 : mine;  // of kNone: anything
+    const u32x4 *from = reinterpret_cast<const u32x4 *>(keys + c * 64 + half);
+    if (c != own / 64) {
+      const unsigned below = c < own / 64 ? mine + 1 : mine;  // of kNone: anything
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < 8; ++j) {
         const u32x4 k = from[j];
 #pragma unroll
         for (int e = 0; e < 4; ++e) count += k[e] < below ? 1u : 0u;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
+      for (int j = 0; j < 8; ++j) {
         const u32x4 k = from[j];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          count += k[e] < mine || (k[e] == mine && j * 4 + e < lane) ? 1u : 0u;
+          count += k[e] < mine || (k[e] == mine && half + j * 4 + e < at % 64) ? 1u : 0u;
       }
     }
   }
-  counts[wave][lane] = count;
+  count += __shfl_xor(count, 32, 64);
+  if (lane < kPlaced) counts[wave][lane] = count;
   __syncthreads();
-  if (wave == 0 && own * 64 + lane < n) {
+  if (wave == 0 && lane < kPlaced && at < n) {
     unsigned place = 0;
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w) place += counts[w][lane];
     A.keys[tile + place] = mine;
-    A.order[tile + place] = int(tile + own * 64 + lane);
+    A.order[tile + place] = int(tile + at);
   }
 }
 
@@ -235,13 +244,18 @@ struct SumArgs {
   int32_t rows;       // that a workgroup clears
 };
 
-// The first of keys[lo, hi) that is not below `key`, hi if none.
+// The first of keys[lo, hi) that is not below `key`, hi if none: eight looks side by
+// side, each time an eighth is left.
 __device__ __forceinline__ int64_t first_not_below(const unsigned *keys, int64_t lo, int64_t hi,
                                                    unsigned key) {
   while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (keys[mid] < key) lo = mid + 1;
-    else hi = mid;
+    const int64_t span = hi - lo;
+    int below = 0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) below += keys[lo + (span * q >> 3)] < key ? 1 : 0;
+    if (below == 0) return lo;
+    if (below < 8) hi = lo + (span * below >> 3);
+    lo += (span * (below - 1) >> 3) + 1;
   }
   return lo;
 }
@@ -283,18 +297,21 @@ __device__ __forceinline__ void clear_rows(const SumArgs &A, int64_t block) {
     used[threadIdx.x] = at < A.tokens && A.keys[at] == key;
   }
   __syncthreads();
+  // in elements, or in sixteen bytes side by side
+  using raw = typename TG::raw;
+  constexpr int64_t kUnit = TAIL ? 1 : 16 / sizeof(raw);
+  const int64_t units = A.cols / kUnit;
   // `across` threads a row, several rows at a time where rows are short
-  const unsigned across = A.per < kThreads ? A.per : kThreads;
+  const unsigned across = units < kThreads ? unsigned(units) : kThreads;
   const unsigned sub = threadIdx.x / across, subs = kThreads / across;
   if (sub >= subs) return;
-  Eight<TG> zero;
-  const float none[8] = {};
-  zero.set(none);
   for (int r = int(sub); r < rows; r += int(subs)) {
     if (used[r]) continue;
-    void *to = row_of<TG>(A.out, r0 + r, A.ld_out);
-    for (unsigned c = threadIdx.x - sub * across; c < A.per; c += across)
-      zero.template store<TAIL, true>(to, c * 8, A.cols - int64_t(c) * 8);
+    raw *to = static_cast<raw *>(row_of<TG>(A.out, r0 + r, A.ld_out));
+    for (int64_t c = threadIdx.x - sub * across; c < units; c += across) {
+      if constexpr (TAIL) to[c] = raw(0);
+      else __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, reinterpret_cast<u32x4 *>(to) + c);
+    }
   }
 }
 
@@ -528,11 +545,11 @@ int sort(const zs_embedding_desc &d, const Plan &p, const void *ids, char *ws, h
   const auto keys = [&](int k) { return reinterpret_cast<unsigned *>(ws + p.keys[k]); };
   const auto order = [&](int k) { return reinterpret_cast<int *>(ws + p.order[k]); };
   turn = 0;
-  // whole tiles have 128 workgroups each, the last one as many as it has chunks
-  const int64_t blocks = (d.tokens + 63) / 64;
+  const int64_t blocks = (d.tokens + kPlaced - 1) / kPlaced;
+  const int32_t tile = d.tokens <= kTile ? kTile : kSmallTile;
   hipLaunchKernelGGL(embed_sort_kernel, dim3(unsigned(blocks)), dim3(kSortThreads), 0, st,
-                     SortArgs{ids_of(d, ids), d.tokens, keys(0), order(0)});
-  for (int64_t run = kTile; run < d.tokens; run *= kRuns, turn ^= 1) {
+                     SortArgs{ids_of(d, ids), d.tokens, tile, keys(0), order(0)});
+  for (int64_t run = tile; run < d.tokens; run *= kRuns, turn ^= 1) {
     hipLaunchKernelGGL(embed_merge_kernel, dim3(unsigned((d.tokens + kThreads - 1) / kThreads)),
                        dim3(kThreads), 0, st,
                        MergeArgs{int32_t(d.tokens), int32_t(run), keys(turn), order(turn), keys(turn ^ 1),
