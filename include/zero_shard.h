@@ -577,7 +577,7 @@ int zero_shard_blocknorm_bwd(const zs_blocknorm_desc *d, const void *dy, const v
 #define ZS_EMBEDDING_MAX_TOKENS (INT64_C(1) << 27)
 #define ZS_EMBEDDING_MAX_VOCAB INT64_C(0x7fffffff)
 typedef struct zs_embedding_desc {
-  int64_t tokens;      /* 0 .. ZS_EMBEDDING_MAX_TOKENS                        */
+  int64_t tokens;      /* 0 .. ZS_EMBEDDING_MAX_TOKENS; tokens * cols < 2^34  */
   int64_t vocab;       /* rows of the table, 1 .. ZS_EMBEDDING_MAX_VOCAB      */
   int64_t cols;        /* 1 .. 2^20                                           */
   int64_t first;       /* the id of the table's first row; the last row's has to fit */
@@ -604,8 +604,8 @@ int zero_shard_embedding(const zs_embedding_desc *d, const void *ids, const void
 int64_t zero_shard_embedding_workspace(const zs_embedding_desc *d);
 
 /* dtable[v] = scale sum dy[t] over the tokens t of row v, in binary32 and in the
- * order of t: runs of 32 tokens of the row each, the runs then in order (eight stretches
- * of runs side by side); rounded once.  accumulate: dtable[v] + that, rounded
+ * order of t: runs of 32 tokens of the row each (8 up to 2048 tokens in all), the runs
+ * then in order (four stretches of runs side by side); rounded once.  accumulate: dtable[v] + that, rounded
  * once; rows without tokens are left as they are.  Otherwise they become zeros.
  * dtable overlaps nothing; workspace: device, 256-byte aligned, at least
  * zero_shard_embedding_workspace(d) bytes.  Errors: as above. */

@@ -15,7 +15,7 @@
 //          tokens of its tile that come before it.  One launch, no passes over
 //          digits that wait for each other.  Longer lists merge up to eight runs
 //          at a time, each token finding its place by binary search in the other runs.
-//   sum    pieces of kPiece sorted tokens.  A row is cut every kRun tokens, and
+//   sum    pieces of kPiece sorted tokens.  A row is cut every `run` tokens, and
 //          each part, or the whole of a shorter row, belongs to the piece that it
 //          begins in, so that no piece does much more than its share however
 //          the tokens are distributed.
@@ -43,9 +43,15 @@ constexpr int kPlaced = 32;       // of them, that a workgroup places
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kRuns = 8;          // runs merged at a time
-constexpr int kRun = 32;          // tokens of a long row's part
+// Tokens of a long row's part: 8 where there are few tokens and their chains of loads
+// are what takes time (333 tokens: 16 us for 21), 32 where the parts' traffic counts.
+constexpr int kRun = 32, kShortRun = 8;
+constexpr int64_t kFew = 2048;
 constexpr int kPiece = 8;         // tokens of a piece, and rows of dy in flight
-constexpr int kJoinWaves = 8;
+// Waves that share a long row's parts: most workgroups find no such row, so few
+// (65536 x 5120: 16 us with 4 waves, 24 with 8; one row of 8192 tokens 24 and 16).
+constexpr int kJoinWaves = 4;
+constexpr unsigned kWide = 48;    // pieces of eight columns from which a wave has one row's
 constexpr int kEach = 4;          // pieces of eight columns of a forward thread
 constexpr unsigned kNone = 0xffffffffu;  // sorts behind every row
 constexpr int64_t kMaxGrid = 0x7fffffff;
@@ -85,10 +91,8 @@ struct FwdArgs {
 // whatever token they belong to.
 template <class TW, class TY, bool TAIL>
 __global__ void __launch_bounds__(kThreads) embed_kernel(const FwdArgs A) {
-  const int64_t total = A.tokens * A.per;
-  const int64_t base = int64_t(blockIdx.x) * (kThreads * kEach);
-  const int64_t t0 = base / A.per;
-  const unsigned c0 = unsigned(base - t0 * A.per);
+  const unsigned base = blockIdx.x * (kThreads * kEach), t0 = base / A.per;  // below 2^31
+  const unsigned c0 = base - t0 * A.per;
   int64_t token[kEach], row[kEach];
   unsigned col[kEach];
   Eight<TW> w[kEach];
@@ -96,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const FwdArgs A) {
   for (int k = 0; k < kEach; ++k) {
     const unsigned q = c0 + unsigned(k * kThreads) + threadIdx.x;
     const unsigned up = q / A.per;
-    token[k] = t0 + up;
+    token[k] = int64_t(t0) + up;
     col[k] = (q - up * A.per) * 8;
     row[k] = token[k] < A.tokens ? A.ids.row(A.ids.id(token[k])) : -1;
   }
@@ -106,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const FwdArgs A) {
                              row[k] >= 0 ? A.cols - col[k] : 0);
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    if (base + k * kThreads + threadIdx.x >= total) break;
+    if (token[k] >= A.tokens) break;
     float v[8];
     Eight<TY> y;
 #pragma unroll
@@ -125,24 +129,23 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const FwdArgs A) {
 struct SortArgs {
   Ids ids;
   int64_t tokens;
-  int32_t tile;
+  int32_t tile, groups;  // of kPlaced tokens, of a workgroup
   unsigned *keys;  // rows, sorted; vocab: no row of this table
   int *order;      // their tokens
 };
 
-// A workgroup places kPlaced tokens.  Its waves share the tile's tokens in chunks of 64;
-// in each wave two lanes take a token, one for either half of a chunk (with 64
-// tokens a wave, half of the CUs had nothing to do and each of the others
-// read all keys out of LDS twice as often: 17 us for SORTUS).  Of equal rows the
-// earlier token comes first: tokens of earlier chunks count up to the same row,
-// those of later ones below it.
+// A workgroup places `groups` times kPlaced tokens.  Its waves share the tile's tokens
+// in chunks of 64; in each wave two lanes take a token, one for either half of a
+// chunk (with 64 tokens a wave, half of the CUs had nothing to do with 8192 of them
+// and each of the others read all keys out of LDS twice as often: 17 us for 10).
+// Of equal rows the earlier token comes first: tokens of earlier chunks count up to
+// the same row, those of later ones below it.
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs A) {
   __shared__ __align__(16) unsigned keys[kTile];
   __shared__ unsigned counts[kSortWaves][kPlaced];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const unsigned blocks = unsigned(A.tile) / kPlaced;  // of a tile
+  const unsigned blocks = unsigned(A.tile / (kPlaced * A.groups));  // of a tile
   const int64_t tile = int64_t(blockIdx.x / blocks) * A.tile;
-  const int own = int(blockIdx.x % blocks) * kPlaced;  // in the tile
   const int64_t left = A.tokens - tile;
   const int n = left < A.tile ? int(left) : A.tile, chunks = (n + 63) / 64;
 #pragma unroll
@@ -151,38 +154,43 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
     if (s < chunks * 64) keys[s] = s < n ? A.ids.key(tile + s) : kNone;
   }
   __syncthreads();
-  const int at = own + lane % kPlaced, half = lane / kPlaced * 32;
-  const unsigned mine = keys[at];
-  unsigned count = 0;
-  for (int c = wave; c < chunks; c += kSortWaves) {
-    const u32x4 *from = reinterpret_cast<const u32x4 *>(keys + c * 64 + half);
-    if (c != own / 64) {
-      const unsigned below = c < own / 64 ? mine + 1 : mine;  // of kNone: anything
+  for (int g = 0; g < A.groups; ++g) {
+    const int own = (int(blockIdx.x % blocks) * A.groups + g) * kPlaced;  // in the tile
+    if (own >= n) break;
+    const int at = own + lane % kPlaced, half = lane / kPlaced * 32;
+    const unsigned mine = keys[at];
+    unsigned count = 0;
+    for (int c = wave; c < chunks; c += kSortWaves) {
+      const u32x4 *from = reinterpret_cast<const u32x4 *>(keys + c * 64 + half);
+      if (c != own / 64) {
+        const unsigned below = c < own / 64 ? mine + 1 : mine;  // of kNone: anything
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const u32x4 k = from[j];
+        for (int j = 0; j < 8; ++j) {
+          const u32x4 k = from[j];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) count += k[e] < below ? 1u : 0u;
-      }
-    } else {
+          for (int e = 0; e < 4; ++e) count += k[e] < below ? 1u : 0u;
+        }
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const u32x4 k = from[j];
+        for (int j = 0; j < 8; ++j) {
+          const u32x4 k = from[j];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          count += k[e] < mine || (k[e] == mine && half + j * 4 + e < at % 64) ? 1u : 0u;
+          for (int e = 0; e < 4; ++e)
+            count += k[e] < mine || (k[e] == mine && half + j * 4 + e < at % 64) ? 1u : 0u;
+        }
       }
     }
-  }
-  count += __shfl_xor(count, 32, 64);
-  if (lane < kPlaced) counts[wave][lane] = count;
-  __syncthreads();
-  if (wave == 0 && lane < kPlaced && at < n) {
-    unsigned place = 0;
+    count += __shfl_xor(count, 32, 64);
+    if (lane < kPlaced) counts[wave][lane] = count;
+    __syncthreads();
+    if (wave == 0 && lane < kPlaced && at < n) {
+      unsigned place = 0;
 #pragma unroll
-    for (int w = 0; w < kSortWaves; ++w) place += counts[w][lane];
-    A.keys[tile + place] = mine;
-    A.order[tile + place] = int(tile + at);
+      for (int w = 0; w < kSortWaves; ++w) place += counts[w][lane];
+      A.keys[tile + place] = mine;
+      A.order[tile + place] = int(tile + at);
+    }
+    __syncthreads();  // before the counts of the next group
   }
 }
 
@@ -236,10 +244,12 @@ struct SumArgs {
   const int *order;
   const void *dy;
   void *out;
-  float *part;  // [2 tokens / kRun][per * 8], see part_of
+  float *part;  // [2 tokens / run][per * 8], see part_of
+  int32_t run;  // tokens of a long row's part
   float scale;
   int32_t add;        // to what is there
   unsigned per;       // pieces of eight columns
+  unsigned waves;     // of a piece of tokens
   int64_t sum_blocks; // workgroups that sum; the others clear
   int32_t rows;       // that a workgroup clears
 };
@@ -261,10 +271,10 @@ __device__ __forceinline__ int64_t first_not_below(const unsigned *keys, int64_t
 }
 
 // Where the part of a long row that begins at sorted token `at` is kept.  Of the parts
-// that begin within kRun tokens one at most is its row's first (its row goes on
+// that begin within `run` tokens one at most is its row's first (its row goes on
 // for all of them) and one at most is not.
-__device__ __forceinline__ int64_t part_of(int64_t at, bool first) {
-  return at / kRun * 2 + (first ? 1 : 0);
+__device__ __forceinline__ int64_t part_of(const SumArgs &A, int64_t at, bool first) {
+  return (A.run == kRun ? at / kRun : at / kShortRun) * 2 + (first ? 1 : 0);
 }
 
 // A row's sum, scaled and joined with what is there, into the table's gradient.
@@ -315,151 +325,195 @@ __device__ __forceinline__ void clear_rows(const SumArgs &A, int64_t block) {
   }
 }
 
-// Keys and tokens of kPiece sorted places from `at` on, a multiple of kPiece.
+// The sorted lists are not written while they are read here: the scalar units may
+// load from them where the place is the whole wave's.
+template <class T>
+__device__ __forceinline__ const T __attribute__((address_space(4))) *sorted(const void *p) {
+  return (const T __attribute__((address_space(4))) *)uintptr_t(p);
+}
+
+// kPiece sorted places from `at` on, a multiple of kPiece: their tokens, and a bit for each
+// that is of another row than the place before it (`prev`: the first one's) or of
+// the row `key`; the first `live` of them are of rows of the table.
 struct Places {
-  unsigned key[kPiece];
   int token[kPiece];
+  unsigned begins, same, first, last;
+  int live;
   __device__ __forceinline__ void load(const SumArgs &A, int64_t at) {
     if (at + kPiece <= A.tokens) {
 #pragma unroll
       for (int q = 0; q < kPiece / 4; ++q) {
-        const u32x4 k = *reinterpret_cast<const u32x4 *>(A.keys + at + q * 4);
-        const u32x4 t = *reinterpret_cast<const u32x4 *>(A.order + at + q * 4);
+        const u32x4 k = *sorted<u32x4>(A.keys + at + q * 4);
+        const u32x4 t = *sorted<u32x4>(A.order + at + q * 4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          key[q * 4 + e] = k[e];
+          row[q * 4 + e] = k[e];
           token[q * 4 + e] = int(t[e]);
         }
       }
     } else {
 #pragma unroll
       for (int e = 0; e < kPiece; ++e) {
-        key[e] = at + e < A.tokens ? A.keys[at + e] : kNone;
-        token[e] = at + e < A.tokens ? A.order[at + e] : 0;
+        row[e] = at + e < A.tokens ? *sorted<unsigned>(A.keys + at + e) : kNone;
+        token[e] = at + e < A.tokens ? *sorted<int>(A.order + at + e) : 0;
       }
     }
   }
+  __device__ __forceinline__ void look(const SumArgs &A, unsigned prev, unsigned key) {
+    begins = same = 0;
+    live = 0;
+#pragma unroll
+    for (int e = 0; e < kPiece; ++e) {
+      begins |= row[e] != (e ? row[e - 1] : prev) ? 1u << e : 0u;
+      same |= row[e] == key ? 1u << e : 0u;
+      live += row[e] < unsigned(A.vocab) ? 1 : 0;
+    }
+    first = row[0];
+    last = row[kPiece - 1];
+  }
+  unsigned row[kPiece];  // until look
 };
 
-template <class TY, class TG, bool TAIL>
+// WAVES: a wave has one piece, and what concerns its rows is the scalar units' work; a
+// piece has A.waves of them (65536 x 5120: 205 us for 319 with each thread on its own).
+// Rows of too few columns to fill a wave share waves: a thread is any piece's.
+template <class TY, class TG, bool TAIL, bool WAVES>
 __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const SumArgs A) {
   if (int64_t(blockIdx.x) >= A.sum_blocks) {
     clear_rows<TG, TAIL>(A, int64_t(blockIdx.x) - A.sum_blocks);
     return;
   }
-  const int64_t base = int64_t(blockIdx.x) * kThreads;
-  const int64_t p0 = base / A.per;
-  const unsigned q = unsigned(base - p0 * A.per) + threadIdx.x, up = q / A.per;
-  const unsigned col = (q - up * A.per) * 8;
-  const int64_t from = (p0 + up) * kPiece;
+  unsigned piece, col;
+  if constexpr (WAVES) {
+    const unsigned wave =
+        __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6));
+    piece = wave / A.waves;
+    col = ((wave - piece * A.waves) * 64 + (threadIdx.x & 63)) * 8;
+  } else {
+    const unsigned id = blockIdx.x * kThreads + threadIdx.x;  // below 2^31
+    piece = id / A.per;
+    col = (id - piece * A.per) * 8;
+  }
+  const int64_t width = int64_t(A.per) * 8, columns = A.cols - col;
+  const int64_t from = int64_t(piece) * kPiece, to = from + kPiece;
   if (from >= A.tokens) return;
-  // this piece's places, the next one's, and how many of the kRun before it are of its
-  // first row: three loads side by side
+  // this piece's places, the next one's, and how many of the kRun before it (a multiple
+  // of any run) are of its first row: loads side by side
   Places now, next;
   now.load(A, from);
-  next.load(A, from + kPiece);
+  next.load(A, to);
   int before = 0;
 #pragma unroll
   for (int k = kPiece; k <= kRun; k += kPiece)
     if (from >= k) {
 #pragma unroll
       for (int h = 0; h < kPiece / 4; ++h) {
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(A.keys + from - k + h * 4);
+        const u32x4 v = *sorted<u32x4>(A.keys + from - k + h * 4);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) before += v[e] == now.key[0] ? 1 : 0;
+        for (int e = 0; e < 4; ++e) before += v[e] == now.row[0] ? 1 : 0;
       }
     }
-  // a row that began before this piece: its next part may begin in here
-  const unsigned first = now.key[0], last = now.key[kPiece - 1];
-  int64_t part = from;
+  now.look(A, before ? now.row[0] : kNone, now.row[0]);
+  next.look(A, now.last, now.last);
+  // Where a part may begin: at a row's first place, and where the next part of a row that
+  // began before this piece does, if that row is still there.
+  unsigned starts = now.begins, mine = now.begins ? ~0u << __builtin_ctz(now.begins) : 0u;
   if (before) {
     const int64_t row0 =
-        before < kRun ? from - before : first_not_below(A.keys, 0, from - kRun, first);
-    part = row0 + (from - row0 + kRun - 1) / kRun * kRun;
-  }
-  const int64_t to = from + kPiece;
-  unsigned key = kNone;  // of the row being summed
-  int64_t start = 0;     // its part's first place
-  bool active = false, whole = false;  // whole: that is the row's first place too
-  float acc[8];
-  const auto flush = [&](bool ended) {
-    if (whole && ended) {
-      put_row<TG, TAIL>(A, key, col, acc);
-    } else {
-      Eight<F32> v;
-      v.set(acc);
-      v.template store<false>(A.part + part_of(start, whole) * (int64_t(A.per) * 8), col, 8);
+        before < kRun ? from - before : first_not_below(A.keys, 0, from - kRun, now.first);
+    const int64_t part = row0 + ((from - row0 + A.run - 1) & -int64_t(A.run));
+    if (part < to && (now.same >> (part - from) & 1)) {
+      starts |= 1u << (part - from);
+      mine = ~0u << (part - from);
     }
-  };
+  }
+  mine &= (1u << now.live) - 1u;  // places that are summed here
+  if (!mine) return;
+  int64_t start = 0;                   // of the part being summed
+  bool active = false, whole = false;  // whole: at its row's first place
+  float acc[8];
   for (int64_t at = from;; at += kPiece) {
     Eight<TY> v[kPiece];
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) {
-      const unsigned k = now.key[j];
-      const bool mine = at == from ? !(before && k == first && at + j < part)
-                                   : k == last && at + j - start < kRun;
-      const bool take = mine && k < unsigned(A.vocab);
+      const bool take = mine >> j & 1;
       v[j].template load<TAIL, !TAIL>(row_of<TY>(A.dy, take ? now.token[j] : 0, A.ld_dy), col,
-                                      take ? A.cols - col : 0);
+                                      take ? columns : 0);
     }
-    Places after;
-    after.load(A, at + 2 * kPiece);
-    bool done = false;
-#pragma unroll
-    for (int j = 0; j < kPiece; ++j) {
-      const unsigned k = now.key[j];
-      const int64_t i = at + j;
-      const bool row = j ? k != now.key[j - 1] : at == from ? !before : k != key;
-      const bool none = k >= unsigned(A.vocab);  // and so are all places behind
-      if (active && (row || none || i - start == kRun)) {
-        flush(row || none);
-        active = false;
-      }
-      if (none || (i >= to && !active)) {
-        done = true;
-        break;
-      }
-      if (row || (before && i == part && k == first)) {
-        key = k;
-        start = i;
-        whole = row;
+    int cur = 0;
+    for (;;) {
+      if (!active) {
+        const unsigned left = at == from ? starts & mine & ~0u << cur : 0u;
+        if (!left) return;
+        cur = __builtin_ctz(left);
+        start = at + cur;
+        whole = now.begins >> cur & 1;
         active = true;
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
       }
-      if (active) {
+      // to the next row, behind the table's rows, or to the part's end
+      int end = now.live;
+      const unsigned row = start == at + cur ? now.begins & ~1u << cur : now.begins & ~0u << cur;
+      if (row && __builtin_ctz(row) < end) end = __builtin_ctz(row);
+      if (start + A.run - at < end) end = int(start + A.run - at);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += v[j].get(e);
+      for (int j = 0; j < kPiece; ++j)
+        if (j >= cur && j < end) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] += v[j].get(e);
+        }
+      if (end == kPiece) break;
+      const unsigned key = *sorted<unsigned>(A.keys + start);
+      if (columns <= 0) {
+        // no columns of this thread
+      } else if (whole && (end == now.live || (row >> end & 1))) {
+        put_row<TG, TAIL>(A, key, col, acc);
+      } else {
+        Eight<F32> part;
+        part.set(acc);
+        part.template store<false>(A.part + part_of(A, start, whole) * width, col, 8);
       }
+      active = false;
+      cur = end;
+      if (at != from || end == now.live) return;
     }
-    if (done || !active) break;
+    // the part goes on, or ends with these places
     now = next;
-    next = after;
+    const int64_t left = start + A.run - (at + kPiece);
+    mine = now.same & (now.begins & 1 ? 0u : ~0u);
+    if (now.begins >> 1) mine &= (1u << __builtin_ctz(now.begins & ~1u)) - 1u;
+    if (left < kPiece) mine &= (1u << left) - 1u;
+    if (left >= kPiece) {  // also to see whether the row ends with its part
+      next.load(A, at + 2 * kPiece);
+      next.look(A, now.last, now.last);
+    }
   }
 }
 
-// The parts of the row that begins among the kRun places from blockIdx.x kRun on and
-// goes on for more than kRun, if there is one: each wave adds a stretch of them, then
+// The parts of the row that begins among the `run` places from blockIdx.x run on and
+// goes on for more than `run`, if there is one: each wave adds a stretch of them, then
 // the waves' sums are added in order.
 template <class TG, bool TAIL>
 __global__ void __launch_bounds__(64 * kJoinWaves) embed_join_kernel(const SumArgs A) {
   __shared__ float sums[kJoinWaves][8][64];
-  const int64_t from = int64_t(blockIdx.x) * kRun, to = from + kRun;
+  const int run = A.run;
+  const int64_t from = int64_t(blockIdx.x) * run, to = from + run;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (to >= A.tokens) return;
-  // lanes: the place before, the kRun places, the one behind
+  // lanes: the place before, the run's places, the one behind
   const int64_t look = from - 1 + lane;
-  const unsigned near = lane < kRun + 2 && look >= 0 ? A.keys[look] : kNone;
-  const unsigned key = __builtin_amdgcn_readlane(near, kRun);
+  const unsigned near = lane < run + 2 && look >= 0 ? A.keys[look] : kNone;
+  const unsigned key = __builtin_amdgcn_readlane(near, run);
   if (key >= unsigned(A.vocab)) return;
   const uint64_t same = __ballot(near == key);
-  if (!(same >> (kRun + 1) & 1) || (same & 1)) return;  // ends in here, or began before
+  if (!(same >> (run + 1) & 1) || (same & 1)) return;  // ends in here, or began before
   const int64_t start = from - 1 + __builtin_ctzll(same);
-  if (start + kRun >= A.tokens || A.keys[start + kRun] != key) return;
+  if (start + run >= A.tokens || A.keys[start + run] != key) return;
   // a part a lane: how many begin within the row
   int64_t parts = 1;
   for (;;) {
-    const int64_t at = start + (parts + lane) * kRun;
+    const int64_t at = start + (parts + lane) * run;
     const uint64_t more = __ballot(at < A.tokens && A.keys[at < A.tokens ? at : start] == key);
     parts += __builtin_popcountll(more);
     if (more != ~uint64_t(0)) break;
@@ -469,10 +523,10 @@ __global__ void __launch_bounds__(64 * kJoinWaves) embed_join_kernel(const SumAr
   float acc[8] = {};
   if (c < A.per) {
     const int64_t lo = wave * each, hi = lo + each < parts ? lo + each : parts;
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t j = lo; j < hi; ++j) {
       Eight<F32> v;
-      v.template load<false>(A.part + part_of(start + j * kRun, j == 0) * width, col, 8);
+      v.template load<false>(A.part + part_of(A, start + j * run, j == 0) * width, col, 8);
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] += v.get(e);
     }
@@ -506,6 +560,7 @@ bool desc_ok(const zs_embedding_desc *d) {
 }
 
 unsigned per_of(const zs_embedding_desc &d) { return unsigned((d.cols + 7) / 8); }
+int run_of(const zs_embedding_desc &d) { return d.tokens <= kFew ? kShortRun : kRun; }
 
 // Workspace: the sorted rows and tokens (twice where runs are merged), the
 // parts of long rows.
@@ -513,7 +568,7 @@ struct Plan {
   int64_t keys[2], order[2], part, bytes;
   bool merged;
   explicit Plan(const zs_embedding_desc &d) {
-    const int64_t list = up(d.tokens * 4, 256), runs = (d.tokens + kRun - 1) / kRun;
+    const int64_t list = up(d.tokens * 4, 256), runs = (d.tokens + run_of(d) - 1) / run_of(d);
     merged = d.tokens > kTile;
     keys[0] = 0;
     order[0] = list;
@@ -545,10 +600,13 @@ int sort(const zs_embedding_desc &d, const Plan &p, const void *ids, char *ws, h
   const auto keys = [&](int k) { return reinterpret_cast<unsigned *>(ws + p.keys[k]); };
   const auto order = [&](int k) { return reinterpret_cast<int *>(ws + p.order[k]); };
   turn = 0;
-  const int64_t blocks = (d.tokens + kPlaced - 1) / kPlaced;
   const int32_t tile = d.tokens <= kTile ? kTile : kSmallTile;
+  // a workgroup or two for each CU, at most a tile's
+  int32_t groups = 1;
+  while (d.tokens > int64_t(512) * kPlaced * groups && groups < kSmallTile / kPlaced) groups *= 2;
+  const int64_t blocks = (d.tokens + kPlaced * groups - 1) / (kPlaced * groups);
   hipLaunchKernelGGL(embed_sort_kernel, dim3(unsigned(blocks)), dim3(kSortThreads), 0, st,
-                     SortArgs{ids_of(d, ids), d.tokens, tile, keys(0), order(0)});
+                     SortArgs{ids_of(d, ids), d.tokens, tile, groups, keys(0), order(0)});
   for (int64_t run = tile; run < d.tokens; run *= kRuns, turn ^= 1) {
     hipLaunchKernelGGL(embed_merge_kernel, dim3(unsigned((d.tokens + kThreads - 1) / kThreads)),
                        dim3(kThreads), 0, st,
@@ -572,7 +630,7 @@ int zero_shard_embedding(const zs_embedding_desc *d, const void *ids, const void
   const FwdArgs A{ids_of(*d, ids), d->tokens, d->cols, ld(d->ld_table), ld(d->ld_y), table, y,
                   d->scale, per_of(*d)};
   const int64_t blocks = (A.tokens * A.per + kThreads * kEach - 1) / (kThreads * kEach);
-  if (blocks > kMaxGrid / kThreads) return ZS_EINVAL;
+  if (blocks > kMaxGrid / (kThreads * kEach)) return ZS_EINVAL;
   if (const int rc = device_is_gfx950()) return rc;
   const bool even = rows_even(table, A.ld_table, tsize) && rows_even(y, A.ld_y, size);
   return by_type(d->dtype, d->table_dtype, [&](auto ty, auto tw) {
@@ -601,10 +659,24 @@ int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const 
       !aligned(workspace, 256))
     return ZS_EALIGN;
   const auto ld = [&](int64_t v) { return v ? v : d->cols; };
-  const int64_t pieces = (d->tokens + kPiece - 1) / kPiece, runs = (d->tokens + kRun - 1) / kRun;
-  SumArgs A{d->tokens, d->vocab, d->cols, ld(d->ld_dy), ld(d->ld_dtable), nullptr, nullptr, dy,
-            dtable, nullptr, d->scale, d->accumulate, per_of(*d), 0, 0};
-  A.sum_blocks = (pieces * A.per + kThreads - 1) / kThreads;
+  const int run = run_of(*d);
+  const int64_t pieces = (d->tokens + kPiece - 1) / kPiece, runs = (d->tokens + run - 1) / run;
+  SumArgs A{};
+  A.tokens = d->tokens;
+  A.vocab = d->vocab;
+  A.cols = d->cols;
+  A.ld_dy = ld(d->ld_dy);
+  A.ld_out = ld(d->ld_dtable);
+  A.dy = dy;
+  A.out = dtable;
+  A.run = run;
+  A.scale = d->scale;
+  A.add = d->accumulate;
+  A.per = per_of(*d);
+  A.waves = (A.per + 63) / 64;
+  const bool wide = A.per >= kWide;
+  const int64_t threads = wide ? int64_t(A.waves) * 64 : A.per;
+  A.sum_blocks = (pieces * threads + kThreads - 1) / kThreads;
   // about 64 KiB a workgroup clears, so that its searches are hidden
   A.rows = int32_t((65536 + d->cols * gsize - 1) / (d->cols * gsize));
   if (A.rows > kThreads) A.rows = kThreads;
@@ -624,8 +696,13 @@ int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const 
   return by_type(d->dtype, d->grad_dtype, [&](auto ty, auto tg) {
     using TG = decltype(tg);
     return by_tail(d->cols % 8 != 0 || !even, [&](auto tail) {
-      hipLaunchKernelGGL((embed_sum_kernel<decltype(ty), TG, tail.value>),
-                         dim3(unsigned(A.sum_blocks + clear)), dim3(kThreads), 0, st, A);
+      const dim3 grid(unsigned(A.sum_blocks + clear));
+      if (wide)
+        hipLaunchKernelGGL((embed_sum_kernel<decltype(ty), TG, tail.value, true>), grid,
+                           dim3(kThreads), 0, st, A);
+      else
+        hipLaunchKernelGGL((embed_sum_kernel<decltype(ty), TG, tail.value, false>), grid,
+                           dim3(kThreads), 0, st, A);
       if (runs > 1)
         hipLaunchKernelGGL((embed_join_kernel<TG, tail.value>),
                            dim3(unsigned(runs), (A.per + 63) / 64), dim3(64 * kJoinWaves), 0, st,

@@ -59,7 +59,7 @@ def test_forward(tokens, vocab, cols, dtype, other):
 
 def _reference(ids, dy, vocab, first=0, padding=None, old=None):
     """The table's gradient in 64 bits and its error: a row's tokens in runs of
-    32, the runs in 8 stretches."""
+    32 (8 up to 2048 tokens in all), the runs in 4 stretches."""
     row = ids.long().reshape(-1) - first
     live = (row >= 0) & (row < vocab)
     if padding is not None:
@@ -69,7 +69,8 @@ def _reference(ids, dy, vocab, first=0, padding=None, old=None):
     ref.index_add_(0, row[live], dy.double()[live])
     size.index_add_(0, row[live], dy.double().abs()[live])
     count.index_add_(0, row[live], torch.ones_like(row[live], dtype=torch.float64))
-    chain = torch.minimum(count, 32 + torch.ceil(count / 256) + 8)[:, None]
+    run = 8 if ids.numel() <= 2048 else 32
+    chain = torch.minimum(count, run + torch.ceil(count / (4 * run)) + 4)[:, None]
     s = float(torch.tensor(SCALE))
     ref, tol = ref * s, size * s * chain * R.U + 2 * R.U * abs(ref) * s
     if old is not None:
@@ -112,7 +113,7 @@ def test_more_tokens_than_a_sorted_tile(tokens, power):
 
 @pytest.mark.parametrize("lengths", [
     [1] * 100, [32] * 8, [33] * 8, [31, 33, 1, 64, 65, 32, 96, 2], [5, 200, 1, 1, 30, 2, 33],
-    [1000], [31, 1000, 1], [63, 64, 65, 66], [16, 17] * 9, [257 * 32 + 5, 3], [40000, 17, 300]])
+    [8] * 20, [9] * 20, [7, 8, 9, 16, 17, 1], [1000], [31, 1000, 1], [63, 64, 65, 66], [16, 17] * 9, [257 * 32 + 5, 3], [40000, 17, 300]])
 def test_rows_of_every_length(lengths):
     """Rows of these many tokens, the tokens shuffled: parts that begin and end at
     every place of a piece."""
@@ -125,26 +126,30 @@ def test_rows_of_every_length(lengths):
 
 @pytest.mark.parametrize("shift", range(0, 34, 3))
 def test_long_rows_at_every_offset(shift):
-    ids = torch.tensor([0] * shift + [1] * 100 + [2] * (70 - shift) + [3] * 3, device="cuda")
-    _backward(ids, 5, 16, F32, F32)
+    few = [0] * shift + [1] * 100 + [2] * (70 - shift) + [3] * 3
+    for ids in (few, few + [9] * 3000, [0] * (1000 + shift) + few[shift:] * 20):
+        ids = torch.sort(torch.tensor(ids, device="cuda")).values
+        for cols in (16, 520):
+            _backward(ids, 5, cols, F32, F32)
 
 
 def test_the_order_of_a_rows_sum():
-    """A row's sum is that of its tokens in order, bit for bit: 32 and fewer in one
-    run, more of them in runs."""
-    for n in (20, 32, 100):
-        dy = R.randn(n, 16, seed=7) * torch.exp(4 * R.randn(n, 1, seed=8))
-        ids = torch.full((n,), 3, device="cuda")
+    """A row's sum is that of its tokens in order, bit for bit: in runs of 8 or,
+    among many tokens, of 32."""
+    for n, others, run in ((5, 0, 8), (8, 0, 8), (32, 0, 8), (20, 3000, 32), (128, 3000, 32)):
+        dy = R.randn(n + others, 16, seed=7) * torch.exp(4 * R.randn(n + others, 1, seed=8))
+        ids = torch.full((n + others,), 3, device="cuda")
+        ids[n:] = -1
         out = torch.empty(5, 16, device="cuda")
-        plan = Z.ZeroEmbedding(tokens=n, vocab=5, cols=16, dtype=F32)
+        plan = Z.ZeroEmbedding(tokens=n + others, vocab=5, cols=16, dtype=F32)
         plan.backward(ids, dy, out)
         want = torch.zeros(16, device="cuda")
-        for at in range(0, n, 32):
-            run = torch.zeros(16, device="cuda")
-            for t in range(at, min(n, at + 32)):
-                run = run + dy[t]
-            want = want + run
-        assert torch.equal(out[3], want)
+        for at in range(0, n, run):
+            part = torch.zeros(16, device="cuda")
+            for t in range(at, min(n, at + run)):
+                part = part + dy[t]
+            want = want + part
+        assert torch.equal(out[3], want), (n, others)
 
 
 @pytest.mark.parametrize("tokens", [500, 9000])
