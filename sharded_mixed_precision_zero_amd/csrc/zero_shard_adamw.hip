@@ -35,7 +35,10 @@ using namespace zs_dev;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBlock = ZS_ADAMW_BLOCK;  // elements that share a scale: a wave's
-constexpr int kRounds = 4;              // blocks of a wave
+#ifndef KR
+#define KR 4
+#endif
+constexpr int kRounds = KR;              // blocks of a wave
 constexpr int64_t kChunk = int64_t(kBlock) * kWaves * kRounds;
 constexpr int kGrads = 440;             // a launch's gradients: 3.4 KiB of arguments
 constexpr uint64_t kMagic = 0x31776d6164617a73;  // "szadamw1"
@@ -147,33 +150,30 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// The largest of the wave's magnitudes as bits (a NaN is larger than all else),
-// uniform.
-template <int CTRL, int ROWS = 0xf>
-__device__ __forceinline__ unsigned dpp_max(unsigned v) {
-  const unsigned w = __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
-  return w > v ? w : v;
-}
-__device__ __forceinline__ unsigned wave_max(unsigned v) {
-  v = dpp_max<0xb1>(v);   // lanes 1 apart
-  v = dpp_max<0x4e>(v);   // 2 apart
-  v = dpp_max<0x141>(v);  // half row mirrored
-  v = dpp_max<0x140>(v);  // row mirrored
-  v = dpp_max<0x142, 0xa>(v);  // rows 1 and 3: with the row before
-  v = dpp_max<0x143, 0xc>(v);  // rows 2 and 3: with the first half
-  return __builtin_amdgcn_readlane(v, 63);
-}
-
 // ---- states in 8 bits: e4m3 numbers of at most 256, times a scale
 
-// A block's scale from its largest magnitude, and the factor that takes
-// magnitudes to [0, 256].  Blocks of nothing but numbers below 2^-100 are zeros (NaN is
-// not below), so that neither leaves binary32.
-__device__ __forceinline__ void scale_of(unsigned top_bits, float &scale, float &inv) {
-  const float top = __uint_as_float(top_bits);
-  const bool none = top < 0x1p-100f;
-  scale = none ? 0.0f : top * 0x1p-8f;
-  inv = none ? 0.0f : 1.0f / scale;
+// The larger of two magnitudes as bits: a NaN is larger than all else.
+__device__ __forceinline__ unsigned larger(unsigned a, unsigned b) { return a > b ? a : b; }
+template <int CTRL>
+__device__ __forceinline__ unsigned dpp_larger(unsigned v) {
+  return larger(v, __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, false));
+}
+
+// The largest of the wave's two magnitudes, a's in lanes 0-31, b's in the others:
+// after one exchange of halves each lane carries on with one of them.
+__device__ __forceinline__ unsigned wave_tops(unsigned a, unsigned b) {
+  const auto halves = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  unsigned v = larger(halves[0], halves[1]);
+  const auto rows = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = larger(rows[0], rows[1]);
+  v = dpp_larger<0xb1>(v);     // lanes 1 apart
+  v = dpp_larger<0x4e>(v);     // 2 apart
+  v = dpp_larger<0x141>(v);    // half row mirrored
+  return dpp_larger<0x140>(v); // row mirrored
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
 }
 
 struct Lane {
@@ -228,7 +228,9 @@ __device__ __forceinline__ float grad_of(const Lane &s, int e) {
 // A tensor's constants of the step.
 struct Rates {
   double coef, decay, lr;  // lr times the tensor's factor, and that times its weight decay
-  float coef32, b1, omb1, b2, omb2, root, eps;  // 8 bits: root = 1 / sqrt(bc2)
+  // 8 bits, whose roots are held times 2^16 so that squares of small gradients stay
+  // normal numbers: b2 and omb2 times 2^32, root = 2^-16 / sqrt(bc2)
+  float coef32, b1, omb1, b2, omb2, root, eps;
   double step;                                  // lr / bc1
 };
 
@@ -274,43 +276,59 @@ __device__ __forceinline__ void update32(const Tensor &T, const Consts &k, const
 }
 
 // The same with a state in 8 bits.  The moments are binary32 numbers, which
-// rounding to 4 significant bits makes little of (binary64 as above: 1.5 times the
-// instructions that there is time for); the weights are binary64 as above.
+// rounding to 4 significant bits makes little of, with a root and a quotient of an
+// instruction or two, within 2^-23 and 2^-22: what the memory leaves time for is some
+// 100 instructions an element, and binary64 as above takes more (1034 us for 570 of
+// 163.84M elements).  The weights are binary64 as above.
 template <class TG, bool TAIL>
 __device__ __forceinline__ void update8(const Tensor &T, const Rates &rates, uint32_t base,
                                         Lane &s, int64_t i, int64_t left) {
   float m[4], r[4];
   unsigned mtop = 0, vtop = 0;
+  using Two = float __attribute__((ext_vector_type(2)));
+  const Two m8[2] = {__builtin_amdgcn_cvt_pk_f32_fp8(s.m8, false),
+                     __builtin_amdgcn_cvt_pk_f32_fp8(s.m8, true)};
+  const Two v8[2] = {__builtin_amdgcn_cvt_pk_f32_fp8(s.v8, false),
+                     __builtin_amdgcn_cvt_pk_f32_fp8(s.v8, true)};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float g = rates.coef32 * grad_of<TG>(s, e);
-    const float m0 = __builtin_amdgcn_cvt_f32_fp8(s.m8 >> (8 * e), 0) * s.ms;
-    const float r0 = __builtin_amdgcn_cvt_f32_fp8(s.v8 >> (8 * e), 0) * s.vs;
+    const float m0 = m8[e / 2][e % 2] * s.ms, r0 = v8[e / 2][e % 2] * s.vs;
     m[e] = rates.b1 * m0 + rates.omb1 * g;
-    r[e] = sqrtf((rates.b2 * r0) * r0 + (rates.omb2 * g) * g);
+    r[e] = __builtin_amdgcn_sqrtf((rates.b2 * r0) * r0 + (rates.omb2 * g) * g);
     const double t0 = double(s.w.v[e]);
-    const float u = m[e] / (r[e] * rates.root + rates.eps);
+    const float u = m[e] * __builtin_amdgcn_rcpf(r[e] * rates.root + rates.eps);
     s.w.v[e] = float(t0 - rates.decay * t0 - rates.step * double(u));
     // what is not there counts for nothing: its gradient and state are 0
-    const unsigned a = __float_as_uint(m[e]) & 0x7fffffffu, b = __float_as_uint(r[e]) & 0x7fffffffu;
-    mtop = a > mtop ? a : mtop;
-    vtop = b > vtop ? b : vtop;
+    mtop = larger(mtop, __float_as_uint(m[e]) & 0x7fffffffu);
+    vtop = larger(vtop, __float_as_uint(r[e]) & 0x7fffffffu);
   }
   put_weights<TAIL>(T, s.w, i, left);
-  float ms, vs, minv, vinv;
-  scale_of(wave_max(mtop), ms, minv);
-  scale_of(wave_max(vtop), vs, vinv);
+  // Scales, and the factors that take magnitudes to [0, 256], m's in the wave's first
+  // half, r's in the other.  Blocks of nothing but numbers below 2^-100 are zeros (NaN
+  // is not below), so that neither leaves binary32.
+  const int lane = threadIdx.x & 63;
+  const float held = lane < 32 ? 1.0f : 0x1p-16f;
+  const float top = __uint_as_float(wave_tops(mtop, vtop)) * held;
+  const bool none = top < 0x1p-100f;
+  const float scale = none ? 0.0f : top * 0x1p-8f;
+  const float inv = none ? 0.0f : __builtin_amdgcn_rcpf(scale) * held;
+  const float minv = lane_value(inv, 0), vinv = lane_value(inv, 32);
   // to e4m3, down or up where 20 bits of dither carry into the number
   unsigned mw = 0, vw = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  const auto encode = [&](auto place) {
+    constexpr int e = place.value;
     const uint32_t h = mix(base + uint32_t(i + e));
     const float a = __builtin_amdgcn_fmed3f(m[e] * minv, -256.0f, 256.0f);
     // a root that is there stays above the least number
     const float b = __builtin_amdgcn_fmed3f(r[e] * vinv, r[e] > 0.0f ? 0x1p-9f : 0.0f, 256.0f);
-    mw |= (__builtin_amdgcn_cvt_sr_fp8_f32(a, h << 16 | 0x8000u, 0, 0) & 0xffu) << (8 * e);
-    vw |= (__builtin_amdgcn_cvt_sr_fp8_f32(b, (h & 0xffff0000u) | 0x8000u, 0, 0) & 0xffu) << (8 * e);
-  }
+    mw = __builtin_amdgcn_cvt_sr_fp8_f32(a, h << 16 | 0x8000u, mw, e);
+    vw = __builtin_amdgcn_cvt_sr_fp8_f32(b, (h & 0xffff0000u) | 0x8000u, vw, e);
+  };
+  encode(std::integral_constant<int, 0>{});
+  encode(std::integral_constant<int, 1>{});
+  encode(std::integral_constant<int, 2>{});
+  encode(std::integral_constant<int, 3>{});
   if (!TAIL || left >= 4) {
     using Word = unsigned __attribute__((aligned(1)));
     __builtin_nontemporal_store(mw, (ZS_GLOBAL Word *)global<uint8_t>(T.m_out, i));
@@ -323,10 +341,8 @@ __device__ __forceinline__ void update8(const Tensor &T, const Rates &rates, uin
         *global<uint8_t>(T.v_out, i + e) = uint8_t(vw >> (8 * e));
       }
   }
-  if ((threadIdx.x & 63) == 0 && left > 0) {
-    *global<float>(T.m_scale_out, i / kBlock) = ms;
-    *global<float>(T.v_scale_out, i / kBlock) = vs;
-  }
+  if ((lane == 0 || lane == 32) && i - lane * 4 < T.n)
+    *global<float>(lane ? T.v_scale_out : T.m_scale_out, i / kBlock) = scale;
 }
 
 template <bool EIGHT, class TG, bool TAIL>
@@ -380,10 +396,10 @@ __global__ void __launch_bounds__(kThreads) adamw_step_kernel(const StepArgs A, 
     rates.coef32 = float(rates.coef);
     rates.b1 = float(k.b1);
     rates.omb1 = float(k.omb1);
-    rates.b2 = float(k.b2);
-    rates.omb2 = float(k.omb2);
-    rates.root = float(k.root);
-    rates.eps = float(k.eps);
+    rates.b2 = float(k.b2) * 0x1p32f;
+    rates.omb2 = float(k.omb2) * 0x1p32f;
+    rates.root = float(k.root) * 0x1p-16f;
+    rates.eps = fmaxf(float(k.eps), 0x1p-126f);  // which a quotient by it needs
     rates.step = rates.lr / k.bc1;
     if (T.grad_dtype == ZS_F32) step_any<true, F32>(T, g, k, rates, key, from);
     else if (T.grad_dtype == ZS_BF16) step_any<true, Bf16>(T, g, k, rates, key, from);
