@@ -616,7 +616,7 @@ int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const 
  * AdamW over many tensors at once: what Muon leaves, or whole models.  Each
  * tensor has its own length, weight decay and learning-rate factor, gradients of
  * its own type, and moments in 32 or in 8 bits.  One launch takes up to 440
- * tensors (further ones follow in launches of their own).
+ * tensors of a kind of moments (further ones follow in launches of their own).
  *
  * A plan of the tensors is filled on the host, and copied to device memory by the
  * caller, once; the calls take both copies.  They queue kernel launches only, so
@@ -656,8 +656,8 @@ int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const 
  * has no finite scale from then on.  All zeros are the state at the start. */
 #define ZS_ADAMW_BLOCK 256
 #define ZS_ADAMW_MAX_TENSORS (INT64_C(1) << 20)
-#define ZS_ADAMW_MAX_ELEMENTS (INT64_C(1) << 34) /* of a tensor; all together
-                                     take at most 2^23 - 1 chunks of 4096 */
+#define ZS_ADAMW_MAX_ELEMENTS (INT64_C(1) << 33) /* of a tensor; of all, 2^23 - 1
+                                     chunks of 2048, of which each has its own */
 typedef enum zs_state { ZS_STATE_32 = 0, ZS_STATE_8 = 1 } zs_state;
 
 /* A tensor.  All arrays are flat and contiguous, aligned to their elements; *_out

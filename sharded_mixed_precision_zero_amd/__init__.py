@@ -25,7 +25,7 @@ ZS_ORTHO_MAX_STEPS = 32
 ZS_NORM_LAYER, ZS_NORM_RMS = 0, 1
 ZS_GATE_NONE, ZS_GATE_COLUMN, ZS_GATE_SIGMOID = 0, 1, 2
 ZS_BLOCKNORM_MAX_COLS = 16384
-ZS_ADAMW_BLOCK, ZS_ADAMW_MAX_TENSORS, ZS_ADAMW_MAX_ELEMENTS = 256, 1 << 20, 1 << 34
+ZS_ADAMW_BLOCK, ZS_ADAMW_MAX_TENSORS, ZS_ADAMW_MAX_ELEMENTS = 256, 1 << 20, 1 << 33
 ZS_STATE_32, ZS_STATE_8 = 0, 1
 ZS_EMBEDDING_MAX_TOKENS, ZS_EMBEDDING_MAX_VOCAB = 1 << 27, (1 << 31) - 1
 # how a call's work is split into kernel launches (zero_shard.h)

@@ -2,10 +2,12 @@
 // in 32 or in 8 bits, and the sum of squares that clips it, on MI355X (gfx950)
 // (declarations and the contract: include/zero_shard.h).
 //
-// One launch takes every tensor: the tensors are cut into chunks of kChunk
-// elements, a workgroup takes one, and a table in device memory names each
-// chunk's tensor.  The gradients, which a training program allocates anew, come as
-// kernel arguments, up to kGrads of them a launch.
+// One launch takes all tensors of a kind of state: they are cut into chunks, a
+// workgroup takes one, and a table in device memory names each chunk's tensor.  The
+// gradients, which a training program allocates anew, come as kernel arguments,
+// up to kGrads of them a launch.  The kinds have a launch each because the
+// registers of one (binary64 in the shard step's order) would leave the other too few
+// waves (163.84M elements in 8 bits: ONEUS in one launch, TWOUS in its own).
 //
 // The step is HBM-bound: 28 bytes an element with a 16-bit gradient and copy and
 // a 32-bit state, 16.06 with an 8-bit one.  A wave takes 256 elements at a time,
@@ -35,11 +37,9 @@ using namespace zs_dev;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBlock = ZS_ADAMW_BLOCK;  // elements that share a scale: a wave's
-#ifndef KR
-#define KR 4
-#endif
-constexpr int kRounds = KR;              // blocks of a wave
+constexpr int kRounds = 2;              // blocks of a wave, in flight together
 constexpr int64_t kChunk = int64_t(kBlock) * kWaves * kRounds;
+constexpr int kNormChunks = 4;          // chunks of a wave of the norm
 constexpr int kGrads = 440;             // a launch's gradients: 3.4 KiB of arguments
 constexpr uint64_t kMagic = 0x31776d6164617a73;  // "szadamw1"
 
@@ -62,7 +62,7 @@ static_assert(sizeof(Tensor) == 128, "a tensor of the plan");
 struct Header {
   uint64_t magic;
   int64_t count, chunks, bytes;
-  int64_t map, partials;  // offsets: the chunks' tensors (int32), their sums of squares (double)
+  int64_t map, partials;  // offsets: the chunks' tensors (int32), sums of squares (double)
   int64_t pad[2];
 };
 static_assert(sizeof(Header) == 64, "the plan's header");
@@ -90,9 +90,9 @@ struct StepArgs {
 struct NormArgs {
   const Tensor *tensors;
   const int32_t *map;
-  int64_t chunk0;
+  int64_t chunk0, chunks;  // this launch's
   int32_t tensor0;
-  double *partials;  // of all chunks
+  double *partials;        // a workgroup's each, of this launch
 };
 
 // The plan's addresses are all of global memory, which the compiler cannot see
@@ -102,10 +102,24 @@ template <class T>
 __device__ __forceinline__ const ZS_GLOBAL T *global(const void *p, int64_t i) {
   return (const ZS_GLOBAL T *)(uintptr_t(p) + i * int64_t(sizeof(T)));
 }
-template <class T>
-__device__ __forceinline__ ZS_GLOBAL T *global(void *p, int64_t i) {
-  return (ZS_GLOBAL T *)(uintptr_t(p) + i * int64_t(sizeof(T)));
-}
+
+// Where a lane is in its tensor: element `from`, the same for the workgroup, and
+// `at` behind it, which an access adds by itself.  `left`: elements from there on.
+struct Place {
+  int64_t from;
+  unsigned at;
+  int64_t left;
+  template <class T>
+  __device__ __forceinline__ const ZS_GLOBAL T *of(const void *p, unsigned e = 0) const {
+    return (const ZS_GLOBAL T *)((const ZS_GLOBAL char *)(uintptr_t(p) + from * int64_t(sizeof(T))) +
+                                 (at + e) * unsigned(sizeof(T)));
+  }
+  template <class T>
+  __device__ __forceinline__ ZS_GLOBAL T *of(void *p, unsigned e = 0) const {
+    return (ZS_GLOBAL T *)((ZS_GLOBAL char *)(uintptr_t(p) + from * int64_t(sizeof(T))) +
+                           (at + e) * unsigned(sizeof(T)));
+  }
+};
 
 // Four consecutive elements of any alignment.  They are touched once a step and
 // go past the caches.
@@ -115,22 +129,22 @@ struct Four {
   V v;
   // the first `left` of them where that may be fewer, zeros behind
   template <bool TAIL>
-  __device__ __forceinline__ void get(const void *p, int64_t i, int64_t left) {
-    if (!TAIL || left >= 4) {
-      v = __builtin_nontemporal_load((const ZS_GLOBAL V *)global<T>(p, i));
+  __device__ __forceinline__ void get(const void *p, const Place &i) {
+    if (!TAIL || i.left >= 4) {
+      v = __builtin_nontemporal_load((const ZS_GLOBAL V *)i.of<T>(p));
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = e < left ? *global<T>(p, i + e) : T(0);
+      for (int e = 0; e < 4; ++e) v[e] = e < i.left ? *i.of<T>(p, e) : T(0);
     }
   }
   template <bool TAIL>
-  __device__ __forceinline__ void put(void *p, int64_t i, int64_t left) const {
-    if (!TAIL || left >= 4) {
-      __builtin_nontemporal_store(v, (ZS_GLOBAL V *)global<T>(p, i));
+  __device__ __forceinline__ void put(void *p, const Place &i) const {
+    if (!TAIL || i.left >= 4) {
+      __builtin_nontemporal_store(v, (ZS_GLOBAL V *)i.of<T>(p));
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (e < left) *global<T>(p, i + e) = v[e];
+        if (e < i.left) *i.of<T>(p, e) = v[e];
     }
   }
 };
@@ -186,37 +200,37 @@ struct Lane {
 };
 
 template <bool EIGHT, bool TAIL>
-__device__ __forceinline__ void load_state(const Tensor &T, Lane &s, int64_t i, int64_t left) {
-  s.w.template get<TAIL>(T.master_in, i, left);
+__device__ __forceinline__ void load_state(const Tensor &T, Lane &s, const Place &i) {
+  s.w.template get<TAIL>(T.master_in, i);
   if constexpr (EIGHT) {
     using Word = unsigned __attribute__((aligned(1)));
-    if (!TAIL || left >= 4) {
-      s.m8 = __builtin_nontemporal_load((const ZS_GLOBAL Word *)global<uint8_t>(T.m_in, i));
-      s.v8 = __builtin_nontemporal_load((const ZS_GLOBAL Word *)global<uint8_t>(T.v_in, i));
+    if (!TAIL || i.left >= 4) {
+      s.m8 = __builtin_nontemporal_load((const ZS_GLOBAL Word *)i.of<uint8_t>(T.m_in));
+      s.v8 = __builtin_nontemporal_load((const ZS_GLOBAL Word *)i.of<uint8_t>(T.v_in));
     } else {
       s.m8 = s.v8 = 0;
 #pragma unroll
       for (int e = 0; e < 3; ++e)
-        if (e < left) {
-          s.m8 |= unsigned(*global<uint8_t>(T.m_in, i + e)) << (8 * e);
-          s.v8 |= unsigned(*global<uint8_t>(T.v_in, i + e)) << (8 * e);
+        if (e < i.left) {
+          s.m8 |= unsigned(*i.of<uint8_t>(T.m_in, e)) << (8 * e);
+          s.v8 |= unsigned(*i.of<uint8_t>(T.v_in, e)) << (8 * e);
         }
     }
     // one for the wave
-    const int64_t block = (i - int64_t(threadIdx.x & 63) * 4) / kBlock;
+    const int64_t block = i.from / kBlock + __builtin_amdgcn_readfirstlane(i.at / kBlock);
     const bool in = !TAIL || block * kBlock < T.n;
     s.ms = in ? *global<float>(T.m_scale_in, block) : 0.0f;
     s.vs = in ? *global<float>(T.v_scale_in, block) : 0.0f;
   } else {
-    s.m32.template get<TAIL>(T.m_in, i, left);
-    s.v32.template get<TAIL>(T.v_in, i, left);
+    s.m32.template get<TAIL>(T.m_in, i);
+    s.v32.template get<TAIL>(T.v_in, i);
   }
 }
 
 template <class TG, bool TAIL>
-__device__ __forceinline__ void load_grad(const void *g, Lane &s, int64_t i, int64_t left) {
-  if constexpr (std::is_same_v<TG, F32>) s.g32.template get<TAIL>(g, i, left);
-  else s.g16.template get<TAIL>(g, i, left);
+__device__ __forceinline__ void load_grad(const void *g, Lane &s, const Place &i) {
+  if constexpr (std::is_same_v<TG, F32>) s.g32.template get<TAIL>(g, i);
+  else s.g16.template get<TAIL>(g, i);
 }
 
 template <class TG>
@@ -235,28 +249,27 @@ struct Rates {
 };
 
 template <class T, bool TAIL>
-__device__ __forceinline__ void put_copy(const Tensor &t, const Four<float> &w, int64_t i,
-                                         int64_t left) {
+__device__ __forceinline__ void put_copy(const Tensor &t, const Four<float> &w, const Place &i) {
   Four<uint16_t> p;
 #pragma unroll
   for (int e = 0; e < 4; ++e) p.v[e] = T::store(w.v[e]);
-  p.template put<TAIL>(t.param, i, left);
+  p.template put<TAIL>(t.param, i);
 }
 
 template <bool TAIL>
-__device__ __forceinline__ void put_weights(const Tensor &T, const Four<float> &w, int64_t i,
-                                            int64_t left) {
-  w.template put<TAIL>(T.master_out, i, left);
+__device__ __forceinline__ void put_weights(const Tensor &T, const Four<float> &w,
+                                            const Place &i) {
+  w.template put<TAIL>(T.master_out, i);
   if (!T.param) return;
-  if (T.param_dtype == ZS_BF16) put_copy<Bf16, TAIL>(T, w, i, left);
-  else put_copy<F16, TAIL>(T, w, i, left);
+  if (T.param_dtype == ZS_BF16) put_copy<Bf16, TAIL>(T, w, i);
+  else put_copy<F16, TAIL>(T, w, i);
 }
 
 // AdamW on a lane's four elements: binary64 from the binary32 state, one
 // rounding per stored value, in the shard step's order.
 template <class TG, bool TAIL>
 __device__ __forceinline__ void update32(const Tensor &T, const Consts &k, const Rates &rates,
-                                         Lane &s, int64_t i, int64_t left) {
+                                         Lane &s, const Place &i) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const double g = rates.coef * double(grad_of<TG>(s, e));
@@ -270,9 +283,9 @@ __device__ __forceinline__ void update32(const Tensor &T, const Consts &k, const
     s.m32.v[e] = float(m1);
     s.v32.v[e] = float(v1);
   }
-  put_weights<TAIL>(T, s.w, i, left);
-  s.m32.template put<TAIL>(T.m_out, i, left);
-  s.v32.template put<TAIL>(T.v_out, i, left);
+  put_weights<TAIL>(T, s.w, i);
+  s.m32.template put<TAIL>(T.m_out, i);
+  s.v32.template put<TAIL>(T.v_out, i);
 }
 
 // The same with a state in 8 bits.  The moments are binary32 numbers, which
@@ -282,7 +295,7 @@ __device__ __forceinline__ void update32(const Tensor &T, const Consts &k, const
 // 163.84M elements).  The weights are binary64 as above.
 template <class TG, bool TAIL>
 __device__ __forceinline__ void update8(const Tensor &T, const Rates &rates, uint32_t base,
-                                        Lane &s, int64_t i, int64_t left) {
+                                        Lane &s, const Place &i) {
   float m[4], r[4];
   unsigned mtop = 0, vtop = 0;
   using Two = float __attribute__((ext_vector_type(2)));
@@ -303,7 +316,7 @@ __device__ __forceinline__ void update8(const Tensor &T, const Rates &rates, uin
     mtop = larger(mtop, __float_as_uint(m[e]) & 0x7fffffffu);
     vtop = larger(vtop, __float_as_uint(r[e]) & 0x7fffffffu);
   }
-  put_weights<TAIL>(T, s.w, i, left);
+  put_weights<TAIL>(T, s.w, i);
   // Scales, and the factors that take magnitudes to [0, 256], m's in the wave's first
   // half, r's in the other.  Blocks of nothing but numbers below 2^-100 are zeros (NaN
   // is not below), so that neither leaves binary32.
@@ -318,7 +331,7 @@ __device__ __forceinline__ void update8(const Tensor &T, const Rates &rates, uin
   unsigned mw = 0, vw = 0;
   const auto encode = [&](auto place) {
     constexpr int e = place.value;
-    const uint32_t h = mix(base + uint32_t(i + e));
+    const uint32_t h = mix(base + uint32_t(i.from) + i.at + unsigned(e));
     const float a = __builtin_amdgcn_fmed3f(m[e] * minv, -256.0f, 256.0f);
     // a root that is there stays above the least number
     const float b = __builtin_amdgcn_fmed3f(r[e] * vinv, r[e] > 0.0f ? 0x1p-9f : 0.0f, 256.0f);
@@ -329,40 +342,43 @@ __device__ __forceinline__ void update8(const Tensor &T, const Rates &rates, uin
   encode(std::integral_constant<int, 1>{});
   encode(std::integral_constant<int, 2>{});
   encode(std::integral_constant<int, 3>{});
-  if (!TAIL || left >= 4) {
+  if (!TAIL || i.left >= 4) {
     using Word = unsigned __attribute__((aligned(1)));
-    __builtin_nontemporal_store(mw, (ZS_GLOBAL Word *)global<uint8_t>(T.m_out, i));
-    __builtin_nontemporal_store(vw, (ZS_GLOBAL Word *)global<uint8_t>(T.v_out, i));
+    __builtin_nontemporal_store(mw, (ZS_GLOBAL Word *)i.of<uint8_t>(T.m_out));
+    __builtin_nontemporal_store(vw, (ZS_GLOBAL Word *)i.of<uint8_t>(T.v_out));
   } else {
 #pragma unroll
     for (int e = 0; e < 3; ++e)
-      if (e < left) {
-        *global<uint8_t>(T.m_out, i + e) = uint8_t(mw >> (8 * e));
-        *global<uint8_t>(T.v_out, i + e) = uint8_t(vw >> (8 * e));
+      if (e < i.left) {
+        *i.of<uint8_t>(T.m_out, e) = uint8_t(mw >> (8 * e));
+        *i.of<uint8_t>(T.v_out, e) = uint8_t(vw >> (8 * e));
       }
   }
-  if ((lane == 0 || lane == 32) && i - lane * 4 < T.n)
-    *global<float>(lane ? T.v_scale_out : T.m_scale_out, i / kBlock) = scale;
+  const int64_t block = i.from / kBlock + __builtin_amdgcn_readfirstlane(i.at / kBlock);
+  if ((lane == 0 || lane == 32) && (!TAIL || block * kBlock < T.n))
+    Place{block, 0, 1}.of<float>(lane ? T.v_scale_out : T.m_scale_out)[0] = scale;
 }
 
 template <bool EIGHT, class TG, bool TAIL>
 __device__ __forceinline__ void step_chunk(const Tensor &T, const void *g, const Consts &k,
                                            const Rates &rates, uint32_t key, int64_t from) {
-  const int64_t i0 = from + int64_t(threadIdx.x >> 6) * (kBlock * kRounds) + (threadIdx.x & 63) * 4;
+  const unsigned at = (threadIdx.x >> 6) * (kBlock * kRounds) + (threadIdx.x & 63) * 4;
   const uint32_t base = mix(key + 0x9e3779b9u * uint32_t(T.number + 1)) +
                         mix(uint32_t(uint64_t(from) >> 32)) * 0x9e3779b9u;
+  const auto place = [&](int r) {
+    const unsigned i = at + unsigned(r * kBlock);
+    return Place{from, i, T.n - from - int64_t(i)};
+  };
   Lane s[kRounds];
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
-    const int64_t i = i0 + r * kBlock;
-    load_state<EIGHT, TAIL>(T, s[r], i, T.n - i);
-    load_grad<TG, TAIL>(g, s[r], i, T.n - i);
+    load_state<EIGHT, TAIL>(T, s[r], place(r));
+    load_grad<TG, TAIL>(g, s[r], place(r));
   }
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
-    const int64_t i = i0 + r * kBlock;
-    if constexpr (EIGHT) update8<TG, TAIL>(T, rates, base, s[r], i, T.n - i);
-    else update32<TG, TAIL>(T, k, rates, s[r], i, T.n - i);
+    if constexpr (EIGHT) update8<TG, TAIL>(T, rates, base, s[r], place(r));
+    else update32<TG, TAIL>(T, k, rates, s[r], place(r));
   }
 }
 
@@ -373,7 +389,9 @@ __device__ __forceinline__ void step_any(const Tensor &T, const void *g, const C
   else step_chunk<EIGHT, TG, false>(T, g, k, rates, key, from);
 }
 
-__global__ void __launch_bounds__(kThreads) adamw_step_kernel(const StepArgs A, const Grads G) {
+template <bool EIGHT>
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(6)))
+    adamw_step_kernel(const StepArgs A, const Grads G) {
   const int64_t chunk = A.chunk0 + blockIdx.x;
   const int at = __builtin_amdgcn_readfirstlane(A.map[chunk]) - A.tensor0;
   const Tensor &T = A.tensors[at];
@@ -391,8 +409,7 @@ __global__ void __launch_bounds__(kThreads) adamw_step_kernel(const StepArgs A, 
   rates.coef = A.sumsq ? clip_coef(*A.sumsq, A.max_norm) : 1.0;
   rates.lr = k.lr * double(T.lr_scale);
   rates.decay = rates.lr * double(T.weight_decay);
-  const int64_t from = (chunk - T.chunk0) * kChunk;
-  if (T.state == ZS_STATE_8) {
+  if constexpr (EIGHT) {
     rates.coef32 = float(rates.coef);
     rates.b1 = float(k.b1);
     rates.omb1 = float(k.omb1);
@@ -401,56 +418,82 @@ __global__ void __launch_bounds__(kThreads) adamw_step_kernel(const StepArgs A, 
     rates.root = float(k.root) * 0x1p-16f;
     rates.eps = fmaxf(float(k.eps), 0x1p-126f);  // which a quotient by it needs
     rates.step = rates.lr / k.bc1;
-    if (T.grad_dtype == ZS_F32) step_any<true, F32>(T, g, k, rates, key, from);
-    else if (T.grad_dtype == ZS_BF16) step_any<true, Bf16>(T, g, k, rates, key, from);
-    else step_any<true, F16>(T, g, k, rates, key, from);
-  } else {
-    if (T.grad_dtype == ZS_F32) step_any<false, F32>(T, g, k, rates, key, from);
-    else if (T.grad_dtype == ZS_BF16) step_any<false, Bf16>(T, g, k, rates, key, from);
-    else step_any<false, F16>(T, g, k, rates, key, from);
   }
+  const int64_t from = (chunk - T.chunk0) * kChunk;
+  if (T.grad_dtype == ZS_F32) step_any<EIGHT, F32>(T, g, k, rates, key, from);
+  else if (T.grad_dtype == ZS_BF16) step_any<EIGHT, Bf16>(T, g, k, rates, key, from);
+  else step_any<EIGHT, F16>(T, g, k, rates, key, from);
 }
 
-// A chunk's sum of squares (binary64): a lane's elements in order, a
-// butterfly over the wave, the waves in order.
+// A lane's part of the sum of squares (binary64) of elements [from, n): sixteen bytes
+// at a time, 64 lanes side by side, up to 16 of them in flight.
 template <class TG>
-__device__ __forceinline__ double chunk_squares(const Tensor &T, const void *g, int64_t from) {
-  const int64_t i0 = from + int64_t(threadIdx.x >> 6) * (kBlock * kRounds) + (threadIdx.x & 63) * 4;
-  Lane s[kRounds];
-#pragma unroll
-  for (int r = 0; r < kRounds; ++r)
-    load_grad<TG, true>(g, s[r], i0 + r * kBlock, T.n - i0 - r * kBlock);
+__device__ __forceinline__ double squares(const void *g, int64_t from, int64_t n) {
+  using raw = typename TG::raw;
+  constexpr int kVec = 16 / sizeof(raw), kLoads = 16;
+  using V = unsigned __attribute__((ext_vector_type(4), aligned(sizeof(raw))));
   double sum = 0.0;
+  for (int64_t i0 = from + (threadIdx.x & 63) * kVec; i0 < n; i0 += kLoads * 64 * kVec) {
+    V v[kLoads];
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r)
+    for (int r = 0; r < kLoads; ++r) {
+      const int64_t i = i0 + r * (64 * kVec);
+      v[r] = V{0, 0, 0, 0};
+      if (i + kVec <= n) {
+        v[r] = __builtin_nontemporal_load((const ZS_GLOBAL V *)global<raw>(g, i));
+      } else if (i < n) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const double x = double(grad_of<TG>(s[r], e));
-      sum += x * x;
+        for (int e = 0; e < kVec; ++e)
+          if (i + e < n) {
+            if constexpr (sizeof(raw) == 4) v[r][e] = __float_as_uint(*global<raw>(g, i + e));
+            else v[r][e / 2] |= unsigned(*global<raw>(g, i + e)) << (e % 2 * 16);
+          }
+      }
     }
+#pragma unroll
+    for (int r = 0; r < kLoads; ++r)
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        float x;
+        if constexpr (sizeof(raw) == 4) x = __uint_as_float(v[r][e]);
+        else x = TG::load(raw(v[r][e / 2] >> (e % 2 * 16)));
+        sum += double(x) * double(x);
+      }
+  }
   return sum;
 }
 
+// A wave takes kNormChunks chunks, those of one tensor together (as one at a time:
+// 88 us for 56 over 163.84M bf16 gradients); its lanes' sums, a butterfly over them,
+// the waves in order.
 __global__ void __launch_bounds__(kThreads) adamw_norm_kernel(const NormArgs A, const Grads G) {
   __shared__ double sums[kWaves];
-  const int64_t chunk = A.chunk0 + blockIdx.x;
-  const int at = __builtin_amdgcn_readfirstlane(A.map[chunk]) - A.tensor0;
-  const Tensor &T = A.tensors[at];
-  const int64_t from = (chunk - T.chunk0) * kChunk;
-  double sum = T.grad_dtype == ZS_F32    ? chunk_squares<F32>(T, G.p[at], from)
-               : T.grad_dtype == ZS_BF16 ? chunk_squares<Bf16>(T, G.p[at], from)
-                                         : chunk_squares<F16>(T, G.p[at], from);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t chunk = (int64_t(blockIdx.x) * kWaves + wave) * kNormChunks;
+  const int64_t end = chunk + kNormChunks < A.chunks ? chunk + kNormChunks : A.chunks;
+  double sum = 0.0;
+  while (chunk < end) {
+    const int at = __builtin_amdgcn_readfirstlane(A.map[A.chunk0 + chunk]) - A.tensor0;
+    const Tensor &T = A.tensors[at];
+    const int64_t first = A.chunk0 + chunk - T.chunk0, left = (T.n + kChunk - 1) / kChunk - first;
+    const int64_t take = left < end - chunk ? left : end - chunk;
+    const int64_t from = first * kChunk, to = from + take * kChunk, n = T.n < to ? T.n : to;
+    if (T.grad_dtype == ZS_F32) sum += squares<F32>(G.p[at], from, n);
+    else if (T.grad_dtype == ZS_BF16) sum += squares<Bf16>(G.p[at], from, n);
+    else sum += squares<F16>(G.p[at], from, n);
+    chunk += take;
+  }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = sum;
+  if ((threadIdx.x & 63) == 0) sums[wave] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < kWaves; ++w) sum += sums[w];
-    A.partials[chunk] = sum;
+    A.partials[blockIdx.x] = sum;
   }
 }
 
-// The chunks' sums, each thread a strided run of them, then a tree.
+// The workgroups' sums, each thread a strided run of them, then a tree.
 constexpr int kFinalThreads = 1024;
 __global__ void __launch_bounds__(kFinalThreads) adamw_total_kernel(const double *partials,
                                                                     int64_t n, double *out) {
@@ -573,20 +616,23 @@ int call_ok(const zs_adamw_desc *d, const void *plan, const void *plan_dev,
   return ZS_OK;
 }
 
-// One launch for every kGrads tensors that have elements among them.
+// Each kGrads tensors: their first chunk, how many are of 8-bit states (which
+// come first among them) and how many of others.
 template <class F>
-int by_launch(const void *plan, const void *const *grads, F f) {
+int by_group(const void *plan, const void *const *grads, F f) {
   const Header *h = static_cast<const Header *>(plan);
   const Tensor *t = tensors_of(plan);
+  int64_t chunk = 0;
   for (int64_t k = 0; k < h->count; k += kGrads) {
     const int64_t to = k + kGrads < h->count ? k + kGrads : h->count;
-    const int64_t from_chunk = t[k].chunk0;
-    const int64_t chunks = (to < h->count ? t[to].chunk0 : h->chunks) - from_chunk;
-    if (chunks == 0) continue;
     Grads G;
-    for (int64_t j = k; j < to; ++j) G.p[j - k] = grads[j];
-    f(k, from_chunk, unsigned(chunks), G);
-    if (const int rc = launched()) return rc;
+    int64_t chunks[2] = {0, 0};
+    for (int64_t j = k; j < to; ++j) {
+      G.p[j - k] = grads[j];
+      chunks[t[j].state == ZS_STATE_8 ? 0 : 1] += chunks_of(t[j].n);
+    }
+    if (const int rc = f(k, chunk, chunks[0], chunks[1], G)) return rc;
+    chunk += chunks[0] + chunks[1];
   }
   return ZS_OK;
 }
@@ -607,13 +653,20 @@ int step(const zs_adamw_desc *d, const void *plan, void *plan_dev, const void *c
     k.root = 1.0 / std::sqrt(k.bc2);
   }
   const char *dev = static_cast<const char *>(plan_dev);
-  return by_launch(plan, grads, [&](int64_t tensor0, int64_t chunk0, unsigned chunks,
-                                    const Grads &G) {
-    const StepArgs A{tensors_of(plan_dev) + tensor0,
-                     reinterpret_cast<const int32_t *>(dev + h->map), chunk0, int32_t(tensor0), key,
-                     k, dyn, sumsq, double(d->max_norm)};
-    hipLaunchKernelGGL(adamw_step_kernel, dim3(chunks), dim3(kThreads), 0,
-                       static_cast<hipStream_t>(d->stream), A, G);
+  const hipStream_t st = static_cast<hipStream_t>(d->stream);
+  return by_group(plan, grads, [&](int64_t tensor0, int64_t chunk0, int64_t eights, int64_t others,
+                                   const Grads &G) {
+    StepArgs A{tensors_of(plan_dev) + tensor0,
+               reinterpret_cast<const int32_t *>(dev + h->map), chunk0, int32_t(tensor0), key,
+               k, dyn, sumsq, double(d->max_norm)};
+    if (eights)
+      hipLaunchKernelGGL(adamw_step_kernel<true>, dim3(unsigned(eights)), dim3(kThreads), 0, st, A,
+                         G);
+    A.chunk0 += eights;
+    if (others)
+      hipLaunchKernelGGL(adamw_step_kernel<false>, dim3(unsigned(others)), dim3(kThreads), 0, st,
+                         A, G);
+    return launched();
   });
 }
 
@@ -646,12 +699,18 @@ int zero_shard_adamw_plan(const zs_adamw_desc *d, const zs_adamw_tensor *tensors
   Tensor *out = reinterpret_cast<Tensor *>(at + sizeof h);
   int32_t *map = reinterpret_cast<int32_t *>(at + l.map);
   int64_t chunk = 0;
-  for (int64_t k = 0; k < d->count; ++k) {
-    const zs_adamw_tensor &t = tensors[k];
-    out[k] = Tensor{t.n, chunk, t.master_in, t.master_out, t.m_in, t.v_in, t.m_out, t.v_out,
-                    t.m_scale_in, t.v_scale_in, t.m_scale_out, t.v_scale_out, t.param_out,
-                    t.weight_decay, t.lr_scale, t.state, t.grad_dtype, t.param_dtype, int32_t(k)};
-    for (int64_t c = chunks_of(t.n); c > 0; --c) map[chunk++] = int32_t(k);
+  for (int64_t k = 0; k < d->count; k += kGrads) {
+    const int64_t to = k + kGrads < d->count ? k + kGrads : d->count;
+    for (const int32_t state : {ZS_STATE_8, ZS_STATE_32})  // see by_group
+      for (int64_t j = k; j < to; ++j) {
+        const zs_adamw_tensor &t = tensors[j];
+        if (t.state != state) continue;
+        out[j] = Tensor{t.n, chunk, t.master_in, t.master_out, t.m_in, t.v_in, t.m_out, t.v_out,
+                        t.m_scale_in, t.v_scale_in, t.m_scale_out, t.v_scale_out, t.param_out,
+                        t.weight_decay, t.lr_scale, t.state, t.grad_dtype, t.param_dtype,
+                        int32_t(j)};
+        for (int64_t c = chunks_of(t.n); c > 0; --c) map[chunk++] = int32_t(j);
+      }
   }
   return ZS_OK;
 }
@@ -666,15 +725,21 @@ int zero_shard_adamw_gnorm(const zs_adamw_desc *d, const void *plan, void *plan_
   char *dev = static_cast<char *>(plan_dev);
   double *partials = reinterpret_cast<double *>(dev + h->partials);
   const hipStream_t st = static_cast<hipStream_t>(d->stream);
-  if (const int rc = by_launch(plan, grads, [&](int64_t tensor0, int64_t chunk0, unsigned chunks,
-                                                const Grads &G) {
+  int64_t sums = 0;
+  if (const int rc = by_group(plan, grads, [&](int64_t tensor0, int64_t chunk0, int64_t eights,
+                                               int64_t others, const Grads &G) {
+        const int64_t chunks = eights + others, each = kWaves * kNormChunks;
+        const int64_t blocks = (chunks + each - 1) / each;
+        if (blocks == 0) return int(ZS_OK);
         const NormArgs A{tensors_of(plan_dev) + tensor0,
-                         reinterpret_cast<const int32_t *>(dev + h->map), chunk0,
-                         int32_t(tensor0), partials};
-        hipLaunchKernelGGL(adamw_norm_kernel, dim3(chunks), dim3(kThreads), 0, st, A, G);
+                         reinterpret_cast<const int32_t *>(dev + h->map), chunk0, chunks,
+                         int32_t(tensor0), partials + sums};
+        hipLaunchKernelGGL(adamw_norm_kernel, dim3(unsigned(blocks)), dim3(kThreads), 0, st, A, G);
+        sums += blocks;
+        return launched();
       }))
     return rc;
-  hipLaunchKernelGGL(adamw_total_kernel, dim3(1), dim3(kFinalThreads), 0, st, partials, h->chunks,
+  hipLaunchKernelGGL(adamw_total_kernel, dim3(1), dim3(kFinalThreads), 0, st, partials, sums,
                      sumsq_dev);
   return launched();
 }
