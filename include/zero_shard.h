@@ -656,8 +656,8 @@ int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const 
  * has no finite scale from then on.  All zeros are the state at the start. */
 #define ZS_ADAMW_BLOCK 256
 #define ZS_ADAMW_MAX_TENSORS (INT64_C(1) << 20)
-#define ZS_ADAMW_MAX_ELEMENTS (INT64_C(1) << 33) /* of a tensor; of all, 2^23 - 1
-                                     chunks of 2048, of which each has its own */
+#define ZS_ADAMW_MAX_ELEMENTS (INT64_C(1) << 33) /* of a tensor; of all, 2^24 - 1
+                                     chunks of 1024 (32 bits) or 2048 (8) */
 typedef enum zs_state { ZS_STATE_32 = 0, ZS_STATE_8 = 1 } zs_state;
 
 /* A tensor.  All arrays are flat and contiguous, aligned to their elements; *_out

@@ -7,7 +7,7 @@
 // gradients, which a training program allocates anew, come as kernel arguments,
 // up to kGrads of them a launch.  The kinds have a launch each because the
 // registers of one (binary64 in the shard step's order) would leave the other too few
-// waves (163.84M elements in 8 bits: ONEUS in one launch, TWOUS in its own).
+// waves (163.84M elements in 8 bits: 543 us in one launch, 485 in its own).
 //
 // The step is HBM-bound: 28 bytes an element with a 16-bit gradient and copy and
 // a 32-bit state, 16.06 with an 8-bit one.  A wave takes 256 elements at a time,
@@ -37,9 +37,18 @@ using namespace zs_dev;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBlock = ZS_ADAMW_BLOCK;  // elements that share a scale: a wave's
-constexpr int kRounds = 2;              // blocks of a wave, in flight together
-constexpr int64_t kChunk = int64_t(kBlock) * kWaves * kRounds;
-constexpr int kNormChunks = 4;          // chunks of a wave of the norm
+// Blocks of a wave, in flight together, and elements of a workgroup.  A 32-bit state
+// has bytes enough in flight with one block, and short chains of work a wave (160
+// tensors of 5120: 6.0 us for 8.4 with two; 163.84M elements 778 for 811); an 8-bit
+// one is a little faster with two (513 for 527).
+template <bool EIGHT>
+constexpr int kRounds = EIGHT ? 2 : 1;
+template <bool EIGHT>
+constexpr int64_t kChunk = int64_t(kBlock) * kWaves * kRounds<EIGHT>;
+// Chunks of a wave of the norm: 8, or 1 where the waves would be few (160 tensors of
+// 5120: 10 us for 14).
+constexpr int kNormChunks = 8;
+constexpr int64_t kFewChunks = 8192;
 constexpr int kGrads = 440;             // a launch's gradients: 3.4 KiB of arguments
 constexpr uint64_t kMagic = 0x31776d6164617a73;  // "szadamw1"
 
@@ -91,7 +100,7 @@ struct NormArgs {
   const Tensor *tensors;
   const int32_t *map;
   int64_t chunk0, chunks;  // this launch's
-  int32_t tensor0;
+  int32_t tensor0, each;   // each: chunks of a wave
   double *partials;        // a workgroup's each, of this launch
 };
 
@@ -362,21 +371,21 @@ __device__ __forceinline__ void update8(const Tensor &T, const Rates &rates, uin
 template <bool EIGHT, class TG, bool TAIL>
 __device__ __forceinline__ void step_chunk(const Tensor &T, const void *g, const Consts &k,
                                            const Rates &rates, uint32_t key, int64_t from) {
-  const unsigned at = (threadIdx.x >> 6) * (kBlock * kRounds) + (threadIdx.x & 63) * 4;
+  const unsigned at = (threadIdx.x >> 6) * (kBlock * kRounds<EIGHT>) + (threadIdx.x & 63) * 4;
   const uint32_t base = mix(key + 0x9e3779b9u * uint32_t(T.number + 1)) +
                         mix(uint32_t(uint64_t(from) >> 32)) * 0x9e3779b9u;
   const auto place = [&](int r) {
     const unsigned i = at + unsigned(r * kBlock);
     return Place{from, i, T.n - from - int64_t(i)};
   };
-  Lane s[kRounds];
+  Lane s[kRounds<EIGHT>];
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
+  for (int r = 0; r < kRounds<EIGHT>; ++r) {
     load_state<EIGHT, TAIL>(T, s[r], place(r));
     load_grad<TG, TAIL>(g, s[r], place(r));
   }
 #pragma unroll
-  for (int r = 0; r < kRounds; ++r) {
+  for (int r = 0; r < kRounds<EIGHT>; ++r) {
     if constexpr (EIGHT) update8<TG, TAIL>(T, rates, base, s[r], place(r));
     else update32<TG, TAIL>(T, k, rates, s[r], place(r));
   }
@@ -385,7 +394,7 @@ __device__ __forceinline__ void step_chunk(const Tensor &T, const void *g, const
 template <bool EIGHT, class TG>
 __device__ __forceinline__ void step_any(const Tensor &T, const void *g, const Consts &k,
                                          const Rates &rates, uint32_t key, int64_t from) {
-  if (T.n - from < kChunk) step_chunk<EIGHT, TG, true>(T, g, k, rates, key, from);
+  if (T.n - from < kChunk<EIGHT>) step_chunk<EIGHT, TG, true>(T, g, k, rates, key, from);
   else step_chunk<EIGHT, TG, false>(T, g, k, rates, key, from);
 }
 
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(6
     rates.eps = fmaxf(float(k.eps), 0x1p-126f);  // which a quotient by it needs
     rates.step = rates.lr / k.bc1;
   }
-  const int64_t from = (chunk - T.chunk0) * kChunk;
+  const int64_t from = (chunk - T.chunk0) * kChunk<EIGHT>;
   if (T.grad_dtype == ZS_F32) step_any<EIGHT, F32>(T, g, k, rates, key, from);
   else if (T.grad_dtype == ZS_BF16) step_any<EIGHT, Bf16>(T, g, k, rates, key, from);
   else step_any<EIGHT, F16>(T, g, k, rates, key, from);
@@ -463,25 +472,25 @@ __device__ __forceinline__ double squares(const void *g, int64_t from, int64_t n
   return sum;
 }
 
-// A wave takes kNormChunks chunks, those of one tensor together (as one at a time:
-// 88 us for 56 over 163.84M bf16 gradients); its lanes' sums, a butterfly over them,
+// A wave takes A.each chunks, those of one tensor together (2048 elements at a
+// time: 88 us for 56 over 163.84M bf16 gradients); its lanes' sums, a butterfly over them,
 // the waves in order.
 __global__ void __launch_bounds__(kThreads) adamw_norm_kernel(const NormArgs A, const Grads G) {
   __shared__ double sums[kWaves];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int64_t chunk = (int64_t(blockIdx.x) * kWaves + wave) * kNormChunks;
-  const int64_t end = chunk + kNormChunks < A.chunks ? chunk + kNormChunks : A.chunks;
+  int64_t chunk = (int64_t(blockIdx.x) * kWaves + wave) * A.each;
+  const int64_t end = chunk + A.each < A.chunks ? chunk + A.each : A.chunks;
   double sum = 0.0;
   while (chunk < end) {
     const int at = __builtin_amdgcn_readfirstlane(A.map[A.chunk0 + chunk]) - A.tensor0;
     const Tensor &T = A.tensors[at];
-    const int64_t first = A.chunk0 + chunk - T.chunk0, left = (T.n + kChunk - 1) / kChunk - first;
-    const int64_t take = left < end - chunk ? left : end - chunk;
-    const int64_t from = first * kChunk, to = from + take * kChunk, n = T.n < to ? T.n : to;
+    const int64_t length = T.state == ZS_STATE_8 ? kChunk<true> : kChunk<false>;
+    const int64_t first = A.chunk0 + chunk - T.chunk0, from = first * length;
+    const int64_t most = from + (end - chunk) * length, n = T.n < most ? T.n : most;
     if (T.grad_dtype == ZS_F32) sum += squares<F32>(G.p[at], from, n);
     else if (T.grad_dtype == ZS_BF16) sum += squares<Bf16>(G.p[at], from, n);
     else sum += squares<F16>(G.p[at], from, n);
-    chunk += take;
+    chunk += (n - from + length - 1) / length;
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
@@ -521,7 +530,10 @@ bool desc_ok(const zs_adamw_desc *d) {
 }
 
 int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
-int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
+int64_t chunks_of(int64_t n, int32_t state) {
+  const int64_t length = state == ZS_STATE_8 ? kChunk<true> : kChunk<false>;
+  return (n + length - 1) / length;
+}
 
 // One tensor's fields and pointers.
 int tensor_ok(const zs_adamw_tensor &t) {
@@ -582,9 +594,9 @@ struct Layout {
     if (!desc_ok(d) || (d->count && !t)) return;
     for (int64_t k = 0; k < d->count; ++k) {
       if (t[k].n < 0 || t[k].n > ZS_ADAMW_MAX_ELEMENTS) return;
-      chunks += chunks_of(t[k].n);
+      chunks += chunks_of(t[k].n, t[k].state);
     }
-    if (chunks > INT32_MAX / kThreads) return;  // a launch takes them all
+    if (chunks > int64_t(UINT32_MAX) / kThreads) return;  // a launch takes them all
     const auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
     map = up(int64_t(sizeof(Header)) + d->count * int64_t(sizeof(Tensor)));
     partials = map + up(chunks * 4);
@@ -629,7 +641,7 @@ int by_group(const void *plan, const void *const *grads, F f) {
     int64_t chunks[2] = {0, 0};
     for (int64_t j = k; j < to; ++j) {
       G.p[j - k] = grads[j];
-      chunks[t[j].state == ZS_STATE_8 ? 0 : 1] += chunks_of(t[j].n);
+      chunks[t[j].state == ZS_STATE_8 ? 0 : 1] += chunks_of(t[j].n, t[j].state);
     }
     if (const int rc = f(k, chunk, chunks[0], chunks[1], G)) return rc;
     chunk += chunks[0] + chunks[1];
@@ -709,7 +721,7 @@ int zero_shard_adamw_plan(const zs_adamw_desc *d, const zs_adamw_tensor *tensors
                         t.m_scale_in, t.v_scale_in, t.m_scale_out, t.v_scale_out, t.param_out,
                         t.weight_decay, t.lr_scale, t.state, t.grad_dtype, t.param_dtype,
                         int32_t(j)};
-        for (int64_t c = chunks_of(t.n); c > 0; --c) map[chunk++] = int32_t(j);
+        for (int64_t c = chunks_of(t.n, state); c > 0; --c) map[chunk++] = int32_t(j);
       }
   }
   return ZS_OK;
@@ -728,12 +740,12 @@ int zero_shard_adamw_gnorm(const zs_adamw_desc *d, const void *plan, void *plan_
   int64_t sums = 0;
   if (const int rc = by_group(plan, grads, [&](int64_t tensor0, int64_t chunk0, int64_t eights,
                                                int64_t others, const Grads &G) {
-        const int64_t chunks = eights + others, each = kWaves * kNormChunks;
-        const int64_t blocks = (chunks + each - 1) / each;
+        const int64_t chunks = eights + others, each = chunks <= kFewChunks ? 1 : kNormChunks;
+        const int64_t blocks = (chunks + kWaves * each - 1) / (kWaves * each);
         if (blocks == 0) return int(ZS_OK);
         const NormArgs A{tensors_of(plan_dev) + tensor0,
                          reinterpret_cast<const int32_t *>(dev + h->map), chunk0, chunks,
-                         int32_t(tensor0), partials + sums};
+                         int32_t(tensor0), int32_t(each), partials + sums};
         hipLaunchKernelGGL(adamw_norm_kernel, dim3(unsigned(blocks)), dim3(kThreads), 0, st, A, G);
         sums += blocks;
         return launched();
