@@ -575,10 +575,12 @@ int zero_shard_blocknorm_bwd(const zs_blocknorm_desc *d, const void *dy, const v
  * belong to other ranks, give rows of zeros and no gradient, so that the ranks'
  * outputs add up to the whole table's. */
 #define ZS_EMBEDDING_MAX_TOKENS (INT64_C(1) << 27)
-#define ZS_EMBEDDING_MAX_VOCAB INT64_C(0x7fffffff)
+#define ZS_EMBEDDING_MAX_VOCAB (INT64_C(1) << 30)
 typedef struct zs_embedding_desc {
-  int64_t tokens;      /* 0 .. ZS_EMBEDDING_MAX_TOKENS; tokens * cols < 2^34  */
-  int64_t vocab;       /* rows of the table, 1 .. ZS_EMBEDDING_MAX_VOCAB      */
+  int64_t tokens;      /* 0 .. ZS_EMBEDDING_MAX_TOKENS; below 2^34 elements,
+                          with cols counted as the multiple of 8 from it on    */
+  int64_t vocab;       /* rows of the table, 1 .. ZS_EMBEDDING_MAX_VOCAB;
+                          vocab * cols <= 2^37                                */
   int64_t cols;        /* 1 .. 2^20                                           */
   int64_t first;       /* the id of the table's first row; the last row's has to fit */
   int64_t padding;     /* an id whose tokens give no gradient                 */
@@ -605,8 +607,9 @@ int64_t zero_shard_embedding_workspace(const zs_embedding_desc *d);
 
 /* dtable[v] = scale sum dy[t] over the tokens t of row v, in binary32 and in the
  * order of t: runs of 32 tokens of the row each (8 up to 2048 tokens in all), the runs
- * then in order (four stretches of runs side by side); rounded once.  accumulate: dtable[v] + that, rounded
- * once; rows without tokens are left as they are.  Otherwise they become zeros.
+ * then in order (four stretches of runs side by side); rounded once.  accumulate:
+ * dtable[v] + that, rounded once; rows without tokens are left as they are.  Otherwise
+ * they become zeros.
  * dtable overlaps nothing; workspace: device, 256-byte aligned, at least
  * zero_shard_embedding_workspace(d) bytes.  Errors: as above. */
 int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const void *dy,
@@ -643,10 +646,10 @@ int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const 
  * Storing values x of a block (of m', or of r'):
  *   top = max |x|;  scale = top / 256
  *   y = |x| binary32(1 / scale), at most 256, and at least 2^-9 for an r' > 0, becomes
- *   an e4m3 number (with x's sign, a zero's too) by chance, the one below or above it in proportion to how near
- *   each is: above where the 2^20ths of its way from the one below to the one above,
- *   cut to a whole number, plus 16 d + 8 reach 2^20.  d is 16 bits of h (the lower ones
- *   for m, the upper ones for r):
+ *   an e4m3 number (with x's sign, a zero's too) by chance, the one below or above it
+ *   in proportion to how near each is: above where the 2^20ths of its way from the one
+ *   below to the one above, cut to a whole number, plus 16 d + 8 reach 2^20.  d is 16
+ *   bits of h (the lower ones for m, the upper ones for r):
  *   h = mix(mix(key + c (k + 1)) + c mix(i >> 32) + i), modulo 2^32, k the tensor's number,
  *   c = 0x9e3779b9, mix(x): x ^= x >> 16; x *= 0x6a09e667; x ^= x >> 15;
  *   x *= 0xbb67ae85; x ^= x >> 16

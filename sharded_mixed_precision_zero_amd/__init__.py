@@ -27,7 +27,7 @@ ZS_GATE_NONE, ZS_GATE_COLUMN, ZS_GATE_SIGMOID = 0, 1, 2
 ZS_BLOCKNORM_MAX_COLS = 16384
 ZS_ADAMW_BLOCK, ZS_ADAMW_MAX_TENSORS, ZS_ADAMW_MAX_ELEMENTS = 256, 1 << 20, 1 << 33
 ZS_STATE_32, ZS_STATE_8 = 0, 1
-ZS_EMBEDDING_MAX_TOKENS, ZS_EMBEDDING_MAX_VOCAB = 1 << 27, (1 << 31) - 1
+ZS_EMBEDDING_MAX_TOKENS, ZS_EMBEDDING_MAX_VOCAB = 1 << 27, 1 << 30
 # how a call's work is split into kernel launches (zero_shard.h)
 ZS_NORM_LAUNCH_LEN = 1 << 26
 ZS_WIDE_LAUNCH_LEN = 1 << 25
@@ -1115,7 +1115,8 @@ class ZeroEmbedding:
 
     @property
     def workspace(self):
-        """Of the backward pass, from its first call on."""
+        """Of the backward pass, from its first call on (or this property's first use,
+        which a program that captures its first backward pass makes before)."""
         if self._workspace is None:
             with torch.cuda.stream(self._stream):
                 self._workspace = torch.empty(self._workspace_bytes, device="cuda",

@@ -54,7 +54,6 @@ constexpr int kJoinWaves = 4;
 constexpr unsigned kWide = 48;    // pieces of eight columns from which a wave has one row's
 constexpr int kEach = 4;          // pieces of eight columns of a forward thread
 constexpr unsigned kNone = 0xffffffffu;  // sorts behind every row
-constexpr int64_t kMaxGrid = 0x7fffffff;
 
 struct Ids {
   const void *p;
@@ -549,6 +548,9 @@ bool desc_ok(const zs_embedding_desc *d) {
   if (d->first > INT64_MAX - (d->vocab - 1)) return false;  // its last id
   if (d->cols < 1 || d->cols > (INT64_C(1) << 20) || d->pad_set < 0 || d->pad_set > 1)
     return false;
+  // what the kernels count in 32 bits, and the threads that a launch takes
+  if (d->tokens * up(d->cols, 8) >= INT64_C(1) << 34) return false;
+  if (d->vocab * d->cols > INT64_C(1) << 37) return false;
   if (d->id_bytes != 4 && d->id_bytes != 8) return false;
   if (!dtype_size(d->dtype) || d->accumulate < 0 || d->accumulate > 1) return false;
   for (const int32_t t : {d->table_dtype, d->grad_dtype})
@@ -630,7 +632,6 @@ int zero_shard_embedding(const zs_embedding_desc *d, const void *ids, const void
   const FwdArgs A{ids_of(*d, ids), d->tokens, d->cols, ld(d->ld_table), ld(d->ld_y), table, y,
                   d->scale, per_of(*d)};
   const int64_t blocks = (A.tokens * A.per + kThreads * kEach - 1) / (kThreads * kEach);
-  if (blocks > kMaxGrid / (kThreads * kEach)) return ZS_EINVAL;
   if (const int rc = device_is_gfx950()) return rc;
   const bool even = rows_even(table, A.ld_table, tsize) && rows_even(y, A.ld_y, size);
   return by_type(d->dtype, d->table_dtype, [&](auto ty, auto tw) {
@@ -681,7 +682,6 @@ int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const 
   A.rows = int32_t((65536 + d->cols * gsize - 1) / (d->cols * gsize));
   if (A.rows > kThreads) A.rows = kThreads;
   const int64_t clear = d->accumulate ? 0 : (d->vocab + A.rows - 1) / A.rows;
-  if (A.sum_blocks + clear > kMaxGrid / kThreads) return ZS_EINVAL;
   if (const int rc = device_is_gfx950()) return rc;
   const hipStream_t st = static_cast<hipStream_t>(d->stream);
   char *ws = static_cast<char *>(workspace);

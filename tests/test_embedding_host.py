@@ -38,7 +38,7 @@ def _bwd(d, ids=P, dy=P, dtable=P, ws=P, size=1 << 40):
 
 BAD = [dict(tokens=-1), dict(tokens=Z.ZS_EMBEDDING_MAX_TOKENS + 1), dict(vocab=0),
        dict(vocab=Z.ZS_EMBEDDING_MAX_VOCAB + 1), dict(cols=0), dict(cols=(1 << 20) + 1),
-       dict(first=(1 << 63) - 49),
+       dict(first=(1 << 63) - 49), dict(tokens=1 << 27, cols=128), dict(vocab=1 << 30, cols=129),
        dict(id_bytes=2), dict(id_bytes=0), dict(dtype=3), dict(table_dtype=Z.ZS_F16),
        dict(grad_dtype=Z.ZS_F16), dict(dtype=Z.ZS_F32), dict(accumulate=2), dict(pad_set=-1),
        dict(scale=float("nan")), dict(scale=float("inf"))]
