@@ -611,7 +611,7 @@ int64_t zero_shard_embedding_workspace(const zs_embedding_desc *d);
  * dtable[v] + that, rounded once; rows without tokens are left as they are.  Otherwise
  * they become zeros.
  * dtable overlaps nothing; workspace: device, 256-byte aligned, at least
- * zero_shard_embedding_workspace(d) bytes.  Errors: as above. */
+ * zero_shard_embedding_workspace(d) bytes (NULL where that is 0).  Errors: as above. */
 int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const void *dy,
                              void *dtable, void *workspace, int64_t workspace_bytes);
 

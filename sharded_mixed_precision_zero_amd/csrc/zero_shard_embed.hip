@@ -20,6 +20,8 @@
 //          begins in, so that no piece does much more than its share however
 //          the tokens are distributed.
 //   join   the parts of those long rows, in order.
+//
+// A few tokens are one launch that sorts nothing (embed_few_kernel).
 
 #include <hip/hip_runtime.h>
 
@@ -47,6 +49,11 @@ constexpr int kRuns = 8;          // runs merged at a time
 // are what takes time (333 tokens: 16 us for 21), 32 where the parts' traffic counts.
 constexpr int kRun = 32, kShortRun = 8;
 constexpr int64_t kFew = 2048;
+// Tokens that are not sorted, and the workgroups up to which that pays: each looks through
+// all tokens (700 x 4096, 5600 of them: 13 us for 16; 512 x 8192, 8192 of them: 18 for
+// 18; 300 x 16384, 9600: 22 for 18).
+constexpr int kFewest = 1024;
+constexpr int64_t kFewestGroups = 6000;
 constexpr int kPiece = 8;         // tokens of a piece, and rows of dy in flight
 // Waves that share a long row's parts: most workgroups find no such row, so few
 // (65536 x 5120: 16 us with 4 waves, 24 with 8; one row of 8192 tokens 24 and 16).
@@ -251,6 +258,7 @@ struct SumArgs {
   unsigned waves;     // of a piece of tokens
   int64_t sum_blocks; // workgroups that sum; the others clear
   int32_t rows;       // that a workgroup clears
+  int32_t flat;       // 1: they are one stretch of whole sixteen bytes
 };
 
 // The first of keys[lo, hi) that is not below `key`, hi if none: eight looks side by
@@ -294,20 +302,32 @@ __device__ __forceinline__ void put_row(const SumArgs &A, unsigned row, unsigned
   w.template store<TAIL>(to, col, A.cols - col);
 }
 
-// Rows without tokens become zeros.
-template <class TG, bool TAIL>
-__device__ __forceinline__ void clear_rows(const SumArgs &A, int64_t block) {
+// Rows without tokens become zeros: A.rows of them from `block` times that on.
+// mark(row, rows, used) says which have some.  ONCE: past the caches, where dy streams
+// as well (8192 x 5120: 93 us for 98; with few tokens 14 us for 17 the other way).
+template <class TG, bool TAIL, bool ONCE, class F>
+__device__ __forceinline__ void clear_rows(const SumArgs &A, int64_t block, F mark) {
   __shared__ int used[kThreads];
   const int64_t r0 = block * A.rows;
   const int rows = int(A.vocab - r0 < A.rows ? A.vocab - r0 : A.rows);
-  if (int(threadIdx.x) < rows) {
-    const unsigned key = unsigned(r0 + threadIdx.x);
-    const int64_t at = first_not_below(A.keys, 0, A.tokens, key);
-    used[threadIdx.x] = at < A.tokens && A.keys[at] == key;
-  }
-  __syncthreads();
-  // in elements, or in sixteen bytes side by side
+  mark(r0, rows, used);
   using raw = typename TG::raw;
+  if (A.flat && !__syncthreads_or(int(threadIdx.x) < rows && used[threadIdx.x])) {
+    // one stretch of memory, from a multiple of sixteen bytes on
+    char *to = static_cast<char *>(A.out) + r0 * A.cols * int64_t(sizeof(raw));
+    const int64_t bytes = rows * A.cols * int64_t(sizeof(raw));
+#pragma unroll 4
+    for (int64_t i = threadIdx.x * 16; i + 16 <= bytes; i += kThreads * 16) {
+      if constexpr (ONCE)
+        __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, reinterpret_cast<u32x4 *>(to + i));
+      else
+        *reinterpret_cast<u32x4 *>(to + i) = u32x4{0, 0, 0, 0};
+    }
+    const int64_t rest = bytes / 16 * 16 + threadIdx.x * int64_t(sizeof(raw));
+    if (rest < bytes) *reinterpret_cast<raw *>(to + rest) = raw(0);
+    return;
+  }
+  // in elements, or in sixteen bytes side by side
   constexpr int64_t kUnit = TAIL ? 1 : 16 / sizeof(raw);
   const int64_t units = A.cols / kUnit;
   // `across` threads a row, several rows at a time where rows are short
@@ -319,9 +339,92 @@ __device__ __forceinline__ void clear_rows(const SumArgs &A, int64_t block) {
     raw *to = static_cast<raw *>(row_of<TG>(A.out, r0 + r, A.ld_out));
     for (int64_t c = threadIdx.x - sub * across; c < units; c += across) {
       if constexpr (TAIL) to[c] = raw(0);
-      else __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, reinterpret_cast<u32x4 *>(to) + c);
+      else if constexpr (ONCE)
+        __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, reinterpret_cast<u32x4 *>(to) + c);
+      else reinterpret_cast<u32x4 *>(to)[c] = u32x4{0, 0, 0, 0};
     }
   }
+}
+
+// A few tokens are not sorted: a workgroup for each token and 64 pieces of
+// eight columns looks through all ids, and if none before it is the same it sums that
+// row, by the same parts as below, a stretch of them a wave (333 x 1601: one launch of
+// 7.0 us for three that took 18).
+template <class TY, class TG, bool TAIL>
+__global__ void __launch_bounds__(kThreads) embed_few_kernel(const SumArgs A, const Ids ids) {
+  const int n = int(A.tokens), lane = threadIdx.x & 63;
+  if (int64_t(blockIdx.x) >= A.sum_blocks) {
+    clear_rows<TG, TAIL, false>(A, int64_t(blockIdx.x) - A.sum_blocks,
+                         [&](int64_t r0, int rows, int *used) {
+                           used[threadIdx.x] = 0;
+                           __syncthreads();
+                           for (int i = threadIdx.x; i < n; i += kThreads) {
+                             const int64_t r = int64_t(ids.key(i)) - r0;
+                             if (r >= 0 && r < rows) used[r] = 1;
+                           }
+                           __syncthreads();
+                         });
+    return;
+  }
+  __shared__ uint16_t lists[kJoinWaves][kFewest];
+  __shared__ float sums[kJoinWaves][8][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint16_t *list = lists[wave];  // every wave its own: no barrier
+  const int token = int(blockIdx.x / A.waves);
+  const unsigned c = (blockIdx.x - unsigned(token) * A.waves) * 64 + lane, col = c * 8;
+  const int64_t mine = ids.id(token), columns = A.cols - col;
+  int64_t all[kFewest / 64];
+#pragma unroll
+  for (int q = 0; q < kFewest / 64; ++q) {
+    const int i = q * 64 + lane;
+    all[q] = i < n ? ids.id(i) : 0;
+  }
+  const unsigned key = ids.key(token);
+  if (key >= unsigned(A.vocab)) return;
+  int total = 0;
+#pragma unroll
+  for (int q = 0; q < kFewest / 64; ++q) {
+    const int i = q * 64 + lane;
+    const bool same = i < n && all[q] == mine;
+    const uint64_t mask = __ballot(same);
+    if (same) list[total + __popcll(mask & ((uint64_t(1) << lane) - 1))] = uint16_t(i);
+    total += __popcll(mask);
+  }
+  // LDS of this wave alone
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  if (list[0] != token) return;  // the row is an earlier one's
+  const int parts = (total + kShortRun - 1) / kShortRun;
+  const int each = (parts + kJoinWaves - 1) / kJoinWaves;
+  const int lo = wave * each, hi = lo + each < parts ? lo + each : parts;
+  float acc[8] = {};
+  for (int p = lo; p < hi; ++p) {
+    Eight<TY> v[kShortRun];
+#pragma unroll
+    for (int j = 0; j < kShortRun; ++j) {
+      const int at = p * kShortRun + j;
+      const int t = __builtin_amdgcn_readfirstlane(int(list[at < total ? at : 0]));
+      v[j].template load<TAIL, !TAIL>(row_of<TY>(A.dy, t, A.ld_dy), col, at < total ? columns : 0);
+    }
+    float part[8] = {};
+#pragma unroll
+    for (int j = 0; j < kShortRun; ++j)
+      if (p * kShortRun + j < total)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part[e] += v[j].get(e);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += part[e];
+  }
+  if (parts > 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[wave][e][lane] = acc[e];
+    __syncthreads();
+  }
+  if (wave != 0 || columns <= 0) return;
+  if (parts > 1)
+    for (int w = 1; w < kJoinWaves; ++w)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += sums[w][e][lane];
+  put_row<TG, TAIL>(A, key, col, acc);
 }
 
 // The sorted lists are not written while they are read here: the scalar units may
@@ -379,7 +482,15 @@ struct Places {
 template <class TY, class TG, bool TAIL, bool WAVES>
 __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const SumArgs A) {
   if (int64_t(blockIdx.x) >= A.sum_blocks) {
-    clear_rows<TG, TAIL>(A, int64_t(blockIdx.x) - A.sum_blocks);
+    clear_rows<TG, TAIL, true>(A, int64_t(blockIdx.x) - A.sum_blocks,
+                         [&](int64_t r0, int rows, int *used) {
+                           if (int(threadIdx.x) < rows) {
+                             const unsigned key = unsigned(r0 + threadIdx.x);
+                             const int64_t at = first_not_below(A.keys, 0, A.tokens, key);
+                             used[threadIdx.x] = at < A.tokens && A.keys[at] == key;
+                           }
+                           __syncthreads();
+                         });
     return;
   }
   unsigned piece, col;
@@ -562,14 +673,18 @@ bool desc_ok(const zs_embedding_desc *d) {
 }
 
 unsigned per_of(const zs_embedding_desc &d) { return unsigned((d.cols + 7) / 8); }
+bool unsorted(const zs_embedding_desc &d) {
+  return d.tokens <= kFewest && d.tokens * ((per_of(d) + 63) / 64) <= kFewestGroups;
+}
 int run_of(const zs_embedding_desc &d) { return d.tokens <= kFew ? kShortRun : kRun; }
 
 // Workspace: the sorted rows and tokens (twice where runs are merged), the
 // parts of long rows.
 struct Plan {
-  int64_t keys[2], order[2], part, bytes;
-  bool merged;
+  int64_t keys[2] = {}, order[2] = {}, part = 0, bytes = 0;
+  bool merged = false;
   explicit Plan(const zs_embedding_desc &d) {
+    if (unsorted(d)) return;
     const int64_t list = up(d.tokens * 4, 256), runs = (d.tokens + run_of(d) - 1) / run_of(d);
     merged = d.tokens > kTile;
     keys[0] = 0;
@@ -654,7 +769,8 @@ int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const 
   if (d->tokens == 0 && d->accumulate) return ZS_OK;
   if (!dtable) return ZS_EINVAL;
   const Plan p(*d);
-  if (d->tokens > 0 && (!ids || !dy || !workspace || workspace_bytes < p.bytes)) return ZS_EINVAL;
+  if (d->tokens > 0 && (!ids || !dy)) return ZS_EINVAL;
+  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return ZS_EINVAL;
   const int size = dtype_size(d->dtype), gsize = dtype_size(d->grad_dtype);
   if (!aligned(ids, d->id_bytes) || !aligned(dy, size) || !aligned(dtable, gsize) ||
       !aligned(workspace, 256))
@@ -675,17 +791,22 @@ int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const 
   A.add = d->accumulate;
   A.per = per_of(*d);
   A.waves = (A.per + 63) / 64;
-  const bool wide = A.per >= kWide;
+  const bool wide = A.per >= kWide, few = unsorted(*d);
   const int64_t threads = wide ? int64_t(A.waves) * 64 : A.per;
-  A.sum_blocks = (pieces * threads + kThreads - 1) / kThreads;
-  // about 64 KiB a workgroup clears, so that its searches are hidden
-  A.rows = int32_t((65536 + d->cols * gsize - 1) / (d->cols * gsize));
+  A.sum_blocks = few ? d->tokens * A.waves : (pieces * threads + kThreads - 1) / kThreads;
+  // A workgroup clears about 32 KiB, to which its searches are little, or 16 where they are
+  // quick (333 x 1601 64 KiB: 8.2 us for 7.0; 8192 x 5120 the same from 16 to 256).
+  const int64_t stretch = few ? 16384 : 32768;
+  A.rows = int32_t((stretch + d->cols * gsize - 1) / (d->cols * gsize));
+  while (d->vocab > (INT64_C(1) << 22) * A.rows) A.rows *= 2;  // what a launch takes
   if (A.rows > kThreads) A.rows = kThreads;
+  if (d->cols * gsize % 16) A.rows = int32_t(up(A.rows, 16 / gsize));
+  A.flat = A.ld_out == d->cols && aligned(dtable, 16);
   const int64_t clear = d->accumulate ? 0 : (d->vocab + A.rows - 1) / A.rows;
   if (const int rc = device_is_gfx950()) return rc;
   const hipStream_t st = static_cast<hipStream_t>(d->stream);
   char *ws = static_cast<char *>(workspace);
-  if (d->tokens > 0) {
+  if (!few) {
     int turn = 0;
     if (const int rc = sort(*d, p, ids, ws, st, turn)) return rc;
     A.keys = reinterpret_cast<const unsigned *>(ws + p.keys[turn]);
@@ -697,6 +818,11 @@ int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const 
     using TG = decltype(tg);
     return by_tail(d->cols % 8 != 0 || !even, [&](auto tail) {
       const dim3 grid(unsigned(A.sum_blocks + clear));
+      if (few) {
+        hipLaunchKernelGGL((embed_few_kernel<decltype(ty), TG, tail.value>), grid, dim3(kThreads),
+                           0, st, A, ids_of(*d, ids));
+        return launched();
+      }
       if (wide)
         hipLaunchKernelGGL((embed_sum_kernel<decltype(ty), TG, tail.value, true>), grid,
                            dim3(kThreads), 0, st, A);

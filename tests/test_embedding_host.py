@@ -22,7 +22,7 @@ def test_struct_layout_matches_header():
 
 
 def _desc(**kw):
-    base = dict(tokens=100, vocab=50, cols=64, id_bytes=8, dtype=Z.ZS_BF16,
+    base = dict(tokens=2000, vocab=50, cols=64, id_bytes=8, dtype=Z.ZS_BF16,
                 table_dtype=Z.ZS_BF16, grad_dtype=Z.ZS_F32, scale=1.0)
     base.update(kw)
     return Z.zs_embedding_desc(**base)
@@ -68,12 +68,16 @@ def test_backward_refuses_bad_pointers(kw, code):
 
 
 def test_workspace_bound_is_exact():
-    for tokens in (1, 33, 8192, 8193):
-        d = _desc(tokens=tokens)
+    for tokens, cols in ((1025, 64), (1000, 4096), (2048, 64), (2049, 64), (8192, 64), (8193, 64)):
+        d = _desc(tokens=tokens, cols=cols)
         need = Z.zero_shard_embedding_workspace(d)
         assert need > 0
         assert _bwd(d, size=need - 1) == Z.ZS_EINVAL
-    assert Z.zero_shard_embedding_workspace(_desc(tokens=0)) == 0
+    for tokens, cols in ((0, 64), (1, 5120), (1024, 64), (600, 5120)):  # nothing is sorted
+        d = _desc(tokens=tokens, cols=cols)
+        assert Z.zero_shard_embedding_workspace(d) == 0
+        if not torch.cuda.is_available():
+            assert _bwd(d, ws=None, size=0) == Z.ZS_EDEVICE
 
 
 def test_products_no_launch_takes_are_refused():

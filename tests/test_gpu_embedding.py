@@ -96,7 +96,8 @@ def _backward(ids, vocab, cols, dtype, other, pad=0, accumulate=False, first=0, 
 @pytest.mark.parametrize("dtype,other", TYPES)
 @pytest.mark.parametrize("tokens,vocab,cols", [
     (1, 1, 1), (1, 1000, 5120), (2, 3, 5), (31, 4, 64), (32, 1, 64), (33, 1, 64), (64, 1, 40),
-    (65, 2, 1601), (333, 1009, 1601), (4096, 7, 256), (1000, 300, 2056), (8191, 5000, 72),
+    (65, 2, 1601), (333, 1009, 1601), (1023, 40, 72), (1024, 3, 520), (1025, 40, 72),
+    (600, 50, 5120), (601, 50, 5120), (64, 5000, 37), (4096, 7, 256), (1000, 300, 2056), (8191, 5000, 72),
     (8192, 1, 16), (8192, 32000, 136)])
 def test_backward(tokens, vocab, cols, dtype, other):
     for pad, ids_t, first, acc in ((0, I64, 0, False), (3, I32, 7, True), (8, I64, -3, False)):
@@ -131,6 +132,34 @@ def test_long_rows_at_every_offset(shift):
         ids = torch.sort(torch.tensor(ids, device="cuda")).values
         for cols in (16, 520):
             _backward(ids, 5, cols, F32, F32)
+
+
+@pytest.mark.parametrize("cols", [24, 1601])
+@pytest.mark.parametrize("tokens", [1, 8, 9, 32, 33, 65, 260, 1000, 1024])
+def test_few_tokens_sum_as_sorted_ones_do(tokens, cols):
+    """Beside tokens of other ranks' rows, so many that all are sorted, the same bits."""
+    ids = torch.cat([_ids(tokens, 0, 40, power=3.0), torch.full((1500 - tokens,), -1, device="cuda")])
+    dy = R.randn(1500, cols, seed=7) * torch.exp(4 * R.randn(1500, 1, seed=8))
+    outs = [torch.empty(40, cols, device="cuda") for _ in range(2)]
+    for n, out in zip((tokens, 1500), outs):
+        Z.ZeroEmbedding(tokens=n, vocab=40, cols=cols, dtype=F32).backward(ids[:n], dy[:n], out)
+    assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("shift", [0, 1, 4, 8])
+@pytest.mark.parametrize("tokens", [5, 1200])
+def test_cleared_stretches_at_every_alignment(tokens, shift):
+    """Gradients that begin anywhere and whose rows end anywhere: all of them are written
+    and nothing beside them."""
+    for vocab, cols in ((3001, 37), (257, 1000), (2, 5121), (70_000, 8), (5000, 1)):
+        buf = torch.full((vocab * cols + 32,), 3.0, device="cuda", dtype=BF)
+        out = buf[8 + shift:8 + shift + vocab * cols].view(vocab, cols)
+        ids = _ids(tokens, 0, vocab, seed=5)
+        Z.ZeroEmbedding(tokens=tokens, vocab=vocab, cols=cols).backward(
+            ids, torch.ones(tokens, cols, device="cuda", dtype=BF), out)
+        want = torch.bincount(ids, minlength=vocab)[:, None].expand(vocab, cols).to(BF)
+        assert torch.equal(out, want)
+        assert (buf[:8 + shift] == 3).all() and (buf[8 + shift + vocab * cols:] == 3).all()
 
 
 def test_the_order_of_a_rows_sum():
