@@ -41,6 +41,62 @@ constexpr int kResident = 1280;    // threads of the forward pass on a CU
 constexpr int kPairThreads = 768;  // most that hold two rows, or sixteen columns, of the
                                   // backward pass without spilling
 
+// A thread's columns: N times eight, `per` threads apart.  Where a row ends inside a
+// thread's eight (TAIL), they are the row's last eight, of which the first `skip` are
+// the thread's before it: every load is of 16 bytes a piece, and nothing waits for one
+// on the way (with the last elements loaded one by one 32768 x 511 bf16 took 67 us
+// forward and 127 backward for 37 and 69).  Not with sixteen columns a thread, where the
+// registers do not hold what that takes (4096 x 9001 bf16 166 us for 151), nor in
+// rows of fewer than eight.  Of sixteen the first eight are always the row's.
+template <bool TAIL, int N>
+struct Mine : Columns<N> {
+  static constexpr bool kShift = TAIL && N == 1;
+  int skip = 0;
+  bool ends = false;  // whether a thread of this wave skips some
+  __device__ __forceinline__ Mine(int t, int per, int cols) : Columns<N>(t, per, cols) {
+    if constexpr (kShift) {
+      int &left = this->left[0];
+      if (left > 0 && left < 8 && cols >= 8) {
+        skip = 8 - left;
+        this->i[0] -= unsigned(skip);
+        left = 8;
+      }
+      ends = __ballot(skip != 0) != 0;
+    }
+  }
+  // Whether element e is the row's and this thread's, or (not TAIL) all eight.
+  __device__ __forceinline__ bool live(int n, int e) const {
+    if (n < N - 1) return true;
+    return TAIL ? (!kShift || e >= skip) && e < this->left[n] : this->left[n] > 0;
+  }
+  template <bool ONCE, class T>
+  __device__ __forceinline__ void get(Eight<T> &v, const void *row, int n, bool in) const {
+    if (n < N - 1) v.template load<false, ONCE>(row, this->i[n], in ? 8 : 0);
+    else v.template load<TAIL, ONCE>(row, this->i[n], in ? this->left[n] : 0);
+  }
+  // Elements that are not become zeros.
+  template <class T>
+  __device__ __forceinline__ void keep(Eight<T> &v, int n) const {
+    if (kShift && ends) {
+      int count = skip;
+      asm volatile("" : "+v"(count));  // worked out here: there are no registers to keep masks in
+      constexpr int kEach = sizeof(typename T::raw) == 4 ? 1 : 2;  // elements of a word
+#pragma unroll
+      for (int q = 0; q < 8 / kEach; ++q) {
+        const unsigned part = kEach == 2 && count == 2 * q + 1 ? 0xffff0000u : ~0u;
+        v.w[q] &= count >= kEach * (q + 1) ? 0u : part;
+      }
+    }
+  }
+  // The thread's elements.
+  template <class T>
+  __device__ __forceinline__ void put(const Eight<T> &v, void *row, int n) const {
+    if (n < N - 1) v.template store<false>(row, this->i[n], 8);
+    else if (!kShift || skip == 0) v.template store<TAIL>(row, this->i[n], this->left[n]);
+    else store_last(v, row, this->i[n], skip);
+  }
+};
+
 // sigmoid and its derivative, from t = exp(-|z|): nothing overflows and 1 - sigmoid
 // loses nothing.  exp2 of the product's leading part, the rest to first order (below
 // 2^-17 of it); the quotient by one Newton step.  Within 4 half steps of binary32.
@@ -149,7 +205,7 @@ struct Moments {
   // Deviations of R rows from their waves' means, in v's place; afterwards
   // (v + shift) rstd is normalised.
   template <bool TAIL, int N, int R>
-  __device__ __forceinline__ void of(float (&v)[R][N][8], Waves &waves, const Columns<N> &c,
+  __device__ __forceinline__ void of(float (&v)[R][N][8], Waves &waves, const Mine<TAIL, N> &c,
                                      float eps, float (&mean)[R], float (&rstd)[R],
                                      float (&shift)[R]) {
     const int lane = threadIdx.x & 63;
@@ -177,7 +233,7 @@ struct Moments {
         const float m = c.left[n] > 0 ? own[k] : 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float d = !TAIL || e < c.left[n] ? v[k][n][e] - m : 0.0f;
+          const float d = !TAIL || c.live(n, e) ? v[k][n][e] - m : 0.0f;
           sq = __builtin_fmaf(d, d, sq);
           off += d;
           v[k][n][e] = d;
@@ -232,8 +288,8 @@ struct FwdArgs {
 };
 
 // R rows at a time, each over `per` threads (a multiple of 64) of the
-// workgroup's blockDim.x / per row groups.  TAIL: the columns are no multiple of 8,
-// or rows start anywhere.  WIDE: a gate for each element.
+// workgroup's blockDim.x / per row groups.  TAIL: the columns are no multiple of 8.
+// WIDE: a gate for each element.
 template <class TX, class TP, int N, int R, bool TAIL, bool WIDE>
 __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
   __shared__ float lds[2][16][8];
@@ -245,8 +301,8 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
   const float other = Moments::columns<N>(threadIdx.x & 15, per, cols);
   Moments moments{1.0f / float(cols), own > 0.0f ? 1.0f / own : 0.0f, other,
                   other > 0.0f ? 1.0f / other : 0.0f};
-  const Columns<N> c(t, per, cols);
-  const auto live = [&](int n, int e) { return (TAIL ? e : 0) < c.left[n]; };
+  const Mine<TAIL, N> c(t, per, cols);
+  const auto live = [&](int n, int e) { return c.live(n, e); };
   // the gate of a column joins the first norm's gain and bias; both are 0 past the
   // row's end, and so is the sum there
   float gain[N][8], bias[N][8];
@@ -278,12 +334,11 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
     for (int k = 0; k < R; ++k)
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const int left = is(r0, k) ? c.left[n] : 0;
-        v.x[k][n].template load<TAIL, kOnce>(row_of<TX>(A.x, r0 + k, A.ld_x), c.i[n], left);
-        v.b[k][n].template load<TAIL, kOnce>(row_of<TX>(A.block, r0 + k, A.ld_b), c.i[n],
-                                             A.block ? left : 0);
+        const bool in = is(r0, k);
+        c.template get<kOnce>(v.x[k][n], row_of<TX>(A.x, r0 + k, A.ld_x), n, in);
+        c.template get<kOnce>(v.b[k][n], row_of<TX>(A.block, r0 + k, A.ld_b), n, in && A.block);
         if constexpr (WIDE)
-          v.z[k][n].template load<TAIL, kOnce>(row_of<TX>(A.z, r0 + k, A.ld_z), c.i[n], left);
+          c.template get<kOnce>(v.z[k][n], row_of<TX>(A.z, r0 + k, A.ld_z), n, in);
       }
   };
   // Rows of values (zeros past their ends) to their normalised ones: v scale + shift.
@@ -334,7 +389,11 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
 #pragma unroll
     for (int k = 0; k < R; ++k)
 #pragma unroll
-      for (int n = 0; n < N; ++n) now.b[k][n].get(v[k][n]);
+      for (int n = 0; n < N; ++n) {
+        c.keep(now.x[k][n], n);
+        c.keep(now.b[k][n], n);
+        now.b[k][n].get(v[k][n]);
+      }
     if (A.post) {
       statistics();
       keep(r0, 0);
@@ -362,7 +421,7 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
         if (A.block) {
           now.x[k][n].set(v[k][n]);
           if (is(r0, k))
-            now.x[k][n].template store<TAIL>(row_of<TX>(A.sum, r0 + k, A.ld_s), c.i[n], c.left[n]);
+            c.put(now.x[k][n], row_of<TX>(A.sum, r0 + k, A.ld_s), n);
         }
         now.x[k][n].get(v[k][n]);  // as it was rounded
       }
@@ -379,7 +438,7 @@ __global__ void __launch_bounds__(1024) seam_fwd_kernel(const FwdArgs A) {
           v[k][n][e] = __builtin_fmaf(h, gamma[n].get(e), beta[n].get(e));
         }
         now.x[k][n].set(v[k][n]);
-        now.x[k][n].template store<TAIL>(row_of<TX>(A.y, r0 + k, A.ld_y), c.i[n], c.left[n]);
+        c.put(now.x[k][n], row_of<TX>(A.y, r0 + k, A.ld_y), n);
       }
     }
   }
@@ -413,9 +472,9 @@ __global__ void __launch_bounds__(kMost) seam_bwd_kernel(const BwdArgs A) {
   const int per = A.per, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / per);
   const int t = threadIdx.x - sub * per, subs = blockDim.x / per;
   Waves waves{lds, sub * per / 64, per / 64};
-  const Columns<N> c(t, per, int(A.cols));
+  const Mine<TAIL, N> c(t, per, int(A.cols));
   // past a row's end: whole threads, or (TAIL) single elements
-  const auto live = [&](int n, int e) { return !TAIL || e < c.left[n]; };
+  const auto live = [&](int n, int e) { return !TAIL || c.live(n, e); };
   // Gains and the like stay in registers, or, with sixteen columns a thread, come
   // out of the caches for each row.
   constexpr bool kHeld = N == 1;
@@ -423,7 +482,7 @@ __global__ void __launch_bounds__(kMost) seam_bwd_kernel(const BwdArgs A) {
   float gain_held[8];  // gate gamma0, of a column
   const auto fetch = [&](Eight<TP> &v, const void *p, float none, int n) {
     if (p) {
-      v.template load<TAIL>(p, c.i[n], c.left[n]);
+      c.template get<false>(v, p, n, true);
     } else {
       const float all[8] = {none, none, none, none, none, none, none, none};
       v.set(all);
@@ -493,15 +552,11 @@ __global__ void __launch_bounds__(kMost) seam_bwd_kernel(const BwdArgs A) {
       v.m1[k] = in && A.center ? A.stats[3 * A.rows + r] : 0.0f;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const int left = in ? c.left[n] : 0;
-        v.dy[k][n].template load<TAIL, kOnce>(row_of<TX>(A.dy, r, A.ld_dy), c.i[n], left);
-        v.s[k][n].template load<TAIL, kOnce>(row_of<TX>(A.sum, r, A.ld_s), c.i[n], left);
-        v.ds[k][n].template load<TAIL, kOnce>(row_of<TX>(A.dsum, r, A.ld_ds), c.i[n],
-                                              A.dsum ? left : 0);
-        v.b[k][n].template load<TAIL, kOnce>(row_of<TX>(A.block, r, A.ld_b), c.i[n],
-                                             A.block ? left : 0);
-        if constexpr (WIDE)
-          v.z[k][n].template load<TAIL, kOnce>(row_of<TX>(A.z, r, A.ld_z), c.i[n], left);
+        c.template get<kOnce>(v.dy[k][n], row_of<TX>(A.dy, r, A.ld_dy), n, in);
+        c.template get<kOnce>(v.s[k][n], row_of<TX>(A.sum, r, A.ld_s), n, in);
+        c.template get<kOnce>(v.ds[k][n], row_of<TX>(A.dsum, r, A.ld_ds), n, in && A.dsum);
+        c.template get<kOnce>(v.b[k][n], row_of<TX>(A.block, r, A.ld_b), n, in && A.block);
+        if constexpr (WIDE) c.template get<kOnce>(v.z[k][n], row_of<TX>(A.z, r, A.ld_z), n, in);
       }
     }
   };
@@ -518,19 +573,25 @@ __global__ void __launch_bounds__(kMost) seam_bwd_kernel(const BwdArgs A) {
       load(now, first);
     }
     // Past a row's end the gradients are 0 and so are the factors they meet: rstd is
-    // taken as 0 there, since mean rstd may be beyond binary32.
+    // taken as 0 there, since mean rstd may be beyond binary32.  Elements that are
+    // another thread's may already be that thread's results where buffers are used in
+    // place, whatever these are.
     const auto own = [&](int n, float v) { return c.left[n] > 0 ? v : 0.0f; };
     const auto h1 = [&](int k, int n, int e) {
-      return (now.s[k][n].get(e) - now.m1[k]) * (live(n, e) ? own(n, now.r1[k]) : 0.0f);
+      const float h = (now.s[k][n].get(e) - now.m1[k]) * own(n, now.r1[k]);
+      return live(n, e) ? h : 0.0f;
     };
     const auto h0 = [&](int k, int n, int e) {
-      return (now.b[k][n].get(e) - now.m0[k]) * (live(n, e) ? own(n, now.r0[k]) : 0.0f);
+      const float h = (now.b[k][n].get(e) - now.m0[k]) * own(n, now.r0[k]);
+      return live(n, e) ? h : 0.0f;
     };
     float both[2 * R] = {};
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       float dh[8] = {}, dd[8] = {};
       if constexpr (!kHeld) fetch(gamma_held, A.gamma, 1.0f, n);
+#pragma unroll
+      for (int k = 0; k < R; ++k) c.keep(now.dy[k][n], n);
 #pragma unroll
       for (int k = 0; k < R; ++k)
 #pragma unroll
@@ -583,8 +644,7 @@ __global__ void __launch_bounds__(kMost) seam_bwd_kernel(const BwdArgs A) {
         }
         now.dy[k][n].set(out);
         if (is(first, k))
-          now.dy[k][n].template store<TAIL>(row_of<TX>(A.dx, first + k, A.ld_dx), c.i[n],
-                                            c.left[n]);
+          c.put(now.dy[k][n], row_of<TX>(A.dx, first + k, A.ld_dx), n);
         if constexpr (WIDE) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -597,8 +657,7 @@ __global__ void __launch_bounds__(kMost) seam_bwd_kernel(const BwdArgs A) {
           }
           now.z[k][n].set(out);
           if (is(first, k) && A.dz)
-            now.z[k][n].template store<TAIL>(row_of<TX>(A.dz, first + k, A.ld_dz), c.i[n],
-                                             c.left[n]);
+            c.put(now.z[k][n], row_of<TX>(A.dz, first + k, A.ld_dz), n);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -636,8 +695,7 @@ __global__ void __launch_bounds__(kMost) seam_bwd_kernel(const BwdArgs A) {
           D[k][n][e] = __builtin_fmaf(D[k][n][e], now.r0[k], d);
         }
         now.b[k][n].set(D[k][n]);
-        now.b[k][n].template store<TAIL>(row_of<TX>(A.dblock, first + k, A.ld_db), c.i[n],
-                                         c.left[n]);
+        c.put(now.b[k][n], row_of<TX>(A.dblock, first + k, A.ld_db), n);
       }
     }
   }
@@ -662,7 +720,7 @@ __global__ void __launch_bounds__(kMost) seam_bwd_kernel(const BwdArgs A) {
         for (int e = 0; e < 8; ++e) sum[e] += (*(place(which, n, e / 4) + w * per))[e % 4];
       Eight<F32> v;
       v.set(sum);
-      v.template store<TAIL>(out, c.i[n], c.left[n]);
+      c.put(v, out, n);
     }
   }
 }
@@ -829,14 +887,11 @@ int zero_shard_blocknorm(const zs_blocknorm_desc *d, const void *x, const void *
                   ld(d->ld_y), x, block, wide ? gate : nullptr, wide ? nullptr : gate, gamma_post,
                   beta_post, gamma, beta, sum, y, stats, d->eps, d->residual_scale,
                   d->kind == ZS_NORM_LAYER, d->post, w.per};
-  const bool even = rows_even(x, A.ld_x, size) && rows_even(block, A.ld_b, size) &&
-                    rows_even(A.z, A.ld_z, size) && rows_even(sum, A.ld_s, size) &&
-                    rows_even(y, A.ld_y, size);
   const int threads = w.per * w.subs;
   return by_type(*d, [&](auto tx, auto tp) {
     using TX = decltype(tx);
     using TP = decltype(tp);
-    return by_way(w.n, d->cols % 8 != 0 || !even, wide, [&](auto n, auto tail, auto wd) {
+    return by_way(w.n, d->cols % 8 != 0, wide, [&](auto n, auto tail, auto wd) {
       const auto launch = [&](auto r) {
         const int64_t groups = (A.rows + w.subs * r.value - 1) / (w.subs * r.value);
         // about as many as there is room for at once: later ones would run alone
@@ -898,17 +953,13 @@ int zero_shard_blocknorm_bwd(const zs_blocknorm_desc *d, const void *dy, const v
                   dbeta_post, dgamma, dbeta, want ? static_cast<float *>(workspace) : nullptr,
                   d->residual_scale, d->kind == ZS_NORM_LAYER, d->post, want,
                   int32_t(parts_of(*d)), w.per};
-  const bool even = rows_even(dy, A.ld_dy, size) && rows_even(dsum, A.ld_ds, size) &&
-                    rows_even(sum, A.ld_s, size) && rows_even(block, A.ld_b, size) &&
-                    rows_even(A.z, A.ld_z, size) && rows_even(dx, A.ld_dx, size) &&
-                    rows_even(dblock, A.ld_db, size) && rows_even(A.dz, A.ld_dz, size);
   const hipStream_t st = static_cast<hipStream_t>(d->stream);
   return by_type(*d, [&](auto tx, auto tp) {
     using TX = decltype(tx);
     using TP = decltype(tp);
     int rc = ZS_OK;
     if (A.rows > 0)
-      rc = by_way(w.n, d->cols % 8 != 0 || !even, wide, [&](auto n, auto tail, auto wd) {
+      rc = by_way(w.n, d->cols % 8 != 0, wide, [&](auto n, auto tail, auto wd) {
         using std::integral_constant;
         const auto launch = [&](auto r, auto most) {
           hipLaunchKernelGGL(

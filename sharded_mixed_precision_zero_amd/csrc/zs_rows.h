@@ -105,6 +105,47 @@ struct Columns {
   }
 };
 
+// The last 8 - skip (1 to 7) of the eight elements i.. of a row: four, two and one of them
+// that end where they do, in words of two elements or of one of 32 bits.
+template <class T>
+__device__ __forceinline__ void store_last(Eight<T> v, void *row, unsigned i, int skip) {
+  v.forget();  // registers, which a choice among them is not to index
+  using raw = typename T::raw;
+  constexpr bool kFull = sizeof(raw) == 4;
+  struct __attribute__((packed, aligned(sizeof(raw)))) Word {
+    unsigned w;
+  };
+  raw *p = reinterpret_cast<raw *>(static_cast<char *>(row) + i * unsigned(sizeof(raw)));
+  const auto word = [&](int at, unsigned w) { reinterpret_cast<Word *>(p + at)->w = w; };
+  const int count = 8 - skip;
+  if (count & 4) {
+    if constexpr (kFull) {
+#pragma unroll
+      for (int e = 4; e < 8; ++e) word(e, v.w[e]);
+    } else {
+      word(4, v.w[2]);
+      word(6, v.w[3]);
+    }
+  }
+  if (count & 2) {
+    const bool low = count & 4;
+    if constexpr (kFull) {
+      word(low ? 2 : 6, low ? v.w[2] : v.w[6]);
+      word(low ? 3 : 7, low ? v.w[3] : v.w[7]);
+    } else {
+      word(low ? 2 : 6, low ? v.w[1] : v.w[3]);
+    }
+  }
+  if (count & 1) {  // the first of them, an odd one
+    constexpr int kOdd = kFull ? 2 : 1, kFrom = kFull ? 1 : 0;  // where odd elements are
+    const unsigned low = skip & 2 ? v.w[kFrom + kOdd] : v.w[kFrom];
+    const unsigned high = skip & 2 ? v.w[kFrom + 3 * kOdd] : v.w[kFrom + 2 * kOdd];
+    const unsigned w = skip & 4 ? high : low;
+    if constexpr (kFull) word(skip, w);
+    else p[skip] = raw(w >> 16);
+  }
+}
+
 // gamma or beta at these columns (`none` where the caller gave none)
 template <bool TAIL, class TP, int N>
 __device__ __forceinline__ void load_params(Eight<TP> (&v)[N], const void *p, float none,

@@ -44,7 +44,7 @@ def _plan(ids, vocab, cols, dtype, other, **kw):
 @pytest.mark.parametrize("dtype,other", TYPES)
 @pytest.mark.parametrize("tokens,vocab,cols", [(1, 1, 1), (1, 32000, 5120), (3, 7, 2), (17, 100, 8),
                                                (333, 50, 1601), (1000, 9, 64), (40, 40, 4104),
-                                               (5000, 300, 24)])
+                                               (5000, 300, 24), (70, 31, 9), (65, 40, 515)])
 def test_forward(tokens, vocab, cols, dtype, other):
     for pad, ids_t, first in ((0, I64, 0), (3, I32, 5), (8, I64, -4)):
         ids = _ids(tokens, first - 2, first + vocab + 2, dtype=ids_t)
@@ -97,7 +97,8 @@ def _backward(ids, vocab, cols, dtype, other, pad=0, accumulate=False, first=0, 
 @pytest.mark.parametrize("tokens,vocab,cols", [
     (1, 1, 1), (1, 1000, 5120), (2, 3, 5), (31, 4, 64), (32, 1, 64), (33, 1, 64), (64, 1, 40),
     (65, 2, 1601), (333, 1009, 1601), (1023, 40, 72), (1024, 3, 520), (1025, 40, 72),
-    (600, 50, 5120), (601, 50, 5120), (64, 5000, 37), (4096, 7, 256), (1000, 300, 2056), (8191, 5000, 72),
+    (600, 50, 5120), (601, 50, 5120), (64, 5000, 37), (1500, 60, 9), (1500, 40, 515),
+    (9000, 200, 13), (4096, 7, 256), (1000, 300, 2056), (8191, 5000, 72),
     (8192, 1, 16), (8192, 32000, 136)])
 def test_backward(tokens, vocab, cols, dtype, other):
     for pad, ids_t, first, acc in ((0, I64, 0, False), (3, I32, 7, True), (8, I64, -3, False)):

@@ -30,7 +30,8 @@ def _gpu_cleanup():
 # (rows, cols): every register shape and its edges, one row, one column, odd
 # widths, more rows than workgroups
 SIZES = [(1, 1), (3, 2), (5, 8), (1, 5120), (7, 511), (6, 512), (9, 1601), (3, 2056), (5, 5120),
-         (3, 8192), (2, 8200), (2, 16383), (3, 16384), (2100, 64), (1030, 2064), (600, 4099)]
+         (3, 8192), (2, 8200), (2, 16383), (3, 16384), (2100, 64), (1030, 2064), (600, 4099),
+         (4, 7), (3, 9), (1100, 15), (1030, 515), (40, 1030), (1500, 2562)]
 TYPES = [(F32, F32), (BF, BF), (BF, F32), (F16, F16), (F16, F32)]
 WAYS = list(itertools.product(("rms", "layer"), ("none", "column", "sigmoid")))
 EPS, SCALE = 1e-5, 0.7
@@ -221,10 +222,11 @@ def test_backward_is_the_forward_differentiated(kind, gate, cols):
 
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 @pytest.mark.parametrize("gate", ["column", "sigmoid"])
-def test_buffers_used_in_place(kind, gate):
+@pytest.mark.parametrize("cols", [1000, 515, 1029])
+def test_buffers_used_in_place(kind, gate, cols):
     """sum over x or block, y over the other; dx and dblock over what they are
     the gradients from, dz over z: the same bits as into new buffers."""
-    rows, cols = 777, 1000
+    rows = 777
     p = _inputs(rows, cols, BF, F32, gate, 0)
     args = {k: v for k, v in p.items() if k not in ("x", "block")}
     plan = Z.ZeroBlockNorm(rows=rows, cols=cols, dtype=BF, param_dtype=F32, kind=kind, gate=gate,
@@ -267,7 +269,7 @@ def test_rows_behind_the_last_are_left_alone():
 
 
 @pytest.mark.parametrize("kind", ["rms", "layer"])
-@pytest.mark.parametrize("cols", [512, 9000])
+@pytest.mark.parametrize("cols", [512, 515, 9000])
 def test_infinities_and_nan_stay_in_their_rows(kind, cols):
     rows = 40
     p = _inputs(rows, cols, BF, F32, "column", 0)
