@@ -11,7 +11,7 @@
 // order: a thread holds eight columns of a row's sum in registers.  No atomics:
 // the same inputs give the same bits.
 //
-//   sort   tiles of kTile tokens by counting: a token's place is the number of
+//   sort   tiles of tokens by counting: a token's place is the number of
 //          tokens of its tile that come before it.  One launch, no passes over
 //          digits that wait for each other.  Longer lists merge up to eight runs
 //          at a time, each token finding its place by binary search in the other runs.
@@ -38,9 +38,11 @@ using namespace zs_dev;
 
 constexpr int kThreads = 256;
 // Tokens sorted by counting: up to kTile as one tile (8192: 10 us, 6 and 11 as four
-// tiles and a merge), more in tiles of kSmallTile, whose cost does not grow with the
-// square of their length (65536: 371 us the whole pass, 418 with long tiles).
-constexpr int kTile = 8192, kSmallTile = 2048;
+// tiles and a merge), up to kOneMerge in tiles that one merge joins (16384 x 64: 35 us the
+// whole pass, 41 with smaller ones and two merges), beyond in small ones, since a tile
+// costs the square of its length (65536 x 64: 66 us for 72, 300000 x 64: 197 for 237).
+constexpr int kTile = 8192, kMiddleTile = 2048, kSmallTile = 1024;
+constexpr int64_t kOneMerge = 8 * kMiddleTile;  // kRuns of them
 constexpr int kPlaced = 32;       // of them, that a workgroup places
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
@@ -236,7 +238,8 @@ struct MergeArgs {
 };
 
 // A token's place among up to kRuns runs: its place in its own and, in each
-// other, the number of tokens that come before it.  The searches run side by side.
+// other, the number of tokens that come before it.  The searches run side by side, all
+// loads of a step in flight (with branches around them 16000 tokens took 21 us for 8).
 __global__ void __launch_bounds__(kThreads) embed_merge_kernel(const MergeArgs A) {
   const int i = int(blockIdx.x) * kThreads + int(threadIdx.x);
   if (i >= A.tokens) return;
@@ -251,15 +254,21 @@ __global__ void __launch_bounds__(kThreads) embed_merge_kernel(const MergeArgs A
     if (q == own) hi[q] = lo[q];
   }
   for (int span = A.run; span > 0; span >>= 1) {
+    unsigned k[kRuns];
 #pragma unroll
-    for (int q = 0; q < kRuns; ++q)
-      if (lo[q] < hi[q]) {
-        const int mid = (lo[q] + hi[q]) >> 1;
-        const unsigned k = A.keys[mid];
-        // an earlier run's equals come first
-        if (q < own ? k <= key : k < key) lo[q] = mid + 1;
-        else hi[q] = mid;
-      }
+    for (int q = 0; q < kRuns; ++q) {
+      const int mid = (lo[q] + hi[q]) >> 1;
+      k[q] = A.keys[mid < A.tokens ? mid : i];  // all of them before any is looked at
+    }
+#pragma unroll
+    for (int q = 0; q < kRuns; ++q) {
+      const int mid = (lo[q] + hi[q]) >> 1;
+      // an earlier run's equals come first
+      const bool before = q < own ? k[q] <= key : k[q] < key;
+      const bool open = lo[q] < hi[q];
+      lo[q] = open && before ? mid + 1 : lo[q];
+      hi[q] = open && !before ? mid : hi[q];
+    }
   }
   int place = i - own * A.run;  // its place in its run, behind the group's start
 #pragma unroll
@@ -746,10 +755,12 @@ int sort(const zs_embedding_desc &d, const Plan &p, const void *ids, char *ws, h
   const auto keys = [&](int k) { return reinterpret_cast<unsigned *>(ws + p.keys[k]); };
   const auto order = [&](int k) { return reinterpret_cast<int *>(ws + p.order[k]); };
   turn = 0;
-  const int32_t tile = d.tokens <= kTile ? kTile : kSmallTile;
+  const int32_t tile = d.tokens <= kTile       ? kTile
+                       : d.tokens <= kOneMerge ? kMiddleTile
+                                               : kSmallTile;
   // a workgroup or two for each CU, at most a tile's
   int32_t groups = 1;
-  while (d.tokens > int64_t(512) * kPlaced * groups && groups < kSmallTile / kPlaced) groups *= 2;
+  while (d.tokens > int64_t(512) * kPlaced * groups && groups < tile / kPlaced) groups *= 2;
   const int64_t blocks = (d.tokens + kPlaced * groups - 1) / (kPlaced * groups);
   hipLaunchKernelGGL(embed_sort_kernel, dim3(unsigned(blocks)), dim3(kSortThreads), 0, st,
                      SortArgs{ids_of(d, ids), d.tokens, tile, groups, keys(0), order(0)});
