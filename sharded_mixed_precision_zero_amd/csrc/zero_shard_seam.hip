@@ -45,7 +45,7 @@ constexpr int kPairThreads = 768;  // most that hold two rows, or sixteen column
 // thread's eight (TAIL), they are the row's last eight, of which the first `skip` are
 // the thread's before it: every load is of 16 bytes a piece, and nothing waits for one
 // on the way (with the last elements loaded one by one 32768 x 511 bf16 took 67 us
-// forward and 127 backward for 37 and 69).  Not with sixteen columns a thread, where the
+// forward and 127 backward for 33 and 64).  Not with sixteen columns a thread, where the
 // registers do not hold what that takes (4096 x 9001 bf16 166 us for 151), nor in
 // rows of fewer than eight.  Of sixteen the first eight are always the row's.
 template <bool TAIL, int N>
@@ -823,10 +823,11 @@ Way way_of(const zs_blocknorm_desc &d, int threads) {
 }
 
 // The backward pass takes two rows at a time once every CU has some, where the
-// registers hold them.
+// registers hold them; of rows that end inside a thread's eight columns only of long ones
+// (8192 x 2049 bf16: 71 us with two, 63 with one; 8192 x 5121: 136 and 149).
 bool pairs(const zs_blocknorm_desc &d) {
   return d.rows >= 4 * kCus && d.cols <= 8 * kPairThreads && d.dtype != ZS_F32 &&
-         d.gate != ZS_GATE_SIGMOID;
+         d.gate != ZS_GATE_SIGMOID && (d.cols % 8 == 0 || d.cols > 4096);
 }
 Way bwd_way_of(const zs_blocknorm_desc &d) { return way_of(d, pairs(d) ? kPairThreads : 1024); }
 
@@ -901,8 +902,9 @@ int zero_shard_blocknorm(const zs_blocknorm_desc *d, const void *x, const void *
                            static_cast<hipStream_t>(d->stream), A);
         return launched();
       };
-      // two rows at a time once every CU has some, where the registers hold them
-      if constexpr (n.value == 1 && sizeof(typename TX::raw) == 2 && !wd.value)
+      // two rows at a time once every CU has some, where the registers hold them and the
+      // work on their ends (32768 x 511 bf16: 37 us with two, 33 with one)
+      if constexpr (n.value == 1 && sizeof(typename TX::raw) == 2 && !wd.value && !tail.value)
         if (A.rows >= 4 * kCus) return launch(std::integral_constant<int, 2>{});
       return launch(std::integral_constant<int, 1>{});
     });
