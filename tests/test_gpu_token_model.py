@@ -158,3 +158,34 @@ def test_captured_steps_are_the_eager_ones(tokens, vocab, width):
                 assert torch.equal(a.view(torch.uint8) if a.element_size() == 1 else a,
                                    b.view(torch.uint8) if b.element_size() == 1 else b), t
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("tokens,vocab,width", [(700, 300, 520), (9000, 500, 72)])
+def test_two_programs_at_once(tokens, vocab, width):
+    """On two streams, call by call in turn, each what it gives alone."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    g = torch.Generator(device="cuda").manual_seed(9)
+    ids = [torch.randint(vocab, (tokens,), device="cuda", generator=g) for _ in range(4)]
+    streams = [torch.cuda.Stream() for _ in range(2)] + [torch.cuda.current_stream()]
+    steps = []
+    for stream in streams:
+        with torch.cuda.stream(stream):
+            steps.append(_Step(tokens, vocab, width, torch.empty(4, device="cuda", dtype=F64)))
+    consts = [torch.tensor(steps[0].adam.consts(0.01, t + 1), dtype=F64, device="cuda")
+              for t in range(4)]
+    torch.cuda.synchronize()
+    for t in range(4):
+        for stream, step in zip(streams[:2], steps):
+            with torch.cuda.stream(stream):
+                step.consts.copy_(consts[t])
+                step.queue(ids[t])
+    torch.cuda.synchronize()
+    for t in range(4):
+        steps[2].consts.copy_(consts[t])
+        steps[2].queue(ids[t])
+        torch.cuda.synchronize()
+    for step in steps[:2]:
+        for a, b in zip(step.results(), steps[2].results()):
+            assert torch.equal(a.view(torch.uint8) if a.element_size() == 1 else a,
+                               b.view(torch.uint8) if b.element_size() == 1 else b)
