@@ -637,8 +637,8 @@ int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const 
  * ZS_STATE_8: m and r = sqrt(v) are each an e4m3 number (sign, 4 bits of exponent with
  * bias 7, 3 of mantissa; no infinities) times the scale of its block, the
  * tensor's elements [256 b, 256 b + 256).  Their moments are binary32 throughout (with
- * coef, b, 1-b and 1/sqrt(bc2) rounded to it), every operation rounded (the root and
- * the quotients within a step of binary32, or two):
+ * coef, b, 1-b and 1/sqrt(bc2) rounded to it), every operation rounded (u's quotient
+ * within two steps of binary32):
  *   m' = b1 m + (1-b1) g'      r' = sqrt((b2 r) r + ((1-b2) g') g')
  *   u = m' / (r' / sqrt(bc2) + eps)
  *   theta' = theta - (lr f wd) theta - (lr f / bc1) u   (binary64, rounded once)

@@ -298,10 +298,12 @@ __device__ __forceinline__ void update32(const Tensor &T, const Consts &k, const
 }
 
 // The same with a state in 8 bits.  The moments are binary32 numbers, which
-// rounding to 4 significant bits makes little of, with a root and a quotient of an
-// instruction or two, within 2^-23 and 2^-22: what the memory leaves time for is some
+// rounding to 4 significant bits makes little of: what the memory leaves time for is some
 // 100 instructions an element, and binary64 as above takes more (1034 us for 570 of
-// 163.84M elements).  The weights are binary64 as above.
+// 163.84M elements).  What is stored is the definition's number for number: its root and
+// its scale's inverse are rounded (467 us for 449 with the instructions' own, within a
+// step, which put one of v's scales in 60 a step off).  u's quotient, which only the
+// weights see, is the instruction's, within 2^-22; they are binary64 as above.
 template <class TG, bool TAIL>
 __device__ __forceinline__ void update8(const Tensor &T, const Rates &rates, uint32_t base,
                                         Lane &s, const Place &i) {
@@ -317,7 +319,7 @@ __device__ __forceinline__ void update8(const Tensor &T, const Rates &rates, uin
     const float g = rates.coef32 * grad_of<TG>(s, e);
     const float m0 = m8[e / 2][e % 2] * s.ms, r0 = v8[e / 2][e % 2] * s.vs;
     m[e] = rates.b1 * m0 + rates.omb1 * g;
-    r[e] = __builtin_amdgcn_sqrtf((rates.b2 * r0) * r0 + (rates.omb2 * g) * g);
+    r[e] = sqrtf((rates.b2 * r0) * r0 + (rates.omb2 * g) * g);
     const double t0 = double(s.w.v[e]);
     const float u = m[e] * __builtin_amdgcn_rcpf(r[e] * rates.root + rates.eps);
     s.w.v[e] = float(t0 - rates.decay * t0 - rates.step * double(u));
@@ -334,7 +336,7 @@ __device__ __forceinline__ void update8(const Tensor &T, const Rates &rates, uin
   const float top = __uint_as_float(wave_tops(mtop, vtop)) * held;
   const bool none = top < 0x1p-100f;
   const float scale = none ? 0.0f : top * 0x1p-8f;
-  const float inv = none ? 0.0f : __builtin_amdgcn_rcpf(scale) * held;
+  const float inv = none ? 0.0f : 1.0f / scale * held;
   const float minv = lane_value(inv, 0), vinv = lane_value(inv, 32);
   // to e4m3, down or up where 20 bits of dither carry into the number
   unsigned mw = 0, vw = 0;
