@@ -642,7 +642,8 @@ int zero_shard_embedding_bwd(const zs_embedding_desc *d, const void *ids, const 
  *   m' = b1 m + (1-b1) g'      r' = sqrt((b2 r) r + ((1-b2) g') g')
  *   u = m' / (r' / sqrt(bc2) + eps)
  *   theta' = theta - (lr f wd) theta - (lr f / bc1) u   (binary64, rounded once)
- * (gradients from 2^53 on count as infinities, those below 2^-74 as zeros in r').
+ * (b2 and 1-b2 times 2^32 there, the root times 2^-16, so that an r' from 2^48 on is an
+ * infinity and one below 2^-91 a zero).
  * Storing values x of a block (of m', or of r'):
  *   top = max |x|;  scale = top / 256
  *   y = |x| binary32(1 / scale), at most 256, and at least 2^-9 for an r' > 0, becomes

@@ -65,3 +65,24 @@ def test_stored_numbers_of_gradients_of_every_size(spread):
         before = case.state()
         opt.step(case.grads(), LR, t, key=t)
         _is_the_definitions(case, before, t, t)
+
+
+@pytest.mark.parametrize("beta2", [0.0, 0.9, 0.999, 0.9999])
+def test_roots_from_2_48_on_are_infinities_and_below_2_91_zeros(beta2):
+    """Whatever beta2 is: blocks of one gradient each, whose roots are just below and just
+    above either border."""
+    root = (1.0 - float(np.float32(beta2))) ** 0.5
+    size = torch.tensor([0.999 * 2.0 ** 48, 1.001 * 2.0 ** 48, 1.01 * 2.0 ** -91,
+                         0.99 * 2.0 ** -91], device="cuda") / root
+    case = Case([1024], 8, F32, param=None)
+    it = case.items[0]
+    it["grad"].copy_(size.repeat_interleave(256))
+    for k in ("m", "v"):
+        it[k].zero_()
+        it[k + "_scale"].zero_()
+    Z.ZeroAdamW(case.tensors(), beta2=beta2).step(case.grads(), LR, 1, key=1)
+    scale = it["v_scale"].tolist()
+    assert abs(scale[0] / (0.999 * 2.0 ** 40) - 1) < 1e-6 and scale[1] == float("inf")
+    # its square times 2^32 is the least number, 2^-149
+    assert abs(scale[2] * 2.0 ** 98.5 - 1) < 1e-6
+    assert scale[3] == 0.0 and (it["v"][768:] == 0).all()
