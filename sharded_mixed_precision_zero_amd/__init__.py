@@ -374,6 +374,17 @@ def contrib_table(contrib) -> ctypes.Array | None:
     return tab
 
 
+def _kept_table(table, owner, check):
+    """A table that the caller keeps.  check(its tensors) runs when ``owner`` first sees
+    it, and again if its entries have changed since; they have to be the tensors'."""
+    entries, seen = bytes(table), getattr(table, "_seen", None)
+    if seen is None or seen[0] is not owner or seen[1] != entries:
+        check(table._keep)
+        _require(entries == bytes(contrib_table(table._keep)), "a table's entries")
+        table._seen = owner, entries
+    return table
+
+
 # ------------------------------------------------------------ C-named calls
 
 def zero_shard_strerror(code: int) -> str:
@@ -1167,8 +1178,9 @@ class ZeroAdamW:
 
     The gradients of a call are a list of contiguous device tensors, one a tensor of its
     ``grad_dtype`` and length (None for an empty one), or a table of theirs that the
-    caller keeps (contrib_table).  ``max_norm`` > 0: gnorm, the all-reduce of its
-    sum across ranks, then step with it.  ``stream`` as for ZeroLayerNorm."""
+    caller keeps (contrib_table), which is checked as a list is when it is first given.
+    ``max_norm`` > 0: gnorm, the all-reduce of its sum across ranks, then step with it.
+    ``stream`` as for ZeroLayerNorm."""
 
     def __init__(self, tensors, *, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                  bias_correction: bool = True, max_norm: float = 0.0, stream=None):
@@ -1189,15 +1201,18 @@ class ZeroAdamW:
 
     def _grads(self, grads):
         if isinstance(grads, ctypes.Array):  # kept by the caller
-            _require(len(grads) >= len(self.tensors), "grads")
-            return grads
+            _require(hasattr(grads, "_keep"), "grads: not a table of contrib_table's")
+            return _kept_table(grads, self, self._check_grads)
         grads = list(grads)
+        self._check_grads(grads)
+        return contrib_table(grads)
+
+    def _check_grads(self, grads) -> None:
         _require(len(grads) == len(self.tensors), "grads")
         for g, t in zip(grads, self.tensors):
             if t.n or g is not None:
                 _require(g is not None and g.numel() == t.n and g.is_cuda and g.is_contiguous()
                          and _DTYPES.get(g.dtype) == t.grad_dtype, "grads")
-        return contrib_table(grads)
 
     @staticmethod
     def _double(t, n: int, what: str):

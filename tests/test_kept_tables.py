@@ -1,0 +1,81 @@
+"""Tables of gradients that a program keeps: what fits is taken, what does not is refused
+as a list of the same tensors is, before anything is queued."""
+
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+import sharded_mixed_precision_zero_amd as Z
+from tests.test_owner_refusals import on_device
+
+BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def _opt(*sizes, dtype=BF):
+    o = object.__new__(Z.ZeroAdamW)
+    o.tensors = [Z.zs_adamw_tensor(n=n, grad_dtype=Z.dtype_code(dtype)) for n in sizes]
+    return o
+
+
+def _new(*shape, dtype=BF):
+    return on_device(torch.zeros(*shape, dtype=dtype))
+
+
+def test_tables_that_fit():
+    o = _opt(600, 0, 32)
+    table = Z.contrib_table([_new(600), None, _new(4, 8)])
+    for _ in range(3):
+        assert o._grads(table) is table
+    assert _opt(600, 0, 32)._grads(table) is table  # another plan of the same sizes
+    assert o._grads(table) is table
+    rows = Z.contrib_table(_new(2, 40))
+    assert _opt(40, 40)._grads(rows) is rows
+    assert len(_opt()._grads(Z.contrib_table([]))) == 1
+
+
+@pytest.mark.parametrize("grads", [
+    lambda: [_new(600)], lambda: [_new(600), _new(3), _new(32)], lambda: [_new(600), None],
+    lambda: [_new(599), None, _new(32)], lambda: [_new(601), None, _new(32)],
+    lambda: [_new(600, dtype=F32), None, _new(32)], lambda: [_new(600, dtype=F16), None, _new(32)],
+    lambda: [None, None, _new(32)], lambda: [_new(1200)[::2], None, _new(32)],
+    lambda: [_new(1).expand(600), None, _new(32)],
+    lambda: [torch.zeros(600, dtype=BF), None, _new(32)],        # on the host
+    lambda: [_new(600), None, _new(32), _new(32)]])
+def test_tables_that_do_not_fit_are_refused(grads):
+    o = _opt(600, 0, 32)
+    for _ in range(2):
+        with pytest.raises(Z.ZeroShardError, match="grads"):
+            o._grads(Z.contrib_table(grads()))
+    table = Z.contrib_table(grads())
+    for _ in range(2):  # nor the second time
+        with pytest.raises(Z.ZeroShardError, match="grads"):
+            o._grads(table)
+
+
+def test_a_table_of_another_plan_is_looked_at_again():
+    table = Z.contrib_table([_new(600)])
+    assert _opt(600)._grads(table) is table
+    for other in (_opt(601), _opt(600, dtype=F32), _opt(600, 600), _opt()):
+        with pytest.raises(Z.ZeroShardError, match="grads"):
+            other._grads(table)
+
+
+def test_entries_that_are_not_the_tensors_are_refused():
+    o = _opt(600, 600)
+    a, b, c = (_new(600) for _ in range(3))
+    table = Z.contrib_table([a, b])
+    assert o._grads(table) is table
+    table[1] = c.data_ptr()
+    with pytest.raises(Z.ZeroShardError, match="entries"):
+        o._grads(table)
+    table[1] = b.data_ptr()
+    assert o._grads(table) is table
+    table[0] = None
+    with pytest.raises(Z.ZeroShardError, match="entries"):
+        o._grads(table)
+    bare = (ctypes.c_void_p * 2)(a.data_ptr(), b.data_ptr())
+    with pytest.raises(Z.ZeroShardError, match="contrib_table"):
+        o._grads(bare)
