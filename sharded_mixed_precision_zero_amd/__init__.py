@@ -1323,16 +1323,21 @@ class ZeroMuon:
     def _table(self, contrib):
         """The table of n_d contributions, each n contiguous bf16 elements or more
         (a row may be padded at its end)."""
-        n, n_d = self.desc.n, self.desc.n_d
         if isinstance(contrib, ctypes.Array):  # kept by the caller
-            _require(len(contrib) == n_d, "contrib")
-            return contrib
+            _require(len(contrib) == self.desc.n_d, "contrib")
+            # one that contrib_table did not make is addresses, which nothing is known of
+            return (_kept_table(contrib, self, self._check_rows) if hasattr(contrib, "_keep")
+                    else contrib)
         rows = list(contrib)  # also of a 2-D tensor
+        self._check_rows(rows)
+        return contrib_table(rows)
+
+    def _check_rows(self, rows) -> None:
+        n, n_d = self.desc.n, self.desc.n_d
         _require(len(rows) == n_d, "contrib")
         for r in rows:
             _require(r is not None and r.numel() >= n and r.dtype in _BF16_LIKE
                      and r.is_contiguous() and r.is_cuda, "contrib")
-        return contrib_table(rows)
 
     def step(self, contrib, lr: float) -> None:
         """Momentum over the mean of the contributions, its orthogonalisation,

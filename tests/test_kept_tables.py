@@ -79,3 +79,36 @@ def test_entries_that_are_not_the_tensors_are_refused():
     bare = (ctypes.c_void_p * 2)(a.data_ptr(), b.data_ptr())
     with pytest.raises(Z.ZeroShardError, match="contrib_table"):
         o._grads(bare)
+
+
+def _muon(n=32, n_d=3):
+    muon = object.__new__(Z.ZeroMuon)
+    muon.desc = Z.zs_muon_desc(n=n, n_d=n_d)
+    return muon
+
+
+def test_contributions_that_fit():
+    muon = _muon()
+    table = Z.contrib_table([_new(32), _new(4, 8), _new(40)])
+    for _ in range(2):
+        assert muon._table(table) is table
+    rows = Z.contrib_table(_new(3, 40))
+    assert muon._table(rows) is rows
+    bare = (ctypes.c_void_p * 3)(*[_new(32).data_ptr() for _ in range(3)])
+    assert muon._table(bare) is bare
+
+
+@pytest.mark.parametrize("bad", [
+    lambda: _new(31), lambda: _new(32, dtype=F32), lambda: _new(32, dtype=F16),
+    lambda: _new(64)[::2], lambda: torch.zeros(32, dtype=BF), lambda: None])
+def test_contributions_that_do_not_fit_are_refused(bad):
+    muon = _muon()
+    table = Z.contrib_table([_new(32), bad(), _new(32)])
+    for _ in range(2):
+        with pytest.raises(Z.ZeroShardError, match="contrib"):
+            muon._table(table)
+    table = Z.contrib_table([_new(32)] * 3)
+    assert muon._table(table) is table
+    table[0] = 1 << 20
+    with pytest.raises(Z.ZeroShardError, match="entries"):
+        muon._table(table)
