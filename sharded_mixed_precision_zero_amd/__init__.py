@@ -795,25 +795,41 @@ def adamw_desc(*, count: int, beta1: float = 0.9, beta2: float = 0.999, eps: flo
 
 def zero_shard_adamw_plan_bytes(desc: zs_adamw_desc, tensors) -> int:
     """tensors: an array of zs_adamw_tensor ((zs_adamw_tensor * n)(...))."""
+    if tensors is not None and len(tensors) < desc.count:
+        return -1
     return int(_lib.zero_shard_adamw_plan_bytes(ctypes.byref(desc), tensors))
 
 
 def zero_shard_adamw_plan(desc: zs_adamw_desc, tensors, plan) -> int:
     """plan: a contiguous CPU tensor (its size in bytes is passed on)."""
+    if tensors is not None and len(tensors) < desc.count or plan is not None and plan.is_cuda:
+        return ZS_EINVAL
     return _lib.zero_shard_adamw_plan(ctypes.byref(desc), tensors, _ptr(plan), _nbytes(plan))
+
+
+def _adamw_fits(desc: zs_adamw_desc, plan, table) -> bool:
+    """What the call reads on the host is there: a gradient's address for each tensor, and a
+    plan that is not the device's copy."""
+    return ((table is None or len(table) >= desc.count)
+            and (plan is None or not plan.is_cuda))
 
 
 def zero_shard_adamw_gnorm(desc: zs_adamw_desc, plan, plan_dev, grads, sumsq_dev) -> int:
     """plan, plan_dev: the plan on the CPU and its copy on the device."""
-    return _lib.zero_shard_adamw_gnorm(ctypes.byref(desc), _ptr(plan), _ptr(plan_dev),
-                                       contrib_table(grads), _ptr(sumsq_dev))
+    table = contrib_table(grads)
+    if not _adamw_fits(desc, plan, table):
+        return ZS_EINVAL
+    return _lib.zero_shard_adamw_gnorm(ctypes.byref(desc), _ptr(plan), _ptr(plan_dev), table,
+                                       _ptr(sumsq_dev))
 
 
 def zero_shard_adamw(desc: zs_adamw_desc, plan, plan_dev, grads, lr: float, t: int, key: int,
                      global_sumsq_dev=None) -> int:
-    return _lib.zero_shard_adamw(ctypes.byref(desc), _ptr(plan), _ptr(plan_dev),
-                                 contrib_table(grads), float(lr), int(t), int(key) & 0xFFFFFFFF,
-                                 _ptr(global_sumsq_dev))
+    table = contrib_table(grads)
+    if not _adamw_fits(desc, plan, table):
+        return ZS_EINVAL
+    return _lib.zero_shard_adamw(ctypes.byref(desc), _ptr(plan), _ptr(plan_dev), table, float(lr),
+                                 int(t), int(key) & 0xFFFFFFFF, _ptr(global_sumsq_dev))
 
 
 def zero_shard_adamw_consts(desc: zs_adamw_desc, lr: float, t: int, key: int):
@@ -826,9 +842,11 @@ def zero_shard_adamw_consts(desc: zs_adamw_desc, lr: float, t: int, key: int):
 
 def zero_shard_adamw_dev(desc: zs_adamw_desc, plan, plan_dev, grads, consts_dev,
                          global_sumsq_dev=None) -> int:
-    return _lib.zero_shard_adamw_dev(ctypes.byref(desc), _ptr(plan), _ptr(plan_dev),
-                                     contrib_table(grads), _ptr(consts_dev),
-                                     _ptr(global_sumsq_dev))
+    table = contrib_table(grads)
+    if not _adamw_fits(desc, plan, table):
+        return ZS_EINVAL
+    return _lib.zero_shard_adamw_dev(ctypes.byref(desc), _ptr(plan), _ptr(plan_dev), table,
+                                     _ptr(consts_dev), _ptr(global_sumsq_dev))
 
 
 # ------------------------------------------------------------ owner objects

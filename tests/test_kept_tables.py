@@ -112,3 +112,37 @@ def test_contributions_that_do_not_fit_are_refused(bad):
     table[0] = 1 << 20
     with pytest.raises(Z.ZeroShardError, match="entries"):
         muon._table(table)
+
+
+def _desc(count):
+    return Z.zs_adamw_desc(count=count, beta1=0.9, beta2=0.999, eps=1e-8, bias_correction=1)
+
+
+def _tensors(count):
+    at = [(1 << 20) + k * 65536 for k in range(3 * count)]  # stand-in addresses
+    return (Z.zs_adamw_tensor * max(1, count))(*[
+        Z.zs_adamw_tensor(n=1000, master_in=a, master_out=a, m_in=b, m_out=b, v_in=c, v_out=c,
+                          lr_scale=1.0, grad_dtype=Z.ZS_BF16, param_dtype=Z.ZS_BF16)
+        for a, b, c in zip(at[0::3], at[1::3], at[2::3])])
+
+
+def test_named_calls_refuse_fewer_tensors_or_gradients_than_counted(monkeypatch):
+    """The host arrays are not read past their ends: the library is not called."""
+    class Closed:
+        def __getattr__(self, name):
+            raise AssertionError(name)
+
+    d, two = _desc(3), _tensors(2)
+    plan = torch.zeros(Z.zero_shard_adamw_plan_bytes(d, _tensors(3)), dtype=torch.uint8)
+    assert Z.zero_shard_adamw_plan(d, _tensors(3), plan) == Z.ZS_OK
+    monkeypatch.setattr(Z, "_lib", Closed())
+    assert Z.zero_shard_adamw_plan_bytes(d, two) == -1
+    assert Z.zero_shard_adamw_plan(d, two, plan) == Z.ZS_EINVAL
+    assert Z.zero_shard_adamw_plan(d, _tensors(3), on_device(plan)) == Z.ZS_EINVAL
+    dev, s = _new(1), _new(1, dtype=torch.float64)
+    three = [_new(1000) for _ in range(3)]
+    for p, grads in ((plan, three[:2]), (plan, Z.contrib_table(three[:2])), (plan, []),
+                     (on_device(plan), three)):
+        assert Z.zero_shard_adamw_gnorm(d, p, dev, grads, s) == Z.ZS_EINVAL
+        assert Z.zero_shard_adamw(d, p, dev, grads, 1e-3, 1, 0) == Z.ZS_EINVAL
+        assert Z.zero_shard_adamw_dev(d, p, dev, grads, s) == Z.ZS_EINVAL
