@@ -498,7 +498,8 @@ typedef enum zs_norm_kind { ZS_NORM_LAYER = 0, ZS_NORM_RMS = 1 } zs_norm_kind;
 typedef enum zs_gate {
   ZS_GATE_NONE = 0,
   ZS_GATE_COLUMN = 1, /* a factor for each column: param_dtype, cols elements  */
-  ZS_GATE_SIGMOID = 2 /* sigmoid(z) for each element: z is dtype, rows x cols  */
+  ZS_GATE_SIGMOID = 2 /* sigmoid(z) for each element: z is dtype, rows x cols;
+                         it and its slope are 0 where they are below 2^-126   */
 } zs_gate;
 
 typedef struct zs_blocknorm_desc {

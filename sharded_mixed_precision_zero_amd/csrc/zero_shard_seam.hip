@@ -99,7 +99,9 @@ struct Mine : Columns<N> {
 
 // sigmoid and its derivative, from t = exp(-|z|): nothing overflows and 1 - sigmoid
 // loses nothing.  exp2 of the product's leading part, the rest to first order (below
-// 2^-17 of it); the quotient by one Newton step.  Within 4 half steps of binary32.
+// 2^-17 of it); the quotient by one Newton step.  Within 4 half steps of binary32, but 0
+// (and the slope too) where they are below its least normal number, z < -87.34: there the
+// exponential is 0 (from 87.34 on the slope alone is).
 __device__ __forceinline__ float sigmoid(float z, float &slope) {
   constexpr float kLog2e = 1.44269504f, kRest = 1.92596304e-8f;  // of log2 e
   float a = -fabsf(z);
