@@ -7,7 +7,7 @@
 // gradients, which a training program allocates anew, come as kernel arguments,
 // up to kGrads of them a launch.  The kinds have a launch each because the
 // registers of one (binary64 in the shard step's order) would leave the other too few
-// waves (163.84M elements in 8 bits: 543 us in one launch, 485 in its own).
+// waves (163.84M elements in 8 bits, then: 543 us in one launch, 485 in its own).
 //
 // The step is HBM-bound: 28 bytes an element with a 16-bit gradient and copy and
 // a 32-bit state, 16.06 with an 8-bit one.  A wave takes 256 elements at a time,
@@ -40,7 +40,7 @@ constexpr int kBlock = ZS_ADAMW_BLOCK;  // elements that share a scale: a wave's
 // Blocks of a wave, in flight together, and elements of a workgroup.  A 32-bit state
 // has bytes enough in flight with one block, and short chains of work a wave (160
 // tensors of 5120: 6.0 us for 8.4 with two; 163.84M elements 778 for 811); an 8-bit
-// one is a little faster with two (513 for 527).
+// one was a little faster with two (513 for 527).
 template <bool EIGHT>
 constexpr int kRounds = EIGHT ? 2 : 1;
 template <bool EIGHT>
@@ -274,6 +274,18 @@ __device__ __forceinline__ void put_weights(const Tensor &T, const Four<float> &
   else put_copy<F16, TAIL>(T, w, i);
 }
 
+// The root, rounded, of a number from 2^-96 on (below, the products' differences are no
+// normal numbers).  The instruction's is within a step; its neighbour is the nearer one
+// where the number lies beyond the product of the two, which what lies halfway between
+// them exceeds, squared, by less than any number could.  Tried with all of them.
+__device__ __forceinline__ float root_of(float x) {
+  const float s = __builtin_amdgcn_sqrtf(x);
+  const float below = __uint_as_float(__float_as_uint(s) - 1);
+  const float above = __uint_as_float(__float_as_uint(s) + 1);
+  const float r = __builtin_fmaf(-below, s, x) <= 0.0f ? below : s;
+  return __builtin_fmaf(-above, s, x) > 0.0f ? above : r;
+}
+
 // AdamW on a lane's four elements: binary64 from the binary32 state, one
 // rounding per stored value, in the shard step's order.
 template <class TG, bool TAIL>
@@ -301,9 +313,10 @@ __device__ __forceinline__ void update32(const Tensor &T, const Consts &k, const
 // rounding to 4 significant bits makes little of: what the memory leaves time for is some
 // 100 instructions an element, and binary64 as above takes more (1034 us for 570 of
 // 163.84M elements).  What is stored is the definition's number for number: its root and
-// its scale's inverse are rounded (467 us for 449 with the instructions' own, within a
-// step, which put one of v's scales in 60 a step off).  u's quotient, which only the
-// weights see, is the instruction's, within 2^-22; they are binary64 as above.
+// its scale's inverse are rounded (461 us for 449 with the instructions' own, within a
+// step, which put one of v's scales in 60 a step off; 467 with a root that takes every
+// number everywhere).  u's quotient, which only the weights see, is the instruction's,
+// within 2^-22; they are binary64 as above.
 template <class TG, bool TAIL>
 __device__ __forceinline__ void update8(const Tensor &T, const Rates &rates, uint32_t base,
                                         Lane &s, const Place &i) {
@@ -319,7 +332,17 @@ __device__ __forceinline__ void update8(const Tensor &T, const Rates &rates, uin
     const float g = rates.coef32 * grad_of<TG>(s, e);
     const float m0 = m8[e / 2][e % 2] * s.ms, r0 = v8[e / 2][e % 2] * s.vs;
     m[e] = rates.b1 * m0 + rates.omb1 * g;
-    r[e] = sqrtf((rates.b2 * r0) * r0 + (rates.omb2 * g) * g);
+    r[e] = (rates.b2 * r0) * r0 + (rates.omb2 * g) * g;
+  }
+  if (__all(fminf(fminf(r[0], r[1]), fminf(r[2], r[3])) >= 0x1p-96f)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = root_of(r[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = sqrtf(r[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
     const double t0 = double(s.w.v[e]);
     const float u = m[e] * __builtin_amdgcn_rcpf(r[e] * rates.root + rates.eps);
     s.w.v[e] = float(t0 - rates.decay * t0 - rates.step * double(u));
