@@ -37,18 +37,21 @@ namespace {
 using namespace zs_dev;
 
 constexpr int kThreads = 256;
-// Tokens sorted by counting: up to kTile as one tile (8192: 10 us, 6 and 11 as four
-// tiles and a merge), up to kOneMerge in tiles that one merge joins (16384 x 64: 35 us the
-// whole pass, 41 with smaller ones and two merges), beyond in small ones, since a tile
-// costs the square of its length (65536 x 64: 66 us for 72, 300000 x 64: 197 for 237).
+// Tokens sorted by counting: up to kTile as one tile (whole passes: 8192 x 64 27 us, 30 as
+// four tiles and a merge, 4097 x 64 23 and 29, 8192 x 5120 94 and 96), up to kOneMerge in
+// tiles that one merge joins (16384 x 64: 35 us, 41 with smaller ones and two merges),
+// beyond in small ones, since a tile costs the square of its length (65536 x 64: 66 us for
+// 72, 300000 x 64: 197 for 237).
 constexpr int kTile = 8192, kMiddleTile = 2048, kSmallTile = 1024;
 constexpr int64_t kOneMerge = 8 * kMiddleTile;  // kRuns of them
 constexpr int kPlaced = 32;       // of them, that a workgroup places
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kRuns = 8;          // runs merged at a time
-// Tokens of a long row's part: 8 where there are few tokens and their chains of loads
-// are what takes time (333 tokens: 16 us for 21), 32 where the parts' traffic counts.
+// Tokens of a long row's part: 8 where there are few tokens, 32 where the parts' traffic
+// counts.  Between 1100 and 2048 tokens, which are sorted, both are as fast (19 to 73 us
+// from 64 to 5120 columns, within 1 us of each other), but for one row of all tokens
+// (2048 x 1024: 33 us with 8, 29 with 32); the order of sums that the border makes is stated.
 constexpr int kRun = 32, kShortRun = 8;
 constexpr int64_t kFew = 2048;
 // Tokens that are not sorted, and the workgroups up to which that pays: each looks through

@@ -824,9 +824,13 @@ Way way_of(const zs_blocknorm_desc &d, int threads) {
   return w;
 }
 
-// The backward pass takes two rows at a time once every CU has some, where the
-// registers hold them; of rows that end inside a thread's eight columns only of long ones
-// (8192 x 2049 bf16: 71 us with two, 63 with one; 8192 x 5121: 136 and 149).
+// The backward pass takes two rows at a time from 1024 rows on, where the registers hold
+// them.  Row groups are counted for one row each, so that of narrow rows some CUs then
+// have none (1024 x 512: 128 workgroups of 8 rows), which costs nothing there: the row
+// groups' latencies are what takes time (1023 x 512 bf16 13.5 us, 1024 x 512 13.0; x 1024
+// 15.3 and 14.9).  Of rows that end inside a thread's eight columns only long ones (8192
+// rows, bf16, layer, with two and with one: 2049 columns 71 and 63 us, 3585 107 and 90, 4097
+// 123 and 130, 5121 136 and 150, 6143 153 and 165).
 bool pairs(const zs_blocknorm_desc &d) {
   return d.rows >= 4 * kCus && d.cols <= 8 * kPairThreads && d.dtype != ZS_F32 &&
          d.gate != ZS_GATE_SIGMOID && (d.cols % 8 == 0 || d.cols > 4096);
@@ -904,8 +908,8 @@ int zero_shard_blocknorm(const zs_blocknorm_desc *d, const void *x, const void *
                            static_cast<hipStream_t>(d->stream), A);
         return launched();
       };
-      // two rows at a time once every CU has some, where the registers hold them and the
-      // work on their ends (32768 x 511 bf16: 37 us with two, 33 with one)
+      // two rows at a time from 1024 rows on, where the registers hold them and the work
+      // on their ends (32768 x 511 bf16: 37 us with two, 33 with one)
       if constexpr (n.value == 1 && sizeof(typename TX::raw) == 2 && !wd.value && !tail.value)
         if (A.rows >= 4 * kCus) return launch(std::integral_constant<int, 2>{});
       return launch(std::integral_constant<int, 1>{});
