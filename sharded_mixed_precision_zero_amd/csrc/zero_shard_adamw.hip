@@ -274,10 +274,10 @@ __device__ __forceinline__ void put_weights(const Tensor &T, const Four<float> &
   else put_copy<F16, TAIL>(T, w, i);
 }
 
-// The root, rounded, of a number from 2^-96 on (below, the products' differences are no
-// normal numbers).  The instruction's is within a step; its neighbour is the nearer one
-// where the number lies beyond the product of the two, which what lies halfway between
-// them exceeds, squared, by less than any number could.  Tried with all of them.
+// The root, rounded, of a number from 2^-96 on (below, differences of products are no
+// normal numbers).  The instruction's is within a step; a neighbour is nearer where the
+// number lies beyond the product of the two: the square of what lies halfway between
+// them is that and a quarter of a step's square, and no number lies in between.
 __device__ __forceinline__ float root_of(float x) {
   const float s = __builtin_amdgcn_sqrtf(x);
   const float below = __uint_as_float(__float_as_uint(s) - 1);
