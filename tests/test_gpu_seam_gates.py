@@ -38,3 +38,19 @@ def test_gates_where_they_leave_binary32(size, cols):
         want = torch.where(part >= NORMAL, part, 0.0) * by
         # a gate or slope, and a product's rounding
         R.within(name, got, want, (2 * GATE + 2 * R.U) * want)
+
+
+@pytest.mark.parametrize("dtype", [F32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("rows,cols", [(40, 7), (700, 511), (1500, 1601), (300, 5123), (20, 9001)])
+def test_y_over_the_gates(rows, cols, kind, dtype):
+    """The bits of a new buffer, sum over x or block at once."""
+    x, block, z = (R.randn(rows, cols, seed=k).to(dtype) for k in range(3))
+    plan = Z.ZeroBlockNorm(rows=rows, cols=cols, dtype=dtype, kind=kind, gate="sigmoid")
+    total, y = torch.empty_like(x), torch.empty_like(x)
+    plan.forward(x, block, total, y, gate=z)
+    for over in (None, "x", "block"):
+        t = {"x": x.clone(), "block": block.clone(), None: torch.empty_like(x)}
+        gates = z.clone()
+        plan.forward(t["x"], t["block"], t[over], gates, gate=gates)
+        assert torch.equal(t[over], total) and torch.equal(gates, y), over
